@@ -83,6 +83,8 @@ extern "C" {
 #define GDN_STATUS_LOG_FULL 0x2u /* append entered with L == C: the slot-head was skipped */
 #define GDN_STATUS_BAD_LEN 0x4u  /* log length outside [0, C]: the slot-head was skipped */
 #define GDN_STATUS_TIMEOUT 0x8u  /* a bounded wait for an asynchronous copy gave up */
+#define GDN_STATUS_NO_PAGES 0x10u /* gdn_kv_plan: not enough free pages: the request was skipped */
+#define GDN_STATUS_BAD_PAGE 0x20u /* a page index outside [0, num_pages): its positions are left out */
 
 /* Flags (gdn_dims.flags). */
 #define GDN_QKV_BF16 (1u << 0)     /* q/k/v (or mixed_qkv and the conv cache) are bf16; else fp32 */
@@ -335,6 +337,129 @@ int gdn_log_bytes(const gdn_dims *dims, gdn_log_sizes *out);
  */
 int gdn_slot_reset(const gdn_dims *dims, const gdn_log *log, void *conv_pool, float *state_pool,
                    const int32_t *slots, int32_t n, int32_t *status, void *stream);
+
+/* ---- the paged cache of the attention layers ------------------------------------------
+ *
+ * Hybrid models interleave the recurrent layers above with attention layers. Their keys
+ * and values live in pages of page_size positions; a request's pages are listed, in order,
+ * in its row of a block table, so position j of request b is row j % page_size of page
+ * block_table[b][j / page_size]. One decode step of such a layer is
+ *
+ *   gdn_kv_plan    (once a step, for all layers) pages for the new tokens, and their slots;
+ *   gdn_kv_append  (every layer) the new tokens' rows written to their slots;
+ *   gdn_attn_decode or gdn_latent_decode (every layer) attention over the pages.
+ *
+ * All three read lengths and tables on the device, so a step is captured into a CUDA graph
+ * once and replayed as the lengths grow. The conventions at the top of this file hold
+ * (stream, status bits, no allocation); what they leave out is said at each call.
+ */
+typedef struct gdn_paged_kv {
+  void *k;               /* bf16 pages: [num_pages][page_size][num_kv_heads][dk] in k_strides */
+  void *v;               /* bf16 pages: [num_pages][page_size][num_kv_heads][dv] in v_strides;
+                            NULL: a latent cache (num_kv_heads 1, dv <= dk): one row a token,
+                            [latent (dv) | tail (dk - dv)], whose first dv elements are also
+                            the token's value */
+  int64_t k_strides[3];  /* elements between pages, positions of a page, heads; elements of one
+                            head are contiguous; multiples of 8, like dk and dv */
+  int64_t v_strides[3];
+  int32_t num_pages, page_size, num_kv_heads;
+  int32_t dk, dv;        /* dk <= 576, dv <= 512 */
+} gdn_paged_kv;
+
+/*
+ * gdn_kv_plan -- pages and slots for the new tokens of a step, in request order.
+ *   cached_len [B]: positions that request b holds before the step; < 0: padding (no tokens,
+ *       kv_len 0, pages untouched). A length that shrank since the last step (rejected
+ *       drafts) keeps its pages.
+ *   new_len [B]: new tokens of each request, or NULL (one each).
+ *   held [B]: pages in each request's row; held_out receives the count after the step.
+ *   block_table [B][max_pages]: entries held[b] .. held_out[b] - 1 are written.
+ *   free_list, free_count [1]: the first *free_count entries are the free pages, handed out
+ *       from the end; *free_count_out is what is left. The list itself is only read.
+ *   kv_len [B]: cached_len + new_len. cu_new [B + 1]: running sums of new_len (where each
+ *       request's tokens start among the packed new tokens; a sum past 2^31 - 1 stays there).
+ *   slot_map [slot_capacity] int64: token cu_new[b] + i gets the slot page * page_size +
+ *       offset of position cached_len[b] + i; entries past the last token get -1.
+ * kv_len may be cached_len, held_out may be held and free_count_out may be free_count.
+ * A request whose pages run out (of the free list: GDN_STATUS_NO_PAGES, and so for every
+ * later request that needs one), or whose length passes max_pages pages, 2^31 - 1 or
+ * slot_capacity, or is negative (GDN_STATUS_BAD_LEN) is skipped: kv_len = cached_len, no page, slots -1. An
+ * entry outside [0, num_pages) (GDN_STATUS_BAD_PAGE) gives its positions the slot -1.
+ * Requires batch <= 4096. free_list holds num_pages entries at most.
+ */
+int gdn_kv_plan(int32_t batch, int32_t max_pages, int32_t page_size, int32_t num_pages, int32_t slot_capacity,
+                const int32_t *cached_len, const int32_t *new_len, const int32_t *held, int32_t *block_table,
+                const int32_t *free_list, const int32_t *free_count, int32_t *kv_len, int32_t *cu_new,
+                int64_t *slot_map, int32_t *held_out, int32_t *free_count_out, int32_t *status, void *stream);
+
+/*
+ * gdn_kv_release -- gives the pages of n finished requests back: the first held[b] entries
+ * of row b = requests[i] are pushed on the free list in order and held[b] becomes 0. Entries
+ * of requests < 0 are ignored; >= batch sets GDN_STATUS_BAD_SLOT; a held count outside
+ * [0, max_pages], or a list that would pass num_pages entries, sets GDN_STATUS_BAD_LEN and
+ * leaves the request as it is. The requests of one call must be distinct.
+ */
+int gdn_kv_release(int32_t batch, int32_t max_pages, int32_t num_pages, const int32_t *requests, int32_t n,
+                   const int32_t *block_table, int32_t *held, int32_t *free_list, int32_t *free_count,
+                   int32_t *status, void *stream);
+
+/*
+ * gdn_kv_append -- rows of new tokens written to their slots.
+ *   k [n][num_kv_heads][dk], v [n][num_kv_heads][dv]; a latent cache: k [n][dv] is the
+ *       latent part and v [n][dk - dv] the tail (NULL when dk == dv).
+ *       k_strides, v_strides: elements between tokens and heads. bf16 with GDN_QKV_BF16 in
+ *       flags (copied bit for bit), else fp32 (rounded to nearest even). 16-byte aligned,
+ *       strides a multiple of 16 bytes.
+ *   slot_map [n] int64: distinct slots; < 0: the token is skipped; past the pages:
+ *       GDN_STATUS_BAD_SLOT, skipped.
+ */
+int gdn_kv_append(const gdn_paged_kv *kv, int32_t n, const void *k, const int64_t k_strides[2], const void *v,
+                  const int64_t v_strides[2], const int64_t *slot_map, uint32_t flags, int32_t *status, void *stream);
+
+typedef struct gdn_attn {
+  int32_t batch;             /* B */
+  int32_t num_tokens;        /* T >= 1: the newest positions of each request (1: decode) */
+  int32_t num_heads;         /* H, a multiple of num_kv_heads: head h reads kv head h / (H / num_kv_heads) */
+  int32_t max_pages;         /* columns of block_table */
+  int32_t window;            /* a query sees the last `window` positions up to its own; 0: all */
+  float scale;               /* multiplies q . k */
+  const void *q;             /* bf16 [B][T][H][dk] in q_strides */
+  int64_t q_strides[3];      /* elements between requests, tokens, heads; multiples of 8 */
+  const int32_t *block_table; /* [B][max_pages] */
+  const int32_t *kv_len;     /* [B] positions in the cache, the T new ones among them */
+  void *o;                   /* bf16 [B][T][H][dv] */
+  float *lse;                /* [B][T][H] log of the sum of exp(score), natural; or NULL */
+} gdn_attn;
+
+/*
+ * gdn_attn_decode -- attention of the newest T positions of every request over its pages:
+ * query t of request b is position p = kv_len[b] - T + t and
+ *   o = sum_j w_j v_j,  w = softmax over j <= p (and j > p - window) of scale * q . k_j.
+ * A query that sees nothing (p < 0, or no page of it is usable) gets o = 0 and
+ * lse = -inf. kv_len < 0 is padding: its rows are left unchanged. A length past max_pages
+ * pages skips the request (GDN_STATUS_BAD_LEN, rows unchanged). A page outside
+ * [0, num_pages) is left out (GDN_STATUS_BAD_PAGE). What the pages hold in positions that
+ * no query of the request sees has no influence, NaN included.
+ * Scores, softmax and sums are fp32; each weight is rounded to bf16 where it meets the
+ * values (head sizes 64, 128 and 256 with page sizes 16, 32, 64 or a multiple of 128, on the
+ * tensor cores); every other shape runs in fp32 on the CUDA cores.
+ * workspace: gdn_attn_workspace() bytes, 16-byte aligned; its contents need no care, but two
+ * calls that may run at the same time need one each. T * H / num_kv_heads <= 4096.
+ */
+int gdn_attn_decode(const gdn_paged_kv *kv, const gdn_attn *attn, void *workspace, size_t workspace_bytes,
+                    int32_t *status, void *stream);
+
+/*
+ * gdn_latent_decode -- the same over a latent cache (kv->v == NULL): every head reads the
+ * one row of a token, scores against all dk of it and sums its first dv (the absorbed form
+ * of latent attention: q already multiplied by the key expansion, o still to be multiplied
+ * by the value expansion). dk = 576, dv = 512 runs on the tensor cores.
+ */
+int gdn_latent_decode(const gdn_paged_kv *kv, const gdn_attn *attn, void *workspace, size_t workspace_bytes,
+                      int32_t *status, void *stream);
+
+/* Bytes of workspace for a call of either with this cache, batch, T and H. Host only. */
+int gdn_attn_workspace(const gdn_paged_kv *kv, int32_t batch, int32_t num_tokens, int32_t num_heads, size_t *bytes);
 
 #ifdef __cplusplus
 }

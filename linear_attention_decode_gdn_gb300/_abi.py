@@ -25,6 +25,8 @@ STATUS_BAD_SLOT = 0x1
 STATUS_LOG_FULL = 0x2
 STATUS_BAD_LEN = 0x4
 STATUS_TIMEOUT = 0x8
+STATUS_NO_PAGES = 0x10
+STATUS_BAD_PAGE = 0x20
 
 # flags
 QKV_BF16 = 1 << 0
@@ -43,7 +45,8 @@ TEST_STARVE_WAIT = 1 << 31
 # every symbol include/gdn.h declares
 EXPORTS = ("gdn_version", "gdn_strerror", "gdn_last_error", "gdn_conv_l2norm", "gdn_decode_dense",
            "gdn_decode_append", "gdn_decode_merge", "gdn_decode_step", "gdn_decode_verify",
-           "gdn_prefill", "gdn_log_bytes", "gdn_slot_reset")
+           "gdn_prefill", "gdn_log_bytes", "gdn_slot_reset", "gdn_kv_plan", "gdn_kv_release",
+           "gdn_kv_append", "gdn_attn_decode", "gdn_latent_decode", "gdn_attn_workspace")
 
 
 class Dims(ctypes.Structure):
@@ -72,6 +75,20 @@ class LogSizes(ctypes.Structure):
     _fields_ = [("k_log", ctypes.c_size_t), ("u_log", ctypes.c_size_t), ("lam_log", ctypes.c_size_t),
                 ("ell", ctypes.c_size_t), ("len", ctypes.c_size_t), ("residency", ctypes.c_size_t),
                 ("total", ctypes.c_size_t)]
+
+
+class PagedKV(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_strides", ctypes.c_int64 * 3),
+                ("v_strides", ctypes.c_int64 * 3), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("dk", ctypes.c_int32),
+                ("dv", ctypes.c_int32)]
+
+
+class Attn(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("num_tokens", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("window", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("q", ctypes.c_void_p), ("q_strides", ctypes.c_int64 * 3), ("block_table", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p)]
 
 
 _lock = threading.Lock()
@@ -103,6 +120,19 @@ def _declare(lib):
     lib.gdn_log_bytes.argtypes = [P(Dims), P(LogSizes)]
     lib.gdn_slot_reset.restype = ctypes.c_int
     lib.gdn_slot_reset.argtypes = [P(Dims), P(Log), vp, vp, vp, ctypes.c_int32, vp, vp]
+    i32 = ctypes.c_int32
+    lib.gdn_kv_plan.restype = ctypes.c_int
+    lib.gdn_kv_plan.argtypes = [i32] * 5 + [vp] * 13
+    lib.gdn_kv_release.restype = ctypes.c_int
+    lib.gdn_kv_release.argtypes = [i32, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp]
+    lib.gdn_kv_append.restype = ctypes.c_int
+    lib.gdn_kv_append.argtypes = [P(PagedKV), i32, vp, vp, vp, vp, vp, ctypes.c_uint32, vp, vp]
+    for name in ("gdn_attn_decode", "gdn_latent_decode"):
+        fn = getattr(lib, name)
+        fn.restype = ctypes.c_int
+        fn.argtypes = [P(PagedKV), P(Attn), vp, ctypes.c_size_t, vp, vp]
+    lib.gdn_attn_workspace.restype = ctypes.c_int
+    lib.gdn_attn_workspace.argtypes = [P(PagedKV), i32, i32, i32, P(ctypes.c_size_t)]
     return lib
 
 

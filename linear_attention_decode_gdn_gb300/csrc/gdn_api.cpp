@@ -8,6 +8,7 @@
 
 #include "gdn.h"
 #include "gdn_internal.h"
+#include "gdn_kv.h"
 
 namespace {
 
@@ -191,6 +192,101 @@ int decode_common(int mode, const gdn_dims* dims, const gdn_inputs* in, float* p
   return launched(gdn::launch_decode(mode, p, static_cast<cudaStream_t>(stream)), name);
 }
 
+// ---- the paged cache ---------------------------------------------------------------------
+constexpr int kMaxCacheDk = 576, kMaxCacheDv = 512;
+constexpr int kMaxAttnCols = 4096;  // query rows per kv head in one call
+
+bool strides_ok(const int64_t* s, int n, int multiple) {
+  for (int i = 0; i < n; ++i)
+    if (s[i] < 0 || s[i] % multiple != 0) return false;
+  return true;
+}
+
+int check_kv(const gdn_paged_kv* kv) {
+  if (kv == nullptr) return fail(GDN_ERR_INVALID_ARG, "kv is NULL");
+  if (kv->num_pages <= 0 || kv->page_size <= 0 || kv->num_kv_heads <= 0 || kv->dk <= 0 || kv->dv <= 0)
+    return fail(GDN_ERR_INVALID_ARG, "num_pages, page_size, num_kv_heads, dk and dv must be > 0");
+  if (kv->k == nullptr) return fail(GDN_ERR_INVALID_ARG, "kv->k is required");
+  if (kv->dk > kMaxCacheDk || kv->dv > kMaxCacheDv || kv->dk % 8 != 0 || kv->dv % 8 != 0)
+    return fail(GDN_ERR_UNSUPPORTED, "cache rows dk=%d dv=%d not built (multiples of 8, dk <= %d, dv <= %d)", kv->dk,
+                kv->dv, kMaxCacheDk, kMaxCacheDv);
+  if (kv->v == nullptr && (kv->num_kv_heads != 1 || kv->dv > kv->dk))
+    return fail(GDN_ERR_INVALID_ARG, "a latent cache (v NULL) has one head and dv <= dk");
+  if (!aligned16(kv->k) || !aligned16(kv->v) || !strides_ok(kv->k_strides, 3, 8) ||
+      (kv->v != nullptr && !strides_ok(kv->v_strides, 3, 8)))
+    return fail(GDN_ERR_UNSUPPORTED, "cache pages must be 16-byte aligned, with strides >= 0 that are multiples of 8");
+  return GDN_OK;
+}
+
+int check_attn(const gdn_paged_kv* kv, const gdn_attn* a, const void* workspace) {
+  if (int rc = check_kv(kv)) return rc;
+  if (a == nullptr) return fail(GDN_ERR_INVALID_ARG, "attn is NULL");
+  if (a->batch < 0 || a->num_tokens <= 0 || a->num_heads <= 0 || a->max_pages <= 0 || a->window < 0)
+    return fail(GDN_ERR_INVALID_ARG, "batch and window must be >= 0, num_tokens, num_heads and max_pages > 0");
+  if (a->num_heads % kv->num_kv_heads != 0)
+    return fail(GDN_ERR_INVALID_ARG, "num_heads %d is not a multiple of num_kv_heads %d", a->num_heads, kv->num_kv_heads);
+  if (static_cast<long long>(a->num_tokens) * (a->num_heads / kv->num_kv_heads) > kMaxAttnCols)
+    return fail(GDN_ERR_UNSUPPORTED, "num_tokens * num_heads / num_kv_heads must be at most %d", kMaxAttnCols);
+  if (static_cast<long long>(a->batch) * a->num_tokens * a->num_heads > 0x7fffffffLL ||
+      static_cast<long long>(a->max_pages) * kv->page_size > 0x7fffffffLL)
+    return fail(GDN_ERR_INVALID_ARG, "batch * num_tokens * num_heads or max_pages * page_size too large");
+  if (a->batch == 0) return GDN_OK;
+  if (a->q == nullptr || a->block_table == nullptr || a->kv_len == nullptr || a->o == nullptr || workspace == nullptr)
+    return fail(GDN_ERR_INVALID_ARG, "q, block_table, kv_len, o and workspace are required");
+  if (!aligned16(a->q) || !aligned16(a->o) || !aligned16(workspace) || !strides_ok(a->q_strides, 3, 8))
+    return fail(GDN_ERR_UNSUPPORTED, "q, o and workspace must be 16-byte aligned, q strides >= 0 and multiples of 8");
+  return GDN_OK;
+}
+
+int attend(const gdn_paged_kv* kv, const gdn_attn* a, void* workspace, size_t workspace_bytes, int32_t* status,
+           void* stream, bool latent, const char* name) {
+  if (int rc = check_attn(kv, a, workspace)) return rc;
+  if ((kv->v == nullptr) != latent)
+    return fail(GDN_ERR_INVALID_ARG, latent ? "gdn_latent_decode reads a latent cache (kv->v NULL)"
+                                            : "gdn_attn_decode needs kv->v (gdn_latent_decode reads latent caches)");
+  if (a->batch == 0) return GDN_OK;
+  const int group = a->num_heads / kv->num_kv_heads;
+  const gdn::AttnPlan plan = gdn::attn_plan(*kv, a->num_tokens * group);
+  const size_t need = gdn::attn_workspace_bytes(plan, kv->dv);
+  if (workspace_bytes < need)
+    return fail(GDN_ERR_INVALID_ARG, "workspace of %zu bytes, %zu are needed (gdn_attn_workspace)", workspace_bytes, need);
+  gdn::AttnParams p{};
+  p.B = a->batch;
+  p.T = a->num_tokens;
+  p.H = a->num_heads;
+  p.heads_kv = kv->num_kv_heads;
+  p.group = group;
+  p.dk = kv->dk;
+  p.dv = kv->dv;
+  p.num_pages = kv->num_pages;
+  p.page_size = kv->page_size;
+  p.max_pages = a->max_pages;
+  p.window = a->window;
+  p.cols = a->num_tokens * group;
+  p.scale_log2 = a->scale * 1.44269504088896340736f;
+  p.q = a->q;
+  p.q_b = a->q_strides[0];
+  p.q_t = a->q_strides[1];
+  p.q_h = a->q_strides[2];
+  const int64_t* vs = latent ? kv->k_strides : kv->v_strides;
+  p.k = kv->k;
+  p.v = latent ? kv->k : kv->v;
+  p.k_page = kv->k_strides[0];
+  p.k_pos = kv->k_strides[1];
+  p.k_head = kv->k_strides[2];
+  p.v_page = vs[0];
+  p.v_pos = vs[1];
+  p.v_head = vs[2];
+  p.table = a->block_table;
+  p.kv_len = a->kv_len;
+  p.o = a->o;
+  p.lse = a->lse;
+  p.status = status;
+  p.records = static_cast<int64_t*>(workspace);
+  p.partials = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + gdn::kRecordBytes);
+  return launched(gdn::launch_attn(plan, p, static_cast<cudaStream_t>(stream)), name);
+}
+
 }  // namespace
 
 extern "C" {
@@ -357,6 +453,93 @@ int gdn_slot_reset(const gdn_dims* dims, const gdn_log* log, void* conv_pool, fl
   p.state = state_pool;
   p.status = status;
   return launched(gdn::launch_slot_reset(p, static_cast<cudaStream_t>(stream)), "gdn_slot_reset");
+}
+
+int gdn_kv_plan(int32_t batch, int32_t max_pages, int32_t page_size, int32_t num_pages, int32_t slot_capacity,
+                const int32_t* cached_len, const int32_t* new_len, const int32_t* held, int32_t* block_table,
+                const int32_t* free_list, const int32_t* free_count, int32_t* kv_len, int32_t* cu_new,
+                int64_t* slot_map, int32_t* held_out, int32_t* free_count_out, int32_t* status, void* stream) {
+  if (batch < 0 || max_pages <= 0 || page_size <= 0 || num_pages <= 0 || slot_capacity < 0)
+    return fail(GDN_ERR_INVALID_ARG, "batch and slot_capacity must be >= 0, max_pages, page_size and num_pages > 0");
+  if (batch > gdn::kMaxPlanBatch)
+    return fail(GDN_ERR_UNSUPPORTED, "batch %d > %d", batch, gdn::kMaxPlanBatch);
+  if (batch == 0) return GDN_OK;
+  if (cached_len == nullptr || held == nullptr || block_table == nullptr || free_list == nullptr ||
+      free_count == nullptr || kv_len == nullptr || cu_new == nullptr || held_out == nullptr ||
+      free_count_out == nullptr || (slot_map == nullptr && slot_capacity > 0))
+    return fail(GDN_ERR_INVALID_ARG, "every array but new_len and status is required");
+  gdn::KvPlanParams p{batch,   max_pages, page_size,  num_pages, slot_capacity, cached_len, new_len,        held,
+                      block_table, free_list, free_count, kv_len,    cu_new,        slot_map,   held_out, free_count_out,
+                      status};
+  return launched(gdn::launch_kv_plan(p, static_cast<cudaStream_t>(stream)), "gdn_kv_plan");
+}
+
+int gdn_kv_release(int32_t batch, int32_t max_pages, int32_t num_pages, const int32_t* requests, int32_t n,
+                   const int32_t* block_table, int32_t* held, int32_t* free_list, int32_t* free_count,
+                   int32_t* status, void* stream) {
+  if (batch < 0 || max_pages <= 0 || num_pages <= 0 || n < 0)
+    return fail(GDN_ERR_INVALID_ARG, "batch and n must be >= 0, max_pages and num_pages > 0");
+  if (n == 0) return GDN_OK;
+  if (requests == nullptr || block_table == nullptr || held == nullptr || free_list == nullptr || free_count == nullptr)
+    return fail(GDN_ERR_INVALID_ARG, "requests, block_table, held, free_list and free_count are required");
+  gdn::KvReleaseParams p{batch, max_pages, num_pages, n, requests, block_table, held, free_list, free_count, status};
+  return launched(gdn::launch_kv_release(p, static_cast<cudaStream_t>(stream)), "gdn_kv_release");
+}
+
+int gdn_kv_append(const gdn_paged_kv* kv, int32_t n, const void* k, const int64_t k_strides[2], const void* v,
+                  const int64_t v_strides[2], const int64_t* slot_map, uint32_t flags, int32_t* status,
+                  void* stream) {
+  if (int rc = check_kv(kv)) return rc;
+  if (n < 0) return fail(GDN_ERR_INVALID_ARG, "n < 0");
+  if ((flags & ~GDN_QKV_BF16) != 0u) return fail(GDN_ERR_INVALID_ARG, "gdn_kv_append knows GDN_QKV_BF16 only");
+  const bool latent = kv->v == nullptr;
+  const int tail = latent ? kv->dk - kv->dv : kv->dv;
+  if (n == 0) return GDN_OK;
+  if (k == nullptr || k_strides == nullptr || slot_map == nullptr || (tail > 0 && (v == nullptr || v_strides == nullptr)))
+    return fail(GDN_ERR_INVALID_ARG, "k, v, their strides and slot_map are required");
+  const bool bf16 = (flags & GDN_QKV_BF16) != 0u;
+  const int multiple = bf16 ? 8 : 4;
+  if (!aligned16(k) || !strides_ok(k_strides, 2, multiple) ||
+      (tail > 0 && (!aligned16(v) || !strides_ok(v_strides, 2, multiple))))
+    return fail(GDN_ERR_UNSUPPORTED, "k and v must be 16-byte aligned, with strides >= 0 that are multiples of 16 bytes");
+  gdn::KvAppendParams p{};
+  p.n = n;
+  p.heads = kv->num_kv_heads;
+  p.page_size = kv->page_size;
+  p.num_slots = static_cast<int64_t>(kv->num_pages) * kv->page_size;
+  p.bf16 = bf16;
+  p.a = {k, k_strides[0], k_strides[1], kv->k, kv->k_strides[0], kv->k_strides[1], kv->k_strides[2],
+         static_cast<uint32_t>((latent ? kv->dv : kv->dk) / 8)};
+  if (tail > 0) {
+    const int64_t* to = latent ? kv->k_strides : kv->v_strides;
+    void* dst = latent ? static_cast<void*>(static_cast<uint16_t*>(kv->k) + kv->dv) : kv->v;
+    p.b = {v, v_strides[0], v_strides[1], dst, to[0], to[1], to[2], static_cast<uint32_t>(tail / 8)};
+  }
+  p.slot_map = slot_map;
+  p.status = status;
+  return launched(gdn::launch_kv_append(p, static_cast<cudaStream_t>(stream)), "gdn_kv_append");
+}
+
+int gdn_attn_decode(const gdn_paged_kv* kv, const gdn_attn* attn, void* workspace, size_t workspace_bytes,
+                    int32_t* status, void* stream) {
+  return attend(kv, attn, workspace, workspace_bytes, status, stream, false, "gdn_attn_decode");
+}
+
+int gdn_latent_decode(const gdn_paged_kv* kv, const gdn_attn* attn, void* workspace, size_t workspace_bytes,
+                      int32_t* status, void* stream) {
+  return attend(kv, attn, workspace, workspace_bytes, status, stream, true, "gdn_latent_decode");
+}
+
+int gdn_attn_workspace(const gdn_paged_kv* kv, int32_t batch, int32_t num_tokens, int32_t num_heads, size_t* bytes) {
+  if (int rc = check_kv(kv)) return rc;
+  if (bytes == nullptr) return fail(GDN_ERR_INVALID_ARG, "bytes is NULL");
+  if (batch < 0 || num_tokens <= 0 || num_heads <= 0 || num_heads % kv->num_kv_heads != 0)
+    return fail(GDN_ERR_INVALID_ARG, "batch >= 0, num_tokens > 0 and num_heads a multiple of num_kv_heads");
+  const long long cols = static_cast<long long>(num_tokens) * (num_heads / kv->num_kv_heads);
+  if (cols > kMaxAttnCols)
+    return fail(GDN_ERR_UNSUPPORTED, "num_tokens * num_heads / num_kv_heads must be at most %d", kMaxAttnCols);
+  *bytes = gdn::attn_workspace_bytes(gdn::attn_plan(*kv, static_cast<int>(cols)), kv->dv);
+  return GDN_OK;
 }
 
 }  // extern "C"

@@ -1,0 +1,320 @@
+// gdn_attn.cu -- attention over the paged cache on the CUDA cores (every shape), and the
+// kernel that joins the partial results of split units for both attention kernels.
+#include "gdn_attn.cuh"
+
+#include <cuda_bf16.h>
+
+namespace gdn {
+
+namespace {
+
+using namespace attn;
+
+constexpr int kThreads = 128;  // one thread a position of the tile
+constexpr int kCols = 8;       // query rows a CTA takes at a time
+constexpr int kMaxDk = 576, kMaxDv = 512;
+constexpr int kPairs = kMaxDv / (2 * kThreads);  // pairs of value elements a thread sums
+
+__device__ __forceinline__ float lo_bf16(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+
+struct GeneralSmem {
+  float q[kMaxDk][kCols];  // element-major: a thread reads its columns as two vectors
+  float w[kTile][kCols];
+  int64_t v_at[kTile];     // element offset of the position's value row; -1: not in use
+  float warp_max[kThreads / 32][kCols], warp_sum[kThreads / 32][kCols];
+  ShareScratch scratch;
+};
+
+// One online softmax over the unit's tiles, in fp32 throughout. Scores: a thread owns a
+// position and reads its key row in 16-byte vectors, the query elements are broadcast from
+// shared memory. Sums: a thread owns pairs of value elements and runs over the positions.
+// This is the kernel for shapes that have no tensor-core instance, so it trades speed for
+// having no shape conditions but multiples of eight.
+__global__ void __launch_bounds__(kThreads) gdn_attn_general_kernel(const AttnParams p) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  GeneralSmem& sm = *reinterpret_cast<GeneralSmem*>(smem_raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  griddep_launch_dependents();
+  griddep_wait();
+  write_empty<kThreads>(p);
+  const Share share = find_share<kThreads>(p, sm.scratch);
+  if (tid == 0) write_record(p, share);
+  Walk walk(share);
+  Segment seg;
+  uint32_t bad = 0;
+  while (walk.next(p, &seg)) {
+    const int cols = min(p.ncol, p.cols - seg.col_base);
+    __syncthreads();  // the last segment's shared arrays are free
+    for (int i = tid; i < p.dk / 8 * kCols; i += kThreads) {
+      const int c = i % kCols, e = i / kCols * 8;
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      if (c < cols) {
+        const int col = seg.col_base + c, t = col / p.group, h = seg.kv_head * p.group + (col - t * p.group);
+        x = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + seg.b * p.q_b + t * p.q_t +
+                                                 h * p.q_h + e));
+      }
+      const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        sm.q[e + 2 * k][c] = lo_bf16(u[k]);
+        sm.q[e + 2 * k + 1][c] = hi_bf16(u[k]);
+      }
+    }
+    float m[kCols], l[kCols], acc[kPairs][kCols][2];
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) {
+      m[c] = -INFINITY;
+      l[c] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) acc[j][c][0] = acc[j][c][1] = 0.0f;
+    }
+    const int32_t lower = lower_bound_of(p, seg.n, seg.col_base / p.group);
+    __syncthreads();
+
+    for (int tile = seg.tile; tile < seg.tile + seg.tiles; ++tile) {
+      const int32_t pos = tile * kTile + tid;
+      float s[kCols];
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) s[c] = 0.0f;
+      int64_t v_at = -1;
+      if (pos < seg.n && pos >= lower) {
+        const int32_t page = __ldg(p.table + static_cast<int64_t>(seg.b) * p.max_pages + pos / p.page_size);
+        if (page < 0 || page >= p.num_pages) {
+          bad = GDN_STATUS_BAD_PAGE;
+        } else {
+          const int32_t in = pos % p.page_size;
+          v_at = page * p.v_page + in * p.v_pos + seg.kv_head * p.v_head;
+          const uint16_t* k = static_cast<const uint16_t*>(p.k) + page * p.k_page + in * p.k_pos + seg.kv_head * p.k_head;
+          for (int e = 0; e < p.dk; e += 8) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4*>(k + e));
+            const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float kj = j & 1 ? hi_bf16(u[j >> 1]) : lo_bf16(u[j >> 1]);
+#pragma unroll
+              for (int c = 0; c < kCols; ++c) s[c] = fmaf(kj, sm.q[e + j][c], s[c]);
+            }
+          }
+        }
+      }
+      sm.v_at[tid] = v_at;
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) {
+        const int col = seg.col_base + c, t = col / p.group;
+        const int32_t last = seg.n - p.T + t;
+        const bool seen = c < cols && v_at >= 0 && pos <= last && (p.window <= 0 || pos > last - p.window);
+        s[c] = seen ? s[c] * p.scale_log2 : -INFINITY;
+        float x = s[c];
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+        if (lane == 0) sm.warp_max[warp][c] = x;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) {
+        float top = m[c];
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) top = fmaxf(top, sm.warp_max[w][c]);
+        const float ref = top == -INFINITY ? 0.0f : top;  // nothing seen yet: every weight is 0
+        const float f = exp2f(m[c] - ref);
+        m[c] = top;
+        const float w = exp2f(s[c] - ref);
+        l[c] = l[c] * f + w;
+        sm.w[tid][c] = w;
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          acc[j][c][0] *= f;
+          acc[j][c][1] *= f;
+        }
+      }
+      __syncthreads();
+      for (int i = 0; i < kTile; ++i) {
+        const int64_t at = sm.v_at[i];
+        if (at < 0) continue;
+        float w[kCols];
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) w[c] = sm.w[i][c];
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          const int d = 2 * (tid + j * kThreads);
+          if (d >= p.dv) continue;
+          const uint32_t x = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.v) + at + d));
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) {
+            // a weight of zero leaves the value out, whatever it holds
+            if (w[c] == 0.0f) continue;
+            acc[j][c][0] = fmaf(w[c], lo_bf16(x), acc[j][c][0]);
+            acc[j][c][1] = fmaf(w[c], hi_bf16(x), acc[j][c][1]);
+          }
+        }
+      }
+      __syncthreads();  // weights, offsets and maxima are read
+    }
+
+    // the threads' sums of weights, added
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) {
+      const float x = warp_sum(l[c]);
+      if (lane == 0) sm.warp_sum[warp][c] = x;
+    }
+    __syncthreads();
+    float* part = partial_of(p, blockIdx.x, seg.index == 0 ? 0 : 1);
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) {
+      if (c >= cols) continue;
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) sum += sm.warp_sum[w][c];
+      if (seg.whole) {
+        const int64_t row = row_of(p, seg.b, seg.kv_head, seg.col_base + c);
+        const float inv = sum > 0.0f ? 1.0f / sum : (sum == sum ? 0.0f : sum);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          const int d = 2 * (tid + j * kThreads);
+          if (d < p.dv)
+            *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.o) + row * p.dv + d) =
+                __floats2bfloat162_rn(acc[j][c][0] * inv, acc[j][c][1] * inv);
+        }
+        if (tid == 0 && p.lse != nullptr) p.lse[row] = lse_of(m[c], sum);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+          const int d = 2 * (tid + j * kThreads);
+          if (d < p.dv) *reinterpret_cast<float2*>(part + c * p.dv + d) = make_float2(acc[j][c][0], acc[j][c][1]);
+        }
+        if (tid == 0) {
+          part[p.ncol * p.dv + c] = m[c];
+          part[p.ncol * p.dv + p.ncol + c] = sum;
+        }
+      }
+    }
+  }
+  if (bad != 0u) atomic_status(p.status, bad);
+}
+
+constexpr int kJoinThreads = 128;
+
+// Block (i, part) looks at the border between the shares of CTAs i - 1 and i (i >= 1). Where
+// it is the first border inside a unit, the block adds the unit's partial results for the
+// columns part, part + parts, ... in the order of the CTAs, so the sums do not depend on
+// timing: m = max m_j, l = sum 2^(m_j - m) l_j, o = sum 2^(m_j - m) o_j / l.
+__global__ void __launch_bounds__(kJoinThreads) gdn_attn_join_kernel(const AttnParams p) {
+  __shared__ float weight[kMaxAttnCtas];
+  __shared__ float total[2];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int i = blockIdx.x + 1, tid = threadIdx.x;
+  const int64_t* rec = p.records + static_cast<size_t>(i) * kRecordInts;
+  if (rec[1] < 0 || rec[0] <= rec[2]) return;       // no work, or the unit begins here
+  const int64_t unit_start = rec[2], unit_end = rec[3];
+  if (rec[-kRecordInts] > unit_start) return;       // an earlier border is inside the unit too
+  const int b = static_cast<int>(rec[4]), unit = static_cast<int>(rec[5]);
+  const int kv_head = unit / p.col_groups, col_base = (unit - kv_head * p.col_groups) * p.ncol;
+  const int cols = min(p.ncol, p.cols - col_base);
+  // CTAs i - 1 .. last - 1 hold a part of it; shares are equal, so `last` is not far to seek
+  int last = i + 1;
+  while (last < p.ctas) {
+    const int64_t* r = p.records + static_cast<size_t>(last) * kRecordInts;
+    if (r[1] < 0 || r[0] >= unit_end) break;
+    ++last;
+  }
+  const int parts = last - (i - 1);
+  // the unit is CTA i - 1's last segment: its first one only where the share begins with it
+  const int slot0 = rec[-kRecordInts] == unit_start ? 0 : 1;
+  for (int c = blockIdx.y; c < cols; c += gridDim.y) {
+    __syncthreads();
+    for (int j = tid; j < parts; j += kJoinThreads)
+      weight[j] = partial_of(p, i - 1 + j, j == 0 ? slot0 : 0)[p.ncol * p.dv + c];
+    __syncthreads();
+    if (tid < 32) {
+      float m = -INFINITY;
+      for (int j = tid; j < parts; j += 32) m = fmaxf(m, weight[j]);
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      const float ref = m == -INFINITY ? 0.0f : m;
+      float l = 0.0f;
+      for (int j = tid; j < parts; j += 32) {
+        const float f = exp2f(weight[j] - ref);
+        weight[j] = f;
+        l += f * partial_of(p, i - 1 + j, j == 0 ? slot0 : 0)[p.ncol * p.dv + p.ncol + c];
+      }
+      l = warp_sum(l);
+      if (tid == 0) {
+        total[0] = m;
+        total[1] = l;
+      }
+    }
+    __syncthreads();
+    const float l = total[1], inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
+    const int64_t row = row_of(p, b, kv_head, col_base + c);
+    for (int d = 2 * tid; d < p.dv; d += 2 * kJoinThreads) {
+      float2 o = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+      for (int j = 0; j < parts; ++j) {
+        const float2 x =
+            *reinterpret_cast<const float2*>(partial_of(p, i - 1 + j, j == 0 ? slot0 : 0) + c * p.dv + d);
+        o.x = fmaf(weight[j], x.x, o.x);
+        o.y = fmaf(weight[j], x.y, o.y);
+      }
+      *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.o) + row * p.dv + d) =
+          __floats2bfloat162_rn(o.x * inv, o.y * inv);
+    }
+    if (tid == 0 && p.lse != nullptr) p.lse[row] = lse_of(total[0], l);
+  }
+}
+
+cudaError_t launch_overlapped(void (*kernel)(const AttnParams), const AttnParams& p, dim3 grid, unsigned threads,
+                              size_t smem, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace
+
+AttnPlan attn_plan(const gdn_paged_kv& kv, int cols) {
+  (void)kv;
+  (void)cols;
+  return {false, kCols, kMaxAttnCtas};
+}
+
+size_t attn_workspace_bytes(const AttnPlan& plan, int dv) {
+  return kRecordBytes + static_cast<size_t>(plan.max_ctas) * 2 * plan.ncol * (dv + 2) * sizeof(float);
+}
+
+cudaError_t launch_attn_general(AttnParams& p, cudaStream_t stream) {
+  const cudaError_t err = cudaFuncSetAttribute(gdn_attn_general_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(sizeof(GeneralSmem)));
+  if (err != cudaSuccess) return err;
+  return launch_overlapped(gdn_attn_general_kernel, p, dim3(p.ctas), kThreads, sizeof(GeneralSmem), stream);
+}
+
+cudaError_t launch_attn_join(const AttnParams& p, cudaStream_t stream) {
+  const unsigned parts = static_cast<unsigned>(p.cols < p.ncol ? p.cols : p.ncol);
+  return launch_overlapped(gdn_attn_join_kernel, p, dim3(p.ctas - 1, parts), kJoinThreads, 0, stream);
+}
+
+cudaError_t launch_attn(const AttnPlan& plan, AttnParams& p, cudaStream_t stream) {
+  p.ncol = plan.ncol;
+  p.col_groups = (p.cols + p.ncol - 1) / p.ncol;
+  // at most one CTA a tile that there could be
+  const int64_t positions = static_cast<int64_t>(p.max_pages) * p.page_size;
+  const int64_t per_unit = (positions + kTile - 1) / kTile;
+  const int64_t most = per_unit * p.B * p.heads_kv * p.col_groups;
+  p.ctas = static_cast<int>(most < 1 ? 1 : most < plan.max_ctas ? most : plan.max_ctas);
+  const cudaError_t err = launch_attn_general(p, stream);
+  if (err != cudaSuccess) return err;
+  // a unit of one tile is never split
+  return p.ctas > 1 && per_unit > 1 ? launch_attn_join(p, stream) : cudaSuccess;
+}
+
+}  // namespace gdn
