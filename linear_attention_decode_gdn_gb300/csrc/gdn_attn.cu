@@ -51,8 +51,8 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_general_kernel(const AttnPa
       uint4 x = make_uint4(0u, 0u, 0u, 0u);
       if (c < cols) {
         const int col = seg.col_base + c, t = col / p.group, h = seg.kv_head * p.group + (col - t * p.group);
-        x = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + seg.b * p.q_b + t * p.q_t +
-                                                 h * p.q_h + e));
+        x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + seg.b * p.q_b + t * p.q_t +
+                                              h * p.q_h + e);
       }
       const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_general_kernel(const AttnPa
       for (int c = 0; c < kCols; ++c) s[c] = 0.0f;
       int64_t v_at = -1;
       if (pos < seg.n && pos >= lower) {
-        const int32_t page = __ldg(p.table + static_cast<int64_t>(seg.b) * p.max_pages + pos / p.page_size);
+        const int32_t page = p.table[static_cast<int64_t>(seg.b) * p.max_pages + pos / p.page_size];
         if (page < 0 || page >= p.num_pages) {
           bad = GDN_STATUS_BAD_PAGE;
         } else {
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_general_kernel(const AttnPa
           v_at = page * p.v_page + in * p.v_pos + seg.kv_head * p.v_head;
           const uint16_t* k = static_cast<const uint16_t*>(p.k) + page * p.k_page + in * p.k_pos + seg.kv_head * p.k_head;
           for (int e = 0; e < p.dk; e += 8) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4*>(k + e));
+            const uint4 x = *reinterpret_cast<const uint4*>(k + e);
             const uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_general_kernel(const AttnPa
         for (int j = 0; j < kPairs; ++j) {
           const int d = 2 * (tid + j * kThreads);
           if (d >= p.dv) continue;
-          const uint32_t x = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.v) + at + d));
+          const uint32_t x = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.v) + at + d);
 #pragma unroll
           for (int c = 0; c < kCols; ++c) {
             // a weight of zero leaves the value out, whatever it holds
@@ -281,10 +281,22 @@ cudaError_t launch_overlapped(void (*kernel)(const AttnParams), const AttnParams
 
 }  // namespace
 
+// The tensor-core kernel needs rows made of whole 64-element chunks, pages that fill a tile in
+// whole boxes, and strides that a tensor map can hold.
 AttnPlan attn_plan(const gdn_paged_kv& kv, int cols) {
-  (void)kv;
-  (void)cols;
-  return {false, kCols, kMaxAttnCtas};
+  const bool latent = kv.v == nullptr;
+  const bool heads = latent ? kv.dk == 576 && kv.dv == 512
+                            : kv.dk == kv.dv && (kv.dk == 64 || kv.dk == 128 || kv.dk == 256);
+  const int ps = kv.page_size;
+  const bool pages = ps == 16 || ps == 32 || ps == 64 || ps % kTile == 0;
+  auto strides = [&](const int64_t* s) {
+    const int32_t extent[3] = {kv.num_pages, kv.page_size, kv.num_kv_heads};
+    for (int i = 0; i < 3; ++i)
+      if (extent[i] > 1 && (s[i] <= 0 || s[i] >= (int64_t{1} << 39))) return false;
+    return true;
+  };
+  if (!heads || !pages || !strides(kv.k_strides) || (!latent && !strides(kv.v_strides))) return {false, kCols, kMaxAttnCtas};
+  return {true, cols <= 16 ? 16 : cols <= 32 || latent ? 32 : 64, kSms};
 }
 
 size_t attn_workspace_bytes(const AttnPlan& plan, int dv) {
@@ -311,7 +323,7 @@ cudaError_t launch_attn(const AttnPlan& plan, AttnParams& p, cudaStream_t stream
   const int64_t per_unit = (positions + kTile - 1) / kTile;
   const int64_t most = per_unit * p.B * p.heads_kv * p.col_groups;
   p.ctas = static_cast<int>(most < 1 ? 1 : most < plan.max_ctas ? most : plan.max_ctas);
-  const cudaError_t err = launch_attn_general(p, stream);
+  const cudaError_t err = plan.tensor ? launch_attn_tc(p, stream) : launch_attn_general(p, stream);
   if (err != cudaSuccess) return err;
   // a unit of one tile is never split
   return p.ctas > 1 && per_unit > 1 ? launch_attn_join(p, stream) : cudaSuccess;

@@ -24,7 +24,7 @@ struct Tiles {
 
 // Cached positions of request b; -1 where the request is to be skipped.
 __device__ __forceinline__ int32_t length_of(const AttnParams& p, int b) {
-  const int32_t n = __ldg(p.kv_len + b);
+  const int32_t n = p.kv_len[b];
   return n < 0 || n > static_cast<int64_t>(p.max_pages) * p.page_size ? -1 : n;
 }
 
@@ -209,7 +209,7 @@ __device__ __forceinline__ int64_t row_of(const AttnParams& p, int b, int kv_hea
 template <int THREADS>
 __device__ __forceinline__ void write_empty(const AttnParams& p) {
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    const int32_t raw = __ldg(p.kv_len + b);
+    const int32_t raw = p.kv_len[b];
     if (raw > 0 && length_of(p, b) < 0 && threadIdx.x == 0) atomic_status(p.status, GDN_STATUS_BAD_LEN);
     if (raw != 0) continue;
     const int64_t rows = static_cast<int64_t>(p.T) * p.H, at = b * rows;

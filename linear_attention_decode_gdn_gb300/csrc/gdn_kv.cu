@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kAppendThreads) gdn_kv_append_kernel(const KvA
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kAppendThreads + threadIdx.x; i < all; i += step) {
     const int64_t r = i / row_vecs;
     uint32_t v = static_cast<uint32_t>(i - r * row_vecs);
-    const int64_t slot = __ldg(p.slot_map + r);
+    const int64_t slot = p.slot_map[r];
     if (slot < 0) continue;
     if (slot >= p.num_slots) {
       if (v == 0) atomic_status(p.status, GDN_STATUS_BAD_SLOT);
@@ -255,10 +255,10 @@ __global__ void __launch_bounds__(kAppendThreads) gdn_kv_append_kernel(const KvA
     const int64_t from = r * s.src_row + head * s.src_head + e;
     uint4 x;
     if (p.bf16) {
-      x = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(s.src) + from));
+      x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(s.src) + from);
     } else {
       const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(s.src) + from);
-      const float4 lo = __ldg(f), hi = __ldg(f + 1);
+      const float4 lo = f[0], hi = f[1];
       x = make_uint4(pack_bf16(lo.x, lo.y), pack_bf16(lo.z, lo.w), pack_bf16(hi.x, hi.y), pack_bf16(hi.z, hi.w));
     }
     const int64_t page = slot / p.page_size, pos = slot - page * p.page_size;

@@ -58,6 +58,7 @@ struct KvAppendParams {
 };
 
 constexpr int kTile = 128;        // cache positions a CTA takes at a time
+constexpr int kSms = 152;         // of one GB300
 constexpr int kMaxAttnCtas = 608; // CTAs of one attention launch (152 SMs, up to four each)
 
 struct AttnParams {
