@@ -250,6 +250,10 @@ int attend(const gdn_paged_kv* kv, const gdn_attn* a, void* workspace, size_t wo
   const size_t need = gdn::attn_workspace_bytes(plan, kv->dv);
   if (workspace_bytes < need)
     return fail(GDN_ERR_INVALID_ARG, "workspace of %zu bytes, %zu are needed (gdn_attn_workspace)", workspace_bytes, need);
+  const int64_t col_groups = (a->num_tokens * group + plan.ncol - 1) / plan.ncol;
+  const int64_t tiles = (static_cast<int64_t>(a->max_pages) * kv->page_size + gdn::kTile - 1) / gdn::kTile;
+  if (tiles * a->batch > 0x7fffffffLL / (kv->num_kv_heads * col_groups))
+    return fail(GDN_ERR_UNSUPPORTED, "the table could hold 2^31 tiles of %d positions or more", gdn::kTile);
   gdn::AttnParams p{};
   p.B = a->batch;
   p.T = a->num_tokens;
@@ -282,7 +286,7 @@ int attend(const gdn_paged_kv* kv, const gdn_attn* a, void* workspace, size_t wo
   p.o = a->o;
   p.lse = a->lse;
   p.status = status;
-  p.records = static_cast<int64_t*>(workspace);
+  p.records = static_cast<uint32_t*>(workspace);
   p.partials = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + gdn::kRecordBytes);
   return launched(gdn::launch_attn(plan, p, static_cast<cudaStream_t>(stream)), name);
 }

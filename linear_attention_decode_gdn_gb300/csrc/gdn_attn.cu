@@ -23,7 +23,6 @@ struct GeneralSmem {
   float w[kTile][kCols];
   int64_t v_at[kTile];     // element offset of the position's value row; -1: not in use
   float warp_max[kThreads / 32][kCols], warp_sum[kThreads / 32][kCols];
-  ShareScratch scratch;
 };
 
 // One online softmax over the unit's tiles, in fp32 throughout. Scores: a thread owns a
@@ -37,9 +36,9 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_general_kernel(const AttnPa
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_launch_dependents();
   griddep_wait();
-  write_empty<kThreads>(p);
-  const Share share = find_share<kThreads>(p, sm.scratch);
-  if (tid == 0) write_record(p, share);
+  write_empty<kThreads>(p, tid);
+  const Share share = find_share(p, blockIdx.x);
+  if (tid == 0) write_record(p, share, blockIdx.x);
   Walk walk(share);
   Segment seg;
   uint32_t bad = 0;
@@ -194,42 +193,46 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_general_kernel(const AttnPa
 }
 
 constexpr int kJoinThreads = 128;
+constexpr int kJoinAhead = 8;  // parts whose sums are loaded before their weights are known
 
-// Block (i, part) looks at the border between the shares of CTAs i - 1 and i (i >= 1). Where
-// it is the first border inside a unit, the block adds the unit's partial results for the
-// columns part, part + parts, ... in the order of the CTAs, so the sums do not depend on
-// timing: m = max m_j, l = sum 2^(m_j - m) l_j, o = sum 2^(m_j - m) o_j / l.
+// Block (i, c) looks at the border between the shares of workers i and i + 1. Where it is the
+// first border inside a unit, the block adds the unit's partial results for the columns c,
+// c + grid, ... in the order of the workers, so the sums do not depend on timing:
+// m = max m_j, l = sum 2^(m_j - m) l_j, o = sum 2^(m_j - m) o_j / l.
+// Bound by latency: three dependent loads (the record, maxima and sums, the parts).
 __global__ void __launch_bounds__(kJoinThreads) gdn_attn_join_kernel(const AttnParams p) {
   __shared__ float weight[kMaxAttnCtas];
   __shared__ float total[2];
   griddep_launch_dependents();
   griddep_wait();
   const int i = blockIdx.x + 1, tid = threadIdx.x;
-  const int64_t* rec = p.records + static_cast<size_t>(i) * kRecordInts;
-  if (rec[1] < 0 || rec[0] <= rec[2]) return;       // no work, or the unit begins here
-  const int64_t unit_start = rec[2], unit_end = rec[3];
-  if (rec[-kRecordInts] > unit_start) return;       // an earlier border is inside the unit too
-  const int b = static_cast<int>(rec[4]), unit = static_cast<int>(rec[5]);
+  const uint32_t* rec = p.records + static_cast<size_t>(i) * kRecordInts;
+  const uint4 r = *reinterpret_cast<const uint4*>(rec);
+  const uint32_t tiles = r.x, unit_start = r.y, unit_end = r.z;
+  const int b = static_cast<int>(r.w), unit = static_cast<int>(rec[4]);
+  if (tiles == 0) return;
+  const uint32_t before = share_start(tiles, p.workers, i - 1);
+  // the unit begins with worker i, or an earlier border is inside it too
+  if (share_start(tiles, p.workers, i) <= unit_start || before > unit_start) return;
   const int kv_head = unit / p.col_groups, col_base = (unit - kv_head * p.col_groups) * p.ncol;
   const int cols = min(p.ncol, p.cols - col_base);
-  // CTAs i - 1 .. last - 1 hold a part of it; shares are equal, so `last` is not far to seek
-  int last = i + 1;
-  while (last < p.ctas) {
-    const int64_t* r = p.records + static_cast<size_t>(last) * kRecordInts;
-    if (r[1] < 0 || r[0] >= unit_end) break;
-    ++last;
-  }
-  const int parts = last - (i - 1);
-  // the unit is CTA i - 1's last segment: its first one only where the share begins with it
-  const int slot0 = rec[-kRecordInts] == unit_start ? 0 : 1;
+  const int parts = static_cast<int>(worker_from(tiles, p.workers, unit_end)) - (i - 1);  // workers i - 1, i, ...
+  // the unit is worker i - 1's last segment: its first one only where the share begins with it
+  const int slot0 = before == unit_start ? 0 : 1;
+  auto part = [&](int j) { return partial_of(p, i - 1 + j, j == 0 ? slot0 : 0); };
   for (int c = blockIdx.y; c < cols; c += gridDim.y) {
-    __syncthreads();
-    for (int j = tid; j < parts; j += kJoinThreads)
-      weight[j] = partial_of(p, i - 1 + j, j == 0 ? slot0 : 0)[p.ncol * p.dv + c];
-    __syncthreads();
+    const int64_t row = row_of(p, b, kv_head, col_base + c);
+    float2 ahead[kJoinAhead];
+#pragma unroll
+    for (int j = 0; j < kJoinAhead; ++j)
+      if (j < parts && 2 * tid < p.dv) ahead[j] = *reinterpret_cast<const float2*>(part(j) + c * p.dv + 2 * tid);
+    __syncthreads();  // the last column's weights are read
     if (tid < 32) {
       float m = -INFINITY;
-      for (int j = tid; j < parts; j += 32) m = fmaxf(m, weight[j]);
+      for (int j = tid; j < parts; j += 32) {
+        weight[j] = part(j)[p.ncol * p.dv + c];
+        m = fmaxf(m, weight[j]);
+      }
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
       const float ref = m == -INFINITY ? 0.0f : m;
@@ -237,7 +240,7 @@ __global__ void __launch_bounds__(kJoinThreads) gdn_attn_join_kernel(const AttnP
       for (int j = tid; j < parts; j += 32) {
         const float f = exp2f(weight[j] - ref);
         weight[j] = f;
-        l += f * partial_of(p, i - 1 + j, j == 0 ? slot0 : 0)[p.ncol * p.dv + p.ncol + c];
+        l += f * part(j)[p.ncol * p.dv + p.ncol + c];
       }
       l = warp_sum(l);
       if (tid == 0) {
@@ -247,13 +250,18 @@ __global__ void __launch_bounds__(kJoinThreads) gdn_attn_join_kernel(const AttnP
     }
     __syncthreads();
     const float l = total[1], inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
-    const int64_t row = row_of(p, b, kv_head, col_base + c);
     for (int d = 2 * tid; d < p.dv; d += 2 * kJoinThreads) {
       float2 o = make_float2(0.0f, 0.0f);
-#pragma unroll 4
-      for (int j = 0; j < parts; ++j) {
-        const float2 x =
-            *reinterpret_cast<const float2*>(partial_of(p, i - 1 + j, j == 0 ? slot0 : 0) + c * p.dv + d);
+#pragma unroll
+      for (int j = 0; j < kJoinAhead; ++j) {
+        if (j >= parts) break;
+        const float2 x = d == 2 * tid ? ahead[j] : *reinterpret_cast<const float2*>(part(j) + c * p.dv + d);
+        o.x = fmaf(weight[j], x.x, o.x);
+        o.y = fmaf(weight[j], x.y, o.y);
+      }
+#pragma unroll 8
+      for (int j = kJoinAhead; j < parts; ++j) {
+        const float2 x = *reinterpret_cast<const float2*>(part(j) + c * p.dv + d);
         o.x = fmaf(weight[j], x.x, o.x);
         o.y = fmaf(weight[j], x.y, o.y);
       }
@@ -296,37 +304,38 @@ AttnPlan attn_plan(const gdn_paged_kv& kv, int cols) {
     return true;
   };
   if (!heads || !pages || !strides(kv.k_strides) || (!latent && !strides(kv.v_strides))) return {false, kCols, kMaxAttnCtas};
-  return {true, cols <= 16 ? 16 : cols <= 32 || latent ? 32 : 64, kSms};
+  // a latent cache is read by pairs of CTAs
+  return {true, cols <= 16 ? 16 : cols <= 32 ? 32 : 64, latent ? kSms / 2 : kSms};
 }
 
 size_t attn_workspace_bytes(const AttnPlan& plan, int dv) {
-  return kRecordBytes + static_cast<size_t>(plan.max_ctas) * 2 * plan.ncol * (dv + 2) * sizeof(float);
+  return kRecordBytes + static_cast<size_t>(plan.max_workers) * 2 * plan.ncol * (dv + 2) * sizeof(float);
 }
 
 cudaError_t launch_attn_general(AttnParams& p, cudaStream_t stream) {
   const cudaError_t err = cudaFuncSetAttribute(gdn_attn_general_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(sizeof(GeneralSmem)));
   if (err != cudaSuccess) return err;
-  return launch_overlapped(gdn_attn_general_kernel, p, dim3(p.ctas), kThreads, sizeof(GeneralSmem), stream);
+  return launch_overlapped(gdn_attn_general_kernel, p, dim3(p.workers), kThreads, sizeof(GeneralSmem), stream);
 }
 
 cudaError_t launch_attn_join(const AttnParams& p, cudaStream_t stream) {
   const unsigned parts = static_cast<unsigned>(p.cols < p.ncol ? p.cols : p.ncol);
-  return launch_overlapped(gdn_attn_join_kernel, p, dim3(p.ctas - 1, parts), kJoinThreads, 0, stream);
+  return launch_overlapped(gdn_attn_join_kernel, p, dim3(p.workers - 1, parts), kJoinThreads, 0, stream);
 }
 
 cudaError_t launch_attn(const AttnPlan& plan, AttnParams& p, cudaStream_t stream) {
   p.ncol = plan.ncol;
   p.col_groups = (p.cols + p.ncol - 1) / p.ncol;
-  // at most one CTA a tile that there could be
+  // at most one worker a tile that there could be
   const int64_t positions = static_cast<int64_t>(p.max_pages) * p.page_size;
   const int64_t per_unit = (positions + kTile - 1) / kTile;
   const int64_t most = per_unit * p.B * p.heads_kv * p.col_groups;
-  p.ctas = static_cast<int>(most < 1 ? 1 : most < plan.max_ctas ? most : plan.max_ctas);
+  p.workers = static_cast<uint32_t>(most < plan.max_workers ? most : plan.max_workers);
   const cudaError_t err = plan.tensor ? launch_attn_tc(p, stream) : launch_attn_general(p, stream);
   if (err != cudaSuccess) return err;
   // a unit of one tile is never split
-  return p.ctas > 1 && per_unit > 1 ? launch_attn_join(p, stream) : cudaSuccess;
+  return p.workers > 1 && per_unit > 1 ? launch_attn_join(p, stream) : cudaSuccess;
 }
 
 }  // namespace gdn

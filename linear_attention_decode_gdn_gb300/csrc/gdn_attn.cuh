@@ -4,11 +4,11 @@
 // The work of a launch is a list of tiles, each kTile = 128 cache positions of one unit; a
 // unit is one (request, kv head, column group), and its columns are the query rows that read
 // the same keys: column c is query token c / group, head c % group of the kv head. The tiles
-// of all units stand in one line, request by request, and every CTA takes an equal, unbroken
-// share of the line, computed from kv_len on the device. So the CTAs are busy equally long
-// whatever the lengths are, one long request is spread over all of them, and a unit is cut
-// only where two shares meet: of a CTA's segments only the first and the last can be part of
-// a unit. Those leave unnormalised sums in the workspace, and gdn_attn_join_kernel adds them.
+// of all units stand in one line, request by request, and every worker (a CTA, or a pair of
+// them) takes an equal, unbroken share of the line, computed from kv_len on the device. So all
+// are busy equally long whatever the lengths are, one long request is spread over the GPU, and
+// a unit is cut only where two shares meet: of a worker's segments only the first and the last
+// can be part of a unit. Those leave unnormalised sums in the workspace, and gdn_attn_join_kernel adds them.
 #pragma once
 
 #include "gdn_device.cuh"
@@ -41,112 +41,88 @@ __device__ __forceinline__ Tiles tiles_of(const AttnParams& p, int32_t n) {
   return {first, (n - 1) / kTile + 1 - first};
 }
 
-// Tiles of the line before the CTA's share begins.
-__device__ __forceinline__ int64_t share_start(int64_t total, int ctas, int cta) {
-  const int64_t q = total / ctas, r = total - q * ctas;
-  return cta * q + (cta < r ? cta : r);
+// Tiles of the line before worker w's share begins (a worker: a CTA, or a pair of them).
+__device__ __forceinline__ uint32_t share_start(uint32_t total, uint32_t workers, uint32_t w) {
+  const uint32_t q = total / workers, r = total - q * workers;
+  return w * q + min(w, r);
+}
+// The first worker whose share begins at or after line position `at`.
+__device__ __forceinline__ uint32_t worker_from(uint32_t total, uint32_t workers, uint32_t at) {
+  const uint32_t q = total / workers, r = total - q * workers, wide = r * (q + 1);
+  if (at <= wide) return (at + q) / (q + 1);
+  return r + (at - wide + q - 1) / q;  // at > wide: q > 0
 }
 
-// Where a CTA's share begins: the request, the unit of it (kv head * col_groups + column
-// group) and the tile in the unit.
+// Where a worker's share begins: the request, the unit of it (kv head * col_groups + column
+// group) and the tile in the unit. The host keeps the tiles of a launch below 2^31.
 struct Share {
-  int64_t total, start, count;
-  int64_t unit_start;  // line position of the first unit's first tile
+  uint32_t total, count;
+  uint32_t unit_start;  // line position of the first unit's first tile
   int32_t b, unit, tile;
 };
 
-// Called by all THREADS of the block; `scratch` is for this call alone (three barriers).
-struct ShareScratch {
-  int64_t warp_sums[32];
-  Share share;
-};
-
-template <int THREADS>
-__device__ __forceinline__ int64_t scan_tiles(int64_t x, int64_t* warp_sums, int64_t* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Called by all lanes of a warp; every warp finds the same share for itself, which costs one
+// pass over the lengths and no barrier. A lane sums consecutive requests.
+__device__ __forceinline__ Share find_share(const AttnParams& p, uint32_t worker) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t units = static_cast<uint32_t>(p.heads_kv * p.col_groups);
+  const int per = (p.B + 31) / 32, from = min(lane * per, p.B), to = min(from + per, p.B);
+  uint32_t mine = 0;
+#pragma unroll 4
+  for (int b = from; b < to; ++b) mine += static_cast<uint32_t>(tiles_of(p, length_of(p, b)).count);
+  uint32_t upto = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int64_t y = static_cast<int64_t>(__shfl_up_sync(0xffffffffu, static_cast<unsigned long long>(x), d));
-    if (lane >= d) x += y;
-  }
-  __syncthreads();
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  int64_t before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
-    const int64_t s = warp_sums[w];
-    before += w < warp ? s : 0;
-    all += s;
-  }
-  *total = all;
-  return x + before;
-}
-
-template <int THREADS>
-__device__ __forceinline__ Share find_share(const AttnParams& p, ShareScratch& scratch) {
-  const int tid = threadIdx.x;
-  const int units = p.heads_kv * p.col_groups;
-  // a batch of up to THREADS requests: one load a thread and one sum
-  const int32_t mine = tid < p.B ? tiles_of(p, length_of(p, tid)).count : 0;
-  int64_t all;
-  int64_t upto = scan_tiles<THREADS>(mine, scratch.warp_sums, &all);
-  int64_t total = all;
-  for (int base = THREADS; base < p.B; base += THREADS) {
-    const int b = base + tid;
-    scan_tiles<THREADS>(b < p.B ? tiles_of(p, length_of(p, b)).count : 0, scratch.warp_sums, &all);
-    total += all;
+    const uint32_t y = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += y;
   }
   Share s{};
-  s.total = total * units;
-  s.start = share_start(s.total, gridDim.x, blockIdx.x);
-  s.count = share_start(s.total, gridDim.x, blockIdx.x + 1) - s.start;
-  int64_t before = 0;
-  for (int base = 0; base < p.B; base += THREADS) {
-    const int b = base + tid;
-    int32_t count = mine;
-    if (base > 0) {
-      count = b < p.B ? tiles_of(p, length_of(p, b)).count : 0;
-      upto = scan_tiles<THREADS>(count, scratch.warp_sums, &all);
-    } else if (p.B > THREADS) {
-      upto = scan_tiles<THREADS>(count, scratch.warp_sums, &all);
-    }
-    const int64_t lo = (before + upto - count) * units, hi = (before + upto) * units;
-    if (count > 0 && s.count > 0 && s.start >= lo && s.start < hi) {
-      Share f = s;
-      const int64_t in = s.start - lo;
-      f.b = b;
-      f.unit = static_cast<int32_t>(in / count);
-      f.tile = static_cast<int32_t>(in - static_cast<int64_t>(f.unit) * count);
-      f.unit_start = s.start - f.tile;
-      scratch.share = f;
-    }
-    before += all;
-  }
+  s.total = __shfl_sync(0xffffffffu, upto, 31) * units;
+  const uint32_t start = share_start(s.total, p.workers, worker);
+  s.count = share_start(s.total, p.workers, worker + 1) - start;
   if (s.count == 0) return s;
-  __syncthreads();
-  return scratch.share;
+  const bool here = start >= (upto - mine) * units && start < upto * units;
+  uint32_t before = upto - mine;
+  int32_t b = from;
+  if (here) {
+    for (;; ++b) {
+      const uint32_t count = static_cast<uint32_t>(tiles_of(p, length_of(p, b)).count);
+      if (start < (before + count) * units) {
+        const uint32_t in = start - before * units;
+        s.unit = static_cast<int32_t>(in / count);
+        s.tile = static_cast<int32_t>(in - s.unit * count);
+        break;
+      }
+      before += count;
+    }
+  }
+  const int owner = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+  s.b = __shfl_sync(0xffffffffu, b, owner);
+  s.unit = __shfl_sync(0xffffffffu, s.unit, owner);
+  s.tile = __shfl_sync(0xffffffffu, s.tile, owner);
+  s.unit_start = start - s.tile;
+  return s;
 }
 
-// A CTA's run of tiles within one unit.
+// A worker's run of tiles within one unit.
 struct Segment {
   int32_t b, unit, kv_head, col_base;
-  int32_t n;          // cached positions
+  int32_t n;           // cached positions
   int32_t tile, tiles; // first tile (absolute) and how many
-  int32_t index;      // 0 for the CTA's first
-  bool whole;         // covers the unit
+  int32_t index;       // 0 for the worker's first
+  bool whole;          // covers the unit
 };
 
 // Walks the segments of a share; every thread that walks sees the same ones.
 struct Walk {
-  int64_t left;
+  uint32_t left;
   int32_t b, unit, tile, index;
 
   __device__ __forceinline__ explicit Walk(const Share& s)
       : left(s.count), b(s.b), unit(s.unit), tile(s.tile), index(0) {}
 
   __device__ __forceinline__ bool next(const AttnParams& p, Segment* seg) {
-    if (left <= 0) return false;
+    if (left == 0) return false;
     const int units = p.heads_kv * p.col_groups;
     int32_t n = length_of(p, b);
     Tiles t = tiles_of(p, n);
@@ -158,7 +134,7 @@ struct Walk {
         t = tiles_of(p, n);
       } while (t.count == 0);
     }
-    const int64_t rest = t.count - tile;
+    const uint32_t rest = static_cast<uint32_t>(t.count - tile);
     const int32_t take = static_cast<int32_t>(left < rest ? left : rest);
     seg->b = b;
     seg->unit = unit;
@@ -177,25 +153,24 @@ struct Walk {
 };
 
 // ---- the workspace ----------------------------------------------------------------------
-// Record of a CTA: [start, share's end or -1 without work, unit_start, unit's end, b, unit] of
-// its first segment's unit. A partial result: dv x ncol sums (column by column, fp32), then the
-// columns' maxima (in the scaled log2 domain) and sums.
+// Record of a worker: [tiles of the launch, or 0 without work; line positions of the first
+// segment's unit, begin and end; request; unit]. A partial result: dv x ncol sums (column by
+// column, fp32), then the columns' maxima (in the scaled log2 domain) and sums.
 __device__ __forceinline__ size_t partial_floats(const AttnParams& p) {
   return static_cast<size_t>(p.ncol) * (p.dv + 2);
 }
-__device__ __forceinline__ float* partial_of(const AttnParams& p, int cta, int slot) {
-  return p.partials + (static_cast<size_t>(cta) * 2 + slot) * partial_floats(p);
+__device__ __forceinline__ float* partial_of(const AttnParams& p, int worker, int slot) {
+  return p.partials + (static_cast<size_t>(worker) * 2 + slot) * partial_floats(p);
 }
 
-__device__ __forceinline__ void write_record(const AttnParams& p, const Share& s) {
-  int64_t* r = p.records + static_cast<size_t>(blockIdx.x) * kRecordInts;
-  r[0] = s.start;
-  r[1] = s.count > 0 ? s.start + s.count : -1;
-  if (s.count <= 0) return;
-  r[2] = s.unit_start;
-  r[3] = s.unit_start + tiles_of(p, length_of(p, s.b)).count;
-  r[4] = s.b;
-  r[5] = s.unit;
+__device__ __forceinline__ void write_record(const AttnParams& p, const Share& s, uint32_t worker) {
+  uint32_t* r = p.records + static_cast<size_t>(worker) * kRecordInts;
+  r[0] = s.count > 0 ? s.total : 0;
+  if (s.count == 0) return;
+  r[1] = s.unit_start;
+  r[2] = s.unit_start + tiles_of(p, length_of(p, s.b)).count;
+  r[3] = s.b;
+  r[4] = s.unit;
 }
 
 // Row of column c of a request and kv head: [B][T][H].
@@ -205,18 +180,18 @@ __device__ __forceinline__ int64_t row_of(const AttnParams& p, int b, int kv_hea
 }
 
 // Requests with nothing in the cache belong to no share: their rows are written here, and
-// lengths that cannot be are reported. Every thread of the block calls it.
+// lengths that cannot be are reported. Called by THREADS threads of the block, numbered `tid`.
 template <int THREADS>
-__device__ __forceinline__ void write_empty(const AttnParams& p) {
+__device__ __forceinline__ void write_empty(const AttnParams& p, int tid) {
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
     const int32_t raw = p.kv_len[b];
-    if (raw > 0 && length_of(p, b) < 0 && threadIdx.x == 0) atomic_status(p.status, GDN_STATUS_BAD_LEN);
+    if (raw > 0 && length_of(p, b) < 0 && tid == 0) atomic_status(p.status, GDN_STATUS_BAD_LEN);
     if (raw != 0) continue;
     const int64_t rows = static_cast<int64_t>(p.T) * p.H, at = b * rows;
     uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + at * p.dv);
-    for (int64_t i = threadIdx.x; i < rows * (p.dv / 8); i += THREADS) o[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int64_t i = tid; i < rows * (p.dv / 8); i += THREADS) o[i] = make_uint4(0u, 0u, 0u, 0u);
     if (p.lse != nullptr)
-      for (int64_t i = threadIdx.x; i < rows; i += THREADS) p.lse[at + i] = __int_as_float(0xff800000);
+      for (int64_t i = tid; i < rows; i += THREADS) p.lse[at + i] = __int_as_float(0xff800000);
   }
 }
 

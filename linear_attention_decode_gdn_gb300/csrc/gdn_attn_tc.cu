@@ -13,14 +13,22 @@
 // So neither K nor V is transposed or padded, the accumulators take (2 + dv / 128) N columns of
 // TMEM, and a query group of 4 or 16 costs the same as it streams by.
 //
-// One CTA an SM, 256 threads. Warp 0 gathers pages by TMA into a ring of 16 KB chunks (128
-// positions x 64 elements, 128-byte swizzle; pages of 16 .. 128 positions are boxes of one
-// chunk). Warp 1 issues the MMAs: scores of tile i + 1 before values of tile i, so the tensor
-// core works while the softmax does. Warps 2 and 3 lay out the next unit's queries. Warps 4 - 7
-// are the softmax: one thread a position, N columns each; sums of weights stay in the threads
-// until the unit ends. The running maximum is raised (and O^T rescaled in TMEM) only where a
-// score passes it by 2^8, so most tiles need one barrier and no reduction; weights up to 2^8
-// lose nothing in bf16 or fp32.
+// One CTA an SM. Warp 0 gathers pages by TMA into a ring of slots (128 positions x 64 or 128
+// elements, 128-byte swizzle; pages of 16 .. 128 positions are boxes of a slot). Warp 1 issues
+// the MMAs: scores of tile i + 1 before values of tile i, so the tensor core works while the
+// softmax does. Warps 2 and 3 lay out the next unit's queries. The other warps are the softmax,
+// four for every 32 columns: one thread a position; sums of weights stay in the threads until
+// the unit ends. The running maximum is raised (and O^T rescaled in TMEM) only where a score
+// passes it by 2^8, so most tiles need one barrier and no reduction; weights up to 2^8 lose
+// nothing in bf16 or fp32.
+//
+// Latent rows: the value is the key's own row, so a tile's 147 KB would have to stay until the
+// values' product, and with them alone shared memory is full: loads, scores, softmax and values
+// would take turns. A pair of CTAs (one cluster) therefore splits the row: each CTA holds half
+// of the latent and of the tail, two tiles deep, forms its half of every score's sum, sends it
+// to the other CTA's shared memory (st.async, counted on an mbarrier), and adds what it is
+// sent. Both then take the same softmax (the sum of two is the same in either order) and each
+// its half of O^T. No byte of the cache and no product is taken twice.
 #include "gdn_attn.cuh"
 #include "gdn_tc.cuh"
 #include "gdn_tmap.h"
@@ -33,56 +41,67 @@ namespace {
 
 using namespace attn;
 
-constexpr int kThreads = 256;
 constexpr int kChunk = kTile * 128;          // bytes: 128 positions x 64 bf16
 constexpr int kSmemMost = 227 * 1024;
-constexpr int kMiscBytes = 3072;
+constexpr int kMiscBytes = 4096;
+constexpr int kMaxSlots = 12;
 constexpr float kRaise = 8.0f;               // log2 of what a weight may grow to
 
 template <int DK_, int DV_, int N_, bool LATENT_>
 struct Cfg {
   static constexpr int DK = DK_, DV = DV_, N = N_;
   static constexpr bool LATENT = LATENT_;
-  static constexpr int KC = LATENT ? DV / 64 : DK / 64;   // key chunks of the ring
-  static constexpr int VC = LATENT ? 0 : DV / 64;         // value chunks (a latent row's key is its value)
-  static constexpr int PER = KC + VC;                     // ring chunks a tile
-  static constexpr int TAILC = LATENT ? (DK - DV) / 64 : 0;  // chunks of the key's tail, in a ring of their own
-  static constexpr int MB = DV > 128 ? DV / 128 : 1;      // blocks of 128 rows of O^T
-  static constexpr int PB = LATENT && N > 16 ? 1 : 2;     // buffers of weights
-  static constexpr int TAILS = LATENT ? (N > 16 ? 1 : 2) : 0;
-  static constexpr int QBYTES = N * DK * 2, PBYTES = N * kTile * 2;
-  static constexpr int FIXED = kMiscBytes + QBYTES + PB * PBYTES + TAILS * kChunk;
-  static constexpr int FIT = (kSmemMost - FIXED) / kChunk;
-  static constexpr int RING = (FIT > 12 ? 12 : FIT) & ~1;  // even: a block of V is two chunks side by side
-  static constexpr size_t SMEM = static_cast<size_t>(FIXED) + RING * kChunk;
+  static constexpr int CL = LATENT ? 2 : 1;                // CTAs that share a unit
+  static constexpr int KCOLS = LATENT ? DV / CL : DK;      // key elements of this CTA, but for the tail
+  static constexpr int VCOLS = DV / CL;                    // value elements of this CTA
+  static constexpr int TCOLS = LATENT ? (DK - DV) / CL : 0;  // tail elements of this CTA
+  static constexpr int SLOTC = VCOLS >= 128 ? 2 : 1;       // chunks of a slot
+  static constexpr int SLOT = SLOTC * kChunk;
+  static constexpr int KS = KCOLS / 64 / SLOTC;            // key slots of a tile
+  static constexpr int VS = LATENT ? 0 : VCOLS / 64 / SLOTC;
+  static constexpr int PER = KS + VS;
+  static constexpr int MB = VCOLS > 128 ? VCOLS / 128 : 1; // blocks of 128 rows of O^T
+  static constexpr int G = N > 32 ? 2 : 1, NC = N / G;     // softmax groups and their columns
+  static constexpr int THREADS = 128 + 128 * G;
+  static constexpr int PB = LATENT && N > 32 ? 1 : 2;      // buffers of weights
+  static constexpr int QB = !LATENT && DK < 256 && N <= 32 ? 2 : 1;  // and of queries
+  static constexpr int RB = LATENT ? (N > 32 ? 1 : 2) : 0; // and of received scores
+  static constexpr int TAIL = kTile * TCOLS * 2, TAILS = LATENT ? (N > 32 ? 1 : 2) : 0;
+  static constexpr int QBYTES = N * (KCOLS + TCOLS) * 2, PBYTES = N * kTile * 2, RBYTES = LATENT ? N * kTile * 4 : 0;
+  static constexpr int FIXED = kMiscBytes + QB * QBYTES + PB * PBYTES + RB * RBYTES + TAILS * TAIL;
+  static constexpr int FIT = (kSmemMost - FIXED) / SLOT < kMaxSlots ? (kSmemMost - FIXED) / SLOT : kMaxSlots;
+  static constexpr int SLOTS = SLOTC == 1 ? FIT & ~1 : FIT;
+  static constexpr int SMEM = FIXED + SLOTS * SLOT;
   static constexpr int TMEM_USED = (2 + MB) * N;
   static constexpr int TMEM = TMEM_USED <= 32 ? 32 : TMEM_USED <= 64 ? 64 : TMEM_USED <= 128 ? 128 : TMEM_USED <= 256 ? 256 : 512;
-  // key chunks of the next tile that fit beside a tile whose values are still needed
-  static constexpr int AHEAD = LATENT ? (RING - PER < KC ? RING - PER : KC) : KC;
-  static_assert(RING >= PER && TAILC <= 1, "a tile fits the rings");
+  // the scores of a tile are taken while the values of the one before still need their slots
+  static_assert(SLOTS >= KS + (LATENT ? KS : VS), "the ring holds what both products need");
   static_assert(N % 16 == 0 && N <= 64 && SMEM <= kSmemMost && TMEM_USED <= 512, "fits");
 };
 
 struct Misc {
-  uint64_t full[12], empty[12];
+  uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t tail_full[2], tail_empty[2];
-  uint64_t q_full, q_empty;
+  uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], s_empty[2];
   uint64_t p_full[2], pv_done[2];
+  uint64_t got[2], may_send[2];  // scores received; the other CTA has read what was sent
   uint64_t drained;
   uint32_t tmem;
   uint32_t timeout;
   float m[64];
+  float inv[64];
   float per_warp[4][64];
-  int64_t rows[64];
-  ShareScratch scratch;
+  int32_t last[64];  // the last position that each column sees
+  int32_t rows[64];  // the column's row of o
 };
 static_assert(sizeof(Misc) <= kMiscBytes, "shared memory plan");
 
 struct TcParams {
   AttnParams a;
-  int32_t box;  // positions of one TMA box: min(page_size, 128)
-  CUtensorMap k, v;
+  int32_t box, box_shift;  // positions of one TMA box, min(page_size, 128), and its log2
+  int32_t page_tiles;      // tiles of a page of 128 positions or more
+  CUtensorMap k, v;        // v: the tail of a latent row
 };
 
 // ---- PTX ----------------------------------------------------------------------------------
@@ -90,9 +109,12 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn, bool 
   return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
-// Operand tile of 128-byte rows, 128-byte swizzle (8 rows = 1024 bytes repeat).
+// Operand tiles of 128-byte (64-byte) rows with the swizzle of that width; 8 rows repeat.
 __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
   return tc::smem_desc(saddr, lbo, sbo) | (2ull << 61);
+}
+__device__ __forceinline__ uint64_t desc_sw64(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return tc::smem_desc(saddr, lbo, sbo) | (4ull << 61);
 }
 // kind::f16, called by a whole warp with uniform operands; one elected lane issues.
 __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -113,13 +135,47 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
       "l"(map), "r"(smem_addr(bar)), "r"(x), "r"(head), "r"(pos), "r"(page)
       : "memory");
 }
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool softmax_any(bool pred) {
+// 16 bytes to shared memory, zeros where `from_there` is false (then nothing is read)
+__device__ __forceinline__ void cp_async16_or_zero(void* dst, const void* src, bool from_there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(from_there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t in_cta(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
+}
+// 16 bytes to another CTA's shared memory, counted on that CTA's mbarrier
+__device__ __forceinline__ void send16(uint32_t dst, float a, float b, float c, float d, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
+               "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "r"(__float_as_uint(c)), "r"(__float_as_uint(d)), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void arrive_there(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+template <int ID>
+__device__ __forceinline__ void group_sync_id() {
+  asm volatile("bar.sync %0, 128;" ::"n"(ID) : "memory");
+}
+// Barriers of one softmax group (four warps).
+__device__ __forceinline__ void group_sync(int g) {
+  if (g == 0) group_sync_id<1>(); else group_sync_id<2>();
+}
+__device__ __forceinline__ bool group_any(int g, bool pred) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred a, b;\n setp.ne.u32 a, %1, 0;\n bar.red.or.pred b, 1, 128, a;\n selp.u32 %0, 1, 0, b;\n}\n"
+      "{\n .reg .pred a, b;\n setp.ne.u32 a, %1, 0;\n bar.red.or.pred b, %2, 128, a;\n selp.u32 %0, 1, 0, b;\n}\n"
       : "=r"(r)
-      : "r"(static_cast<uint32_t>(pred))
+      : "r"(static_cast<uint32_t>(pred)), "r"(g + 1)
       : "memory");
   return r != 0u;
 }
@@ -139,8 +195,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-// Sums of N columns over the warp's lanes: afterwards lane holds the sums of columns
-// lane * N / 32 .. (N >= 32) or of column lane * N / 32 (N = 16).
+// Sums of N columns over the warp's lanes: afterwards a lane holds the sum of column lane
+// (N = 32) or lane / 2 (N = 16).
 template <int N>
 __device__ __forceinline__ void column_sums(float (&v)[N], int lane) {
 #pragma unroll
@@ -161,13 +217,37 @@ __device__ __forceinline__ void column_sums(float (&v)[N], int lane) {
   }
 }
 
+// mbar_try_wait that also sees what another CTA of the cluster has written
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0u;
+}
+
+// Whether the phase is complete, without waiting for it.
+__device__ __forceinline__ bool test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0u;
+}
+
 // A wait with a limit. The first one that runs out raises a flag that ends every other wait of
 // the CTA, so the kernel returns soon after (and reports GDN_STATUS_TIMEOUT).
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool waited(uint64_t* bar, uint32_t parity, Misc& sm) {
-  if (mbar_try_wait(bar, parity)) return true;
+  auto done = [&] { return CLUSTER ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
+  if (done()) return true;
   volatile uint32_t* const flag = &sm.timeout;
   const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
+  while (!done()) {
     if (*flag != 0u) return false;
     if (clock64() - t0 > kWaitLimitCycles) {
       *flag = 1u;
@@ -182,145 +262,176 @@ __device__ __forceinline__ bool warp_waited(uint64_t* bar, uint32_t parity, Misc
 }
 
 template <class C>
-__global__ void __launch_bounds__(kThreads, 1) gdn_attn_tc_kernel(const __grid_constant__ TcParams tp) {
+__global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid_constant__ TcParams tp) {
   extern __shared__ __align__(1024) unsigned char smem[];
   const AttnParams& p = tp.a;
-  constexpr int N = C::N;
-  constexpr uint32_t kTails = C::TAILS > 0 ? C::TAILS : 1;
+  constexpr int N = C::N, NC = C::NC;
+  constexpr uint32_t kTails = C::TAILS > 0 ? C::TAILS : 1, kRecv = C::RB > 0 ? C::RB : 1;
   unsigned char* const ring = smem;
-  unsigned char* const tails = ring + C::RING * kChunk;
-  unsigned char* const weights = tails + C::TAILS * kChunk;
-  unsigned char* const queries = weights + C::PB * C::PBYTES;
-  Misc& sm = *reinterpret_cast<Misc*>(queries + C::QBYTES);
+  unsigned char* const tails = ring + C::SLOTS * C::SLOT;
+  unsigned char* const weights = tails + C::TAILS * C::TAIL;
+  unsigned char* const received = weights + C::PB * C::PBYTES;
+  unsigned char* const queries = received + C::RB * C::RBYTES;
+  Misc& sm = *reinterpret_cast<Misc*>(queries + C::QB * C::QBYTES);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const uint32_t rank = C::CL > 1 ? cluster_rank() : 0u;
+  const uint32_t worker = blockIdx.x / C::CL;
 
   griddep_launch_dependents();
   if (tid == 0) {
-    for (int i = 0; i < C::RING; ++i) {
+    for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(&sm.full[i], 1);
       mbar_init(&sm.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.tail_full[i], 1);
       mbar_init(&sm.tail_empty[i], 1);
+      mbar_init(&sm.q_full[i], 64);
+      mbar_init(&sm.q_empty[i], 1);
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.s_empty[i], 128);
-      mbar_init(&sm.p_full[i], 128);
+      mbar_init(&sm.s_empty[i], 128 * C::G);
+      mbar_init(&sm.p_full[i], 128 * C::G);
       mbar_init(&sm.pv_done[i], 1);
+      mbar_init(&sm.got[i], 1);
+      mbar_init(&sm.may_send[i], 128);
     }
-    mbar_init(&sm.q_full, 64);
-    mbar_init(&sm.q_empty, 1);
     mbar_init(&sm.drained, 1);
     sm.timeout = 0u;
     fence_mbar_init();
+    if (C::LATENT)  // each barrier's first round of scores is expected from the start
+      for (int i = 0; i < C::RB * C::G; ++i) mbar_arrive_expect_tx(&sm.got[i], NC * kTile * 4);
   }
   if (warp == 1) {
     tc::tmem_alloc(&sm.tmem, C::TMEM);
     tc::tmem_relinquish();
   }
-  griddep_wait();
-  write_empty<kThreads>(p);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  if (C::CL > 1) cluster_sync_all();  // the other CTA's barriers are there
   const uint32_t tmem = sm.tmem;
-  const Share share = find_share<kThreads>(p, sm.scratch);
-  if (tid == 0) write_record(p, share);
-
+  griddep_wait();
+  const Share share = find_share(p, worker);
   Walk walk(share);
   Segment seg;
 
   if (warp == 0) {
     // ---- pages into the ring --------------------------------------------------------------
-    uint32_t put = 0, tail_put = 0;  // chunks issued
-    uint32_t bad = 0;
-    const int boxes = kTile / tp.box;  // of one chunk; lane l issues box l
+    if (lane == 0 && rank == 0) write_record(p, share, worker);
+    uint32_t slot = 0, round = 1, tile_no = 0;  // next slot, the parity its barrier has when free
+    uint32_t put = 0;
+    bool bad = false;
+    const int boxes = kTile / tp.box;  // of one chunk; lane l looks up the page of box l
     bool ok = true;
     while (ok && walk.next(p, &seg)) {
       const int32_t lower = lower_bound_of(p, seg.n, seg.col_base / p.group);
       const int32_t* row = p.table + static_cast<int64_t>(seg.b) * p.max_pages;
-      auto page_at = [&](int tile) -> int32_t {
-        const int64_t at = static_cast<int64_t>(tile) * kTile + lane * tp.box;
-        // a box that no query of the unit sees reads as zero, as one of a page that is none
-        if (lane >= boxes || at >= seg.n || at + tp.box <= lower) return p.num_pages;
-        const int32_t page = row[at / p.page_size];
-        if (page >= 0 && page < p.num_pages) return page;
-        bad = GDN_STATUS_BAD_PAGE;
-        return p.num_pages;
+      // the entry is only looked at when its tile's turn comes, a tile later
+      auto entry = [&](int tile) -> int32_t {
+        const int32_t at = min(tile * kTile + (lane & (boxes - 1)) * tp.box, seg.n - 1);
+        return row[boxes > 1 ? at >> tp.box_shift : tile / tp.page_tiles];
       };
-      int32_t page = page_at(seg.tile);
-      for (int tile = seg.tile; ok && tile < seg.tile + seg.tiles; ++tile) {
-        const int32_t next = tile + 1 < seg.tile + seg.tiles ? page_at(tile + 1) : 0;
-        const int32_t pos = (tile * kTile + lane * tp.box) % p.page_size;
-        for (int c = 0; c < C::PER; ++c, ++put) {
-          const uint32_t slot = put % C::RING;
-          ok = warp_waited(&sm.empty[slot], ((put / C::RING) & 1u) ^ 1u, sm);
+      int32_t next = entry(seg.tile);
+      for (int tile = seg.tile; ok && tile < seg.tile + seg.tiles; ++tile, ++tile_no) {
+        int32_t page = next;
+        if (tile + 1 < seg.tile + seg.tiles) next = entry(tile + 1);
+        // a box that no query of the unit sees reads as zero, as one of a page that is none
+        const int32_t at = tile * kTile + (lane & (boxes - 1)) * tp.box;
+        const bool seen = at < seg.n && at + tp.box > lower, valid = page >= 0 && page < p.num_pages;
+        bad |= seen && !valid;
+        if (!seen || !valid) page = p.num_pages;
+        const int32_t pos = boxes > 1 ? 0 : tile % tp.page_tiles * kTile;
+        for (int s = 0; s < C::PER; ++s) {
+          ok = warp_waited(&sm.empty[slot], round, sm);
           if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], kChunk);
-          __syncwarp();
-          const bool value = !C::LATENT && c >= C::KC;
-          if (lane < boxes)
-            tma_box(smem_addr(ring) + slot * kChunk + lane * tp.box * 128, value ? &tp.v : &tp.k,
-                    (value ? c - C::KC : c) * 64, seg.kv_head, pos, page, &sm.full[slot]);
-        }
-        if (C::TAILC > 0 && ok) {
-          const uint32_t slot = tail_put % kTails;
-          ok = warp_waited(&sm.tail_empty[slot], ((tail_put / kTails) & 1u) ^ 1u, sm);
-          if (ok) {
-            if (lane == 0) mbar_arrive_expect_tx(&sm.tail_full[slot], kChunk);
-            __syncwarp();
-            if (lane < boxes)
-              tma_box(smem_addr(tails) + slot * kChunk + lane * tp.box * 128, &tp.k, C::KC * 64, seg.kv_head, pos, page,
-                      &sm.tail_full[slot]);
-            ++tail_put;
+          const bool value = !C::LATENT && s >= C::KS;
+          const CUtensorMap* map = value ? &tp.v : &tp.k;
+          const int32_t x = (C::LATENT ? static_cast<int32_t>(rank) * C::KCOLS : 0) + (value ? s - C::KS : s) * (C::SLOTC * 64);
+          const uint32_t dst = smem_addr(ring) + slot * C::SLOT;
+          if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], C::SLOT);
+          for (int b = 0; b < boxes; ++b) {
+            const int32_t pg = __shfl_sync(0xffffffffu, page, b);
+            if (lane == 0) {
+#pragma unroll
+              for (int c = 0; c < C::SLOTC; ++c)
+                tma_box(dst + c * kChunk + b * tp.box * 128, map, x + c * 64, seg.kv_head, pos, pg, &sm.full[slot]);
+            }
+          }
+          ++put;
+          if (++slot == C::SLOTS) {
+            slot = 0;
+            round ^= 1u;
           }
         }
-        page = next;
+        if (C::LATENT && ok) {
+          const uint32_t t = tile_no % kTails;
+          ok = warp_waited(&sm.tail_empty[t], ((tile_no / kTails) & 1u) ^ 1u, sm);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&sm.tail_full[t], C::TAIL);
+          for (int b = 0; b < boxes; ++b) {
+            const int32_t pg = __shfl_sync(0xffffffffu, page, b);
+            if (lane == 0)
+              tma_box(smem_addr(tails) + t * C::TAIL + b * tp.box * (C::TCOLS * 2), &tp.v, C::DV + static_cast<int32_t>(rank) * C::TCOLS,
+                      0, pos, pg, &sm.tail_full[t]);
+          }
+        }
       }
     }
     if (!ok) {  // nothing may still be on its way into this CTA's memory when it ends
-      for (uint32_t i = put > C::RING ? put - C::RING : 0; i < put; ++i)
-        mbar_wait(&sm.full[i % C::RING], (i / C::RING) & 1u);
-      for (uint32_t i = tail_put > kTails ? tail_put - kTails : 0; i < tail_put; ++i)
-        mbar_wait(&sm.tail_full[i % kTails], (i / kTails) & 1u);
+      for (uint32_t i = put > C::SLOTS ? put - C::SLOTS : 0; i < put; ++i)
+        mbar_wait(&sm.full[i % C::SLOTS], (i / C::SLOTS) & 1u);
+      if (C::LATENT)
+        for (uint32_t i = tile_no > kTails ? tile_no - kTails : 0; i < tile_no; ++i)
+          mbar_wait(&sm.tail_full[i % kTails], (i / kTails) & 1u);
     }
-    if (bad != 0u) atomic_status(p.status, bad);
+    if (__any_sync(0xffffffffu, bad) && lane == 0) atomic_status(p.status, GDN_STATUS_BAD_PAGE);
   } else if (warp == 1) {
     // ---- matrix products --------------------------------------------------------------------
     constexpr uint32_t kScores = idesc_bf16(128, N, false, false), kValues = idesc_bf16(128, N, true, true);
-    const uint32_t ring_at = smem_addr(ring), tails_at = smem_addr(tails), q_at = smem_addr(queries),
-                   w_at = smem_addr(weights);
-    uint32_t i = 0, units = 0;  // tiles and units begun
-    bool ok = true;
+    const uint32_t ring_at = smem_addr(ring), tails_at = smem_addr(tails), w_at = smem_addr(weights);
+    uint32_t i = 0, units = 0;   // tiles and units begun
+    uint32_t k_slot = 0, k_round = 0, v_slot = 0, v_round = 0;  // next slots of keys and of values
     uint32_t first_of_last = 0;  // whether the last tile with scores was its unit's first
+    bool ok = true;
+    auto skip = [](uint32_t& slot, uint32_t& round, uint32_t n) {
+      slot += n;
+      if (slot >= C::SLOTS) {
+        slot -= C::SLOTS;
+        round ^= 1u;
+      }
+    };
+    if (!C::LATENT) skip(v_slot, v_round, C::KS);
 
-    // key chunks [from, to) of tile i against the queries
-    auto scores = [&](int from, int to) {
-      for (int c = from; c < to && ok; ++c) {
-        const uint32_t n = i * C::PER + c, slot = n % C::RING;
-        ok = warp_waited(&sm.full[slot], (n / C::RING) & 1u, sm);
+    auto scores = [&] {
+      const uint32_t q_at = smem_addr(queries) + (C::QB > 1 ? (units & 1u) * C::QBYTES : 0);
+      const uint32_t d = tmem + (i & 1u) * N;
+#pragma unroll
+      for (int s = 0; s < C::KS; ++s) {
+        ok = warp_waited(&sm.full[k_slot], k_round, sm);
         if (!ok) return;
         tc::fence_after_sync();
-        const uint32_t a = ring_at + slot * kChunk, b = q_at + c * (8 * N * 16);
+        const uint32_t a = ring_at + k_slot * C::SLOT, b = q_at + s * (C::SLOTC * 8 * N * 16);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_bf16(tmem + (i & 1u) * N, desc_sw128(a + k * 32, 16, 1024), tc::smem_desc(b + k * (2 * N * 16), N * 16, 128),
-                   kScores, c > 0 || k > 0);
-        if (!C::LATENT) tc::commit(&sm.empty[slot]);
+        for (int k = 0; k < 4 * C::SLOTC; ++k)
+          mma_bf16(d, desc_sw128(a + (k / 4) * kChunk + (k % 4) * 32, 16, 1024), tc::smem_desc(b + k * (2 * N * 16), N * 16, 128),
+                   kScores, s > 0 || k > 0);
+        if (!C::LATENT) tc::commit(&sm.empty[k_slot]);
+        skip(k_slot, k_round, 1);
       }
-      if (C::TAILC > 0 && to == C::KC && ok) {
-        const uint32_t slot = i % kTails;
-        ok = warp_waited(&sm.tail_full[slot], (i / kTails) & 1u, sm);
+      if (C::LATENT) {
+        const uint32_t t = i % kTails;
+        ok = warp_waited(&sm.tail_full[t], (i / kTails) & 1u, sm);
         if (!ok) return;
         tc::fence_after_sync();
-        const uint32_t a = tails_at + slot * kChunk, b = q_at + C::KC * (8 * N * 16);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_bf16(tmem + (i & 1u) * N, desc_sw128(a + k * 32, 16, 1024), tc::smem_desc(b + k * (2 * N * 16), N * 16, 128),
-                   kScores, 1);
-        tc::commit(&sm.tail_empty[slot]);
+        for (int k = 0; k < C::TCOLS / 16; ++k)
+          mma_bf16(d, desc_sw64(tails_at + t * C::TAIL + k * 32, 16, 512),
+                   tc::smem_desc(q_at + (C::KCOLS / 8 + 2 * k) * (N * 16), N * 16, 128), kScores, 1);
+        tc::commit(&sm.tail_empty[t]);
       }
+      skip(k_slot, k_round, C::VS);
+      tc::commit(&sm.s_full[i & 1u]);
     };
     // values of tile j; `first`: of its unit
     auto values = [&](uint32_t j, uint32_t first) {
@@ -328,40 +439,38 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attn_tc_kernel(const __grid_c
       ok = warp_waited(&sm.p_full[buf], (j / C::PB) & 1u, sm);
       if (!ok) return;
       tc::fence_after_sync();
+#pragma unroll
       for (int m = 0; m < C::MB; ++m) {
-        const uint32_t n = j * C::PER + (C::LATENT ? 0 : C::KC) + 2 * m, slot = n % C::RING;
-        constexpr int kUse = C::DV >= 128 ? 2 : 1;
-        if (!C::LATENT)
-          for (int c = 0; c < kUse && ok; ++c) ok = warp_waited(&sm.full[slot + c], (n / C::RING) & 1u, sm);
-        if (!ok) return;
-        tc::fence_after_sync();
+        if (!C::LATENT) {
+          ok = warp_waited(&sm.full[v_slot], v_round, sm);
+          if (!ok) return;
+          tc::fence_after_sync();
+        }
         // dv = 64 is the upper half of the 128 rows; the lower half multiplies the slot before (the
         // tile's keys, or what replaces them) and is never read
-        const uint32_t a = ring_at + (C::DV >= 128 ? slot : slot - 1) * kChunk, b = w_at + buf * C::PBYTES;
+        const uint32_t a = ring_at + (C::DV >= 128 ? v_slot : v_slot - 1) * C::SLOT, b = w_at + buf * C::PBYTES;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          mma_bf16(tmem + 2 * N + m * N, desc_sw128(a + k * 2048, kChunk, 1024),
-                   tc::smem_desc(b + k * 256, 128, kTile * 16), kValues, first == 0u || k > 0);
-        for (int c = 0; c < kUse; ++c) tc::commit(&sm.empty[slot + c]);
+          mma_bf16(tmem + (2 + m) * N, desc_sw128(a + k * 2048, kChunk, 1024), tc::smem_desc(b + k * 256, 128, kTile * 16),
+                   kValues, first == 0u || k > 0);
+        tc::commit(&sm.empty[v_slot]);
+        skip(v_slot, v_round, 1);
       }
+      if (!C::LATENT) skip(v_slot, v_round, C::KS);
       tc::commit(&sm.pv_done[j & 1u]);
     };
 
     while (ok && walk.next(p, &seg)) {
+      const uint32_t qb = units % C::QB;
       for (int t = 0; ok && t < seg.tiles; ++t) {
-        if (t == 0) ok = warp_waited(&sm.q_full, units & 1u, sm);
+        if (t == 0) ok = warp_waited(&sm.q_full[qb], (units / C::QB) & 1u, sm);
         if (ok) ok = warp_waited(&sm.s_empty[i & 1u], ((i >> 1) & 1u) ^ 1u, sm);
         if (!ok) break;
         tc::fence_after_sync();
-        if (C::AHEAD > 0) scores(0, C::AHEAD);
-        if (C::AHEAD < C::KC) {
-          if (ok && i > 0) values(i - 1, first_of_last);
-          if (ok) scores(C::AHEAD, C::KC);
-        }
+        scores();
         if (!ok) break;
-        tc::commit(&sm.s_full[i & 1u]);
-        if (t == seg.tiles - 1) tc::commit(&sm.q_empty);
-        if (C::AHEAD == C::KC && i > 0) values(i - 1, first_of_last);
+        if (t == seg.tiles - 1) tc::commit(&sm.q_empty[qb]);
+        if (i > 0) values(i - 1, first_of_last);
         first_of_last = t == 0;
         ++i;
       }
@@ -370,146 +479,199 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attn_tc_kernel(const __grid_c
     if (ok && i > 0) values(i - 1, first_of_last);
     // the last MMA has left TMEM and shared memory alone when this completes
     tc::commit(&sm.drained);
-    if (!mbar_wait(&sm.drained, 0)) sm.timeout = 1u;
+    if (!mbar_wait(&sm.drained, 0)) *static_cast<volatile uint32_t*>(&sm.timeout) = 1u;
   } else if (warp < 4) {
     // ---- queries of the next unit -----------------------------------------------------------
     // K-major core matrices: 16 bytes of column n, element group e at (e * N + n) * 16
     uint32_t units = 0;
     while (walk.next(p, &seg)) {
-      if (units > 0 && !waited(&sm.q_empty, (units - 1) & 1u, sm)) break;
+      const uint32_t qb = units % C::QB;
+      if (!waited(&sm.q_empty[qb], ((units / C::QB) & 1u) ^ 1u, sm)) break;
       const int cols = min(N, p.cols - seg.col_base);
       const uint16_t* q = static_cast<const uint16_t*>(p.q) + seg.b * p.q_b;
-      constexpr int kVecs = C::DK / 8;
-#pragma unroll 4
+      constexpr int kVecs = (C::KCOLS + C::TCOLS) / 8;
+#pragma unroll 2
       for (int v = tid - 64; v < N * kVecs; v += 64) {
         const int c = v / kVecs, e = v - c * kVecs;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (c < cols) {
-          const int col = seg.col_base + c, t = col / p.group, h = seg.kv_head * p.group + (col - t * p.group);
-          x = *reinterpret_cast<const uint4*>(q + t * p.q_t + h * p.q_h + e * 8);
-        }
-        *reinterpret_cast<uint4*>(queries + (e * N + c) * 16) = x;
+        const int col = seg.col_base + min(c, cols - 1), t = col / p.group, h = seg.kv_head * p.group + (col - t * p.group);
+        const int at = C::LATENT ? (e < C::KCOLS / 8 ? static_cast<int>(rank) * C::KCOLS + e * 8
+                                                     : C::DV + static_cast<int>(rank) * C::TCOLS + (e - C::KCOLS / 8) * 8)
+                                 : e * 8;
+        cp_async16_or_zero(queries + qb * C::QBYTES + (e * N + c) * 16, q + t * p.q_t + h * p.q_h + at, c < cols);
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
       tc::fence_smem_to_async();
-      arrive(&sm.q_full);
+      arrive(&sm.q_full[qb]);
       ++units;
     }
+    write_empty<64>(p, tid - 64);
   } else {
     // ---- softmax ------------------------------------------------------------------------------
-    const int r = tid - 128, w = warp - 4;  // this thread's position of the tile and TMEM lane
+    const int g = C::G > 1 ? (warp - 4) / 4 : 0, w = warp & 3;
+    const int r = w * 32 + lane;      // this thread's position of the tile and TMEM lane
+    const int c_base = g * NC;        // its group's first column
     const uint32_t lanes = tc::lane_base(w);
-    uint32_t i = 0;
+    const uint32_t s_at = tmem + lanes + c_base, o_at = tmem + lanes + 2 * N + c_base;
+    const uint32_t received_there = C::LATENT ? in_cta(smem_addr(received), rank ^ 1u) : 0u;
+    const uint32_t got_there = C::LATENT ? in_cta(smem_addr(sm.got), rank ^ 1u) : 0u;
+    const uint32_t may_send_there = C::LATENT ? in_cta(smem_addr(sm.may_send), rank ^ 1u) : 0u;
+    uint32_t i = 0, sent = 0;
     // After a wait that ran out the threads still go through every barrier together (no later
     // wait holds them up) and write nothing more.
     bool ok = true;
+    auto load_scores = [&](uint32_t tile, float (&s)[NC]) {
+#pragma unroll
+      for (int c = 0; c < NC; c += 16) {
+        float x[16];
+        tc::ld16(s_at + (tile & 1u) * N + c, x);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) s[c + j] = x[j];
+      }
+    };
+    // this CTA's half of the scores of tile `sent` to the other one; they are there (s_full)
+    auto send_scores = [&] {
+      const uint32_t buf = sent % kRecv, bar = buf * C::G + g;
+      if (sent >= C::RB) ok &= waited<true>(&sm.may_send[bar], (sent / kRecv - 1) & 1u, sm);
+      __syncwarp();
+      tc::fence_after_sync();
+      float s[NC];
+      load_scores(sent, s);
+      const uint32_t to = received_there + buf * C::RBYTES + g * (NC * kTile * 4) + r * 16;
+#pragma unroll
+      for (int c = 0; c < NC; c += 4) send16(to + (c / 4) * (kTile * 16), s[c], s[c + 1], s[c + 2], s[c + 3], got_there + bar * 8);
+      ++sent;
+    };
     while (walk.next(p, &seg)) {
       const int cols = min(N, p.cols - seg.col_base);
       const int t_first = seg.col_base / p.group, t_last = (seg.col_base + cols - 1) / p.group;
       const int32_t lower = lower_bound_of(p, seg.n, t_first);
       const int32_t lower_last = lower_bound_of(p, seg.n, t_last);
       const int32_t* row = p.table + static_cast<int64_t>(seg.b) * p.max_pages;
-      auto usable = [&](int tile) -> bool {
-        const int64_t pos = static_cast<int64_t>(tile) * kTile + r;
-        if (pos >= seg.n || pos < lower) return false;
-        const int32_t page = row[pos / p.page_size];
-        return page >= 0 && page < p.num_pages;
+      // the page of this thread's position; looked at a tile later
+      auto entry = [&](int tile) -> int32_t {
+        const int32_t at = min(tile * kTile + r, seg.n - 1);
+        return row[tp.box < kTile ? at >> tp.box_shift : tile / tp.page_tiles];
       };
-      softmax_sync();  // the last unit's rows and maxima are read
-      if (r < N) {
-        sm.m[r] = -INFINITY;
-        sm.rows[r] = r < cols ? row_of(p, seg.b, seg.kv_head, seg.col_base + r) : -1;
+      int32_t next = entry(seg.tile);
+      group_sync(g);  // the last unit's rows and maxima are read
+      if (r < NC) {
+        const int c = c_base + r;
+        sm.m[c] = -INFINITY;
+        sm.last[c] = seg.n - p.T + (seg.col_base + c) / p.group;
+        sm.rows[c] = static_cast<int32_t>(row_of(p, seg.b, seg.kv_head, seg.col_base + c));
       }
-      float l[N];
+      float l[NC];
 #pragma unroll
-      for (int c = 0; c < N; ++c) l[c] = 0.0f;
-      softmax_sync();
-      bool live = usable(seg.tile);
+      for (int c = 0; c < NC; ++c) l[c] = 0.0f;
+      group_sync(g);
       for (int t = 0; t < seg.tiles; ++t, ++i) {
         const int tile = seg.tile + t;
         const int32_t begin = tile * kTile, pos = begin + r;
-        const bool live_next = t + 1 < seg.tiles && usable(tile + 1);
-        ok &= waited(&sm.s_full[i & 1u], (i >> 1) & 1u, sm);
-        __syncwarp();
-        tc::fence_after_sync();
-        float s[N];
+        const bool live = pos < seg.n && pos >= lower && next >= 0 && next < p.num_pages;
+        if (t + 1 < seg.tiles) next = entry(tile + 1);
+        float s[NC];
+        if (!C::LATENT) {
+          ok &= waited(&sm.s_full[i & 1u], (i >> 1) & 1u, sm);
+          __syncwarp();
+          tc::fence_after_sync();
+          load_scores(i, s);
+        } else {
+          if (sent == i) {
+            ok &= waited(&sm.s_full[i & 1u], (i >> 1) & 1u, sm);
+            send_scores();
+          }
+          // the next tile's half goes ahead where it is ready
+          if (C::RB > 1 && t + 1 < seg.tiles &&
+              __all_sync(0xffffffffu, test_wait(&sm.s_full[(i + 1) & 1u], ((i + 1) >> 1) & 1u)))
+            send_scores();
+          load_scores(i, s);
+          const uint32_t buf = i % kRecv, bar = buf * C::G + g;
+          ok &= waited<true>(&sm.got[bar], (i / kRecv) & 1u, sm);
+          if (r == 0) mbar_arrive_expect_tx(&sm.got[bar], NC * kTile * 4);  // the next round's
+          const float4* from = reinterpret_cast<const float4*>(received + buf * C::RBYTES + g * (NC * kTile * 4)) + r;
 #pragma unroll
-        for (int c = 0; c < N; c += 16) {
-          float x[16];
-          tc::ld16(tmem + lanes + (i & 1u) * N + c, x);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) s[c + j] = x[j];
+          for (int c = 0; c < NC; c += 4) {
+            const float4 x = from[(c / 4) * kTile];
+            s[c] += x.x;
+            s[c + 1] += x.y;
+            s[c + 2] += x.z;
+            s[c + 3] += x.w;
+          }
+          arrive_there(may_send_there + bar * 8);
         }
         tc::fence_before_sync();
         arrive(&sm.s_empty[i & 1u]);
         // every column sees every position of the tile, but where it is not live
-        const bool plain = begin + kTile - 1 <= seg.n - p.T + t_first && begin >= lower_last;
-        if (plain) {
+        if (begin + kTile - 1 <= seg.n - p.T + t_first && begin >= lower_last) {
 #pragma unroll
-          for (int c = 0; c < N; ++c) s[c] = live ? s[c] * p.scale_log2 : -INFINITY;
+          for (int c = 0; c < NC; ++c) s[c] = live ? s[c] * p.scale_log2 : -INFINITY;
         } else {
 #pragma unroll
-          for (int c = 0; c < N; ++c) {
-            const int32_t last = seg.n - p.T + (seg.col_base + c) / p.group;
+          for (int c = 0; c < NC; ++c) {
+            const int32_t last = sm.last[c_base + c];
             const bool seen = live && pos <= last && (p.window <= 0 || pos > last - p.window);
             s[c] = seen ? s[c] * p.scale_log2 : -INFINITY;
           }
         }
         bool raise = false;
 #pragma unroll
-        for (int c = 0; c < N; c += 4) {
-          const float4 m = *reinterpret_cast<const float4*>(&sm.m[c]);
+        for (int c = 0; c < NC; c += 4) {
+          const float4 m = *reinterpret_cast<const float4*>(&sm.m[c_base + c]);
           raise |= s[c] > m.x + kRaise || s[c + 1] > m.y + kRaise || s[c + 2] > m.z + kRaise || s[c + 3] > m.w + kRaise;
         }
-        if (softmax_any(raise)) {
+        if (group_any(g, raise)) {
 #pragma unroll
-          for (int c = 0; c < N; ++c) {
+          for (int c = 0; c < NC; ++c) {
             const float x = warp_max(s[c]);
-            if (lane == 0) sm.per_warp[w][c] = x;
+            if (lane == 0) sm.per_warp[w][c_base + c] = x;
           }
-          softmax_sync();
-          float f[N];
+          group_sync(g);
+          float f[NC];
 #pragma unroll
-          for (int c = 0; c < N; ++c) {
-            const float old = sm.m[c];
-            const float top = fmaxf(fmaxf(fmaxf(sm.per_warp[0][c], sm.per_warp[1][c]), fmaxf(sm.per_warp[2][c], sm.per_warp[3][c])), old);
+          for (int c = 0; c < NC; ++c) {
+            const int a = c_base + c;
+            const float old = sm.m[a];
+            const float top = fmaxf(fmaxf(fmaxf(sm.per_warp[0][a], sm.per_warp[1][a]), fmaxf(sm.per_warp[2][a], sm.per_warp[3][a])), old);
             f[c] = top == old ? 1.0f : ex2(old - top);
             l[c] *= f[c];
           }
-          softmax_sync();
-          if (r < N)
-            sm.m[r] = fmaxf(fmaxf(fmaxf(sm.per_warp[0][r], sm.per_warp[1][r]), fmaxf(sm.per_warp[2][r], sm.per_warp[3][r])), sm.m[r]);
+          group_sync(g);
+          if (r < NC) {
+            const int a = c_base + r;
+            sm.m[a] = fmaxf(fmaxf(fmaxf(sm.per_warp[0][a], sm.per_warp[1][a]), fmaxf(sm.per_warp[2][a], sm.per_warp[3][a])), sm.m[a]);
+          }
           if (t > 0) {  // what has been summed so far; no MMA writes it until p_full
             ok &= waited(&sm.pv_done[(i - 1) & 1u], ((i - 1) >> 1) & 1u, sm);
             __syncwarp();
             tc::fence_after_sync();
-#pragma unroll
+#pragma unroll 1
             for (int m = 0; m < C::MB; ++m) {
 #pragma unroll
-              for (int c = 0; c < N; c += 16) {
+              for (int c = 0; c < NC; c += 16) {
                 float x[16];
-                tc::ld16(tmem + lanes + 2 * N + m * N + c, x);
+                tc::ld16(o_at + m * N + c, x);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) x[j] *= f[c + j];
-                tc::st16(tmem + lanes + 2 * N + m * N + c, x);
+                tc::st16(o_at + m * N + c, x);
               }
             }
             tc::wait_st();
             tc::fence_before_sync();
           }
-          softmax_sync();
+          group_sync(g);
         }
         // this tile's buffer of weights was last read by the products of tile i - PB
         if (i >= C::PB) {
           const uint32_t j = i - C::PB;
           ok &= waited(&sm.pv_done[j & 1u], (j >> 1) & 1u, sm);
         }
-        unsigned char* const to = weights + (i % C::PB) * C::PBYTES + r * 16;
+        unsigned char* const to = weights + (i % C::PB) * C::PBYTES + (c_base / 8) * (kTile * 16) + r * 16;
 #pragma unroll
-        for (int c = 0; c < N; c += 8) {
+        for (int c = 0; c < NC; c += 8) {
           uint32_t x[4];
 #pragma unroll
           for (int j = 0; j < 8; j += 4) {
-            float4 m = *reinterpret_cast<const float4*>(&sm.m[c + j]);
+            float4 m = *reinterpret_cast<const float4*>(&sm.m[c_base + c + j]);
             // a column that has seen nothing: 2^(-inf - 0) = 0
             m.x = m.x == -INFINITY ? 0.0f : m.x;
             m.y = m.y == -INFINITY ? 0.0f : m.y;
@@ -529,68 +691,69 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attn_tc_kernel(const __grid_c
         if (begin + kTile > seg.n || begin < lower) {
           // Positions outside the request share its pages: whatever their values are (another
           // request's, or never written), a weight of zero has to meet a zero.
-          constexpr int kValueChunks = C::DV / 64;
+          constexpr int kSlots = C::LATENT ? C::KS : C::VS;
+#pragma unroll 1
+          for (int v = 0; v < kSlots; ++v) {
+            const uint32_t n = i * C::PER + (C::LATENT ? 0 : C::KS) + v, slot = n % C::SLOTS;
+            ok &= waited(&sm.full[slot], (n / C::SLOTS) & 1u, sm);
+            if (pos >= seg.n || pos < lower) {
 #pragma unroll
-          for (int c = 0; c < kValueChunks; ++c) {
-            const uint32_t n = i * C::PER + (C::LATENT ? 0 : C::KC) + c, slot = n % C::RING;
-            ok &= waited(&sm.full[slot], (n / C::RING) & 1u, sm);
-            if (ok && (pos >= seg.n || pos < lower)) {
-              uint4* to16 = reinterpret_cast<uint4*>(ring + slot * kChunk + r * 128);
+              for (int c = 0; c < C::SLOTC; ++c) {
+                uint4* to16 = reinterpret_cast<uint4*>(ring + slot * C::SLOT + c * kChunk + r * 128);
 #pragma unroll
-              for (int j = 0; j < 8; ++j) to16[(j + r) & 7] = make_uint4(0u, 0u, 0u, 0u);
+                for (int j = 0; j < 8; ++j) to16[(j + r) & 7] = make_uint4(0u, 0u, 0u, 0u);
+              }
             }
           }
         }
         tc::fence_smem_to_async();
         tc::fence_before_sync();
         arrive(&sm.p_full[i % C::PB]);
-        live = live_next;
       }
 
       // ---- the unit's (or the share's) end: sums over the positions, then O^T ---------------
+      column_sums<NC>(l, lane);
+      group_sync(g);  // maxima of the last raise are read
+      if (NC == 32) sm.per_warp[w][c_base + lane] = l[0];
+      else if ((lane & 1) == 0) sm.per_warp[w][c_base + lane / 2] = l[0];
+      group_sync(g);
+      float* const part = partial_of(p, worker, seg.index == 0 ? 0 : 1);
+      if (r < NC) {
+        const int c = c_base + r;
+        const float sum = (sm.per_warp[0][c] + sm.per_warp[1][c]) + (sm.per_warp[2][c] + sm.per_warp[3][c]);
+        sm.inv[c] = !seg.whole ? 1.0f : sum > 0.0f ? 1.0f / sum : (sum == sum ? 0.0f : sum);
+        if (ok && c < cols && rank == 0) {
+          if (!seg.whole) {
+            part[N * C::DV + c] = sm.m[c];
+            part[N * C::DV + N + c] = sum;
+          } else if (p.lse != nullptr) {
+            p.lse[sm.rows[c]] = lse_of(sm.m[c], sum);
+          }
+        }
+      }
+      group_sync(g);
       ok &= waited(&sm.pv_done[(i - 1) & 1u], ((i - 1) >> 1) & 1u, sm);
       __syncwarp();
       tc::fence_after_sync();
-      column_sums<N>(l, lane);
-      softmax_sync();  // maxima of the last raise are read
-      if (N >= 32) {
-#pragma unroll
-        for (int j = 0; j < N / 32; ++j) sm.per_warp[w][lane * (N / 32) + j] = l[j];
-      } else if ((lane & 1) == 0) {
-        sm.per_warp[w][lane / 2] = l[0];
-      }
-      softmax_sync();
-      float* part = partial_of(p, blockIdx.x, seg.index == 0 ? 0 : 1);
-      if (ok && r < cols) {
-        const float sum = (sm.per_warp[0][r] + sm.per_warp[1][r]) + (sm.per_warp[2][r] + sm.per_warp[3][r]);
-        if (!seg.whole) {
-          part[p.ncol * C::DV + r] = sm.m[r];
-          part[p.ncol * C::DV + p.ncol + r] = sum;
-        } else if (p.lse != nullptr) {
-          p.lse[sm.rows[r]] = lse_of(sm.m[r], sum);
-        }
-      }
-#pragma unroll
+#pragma unroll 1
       for (int m = 0; m < C::MB; ++m) {
-#pragma unroll
-        for (int c0 = 0; c0 < N; c0 += 16) {
+        const int d = static_cast<int>(rank) * C::VCOLS + (C::DV >= 128 ? m * 128 + r : r - 64);
+#pragma unroll 1
+        for (int c0 = 0; c0 < NC; c0 += 16) {
           float x[16];
-          tc::ld16(tmem + lanes + 2 * N + m * N + c0, x);
-          const int d = C::DV >= 128 ? m * 128 + r : r - 64;
+          tc::ld16(o_at + m * N + c0, x);
           if (ok && d >= 0) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              const int c = c0 + j;
-              if (c >= cols) continue;
-              if (seg.whole) {
-                const float sum = (sm.per_warp[0][c] + sm.per_warp[1][c]) + (sm.per_warp[2][c] + sm.per_warp[3][c]);
-                const float inv = sum > 0.0f ? 1.0f / sum : (sum == sum ? 0.0f : sum);
-                static_cast<__nv_bfloat16*>(p.o)[sm.rows[c] * C::DV + d] = __float2bfloat16_rn(x[j] * inv);
-              } else {
+              const int c = c_base + c0 + j;
+              if (c >= cols) break;
+              if (seg.whole)
+                static_cast<__nv_bfloat16*>(p.o)[static_cast<int64_t>(sm.rows[c]) * C::DV + d] = __float2bfloat16_rn(x[j] * sm.inv[c]);
+              else
                 part[c * C::DV + d] = x[j];
-              }
             }
           }
+          __syncwarp();
         }
       }
       tc::fence_before_sync();  // read before the next unit's products write it (p_full)
@@ -599,6 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attn_tc_kernel(const __grid_c
 
   tc::fence_before_sync();
   __syncthreads();
+  if (C::CL > 1) cluster_sync_all();  // nothing more comes from, or goes to, the other CTA
   if (warp == 1) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, C::TMEM);
@@ -608,59 +772,65 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attn_tc_kernel(const __grid_c
 
 template <class C>
 cudaError_t launch_one(const TcParams& tp, cudaStream_t stream) {
-  const cudaError_t err = cudaFuncSetAttribute(gdn_attn_tc_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(C::SMEM));
+  const cudaError_t err = cudaFuncSetAttribute(gdn_attn_tc_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(tp.a.ctas));
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(tp.a.workers * C::CL);
+  cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1]{};
+  cudaLaunchAttribute attr[2]{};
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {static_cast<unsigned>(C::CL), 1u, 1u};
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = C::CL > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, gdn_attn_tc_kernel<C>, tp);
 }
 
-template <int D>
+template <int DK, int DV, bool LATENT>
 cudaError_t launch_width(const TcParams& tp, cudaStream_t stream) {
   switch (tp.a.ncol) {
-    case 16: return launch_one<Cfg<D, D, 16, false>>(tp, stream);
-    case 32: return launch_one<Cfg<D, D, 32, false>>(tp, stream);
-    default: return launch_one<Cfg<D, D, 64, false>>(tp, stream);
+    case 16: return launch_one<Cfg<DK, DV, 16, LATENT>>(tp, stream);
+    case 32: return launch_one<Cfg<DK, DV, 32, LATENT>>(tp, stream);
+    default: return launch_one<Cfg<DK, DV, 64, LATENT>>(tp, stream);
   }
 }
 
-// Pages as a 4-D tensor (element, head, position, page); boxes of 64 elements of one head,
+// Pages as a 4-D tensor (element, head, position, page); boxes of `width` elements of one head,
 // `box` positions of one page.
 cudaError_t encode_pages(CUtensorMap* map, const AttnParams& p, const void* base, int d, int64_t head, int64_t pos,
-                         int64_t page, int box) {
+                         int64_t page, int box, int width) {
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(p.heads_kv),
                               static_cast<cuuint64_t>(p.page_size), static_cast<cuuint64_t>(p.num_pages)};
   // a dimension of one element has no stride to speak of
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p.heads_kv > 1 ? head : d) * 2u,
                                  static_cast<cuuint64_t>(pos) * 2u,
                                  static_cast<cuuint64_t>(p.num_pages > 1 ? page : d) * 2u};
-  const cuuint32_t boxes[4] = {64u, 1u, static_cast<cuuint32_t>(box), 1u};
-  return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, boxes, CU_TENSOR_MAP_SWIZZLE_128B);
+  const cuuint32_t boxes[4] = {static_cast<cuuint32_t>(width), 1u, static_cast<cuuint32_t>(box), 1u};
+  return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, boxes,
+                      width == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_tc(AttnParams& p, cudaStream_t stream) {
+  const bool latent = p.dk == 576;
   TcParams tp{};
   tp.a = p;
   tp.box = p.page_size < kTile ? p.page_size : kTile;
-  cudaError_t err = encode_pages(&tp.k, p, p.k, p.dk, p.k_head, p.k_pos, p.k_page, tp.box);
-  if (err == cudaSuccess) err = encode_pages(&tp.v, p, p.v, p.dv, p.v_head, p.v_pos, p.v_page, tp.box);
+  tp.box_shift = tp.box == 16 ? 4 : tp.box == 32 ? 5 : tp.box == 64 ? 6 : 7;
+  tp.page_tiles = p.page_size < kTile ? 1 : p.page_size / kTile;
+  cudaError_t err = encode_pages(&tp.k, p, p.k, p.dk, p.k_head, p.k_pos, p.k_page, tp.box, 64);
+  if (err == cudaSuccess)
+    err = latent ? encode_pages(&tp.v, p, p.k, p.dk, p.k_head, p.k_pos, p.k_page, tp.box, 32)
+                 : encode_pages(&tp.v, p, p.v, p.dv, p.v_head, p.v_pos, p.v_page, tp.box, 64);
   if (err != cudaSuccess) return err;
-  if (p.dk == 576)
-    return p.ncol == 16 ? launch_one<Cfg<576, 512, 16, true>>(tp, stream) : launch_one<Cfg<576, 512, 32, true>>(tp, stream);
-  if (p.dk == 64) return launch_width<64>(tp, stream);
-  if (p.dk == 128) return launch_width<128>(tp, stream);
-  return launch_width<256>(tp, stream);
+  if (latent) return launch_width<576, 512, true>(tp, stream);
+  if (p.dk == 64) return launch_width<64, 64, false>(tp, stream);
+  if (p.dk == 128) return launch_width<128, 128, false>(tp, stream);
+  return launch_width<256, 256, false>(tp, stream);
 }
 
 }  // namespace gdn

@@ -59,7 +59,7 @@ struct KvAppendParams {
 
 constexpr int kTile = 128;        // cache positions a CTA takes at a time
 constexpr int kSms = 152;         // of one GB300
-constexpr int kMaxAttnCtas = 608; // CTAs of one attention launch (152 SMs, up to four each)
+constexpr int kMaxAttnCtas = 608; // workers of one attention launch (152 SMs, up to four CTAs each)
 
 struct AttnParams {
   int32_t B, T, H, heads_kv, group;  // group = H / heads_kv
@@ -68,7 +68,7 @@ struct AttnParams {
   int32_t cols;       // T * group: the query rows that share a kv head
   int32_t ncol;       // of these, how many one CTA takes at a time
   int32_t col_groups; // ceil(cols / ncol)
-  int32_t ctas;
+  uint32_t workers;   // CTAs, or pairs of CTAs, that share the tiles
   float scale_log2;   // scale * log2(e)
   const void* q;
   int64_t q_b, q_t, q_h;
@@ -80,8 +80,8 @@ struct AttnParams {
   void* o;
   float* lse;
   int32_t* status;
-  // workspace: one record a CTA, then two partial results a CTA
-  int64_t* records;
+  // workspace: one record a worker, then two partial results a worker
+  uint32_t* records;
   float* partials;
 };
 
@@ -89,16 +89,17 @@ cudaError_t launch_kv_plan(const KvPlanParams& p, cudaStream_t stream);
 cudaError_t launch_kv_release(const KvReleaseParams& p, cudaStream_t stream);
 cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t stream);
 
-// Columns one CTA takes at a time and CTAs at most for a shape, on the path that runs it.
+// Columns one worker takes at a time and workers at most for a shape, on the path that runs it.
 struct AttnPlan {
   bool tensor;  // the tensor-core kernel
-  int ncol, max_ctas;
+  int ncol, max_workers;
 };
 AttnPlan attn_plan(const gdn_paged_kv& kv, int cols);
 size_t attn_workspace_bytes(const AttnPlan& plan, int dv);
 // records, then partials
-constexpr int kRecordInts = 6;
-constexpr size_t kRecordBytes = static_cast<size_t>(kMaxAttnCtas) * kRecordInts * sizeof(int64_t);
+constexpr int kRecordInts = 8;  // five of them in use
+constexpr size_t kRecordBytes = static_cast<size_t>(kMaxAttnCtas) * kRecordInts * sizeof(uint32_t);
+static_assert(kRecordBytes % 16 == 0, "partials are read as vectors");
 
 cudaError_t launch_attn(const AttnPlan& plan, AttnParams& p, cudaStream_t stream);
 cudaError_t launch_attn_general(AttnParams& p, cudaStream_t stream);

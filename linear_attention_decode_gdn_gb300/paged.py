@@ -13,10 +13,17 @@ import torch
 
 from . import _abi
 from ._abi import Attn, PagedKV, check
-from .decode import _ptr, _stream
+from .decode import _ptr
 
 _I2 = ctypes.c_int64 * 2
 _I3 = ctypes.c_int64 * 3
+
+
+def _stream(stream, beside):
+    """The given stream, or the current one of the device that tensor `beside` lives on."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(beside.get_device())
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _want(ok: bool, what: str) -> None:
@@ -78,7 +85,7 @@ def kv_plan(cached_len, new_len, held, block_table, free_list, free_count, *, kv
     check(_abi.load().gdn_kv_plan(batch, block_table.shape[1], page_size, num_pages, slot_map.numel(),
                                   _ptr(cached_len), _ptr(new_len), _ptr(held), _ptr(block_table), _ptr(free_list),
                                   _ptr(free_count), _ptr(kv_len), _ptr(cu_new), _ptr(slot_map), _ptr(held_out),
-                                  _ptr(free_count_out), _ptr(status), _stream(stream)), "gdn_kv_plan")
+                                  _ptr(free_count_out), _ptr(status), _stream(stream, cached_len)), "gdn_kv_plan")
 
 
 def kv_release(requests, held, block_table, free_list, free_count, *, status=None, stream=None):
@@ -92,7 +99,7 @@ def kv_release(requests, held, block_table, free_list, free_count, *, status=Non
     _table(block_table, batch)
     check(_abi.load().gdn_kv_release(batch, block_table.shape[1], free_list.numel(), _ptr(requests),
                                      requests.numel(), _ptr(block_table), _ptr(held), _ptr(free_list),
-                                     _ptr(free_count), _ptr(status), _stream(stream)), "gdn_kv_release")
+                                     _ptr(free_count), _ptr(status), _stream(stream, held)), "gdn_kv_release")
 
 
 def kv_append(kv: PagedKV, k, v, slot_map, *, status=None, stream=None):
@@ -112,7 +119,7 @@ def kv_append(kv: PagedKV, k, v, slot_map, *, status=None, stream=None):
     check(_abi.load().gdn_kv_append(kv, n, k.data_ptr(), _I2(k.stride(0), k.stride(1)), _ptr(v) if tail else None,
                                     v_strides, slot_map.data_ptr(),
                                     _abi.QKV_BF16 if k.dtype is torch.bfloat16 else 0, _ptr(status),
-                                    _stream(stream)), "gdn_kv_append")
+                                    _stream(stream, k)), "gdn_kv_append")
 
 
 def attn_workspace_bytes(kv: PagedKV, batch: int, num_tokens: int, num_heads: int) -> int:
@@ -137,7 +144,7 @@ def _attend(name, kv, q, block_table, kv_len, o, workspace, lse, scale, window, 
     a = Attn(batch, tokens, heads, block_table.shape[1], window, dk ** -0.5 if scale is None else scale, q.data_ptr(),
              _I3(s[0], s[1], s[2]), block_table.data_ptr(), kv_len.data_ptr(), o.data_ptr(), _ptr(lse))
     check(getattr(_abi.load(), name)(kv, a, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                     _ptr(status), _stream(stream)), name)
+                                     _ptr(status), _stream(stream, q)), name)
 
 
 def attn_decode(kv: PagedKV, q, block_table, kv_len, o, workspace, *, lse=None, scale=None, window=0, status=None,
