@@ -33,6 +33,8 @@
 #include "gdn_tc.cuh"
 #include "gdn_tmap.h"
 
+#include <type_traits>
+
 #include <cuda_bf16.h>
 
 namespace gdn {
@@ -127,11 +129,13 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a, uint64_t b
 __device__ __forceinline__ void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
+// One page's box; called by a whole warp with uniform operands, one elected lane issues.
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t head, int32_t pos,
                                         int32_t page, uint64_t* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
-      "[%2];" ::"r"(dst),
+      "{\n .reg .pred e;\n .reg .b32 l;\n elect.sync l|e, 0xffffffff;\n"
+      " @e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+      "[%2];\n}\n" ::"r"(dst),
       "l"(map), "r"(smem_addr(bar)), "r"(x), "r"(head), "r"(pos), "r"(page)
       : "memory");
 }
@@ -159,8 +163,10 @@ __device__ __forceinline__ void send16(uint32_t dst, float a, float b, float c, 
                "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "r"(__float_as_uint(c)), "r"(__float_as_uint(d)), "r"(bar)
                : "memory");
 }
+// An arrival at another CTA's mbarrier that publishes nothing: a release would wait for all that
+// this thread has written.
 __device__ __forceinline__ void arrive_there(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 template <int ID>
 __device__ __forceinline__ void group_sync_id() {
@@ -294,7 +300,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
       mbar_init(&sm.p_full[i], 128 * C::G);
       mbar_init(&sm.pv_done[i], 1);
       mbar_init(&sm.got[i], 1);
-      mbar_init(&sm.may_send[i], 128);
+      mbar_init(&sm.may_send[i], 1);
     }
     mbar_init(&sm.drained, 1);
     sm.timeout = 0u;
@@ -321,62 +327,68 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
     if (lane == 0 && rank == 0) write_record(p, share, worker);
     uint32_t slot = 0, round = 1, tile_no = 0;  // next slot, the parity its barrier has when free
     uint32_t put = 0;
-    bool bad = false;
-    const int boxes = kTile / tp.box;  // of one chunk; lane l looks up the page of box l
-    bool ok = true;
-    while (ok && walk.next(p, &seg)) {
-      const int32_t lower = lower_bound_of(p, seg.n, seg.col_base / p.group);
-      const int32_t* row = p.table + static_cast<int64_t>(seg.b) * p.max_pages;
-      // the entry is only looked at when its tile's turn comes, a tile later
-      auto entry = [&](int tile) -> int32_t {
-        const int32_t at = min(tile * kTile + (lane & (boxes - 1)) * tp.box, seg.n - 1);
-        return row[boxes > 1 ? at >> tp.box_shift : tile / tp.page_tiles];
-      };
-      int32_t next = entry(seg.tile);
-      for (int tile = seg.tile; ok && tile < seg.tile + seg.tiles; ++tile, ++tile_no) {
-        int32_t page = next;
-        if (tile + 1 < seg.tile + seg.tiles) next = entry(tile + 1);
-        // a box that no query of the unit sees reads as zero, as one of a page that is none
-        const int32_t at = tile * kTile + (lane & (boxes - 1)) * tp.box;
-        const bool seen = at < seg.n && at + tp.box > lower, valid = page >= 0 && page < p.num_pages;
-        bad |= seen && !valid;
-        if (!seen || !valid) page = p.num_pages;
-        const int32_t pos = boxes > 1 ? 0 : tile % tp.page_tiles * kTile;
-        for (int s = 0; s < C::PER; ++s) {
-          ok = warp_waited(&sm.empty[slot], round, sm);
-          if (!ok) break;
-          const bool value = !C::LATENT && s >= C::KS;
-          const CUtensorMap* map = value ? &tp.v : &tp.k;
-          const int32_t x = (C::LATENT ? static_cast<int32_t>(rank) * C::KCOLS : 0) + (value ? s - C::KS : s) * (C::SLOTC * 64);
-          const uint32_t dst = smem_addr(ring) + slot * C::SLOT;
-          if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], C::SLOT);
-          for (int b = 0; b < boxes; ++b) {
-            const int32_t pg = __shfl_sync(0xffffffffu, page, b);
-            if (lane == 0) {
+    bool bad = false, ok = true;
+    // BOXES of a chunk; lane l looks up the page of box l
+    auto produce = [&](auto boxes_of_a_chunk) {
+      constexpr int BOXES = decltype(boxes_of_a_chunk)::value, BOX = kTile / BOXES;
+      while (ok && walk.next(p, &seg)) {
+        const int32_t lower = lower_bound_of(p, seg.n, seg.col_base / p.group);
+        const int32_t* row = p.table + static_cast<int64_t>(seg.b) * p.max_pages;
+        // the entry is only looked at when its tile's turn comes, a tile later
+        auto entry = [&](int tile) -> int32_t {
+          const int32_t at = min(tile * kTile + (lane & (BOXES - 1)) * BOX, seg.n - 1);
+          return row[BOXES > 1 ? at / BOX : tile / tp.page_tiles];
+        };
+        int32_t next = entry(seg.tile);
+        for (int tile = seg.tile; ok && tile < seg.tile + seg.tiles; ++tile, ++tile_no) {
+          int32_t page = next;
+          if (tile + 1 < seg.tile + seg.tiles) next = entry(tile + 1);
+          // a box that no query of the unit sees reads as zero, as one of a page that is none
+          const int32_t at = tile * kTile + (lane & (BOXES - 1)) * BOX;
+          const bool seen = at < seg.n && at + BOX > lower, valid = page >= 0 && page < p.num_pages;
+          bad |= seen && !valid;
+          if (!seen || !valid) page = p.num_pages;
+          int32_t pages[BOXES];
+#pragma unroll
+          for (int b = 0; b < BOXES; ++b) pages[b] = __shfl_sync(0xffffffffu, page, b);
+          const int32_t pos = BOXES > 1 ? 0 : tile % tp.page_tiles * kTile;
+          for (int s = 0; s < C::PER; ++s) {
+            ok = warp_waited(&sm.empty[slot], round, sm);
+            if (!ok) break;
+            const bool value = !C::LATENT && s >= C::KS;
+            const CUtensorMap* map = value ? &tp.v : &tp.k;
+            const int32_t x = (C::LATENT ? static_cast<int32_t>(rank) * C::KCOLS : 0) + (value ? s - C::KS : s) * (C::SLOTC * 64);
+            const uint32_t dst = smem_addr(ring) + slot * C::SLOT;
+            tc::expect_tx(&sm.full[slot], C::SLOT);
+#pragma unroll
+            for (int b = 0; b < BOXES; ++b)
 #pragma unroll
               for (int c = 0; c < C::SLOTC; ++c)
-                tma_box(dst + c * kChunk + b * tp.box * 128, map, x + c * 64, seg.kv_head, pos, pg, &sm.full[slot]);
+                tma_box(dst + c * kChunk + b * BOX * 128, map, x + c * 64, seg.kv_head, pos, pages[b], &sm.full[slot]);
+            ++put;
+            if (++slot == C::SLOTS) {
+              slot = 0;
+              round ^= 1u;
             }
           }
-          ++put;
-          if (++slot == C::SLOTS) {
-            slot = 0;
-            round ^= 1u;
-          }
-        }
-        if (C::LATENT && ok) {
-          const uint32_t t = tile_no % kTails;
-          ok = warp_waited(&sm.tail_empty[t], ((tile_no / kTails) & 1u) ^ 1u, sm);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&sm.tail_full[t], C::TAIL);
-          for (int b = 0; b < boxes; ++b) {
-            const int32_t pg = __shfl_sync(0xffffffffu, page, b);
-            if (lane == 0)
-              tma_box(smem_addr(tails) + t * C::TAIL + b * tp.box * (C::TCOLS * 2), &tp.v, C::DV + static_cast<int32_t>(rank) * C::TCOLS,
-                      0, pos, pg, &sm.tail_full[t]);
+          if (C::LATENT && ok) {
+            const uint32_t t = tile_no % kTails;
+            ok = warp_waited(&sm.tail_empty[t], ((tile_no / kTails) & 1u) ^ 1u, sm);
+            if (!ok) break;
+            tc::expect_tx(&sm.tail_full[t], C::TAIL);
+#pragma unroll
+            for (int b = 0; b < BOXES; ++b)
+              tma_box(smem_addr(tails) + t * C::TAIL + b * BOX * (C::TCOLS * 2), &tp.v, C::DV + static_cast<int32_t>(rank) * C::TCOLS,
+                      0, pos, pages[b], &sm.tail_full[t]);
           }
         }
       }
+    };
+    switch (tp.box) {
+      case 16: produce(std::integral_constant<int, 8>{}); break;
+      case 32: produce(std::integral_constant<int, 4>{}); break;
+      case 64: produce(std::integral_constant<int, 2>{}); break;
+      default: produce(std::integral_constant<int, 1>{}); break;
     }
     if (!ok) {  // nothing may still be on its way into this CTA's memory when it ends
       for (uint32_t i = put > C::SLOTS ? put - C::SLOTS : 0; i < put; ++i)
@@ -597,7 +609,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
             s[c + 2] += x.z;
             s[c + 3] += x.w;
           }
-          arrive_there(may_send_there + bar * 8);
         }
         tc::fence_before_sync();
         arrive(&sm.s_empty[i & 1u]);
@@ -619,7 +630,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
           const float4 m = *reinterpret_cast<const float4*>(&sm.m[c_base + c]);
           raise |= s[c] > m.x + kRaise || s[c + 1] > m.y + kRaise || s[c + 2] > m.z + kRaise || s[c + 3] > m.w + kRaise;
         }
-        if (group_any(g, raise)) {
+        const bool any = group_any(g, raise);
+        // every thread of the group has used what it received: the other CTA may send more
+        if (C::LATENT && r == 0) arrive_there(may_send_there + (i % kRecv * C::G + g) * 8);
+        if (any) {
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
             const float x = warp_max(s[c]);
