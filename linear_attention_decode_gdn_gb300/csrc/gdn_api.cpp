@@ -474,7 +474,7 @@ int gdn_kv_plan(int32_t batch, int32_t max_pages, int32_t page_size, int32_t num
     return fail(GDN_ERR_INVALID_ARG, "every array but new_len and status is required");
   gdn::KvPlanParams p{batch,   max_pages, page_size,  num_pages, slot_capacity, cached_len, new_len,        held,
                       block_table, free_list, free_count, kv_len,    cu_new,        slot_map,   held_out, free_count_out,
-                      status};
+                      status, false};
   return launched(gdn::launch_kv_plan(p, static_cast<cudaStream_t>(stream)), "gdn_kv_plan");
 }
 
@@ -508,16 +508,15 @@ int gdn_kv_append(const gdn_paged_kv* kv, int32_t n, const void* k, const int64_
     return fail(GDN_ERR_UNSUPPORTED, "k and v must be 16-byte aligned, with strides >= 0 that are multiples of 16 bytes");
   gdn::KvAppendParams p{};
   p.n = n;
-  p.heads = kv->num_kv_heads;
   p.page_size = kv->page_size;
   p.num_slots = static_cast<int64_t>(kv->num_pages) * kv->page_size;
   p.bf16 = bf16;
   p.a = {k, k_strides[0], k_strides[1], kv->k, kv->k_strides[0], kv->k_strides[1], kv->k_strides[2],
-         static_cast<uint32_t>((latent ? kv->dv : kv->dk) / 8)};
+         static_cast<uint32_t>((latent ? kv->dv : kv->dk) / 8), static_cast<uint32_t>(kv->num_kv_heads)};
   if (tail > 0) {
     const int64_t* to = latent ? kv->k_strides : kv->v_strides;
     void* dst = latent ? static_cast<void*>(static_cast<uint16_t*>(kv->k) + kv->dv) : kv->v;
-    p.b = {v, v_strides[0], v_strides[1], dst, to[0], to[1], to[2], static_cast<uint32_t>(tail / 8)};
+    p.b = {v, v_strides[0], v_strides[1], dst, to[0], to[1], to[2], static_cast<uint32_t>(tail / 8), static_cast<uint32_t>(kv->num_kv_heads)};
   }
   p.slot_map = slot_map;
   p.status = status;

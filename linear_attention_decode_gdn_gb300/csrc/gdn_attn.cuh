@@ -155,7 +155,7 @@ struct Walk {
 // ---- the workspace ----------------------------------------------------------------------
 // Record of a worker: [tiles of the launch, or 0 without work; line positions of the first
 // segment's unit, begin and end; request; unit]. A partial result: dv x ncol sums (column by
-// column, fp32), then the columns' maxima (in the scaled log2 domain) and sums.
+// column, fp32), then the columns' references (in the scaled log2 domain: sums are of 2^(s - m)) and sums.
 __device__ __forceinline__ size_t partial_floats(const AttnParams& p) {
   return static_cast<size_t>(p.ncol) * (p.dv + 2);
 }
@@ -197,7 +197,7 @@ __device__ __forceinline__ void write_empty(const AttnParams& p, int tid) {
 
 constexpr float kLn2 = 0.69314718055994530942f;
 
-// m: the column's maximum of scaled scores (log2 domain), l: its sum of 2^(s - m)
+// m: the column's reference in the scaled log2 domain, l: its sum of 2^(s - m)
 __device__ __forceinline__ float lse_of(float m, float l) {
   return l > 0.0f ? m * kLn2 + logf(l) : (l == l ? __int_as_float(0xff800000) : l);
 }

@@ -6,7 +6,7 @@
 // tcgen05 MMA, the query rows (16, 32 or 64 columns) its narrow side.
 //
 //   S^T [128 positions x N] = K [128 x dk] (q [N x dk])^T        A, B from shared memory
-//   P^T = 2^(S^T - m), m one running maximum a column            in registers, a thread a position
+//   P^T = 2^(S^T - m), m one running reference a column          in registers, a thread a position
 //   O^T [dv x N] += V^T [dv x 128] P^T [128 x N]                 A = V as it lies in memory (its
 //                                                                rows run along dv), B from shared
 //
@@ -17,10 +17,10 @@
 // elements, 128-byte swizzle; pages of 16 .. 128 positions are boxes of a slot). Warp 1 issues
 // the MMAs: scores of tile i + 1 before values of tile i, so the tensor core works while the
 // softmax does. Warps 2 and 3 lay out the next unit's queries. The other warps are the softmax,
-// four for every 32 columns: one thread a position; sums of weights stay in the threads until
-// the unit ends. The running maximum is raised (and O^T rescaled in TMEM) only where a score
-// passes it by 2^8, so most tiles need one barrier and no reduction; weights up to 2^8 lose
-// nothing in bf16 or fp32.
+// four for every 16 columns: one thread a position; sums of weights stay in the threads until
+// the unit ends. The reference is the maximum of the tile that set it, times 2^8; it is raised
+// (and O^T rescaled in TMEM) only where a score passes it, so most tiles need one barrier and no
+// reduction, and no weight is above 1.
 //
 // Latent rows: the value is the key's own row, so a tile's 147 KB would have to stay until the
 // values' product, and with them alone shared memory is full: loads, scores, softmax and values
@@ -47,7 +47,10 @@ constexpr int kChunk = kTile * 128;          // bytes: 128 positions x 64 bf16
 constexpr int kSmemMost = 227 * 1024;
 constexpr int kMiscBytes = 4096;
 constexpr int kMaxSlots = 12;
-constexpr float kRaise = 8.0f;               // log2 of what a weight may grow to
+constexpr int kAhead = 1;                    // tiles that latent rows are fetched into L2 before their load
+constexpr float kHeadroom = 8.0f;            // log2 of what a score may grow by before weights are rescaled
+constexpr float kNothing = -3.0e38f;         // the reference of a column that has seen nothing: finite, so
+                                             // that no difference of infinities is ever taken
 
 template <int DK_, int DV_, int N_, bool LATENT_>
 struct Cfg {
@@ -63,14 +66,13 @@ struct Cfg {
   static constexpr int VS = LATENT ? 0 : VCOLS / 64 / SLOTC;
   static constexpr int PER = KS + VS;
   static constexpr int MB = VCOLS > 128 ? VCOLS / 128 : 1; // blocks of 128 rows of O^T
-  static constexpr int G = N > 32 ? 2 : 1, NC = N / G;     // softmax groups and their columns
+  static constexpr int NC = 16, G = N / NC;                // columns of a softmax group, groups
   static constexpr int THREADS = 128 + 128 * G;
-  static constexpr int PB = LATENT && N > 32 ? 1 : 2;      // buffers of weights
+  static constexpr int PB = LATENT ? 1 : 2;                // buffers of weights
   static constexpr int QB = !LATENT && DK < 256 && N <= 32 ? 2 : 1;  // and of queries
-  static constexpr int RB = LATENT ? (N > 32 ? 1 : 2) : 0; // and of received scores
-  static constexpr int TAIL = kTile * TCOLS * 2, TAILS = LATENT ? (N > 32 ? 1 : 2) : 0;
+  static constexpr int TAIL = kTile * TCOLS * 2, TAILS = LATENT ? 1 : 0;
   static constexpr int QBYTES = N * (KCOLS + TCOLS) * 2, PBYTES = N * kTile * 2, RBYTES = LATENT ? N * kTile * 4 : 0;
-  static constexpr int FIXED = kMiscBytes + QB * QBYTES + PB * PBYTES + RB * RBYTES + TAILS * TAIL;
+  static constexpr int FIXED = kMiscBytes + QB * QBYTES + PB * PBYTES + RBYTES + TAILS * TAIL;
   static constexpr int FIT = (kSmemMost - FIXED) / SLOT < kMaxSlots ? (kSmemMost - FIXED) / SLOT : kMaxSlots;
   static constexpr int SLOTS = SLOTC == 1 ? FIT & ~1 : FIT;
   static constexpr int SMEM = FIXED + SLOTS * SLOT;
@@ -87,7 +89,7 @@ struct Misc {
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], s_empty[2];
   uint64_t p_full[2], pv_done[2];
-  uint64_t got[2], may_send[2];  // scores received; the other CTA has read what was sent
+  uint64_t got[4], may_send[4];  // a group's scores received; the other CTA has read what was sent
   uint64_t drained;
   uint32_t tmem;
   uint32_t timeout;
@@ -126,8 +128,10 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a, uint64_t b
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+// One arrival for a whole warp.
+__device__ __forceinline__ void arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 // One page's box; called by a whole warp with uniform operands, one elected lane issues.
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t head, int32_t pos,
@@ -139,6 +143,7 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
       "l"(map), "r"(smem_addr(bar)), "r"(x), "r"(head), "r"(pos), "r"(page)
       : "memory");
 }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 // 16 bytes to shared memory, zeros where `from_there` is false (then nothing is read)
 __device__ __forceinline__ void cp_async16_or_zero(void* dst, const void* src, bool from_there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(from_there ? 16 : 0)
@@ -168,14 +173,8 @@ __device__ __forceinline__ void send16(uint32_t dst, float a, float b, float c, 
 __device__ __forceinline__ void arrive_there(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-template <int ID>
-__device__ __forceinline__ void group_sync_id() {
-  asm volatile("bar.sync %0, 128;" ::"n"(ID) : "memory");
-}
 // Barriers of one softmax group (four warps).
-__device__ __forceinline__ void group_sync(int g) {
-  if (g == 0) group_sync_id<1>(); else group_sync_id<2>();
-}
+__device__ __forceinline__ void group_sync(int g) { asm volatile("bar.sync %0, 128;" ::"r"(g + 1) : "memory"); }
 __device__ __forceinline__ bool group_any(int g, bool pred) {
   uint32_t r;
   asm volatile(
@@ -201,26 +200,20 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-// Sums of N columns over the warp's lanes: afterwards a lane holds the sum of column lane
-// (N = 32) or lane / 2 (N = 16).
+// Sums of N (16 or 32) columns over the warp's lanes: afterwards a lane holds the sum of column
+// lane * N / 32.
 template <int N>
 __device__ __forceinline__ void column_sums(float (&v)[N], int lane) {
 #pragma unroll
-  for (int off = 16, n = N; off > 0; off >>= 1) {
-    if (n > 1) {
-      const int half = n / 2;
-      const bool upper = (lane & off) != 0;
+  for (int half = N / 2, off = 16; half > 0; half >>= 1, off >>= 1) {
+    const bool upper = (lane & off) != 0;
 #pragma unroll
-      for (int j = 0; j < N / 2; ++j) {
-        if (j >= half) continue;
-        const float keep = upper ? v[j + half] : v[j], send = upper ? v[j] : v[j + half];
-        v[j] = keep + __shfl_xor_sync(0xffffffffu, send, off);
-      }
-      n = half;
-    } else {
-      v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+    for (int j = 0; j < half; ++j) {
+      const float keep = upper ? v[j + half] : v[j], send = upper ? v[j] : v[j + half];
+      v[j] = keep + __shfl_xor_sync(0xffffffffu, send, off);
     }
   }
+  if (N == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
 // mbar_try_wait that also sees what another CTA of the cluster has written
@@ -262,7 +255,16 @@ __device__ __forceinline__ bool waited(uint64_t* bar, uint32_t parity, Misc& sm)
   }
   return true;
 }
-// The same for a whole warp that goes on together.
+// For a warp that polls several barriers: whether it has to stop.
+__device__ __forceinline__ bool gave_up(long long since, Misc& sm) {
+  volatile uint32_t* const flag = &sm.timeout;
+  if (clock64() - since > kWaitLimitCycles) *flag = 1u;
+  return __any_sync(0xffffffffu, *flag != 0u);
+}
+__device__ __forceinline__ bool ready(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, test_wait(bar, parity));
+}
+// A wait with a limit for a whole warp that goes on together.
 __device__ __forceinline__ bool warp_waited(uint64_t* bar, uint32_t parity, Misc& sm) {
   return __all_sync(0xffffffffu, waited(bar, parity, sm));
 }
@@ -272,12 +274,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
   extern __shared__ __align__(1024) unsigned char smem[];
   const AttnParams& p = tp.a;
   constexpr int N = C::N, NC = C::NC;
-  constexpr uint32_t kTails = C::TAILS > 0 ? C::TAILS : 1, kRecv = C::RB > 0 ? C::RB : 1;
+  constexpr uint32_t kTails = C::TAILS > 0 ? C::TAILS : 1;
   unsigned char* const ring = smem;
   unsigned char* const tails = ring + C::SLOTS * C::SLOT;
   unsigned char* const weights = tails + C::TAILS * C::TAIL;
   unsigned char* const received = weights + C::PB * C::PBYTES;
-  unsigned char* const queries = received + C::RB * C::RBYTES;
+  unsigned char* const queries = received + C::RBYTES;
   Misc& sm = *reinterpret_cast<Misc*>(queries + C::QB * C::QBYTES);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -293,20 +295,22 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.tail_full[i], 1);
       mbar_init(&sm.tail_empty[i], 1);
-      mbar_init(&sm.q_full[i], 64);
+      mbar_init(&sm.q_full[i], 2);
       mbar_init(&sm.q_empty[i], 1);
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.s_empty[i], 128 * C::G);
-      mbar_init(&sm.p_full[i], 128 * C::G);
+      mbar_init(&sm.s_empty[i], 4 * C::G);
+      mbar_init(&sm.p_full[i], 4 * C::G);
       mbar_init(&sm.pv_done[i], 1);
+    }
+    for (int i = 0; i < C::G; ++i) {
       mbar_init(&sm.got[i], 1);
       mbar_init(&sm.may_send[i], 1);
     }
     mbar_init(&sm.drained, 1);
     sm.timeout = 0u;
     fence_mbar_init();
-    if (C::LATENT)  // each barrier's first round of scores is expected from the start
-      for (int i = 0; i < C::RB * C::G; ++i) mbar_arrive_expect_tx(&sm.got[i], NC * kTile * 4);
+    if (C::LATENT)  // the first round of scores is expected from the start
+      for (int i = 0; i < C::G; ++i) mbar_arrive_expect_tx(&sm.got[i], C::NC * kTile * 4);
   }
   if (warp == 1) {
     tc::tmem_alloc(&sm.tmem, C::TMEM);
@@ -339,15 +343,19 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
           const int32_t at = min(tile * kTile + (lane & (BOXES - 1)) * BOX, seg.n - 1);
           return row[BOXES > 1 ? at / BOX : tile / tp.page_tiles];
         };
-        int32_t next = entry(seg.tile);
-        for (int tile = seg.tile; ok && tile < seg.tile + seg.tiles; ++tile, ++tile_no) {
-          int32_t page = next;
-          if (tile + 1 < seg.tile + seg.tiles) next = entry(tile + 1);
-          // a box that no query of the unit sees reads as zero, as one of a page that is none
+        // a box that no query of the unit sees reads as zero, as one of a page that is none
+        auto page_of = [&](int tile, int32_t page) -> int32_t {
           const int32_t at = tile * kTile + (lane & (BOXES - 1)) * BOX;
           const bool seen = at < seg.n && at + BOX > lower, valid = page >= 0 && page < p.num_pages;
           bad |= seen && !valid;
-          if (!seen || !valid) page = p.num_pages;
+          return seen && valid ? page : p.num_pages;
+        };
+        const int end = seg.tile + seg.tiles;
+        int32_t next = entry(seg.tile), ahead = 0;
+        if (C::LATENT && seg.tile + kAhead < end) ahead = entry(seg.tile + kAhead);
+        for (int tile = seg.tile; ok && tile < end; ++tile, ++tile_no) {
+          int32_t page = page_of(tile, next);
+          if (tile + 1 < end) next = entry(tile + 1);
           int32_t pages[BOXES];
 #pragma unroll
           for (int b = 0; b < BOXES; ++b) pages[b] = __shfl_sync(0xffffffffu, page, b);
@@ -380,6 +388,23 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
             for (int b = 0; b < BOXES; ++b)
               tma_box(smem_addr(tails) + t * C::TAIL + b * BOX * (C::TCOLS * 2), &tp.v, C::DV + static_cast<int32_t>(rank) * C::TCOLS,
                       0, pos, pages[b], &sm.tail_full[t]);
+          }
+          if (C::LATENT && ok && tile + kAhead < end) {
+            // The ring holds little more than two tiles, so a tile's loads begin when the one two
+            // before is done with: from L2 they are there in time, from memory they are not.
+            const int32_t later = page_of(tile + kAhead, ahead);
+            if (tile + kAhead + 1 < end) ahead = entry(tile + kAhead + 1);
+#pragma unroll
+            for (int j = 0; j < kTile; j += 32) {
+              const int32_t in_tile = j + lane, first = (tile + kAhead) * kTile;
+              const int32_t pg = __shfl_sync(0xffffffffu, later, in_tile / BOX);
+              if (pg == p.num_pages || first + in_tile >= seg.n) continue;
+              const int32_t in_page = BOXES > 1 ? in_tile % BOX : (tile + kAhead) % tp.page_tiles * kTile + in_tile;
+              const uint16_t* from = static_cast<const uint16_t*>(p.k) + pg * p.k_page + in_page * p.k_pos + rank * C::KCOLS;
+#pragma unroll
+              for (int c = 0; c < C::KCOLS / 64; ++c) prefetch_l2(from + c * 64);
+              prefetch_l2(from + C::DV - rank * (C::KCOLS - C::TCOLS));
+            }
           }
         }
       }
@@ -479,10 +504,25 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
         if (ok) ok = warp_waited(&sm.s_empty[i & 1u], ((i >> 1) & 1u) ^ 1u, sm);
         if (!ok) break;
         tc::fence_after_sync();
+        // Whichever is ready first: the last tile's values (their slots are wanted) or these scores.
+        bool due = i > 0;
+        if (C::LATENT && due) {
+          const uint32_t j = i - 1;
+          const long long t0 = clock64();
+          while (ok && !ready(&sm.full[k_slot], k_round)) {
+            if (ready(&sm.p_full[j % C::PB], (j / C::PB) & 1u)) {
+              values(j, first_of_last);
+              due = false;
+              break;
+            }
+            ok = !gave_up(t0, sm);
+          }
+          if (!ok) break;
+        }
         scores();
         if (!ok) break;
         if (t == seg.tiles - 1) tc::commit(&sm.q_empty[qb]);
-        if (i > 0) values(i - 1, first_of_last);
+        if (due) values(i - 1, first_of_last);
         first_of_last = t == 0;
         ++i;
       }
@@ -513,7 +553,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       tc::fence_smem_to_async();
-      arrive(&sm.q_full[qb]);
+      arrive(&sm.q_full[qb], lane);
       ++units;
     }
     write_empty<64>(p, tid - 64);
@@ -524,34 +564,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
     const int c_base = g * NC;        // its group's first column
     const uint32_t lanes = tc::lane_base(w);
     const uint32_t s_at = tmem + lanes + c_base, o_at = tmem + lanes + 2 * N + c_base;
-    const uint32_t received_there = C::LATENT ? in_cta(smem_addr(received), rank ^ 1u) : 0u;
-    const uint32_t got_there = C::LATENT ? in_cta(smem_addr(sm.got), rank ^ 1u) : 0u;
-    const uint32_t may_send_there = C::LATENT ? in_cta(smem_addr(sm.may_send), rank ^ 1u) : 0u;
-    uint32_t i = 0, sent = 0;
+    // the group's part of what the CTAs send each other, and its barriers there
+    const uint32_t mine = g * (NC * kTile * 4) + r * 16;
+    const uint32_t there = C::LATENT ? in_cta(smem_addr(received), rank ^ 1u) + mine : 0u;
+    const uint32_t got_there = C::LATENT ? in_cta(smem_addr(&sm.got[g]), rank ^ 1u) : 0u;
+    const uint32_t may_send_there = C::LATENT ? in_cta(smem_addr(&sm.may_send[g]), rank ^ 1u) : 0u;
+    uint32_t i = 0;
     // After a wait that ran out the threads still go through every barrier together (no later
     // wait holds them up) and write nothing more.
     bool ok = true;
-    auto load_scores = [&](uint32_t tile, float (&s)[NC]) {
+    auto load16 = [](uint32_t at, float* s) {
+      float x[16];
+      tc::ld16(at, x);
 #pragma unroll
-      for (int c = 0; c < NC; c += 16) {
-        float x[16];
-        tc::ld16(s_at + (tile & 1u) * N + c, x);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) s[c + j] = x[j];
-      }
-    };
-    // this CTA's half of the scores of tile `sent` to the other one; they are there (s_full)
-    auto send_scores = [&] {
-      const uint32_t buf = sent % kRecv, bar = buf * C::G + g;
-      if (sent >= C::RB) ok &= waited<true>(&sm.may_send[bar], (sent / kRecv - 1) & 1u, sm);
-      __syncwarp();
-      tc::fence_after_sync();
-      float s[NC];
-      load_scores(sent, s);
-      const uint32_t to = received_there + buf * C::RBYTES + g * (NC * kTile * 4) + r * 16;
-#pragma unroll
-      for (int c = 0; c < NC; c += 4) send16(to + (c / 4) * (kTile * 16), s[c], s[c + 1], s[c + 2], s[c + 3], got_there + bar * 8);
-      ++sent;
+      for (int j = 0; j < 16; ++j) s[j] = x[j];
     };
     while (walk.next(p, &seg)) {
       const int cols = min(N, p.cols - seg.col_base);
@@ -568,13 +594,23 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
       group_sync(g);  // the last unit's rows and maxima are read
       if (r < NC) {
         const int c = c_base + r;
-        sm.m[c] = -INFINITY;
+        sm.m[c] = kNothing;
         sm.last[c] = seg.n - p.T + (seg.col_base + c) / p.group;
         sm.rows[c] = static_cast<int32_t>(row_of(p, seg.b, seg.kv_head, seg.col_base + c));
       }
-      float l[NC];
+      // Sums of weights, and references: in registers, but for the block of 640 threads, which has
+      // 96 of them a thread and reads the references from shared memory.
+      constexpr bool kKeep = C::G <= 2;
+      float l[NC], kept[kKeep ? NC : 4];
 #pragma unroll
-      for (int c = 0; c < NC; ++c) l[c] = 0.0f;
+      for (int c = 0; c < NC; ++c) {
+        l[c] = 0.0f;
+        if (kKeep) kept[c] = kNothing;
+      }
+      auto references = [&](int c) -> float4 {
+        if (kKeep) return make_float4(kept[c], kept[c + 1], kept[c + 2], kept[c + 3]);
+        return *reinterpret_cast<const float4*>(&sm.m[c_base + c]);
+      };
       group_sync(g);
       for (int t = 0; t < seg.tiles; ++t, ++i) {
         const int tile = seg.tile + t;
@@ -582,36 +618,29 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
         const bool live = pos < seg.n && pos >= lower && next >= 0 && next < p.num_pages;
         if (t + 1 < seg.tiles) next = entry(tile + 1);
         float s[NC];
-        if (!C::LATENT) {
-          ok &= waited(&sm.s_full[i & 1u], (i >> 1) & 1u, sm);
-          __syncwarp();
-          tc::fence_after_sync();
-          load_scores(i, s);
-        } else {
-          if (sent == i) {
-            ok &= waited(&sm.s_full[i & 1u], (i >> 1) & 1u, sm);
-            send_scores();
-          }
-          // the next tile's half goes ahead where it is ready
-          if (C::RB > 1 && t + 1 < seg.tiles &&
-              __all_sync(0xffffffffu, test_wait(&sm.s_full[(i + 1) & 1u], ((i + 1) >> 1) & 1u)))
-            send_scores();
-          load_scores(i, s);
-          const uint32_t buf = i % kRecv, bar = buf * C::G + g;
-          ok &= waited<true>(&sm.got[bar], (i / kRecv) & 1u, sm);
-          if (r == 0) mbar_arrive_expect_tx(&sm.got[bar], NC * kTile * 4);  // the next round's
-          const float4* from = reinterpret_cast<const float4*>(received + buf * C::RBYTES + g * (NC * kTile * 4)) + r;
+        ok &= waited(&sm.s_full[i & 1u], (i >> 1) & 1u, sm);
+        __syncwarp();
+        tc::fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < NC; c += 16) load16(s_at + (i & 1u) * N + c, s + c);
+        tc::fence_before_sync();
+        arrive(&sm.s_empty[i & 1u], lane);
+        if (C::LATENT) {
+          if (i > 0) ok &= waited(&sm.may_send[g], (i - 1) & 1u, sm);
+#pragma unroll
+          for (int c = 0; c < NC; c += 4) send16(there + (c / 4) * (kTile * 16), s[c], s[c + 1], s[c + 2], s[c + 3], got_there);
+          ok &= waited<true>(&sm.got[g], i & 1u, sm);
+          if (r == 0) mbar_arrive_expect_tx(&sm.got[g], NC * kTile * 4);  // the next tile's
+          const unsigned char* from = received + mine;
 #pragma unroll
           for (int c = 0; c < NC; c += 4) {
-            const float4 x = from[(c / 4) * kTile];
+            const float4 x = *reinterpret_cast<const float4*>(from + (c / 4) * (kTile * 16));
             s[c] += x.x;
             s[c + 1] += x.y;
             s[c + 2] += x.z;
             s[c + 3] += x.w;
           }
         }
-        tc::fence_before_sync();
-        arrive(&sm.s_empty[i & 1u]);
         // every column sees every position of the tile, but where it is not live
         if (begin + kTile - 1 <= seg.n - p.T + t_first && begin >= lower_last) {
 #pragma unroll
@@ -627,12 +656,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
         bool raise = false;
 #pragma unroll
         for (int c = 0; c < NC; c += 4) {
-          const float4 m = *reinterpret_cast<const float4*>(&sm.m[c_base + c]);
-          raise |= s[c] > m.x + kRaise || s[c + 1] > m.y + kRaise || s[c + 2] > m.z + kRaise || s[c + 3] > m.w + kRaise;
+          const float4 m = references(c);
+          raise |= s[c] > m.x || s[c + 1] > m.y || s[c + 2] > m.z || s[c + 3] > m.w;
         }
         const bool any = group_any(g, raise);
         // every thread of the group has used what it received: the other CTA may send more
-        if (C::LATENT && r == 0) arrive_there(may_send_there + (i % kRecv * C::G + g) * 8);
+        if (C::LATENT && r == 0) arrive_there(may_send_there);
         if (any) {
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
@@ -640,39 +669,51 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
             if (lane == 0) sm.per_warp[w][c_base + c] = x;
           }
           group_sync(g);
-          float f[NC];
-#pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const int a = c_base + c;
-            const float old = sm.m[a];
-            const float top = fmaxf(fmaxf(fmaxf(sm.per_warp[0][a], sm.per_warp[1][a]), fmaxf(sm.per_warp[2][a], sm.per_warp[3][a])), old);
-            f[c] = top == old ? 1.0f : ex2(old - top);
-            l[c] *= f[c];
-          }
-          group_sync(g);
-          if (r < NC) {
-            const int a = c_base + r;
-            sm.m[a] = fmaxf(fmaxf(fmaxf(sm.per_warp[0][a], sm.per_warp[1][a]), fmaxf(sm.per_warp[2][a], sm.per_warp[3][a])), sm.m[a]);
-          }
-          if (t > 0) {  // what has been summed so far; no MMA writes it until p_full
+          if (t > 0) {  // O^T is complete up to the last tile, and no MMA writes it until p_full
             ok &= waited(&sm.pv_done[(i - 1) & 1u], ((i - 1) >> 1) & 1u, sm);
             __syncwarp();
             tc::fence_after_sync();
-#pragma unroll 1
-            for (int m = 0; m < C::MB; ++m) {
+          }
 #pragma unroll
-              for (int c = 0; c < NC; c += 16) {
-                float x[16];
-                tc::ld16(o_at + m * N + c, x);
+          for (int c0 = 0; c0 < NC; c0 += 16) {
+            float f[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] *= f[c + j];
-                tc::st16(o_at + m * N + c, x);
+            for (int j = 0; j < 16; ++j) {
+              const int c = c0 + j, a = c_base + c;
+              const float top = fmaxf(fmaxf(sm.per_warp[0][a], sm.per_warp[1][a]), fmaxf(sm.per_warp[2][a], sm.per_warp[3][a]));
+              const float m = kKeep ? kept[c] : sm.m[a];
+              const float to = top > m ? top + kHeadroom : m;
+              f[j] = ex2(m - to);
+              l[c] *= f[j];
+              if (kKeep) {
+                kept[c] = to;
+                if (r == c) sm.m[a] = to;
               }
             }
+            if (t > 0) {
+#pragma unroll 1
+              for (int block = 0; block < C::MB; ++block) {
+                float x[16];
+                tc::ld16(o_at + block * N + c0, x);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] *= f[j];
+                tc::st16(o_at + block * N + c0, x);
+              }
+            }
+          }
+          if (t > 0) {
             tc::wait_st();
             tc::fence_before_sync();
           }
-          group_sync(g);
+          if (!kKeep) {
+            group_sync(g);  // the old references are read
+            if (r < NC) {
+              const int a = c_base + r;
+              const float top = fmaxf(fmaxf(sm.per_warp[0][a], sm.per_warp[1][a]), fmaxf(sm.per_warp[2][a], sm.per_warp[3][a]));
+              if (top > sm.m[a]) sm.m[a] = top + kHeadroom;
+            }
+            group_sync(g);
+          }
         }
         // this tile's buffer of weights was last read by the products of tile i - PB
         if (i >= C::PB) {
@@ -685,12 +726,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
           uint32_t x[4];
 #pragma unroll
           for (int j = 0; j < 8; j += 4) {
-            float4 m = *reinterpret_cast<const float4*>(&sm.m[c_base + c + j]);
-            // a column that has seen nothing: 2^(-inf - 0) = 0
-            m.x = m.x == -INFINITY ? 0.0f : m.x;
-            m.y = m.y == -INFINITY ? 0.0f : m.y;
-            m.z = m.z == -INFINITY ? 0.0f : m.z;
-            m.w = m.w == -INFINITY ? 0.0f : m.w;
+            const float4 m = references(c + j);
             const float w0 = ex2(s[c + j] - m.x), w1 = ex2(s[c + j + 1] - m.y), w2 = ex2(s[c + j + 2] - m.z),
                         w3 = ex2(s[c + j + 3] - m.w);
             l[c + j] += w0;
@@ -722,14 +758,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
         }
         tc::fence_smem_to_async();
         tc::fence_before_sync();
-        arrive(&sm.p_full[i % C::PB]);
+        arrive(&sm.p_full[i % C::PB], lane);
       }
 
       // ---- the unit's (or the share's) end: sums over the positions, then O^T ---------------
-      column_sums<NC>(l, lane);
+      column_sums(l, lane);
       group_sync(g);  // maxima of the last raise are read
-      if (NC == 32) sm.per_warp[w][c_base + lane] = l[0];
-      else if ((lane & 1) == 0) sm.per_warp[w][c_base + lane / 2] = l[0];
+      if (NC == 32 || (lane & 1) == 0) sm.per_warp[w][c_base + lane * NC / 32] = l[0];
       group_sync(g);
       float* const part = partial_of(p, worker, seg.index == 0 ? 0 : 1);
       if (r < NC) {
@@ -750,12 +785,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
       __syncwarp();
       tc::fence_after_sync();
 #pragma unroll 1
-      for (int m = 0; m < C::MB; ++m) {
-        const int d = static_cast<int>(rank) * C::VCOLS + (C::DV >= 128 ? m * 128 + r : r - 64);
+      for (int block = 0; block < C::MB; ++block) {
+        const int d = static_cast<int>(rank) * C::VCOLS + (C::DV >= 128 ? block * 128 + r : r - 64);
 #pragma unroll 1
         for (int c0 = 0; c0 < NC; c0 += 16) {
           float x[16];
-          tc::ld16(o_at + m * N + c0, x);
+          tc::ld16(o_at + block * N + c0, x);
           if (ok && d >= 0) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) {

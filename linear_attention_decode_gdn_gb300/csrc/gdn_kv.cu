@@ -7,8 +7,9 @@ namespace gdn {
 
 namespace {
 
-constexpr int kPlanThreads = 512;
+constexpr int kReleaseThreads = 512;
 constexpr int kPlanCluster = 8;
+constexpr int kAtOnce = 4;  // tokens a thread gives slots to at a time
 
 __device__ __forceinline__ int64_t shfl_up64(int64_t v, int d) {
   return static_cast<int64_t>(__shfl_up_sync(0xffffffffu, static_cast<unsigned long long>(v), d));
@@ -38,27 +39,35 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* warp_sums, int
   return x + before;
 }
 
-// Largest b in [0, n) with sums[b] <= x (sums rise; sums[0] = 0).
-__device__ __forceinline__ int find_row(const int32_t* sums, int n, int x) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (sums[mid] <= x) lo = mid; else hi = mid;
+// Largest b in [0, n) with sums[b] <= x (sums rise; sums[0] = 0), for COUNT values at once: their
+// searches wait for shared memory together.
+template <int COUNT>
+__device__ __forceinline__ void find_rows(const int32_t* sums, int n, const int (&x)[COUNT], int (&b)[COUNT]) {
+#pragma unroll
+  for (int k = 0; k < COUNT; ++k) b[k] = 0;
+  for (int half = n > 1 ? 1 << (31 - __clz(n - 1)) : 0; half > 0; half >>= 1) {
+#pragma unroll
+    for (int k = 0; k < COUNT; ++k) {
+      const int mid = b[k] + half;
+      if (mid < n && sums[mid] <= x[k]) b[k] = mid;
+    }
   }
-  return lo;
 }
 
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
 }
 
-// Every CTA of the (one) cluster takes the whole batch's sums for itself, in shared memory:
-// that is 12 bytes read a request and spares a second launch or a grid barrier. The cluster
-// barrier stands between the last read of the inputs and the first write of the outputs, so
-// outputs may be the inputs' own arrays. After it the CTAs share the tokens and the pages.
-__global__ void __launch_bounds__(kPlanThreads) gdn_kv_plan_kernel(const KvPlanParams p) {
+// Every CTA takes the whole batch's sums for itself, in shared memory: that is 12 bytes read a
+// request and spares a second launch or a grid barrier. Then the CTAs share the tokens and the
+// pages. Where outputs are the inputs' own arrays (in_place), no CTA may write before all have
+// read: the grid is one cluster then, with its barrier in between.
+// Bound by instructions: a token costs a search over the sums and a division, so the tokens of
+// prompts want many SMs (131,000 tokens: 25 us on one cluster of 8 CTAs).
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) gdn_kv_plan_kernel(const KvPlanParams p) {
   extern __shared__ int32_t sm[];
-  __shared__ int64_t warp_sums[kPlanThreads / 32];
+  __shared__ int64_t warp_sums[THREADS / 32];
   __shared__ int32_t handed;            // free pages handed out
   int32_t* cu = sm;                     // [B + 1] tokens before request b
   int32_t* fresh_cu = cu + p.B + 1;     // [B] pages handed out before request b
@@ -78,7 +87,7 @@ __global__ void __launch_bounds__(kPlanThreads) gdn_kv_plan_kernel(const KvPlanP
   }
   if (tid == 0) handed = 0;
   int64_t tokens = 0, pages = 0;  // of the requests before this chunk
-  for (int base = 0; base < p.B; base += kPlanThreads) {
+  for (int base = 0; base < p.B; base += THREADS) {
     const int b = base + tid;
     int32_t c = -1, n = 0, h = 0;
     if (b < p.B) {
@@ -93,7 +102,7 @@ __global__ void __launch_bounds__(kPlanThreads) gdn_kv_plan_kernel(const KvPlanP
       bad |= GDN_STATUS_BAD_LEN;
     }
     int64_t total;
-    const int64_t upto = tokens + block_scan<kPlanThreads>(n, warp_sums, &total);
+    const int64_t upto = tokens + block_scan<THREADS>(n, warp_sums, &total);
     tokens += total;
     const int64_t length = static_cast<int64_t>(c) + n;
     const int64_t need = (length + p.page_size - 1) / p.page_size;
@@ -103,7 +112,7 @@ __global__ void __launch_bounds__(kPlanThreads) gdn_kv_plan_kernel(const KvPlanP
       bad |= GDN_STATUS_BAD_LEN;
     }
     const int64_t want = skip || need <= h ? 0 : need - h;
-    const int64_t pages_upto = pages + block_scan<kPlanThreads>(want, warp_sums, &total);
+    const int64_t pages_upto = pages + block_scan<THREADS>(want, warp_sums, &total);
     pages += total;
     // The running sum passes `avail` at the first request that does not fit and never comes
     // back below it, so the requests that fit are a prefix of those that want a page, and
@@ -126,9 +135,9 @@ __global__ void __launch_bounds__(kPlanThreads) gdn_kv_plan_kernel(const KvPlanP
     }
   }
   if (bad != 0u && blockIdx.x == 0) atomic_status(p.status, bad);
-  if (gridDim.x > 1) cluster_sync_all(); else __syncthreads();
+  if (p.in_place && gridDim.x > 1) cluster_sync_all(); else __syncthreads();
 
-  const int first = blockIdx.x * kPlanThreads + tid, step = gridDim.x * kPlanThreads;
+  const int first = blockIdx.x * THREADS + tid, step = gridDim.x * THREADS;
   for (int b = first; b <= p.B; b += step) {
     p.cu_new[b] = cu[b];
     if (b == p.B) {
@@ -142,7 +151,10 @@ __global__ void __launch_bounds__(kPlanThreads) gdn_kv_plan_kernel(const KvPlanP
   }
   uint32_t bad_page = 0;
   for (int f = first; f < handed; f += step) {
-    const int b = find_row(fresh_cu, p.B, f);
+    const int wanted[1] = {f};
+    int found[1];
+    find_rows(fresh_cu, p.B, wanted, found);
+    const int b = found[0];
     int32_t page = p.free_list[avail - 1 - f];
     if (page < 0 || page >= p.num_pages) {
       page = -1;
@@ -151,31 +163,45 @@ __global__ void __launch_bounds__(kPlanThreads) gdn_kv_plan_kernel(const KvPlanP
     p.table[static_cast<int64_t>(b) * p.max_pages + held[b] + (f - fresh_cu[b])] = page;
   }
   const int32_t all = cu[p.B];
-  for (int i = first; i < p.slot_capacity; i += step) {
-    int64_t slot = -1;
-    if (i < all) {
-      const int b = find_row(cu, p.B, i);
+  for (int64_t i0 = first; i0 < p.slot_capacity; i0 += static_cast<int64_t>(step) * kAtOnce) {
+    int i[kAtOnce], row[kAtOnce], off[kAtOnce], page[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int64_t at = i0 + static_cast<int64_t>(k) * step;
+      i[k] = at < all ? static_cast<int>(at) : -1;
+    }
+    find_rows(cu, p.B, i, row);
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int b = row[k];
       const int32_t c = start[b];
-      if (c >= 0) {
-        const uint32_t pos = static_cast<uint32_t>(c) + static_cast<uint32_t>(i - cu[b]);
-        const int32_t idx = static_cast<int32_t>(pos / static_cast<uint32_t>(p.page_size));
-        const int32_t off = static_cast<int32_t>(pos - static_cast<uint32_t>(idx) * p.page_size);
-        const int32_t page = idx < held[b] ? p.table[static_cast<int64_t>(b) * p.max_pages + idx]
-                                           : p.free_list[avail - 1 - (fresh_cu[b] + idx - held[b])];
-        if (page >= 0 && page < p.num_pages) slot = static_cast<int64_t>(page) * p.page_size + off;
-        else bad_page = GDN_STATUS_BAD_PAGE;
+      page[k] = -1;
+      off[k] = 0;
+      if (i[k] < 0 || c < 0) continue;
+      const uint32_t pos = static_cast<uint32_t>(c) + static_cast<uint32_t>(i[k] - cu[b]);
+      const int32_t idx = static_cast<int32_t>(pos / static_cast<uint32_t>(p.page_size));
+      off[k] = static_cast<int32_t>(pos - static_cast<uint32_t>(idx) * p.page_size);
+      page[k] = idx < held[b] ? p.table[static_cast<int64_t>(b) * p.max_pages + idx]
+                              : p.free_list[avail - 1 - (fresh_cu[b] + idx - held[b])];
+      if (page[k] < 0 || page[k] >= p.num_pages) {
+        page[k] = -1;
+        bad_page = GDN_STATUS_BAD_PAGE;
       }
     }
-    p.slot_map[i] = slot;
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int64_t at = i0 + static_cast<int64_t>(k) * step;
+      if (at < p.slot_capacity) p.slot_map[at] = page[k] < 0 ? -1 : static_cast<int64_t>(page[k]) * p.page_size + off[k];
+    }
   }
   if (bad_page != 0u) atomic_status(p.status, bad_page);
 }
 
 // One CTA: the requests' page counts are summed so that each knows where its pages go, and
 // the warps copy them. Finished requests are few; nothing here is worth more CTAs.
-__global__ void __launch_bounds__(kPlanThreads) gdn_kv_release_kernel(const KvReleaseParams p) {
-  __shared__ int64_t warp_sums[kPlanThreads / 32];
-  __shared__ int32_t at[kPlanThreads], row[kPlanThreads], count[kPlanThreads];
+__global__ void __launch_bounds__(kReleaseThreads) gdn_kv_release_kernel(const KvReleaseParams p) {
+  __shared__ int64_t warp_sums[kReleaseThreads / 32];
+  __shared__ int32_t at[kReleaseThreads], row[kReleaseThreads], count[kReleaseThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_launch_dependents();
   griddep_wait();
@@ -186,7 +212,7 @@ __global__ void __launch_bounds__(kPlanThreads) gdn_kv_release_kernel(const KvRe
     if (tid == 0) atomic_status(p.status, GDN_STATUS_BAD_LEN);
     return;
   }
-  for (int base = 0; base < p.n; base += kPlanThreads) {
+  for (int base = 0; base < p.n; base += kReleaseThreads) {
     const int i = base + tid;
     int32_t b = i < p.n ? p.requests[i] : -1;
     if (b >= p.B) {
@@ -200,7 +226,7 @@ __global__ void __launch_bounds__(kPlanThreads) gdn_kv_release_kernel(const KvRe
       b = -1;
     }
     int64_t total;
-    const int64_t upto = block_scan<kPlanThreads>(h, warp_sums, &total);
+    const int64_t upto = block_scan<kReleaseThreads>(h, warp_sums, &total);
     // past the list's end this request and the later ones of the chunk keep their pages
     const bool fits = top + upto <= p.num_pages;
     if (h > 0 && !fits) bad |= GDN_STATUS_BAD_LEN;
@@ -209,9 +235,9 @@ __global__ void __launch_bounds__(kPlanThreads) gdn_kv_release_kernel(const KvRe
     count[tid] = fits ? h : 0;
     if (h > 0 && fits) p.held[b] = 0;
     int64_t kept;
-    block_scan<kPlanThreads>(fits ? h : 0, warp_sums, &kept);
+    block_scan<kReleaseThreads>(fits ? h : 0, warp_sums, &kept);
     __syncthreads();
-    for (int j = warp; j < kPlanThreads; j += kPlanThreads / 32) {
+    for (int j = warp; j < kReleaseThreads; j += kReleaseThreads / 32) {
       const int32_t* from = p.table + static_cast<int64_t>(row[j]) * p.max_pages;
       for (int k = lane; k < count[j]; k += 32) p.free_list[at[j] + k] = from[k];
     }
@@ -231,39 +257,61 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-// One thread an 8-element vector: one 16-byte load (two for fp32) and one 16-byte store.
-// Neighbouring threads take neighbouring vectors of a row.
+// A row of 8-element vectors is copied by a warp (or by 2^k lanes of one, where it is that short),
+// kFlight vectors a lane in flight: the slot and its page are looked up once a row, and
+// neighbouring lanes move neighbouring 16 bytes.
+template <bool BF16>
+__device__ __forceinline__ void copy_rows(const KvAppendParams& p, const KvRows& s, int64_t r, int64_t page, int64_t pos,
+                                          int lane, int lanes) {
+  constexpr int kFlight = 4;
+  const uint32_t all = s.vecs * s.heads;
+  const unsigned char* const src = static_cast<const unsigned char*>(s.src) + r * s.src_row * (BF16 ? 2 : 4);
+  uint16_t* const dst = static_cast<uint16_t*>(s.dst) + page * s.dst_page + pos * s.dst_pos;
+  for (uint32_t v0 = lane; v0 < all; v0 += lanes * kFlight) {
+    uint4 x[kFlight];
+    int64_t to[kFlight];
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      const uint32_t v = v0 + k * lanes;
+      if (v >= all) break;
+      const uint32_t head = s.heads == 1 ? 0u : v / s.vecs, e = (v - head * s.vecs) * 8;
+      const int64_t from = head * s.src_head + e;
+      to[k] = head * s.dst_head + e;
+      if (BF16) {
+        x[k] = *reinterpret_cast<const uint4*>(src + from * 2);
+      } else {
+        const float4* f = reinterpret_cast<const float4*>(src + from * 4);
+        const float4 lo = f[0], hi = f[1];
+        x[k] = make_uint4(pack_bf16(lo.x, lo.y), pack_bf16(lo.z, lo.w), pack_bf16(hi.x, hi.y), pack_bf16(hi.z, hi.w));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      if (v0 + k * lanes >= all) break;
+      *reinterpret_cast<uint4*>(dst + to[k]) = x[k];
+    }
+  }
+}
+
+template <bool BF16>
 __global__ void __launch_bounds__(kAppendThreads) gdn_kv_append_kernel(const KvAppendParams p) {
   griddep_launch_dependents();
   griddep_wait();
-  const uint32_t va = p.a.vecs * p.heads, vb = p.b.vecs * p.heads, row_vecs = va + vb;
-  const int64_t all = static_cast<int64_t>(p.n) * row_vecs;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kAppendThreads;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kAppendThreads + threadIdx.x; i < all; i += step) {
-    const int64_t r = i / row_vecs;
-    uint32_t v = static_cast<uint32_t>(i - r * row_vecs);
+  const int lanes = p.lanes, lane = threadIdx.x & (lanes - 1);
+  const int64_t rows_at_once = static_cast<int64_t>(gridDim.x) * (kAppendThreads / lanes);
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * (kAppendThreads / lanes) + threadIdx.x / lanes; r < p.n; r += rows_at_once) {
     const int64_t slot = p.slot_map[r];
     if (slot < 0) continue;
     if (slot >= p.num_slots) {
-      if (v == 0) atomic_status(p.status, GDN_STATUS_BAD_SLOT);
+      if (lane == 0) atomic_status(p.status, GDN_STATUS_BAD_SLOT);
       continue;
     }
-    const bool second = v >= va;
-    if (second) v -= va;
-    const KvRows& s = second ? p.b : p.a;
-    const uint32_t head = v / s.vecs, e = (v - head * s.vecs) * 8;
-    const int64_t from = r * s.src_row + head * s.src_head + e;
-    uint4 x;
-    if (p.bf16) {
-      x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(s.src) + from);
-    } else {
-      const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(s.src) + from);
-      const float4 lo = f[0], hi = f[1];
-      x = make_uint4(pack_bf16(lo.x, lo.y), pack_bf16(lo.z, lo.w), pack_bf16(hi.x, hi.y), pack_bf16(hi.z, hi.w));
-    }
-    const int64_t page = slot / p.page_size, pos = slot - page * p.page_size;
-    uint16_t* to = static_cast<uint16_t*>(s.dst) + page * s.dst_page + pos * s.dst_pos + head * s.dst_head + e;
-    *reinterpret_cast<uint4*>(to) = x;
+    // 32 bits hold most slots, and their division is several times shorter
+    const int64_t page = slot <= 0x7fffffff ? static_cast<int64_t>(static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.page_size))
+                                            : slot / p.page_size;
+    const int64_t pos = slot - page * p.page_size;
+    copy_rows<BF16>(p, p.a, r, page, pos, lane, lanes);
+    if (p.b.vecs > 0) copy_rows<BF16>(p, p.b, r, page, pos, lane, lanes);
   }
 }
 
@@ -289,25 +337,52 @@ cudaError_t launch_overlapped(void (*kernel)(const P), const P& p, unsigned grid
 
 }  // namespace
 
-cudaError_t launch_kv_plan(const KvPlanParams& p, cudaStream_t stream) {
+namespace {
+
+template <int THREADS>
+cudaError_t launch_plan(const KvPlanParams& p, unsigned ctas, cudaStream_t stream) {
   const size_t smem = (5u * p.B + 1u) * sizeof(int32_t);
-  const cudaError_t err = cudaFuncSetAttribute(gdn_kv_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (5 * kMaxPlanBatch + 1) * static_cast<int>(sizeof(int32_t)));
-  if (err != cudaSuccess) return err;
-  // a few rounds of one CTA cost less than the cluster's start and barrier
-  const unsigned ctas = p.slot_capacity > 4 * kPlanThreads || p.B > 4 * kPlanThreads ? kPlanCluster : 1;
-  return launch_overlapped(gdn_kv_plan_kernel, p, ctas, kPlanThreads, smem, ctas, stream);
+  if (smem > 48 * 1024) {
+    const cudaError_t err = cudaFuncSetAttribute(gdn_kv_plan_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 (5 * kMaxPlanBatch + 1) * static_cast<int>(sizeof(int32_t)));
+    if (err != cudaSuccess) return err;
+  }
+  return launch_overlapped(gdn_kv_plan_kernel<THREADS>, p, ctas, THREADS, smem, p.in_place ? ctas : 1u, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_plan(const KvPlanParams& given, cudaStream_t stream) {
+  KvPlanParams p = given;
+  p.in_place = p.kv_len == p.cached || p.held_out == p.held || p.free_count_out == p.free_count;
+  // A decode step is one round of a small CTA.
+  if (p.slot_capacity <= 1024 && p.B <= 1024) return launch_plan<256>(p, 1, stream);
+  if (p.in_place) return launch_plan<1024>(p, kPlanCluster, stream);
+  const unsigned ctas = (p.slot_capacity + 256u * kAtOnce - 1) / (256u * kAtOnce);
+  return launch_plan<256>(p, ctas < 1 ? 1 : ctas < kSms ? ctas : kSms, stream);
 }
 
 cudaError_t launch_kv_release(const KvReleaseParams& p, cudaStream_t stream) {
-  return launch_overlapped(gdn_kv_release_kernel, p, 1u, kPlanThreads, 0, 1u, stream);
+  return launch_overlapped(gdn_kv_release_kernel, p, 1u, kReleaseThreads, 0, 1u, stream);
 }
 
-cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t stream) {
-  const int64_t all = static_cast<int64_t>(p.n) * (p.a.vecs + p.b.vecs) * p.heads;
-  const int64_t blocks = (all + kAppendThreads - 1) / kAppendThreads;
-  const unsigned grid = static_cast<unsigned>(blocks < 152 * 8 ? blocks : 152 * 8);
-  return launch_overlapped(gdn_kv_append_kernel, p, grid, kAppendThreads, 0, 1u, stream);
+cudaError_t launch_kv_append(const KvAppendParams& given, cudaStream_t stream) {
+  KvAppendParams p = given;
+  uint32_t longest = 0;
+  for (KvRows* s : {&p.a, &p.b}) {
+    if (s->heads > 1 && s->src_head == s->vecs * 8 && s->dst_head == s->vecs * 8) {  // heads in one piece
+      s->vecs *= s->heads;
+      s->heads = 1;
+    }
+    const uint32_t all = s->vecs * s->heads;
+    longest = all > longest ? all : longest;
+  }
+  p.lanes = 1;
+  while (p.lanes < 32 && static_cast<uint32_t>(p.lanes) < longest) p.lanes *= 2;
+  const int64_t rows = kAppendThreads / p.lanes, blocks = (p.n + rows - 1) / rows;
+  const unsigned grid = static_cast<unsigned>(blocks < kSms * 8 ? blocks : kSms * 8);
+  return launch_overlapped(p.bf16 ? gdn_kv_append_kernel<true> : gdn_kv_append_kernel<false>, p, grid, kAppendThreads, 0, 1u,
+                           stream);
 }
 
 }  // namespace gdn

@@ -27,6 +27,7 @@ struct KvPlanParams {
   int32_t* held_out;
   int32_t* free_count_out;
   int32_t* status;
+  bool in_place;  // an output is its input's array (set by the launcher)
 };
 
 struct KvReleaseParams {
@@ -39,17 +40,18 @@ struct KvReleaseParams {
   int32_t* status;
 };
 
-// One source of rows and where its elements go: `vecs` 8-element vectors of each head.
+// One source of rows and where its elements go: `vecs` 8-element vectors of each of `heads`.
 struct KvRows {
   const void* src;
   int64_t src_row, src_head;  // elements
   void* dst;
   int64_t dst_page, dst_pos, dst_head;  // elements
-  uint32_t vecs;
+  uint32_t vecs, heads;
 };
 
 struct KvAppendParams {
-  int32_t n, heads, page_size;
+  int32_t n, page_size;
+  int32_t lanes;  // of a warp that share a row (set by the launcher)
   int64_t num_slots;
   bool bf16;
   KvRows a, b;  // b.vecs may be 0
