@@ -139,6 +139,8 @@ def _declare(lib):
 def load(path: str | None = None):
     """Returns the loaded libgdn (raises RuntimeError if it was not built)."""
     global _lib
+    if _lib is not None and path is None:  # loaded once, never unloaded
+        return _lib
     with _lock:
         if _lib is None or path is not None:
             p = path or LIB_PATH
