@@ -192,84 +192,89 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_general_kernel(const AttnPa
   if (bad != 0u) atomic_status(p.status, bad);
 }
 
-constexpr int kJoinThreads = 128;
-constexpr int kJoinAhead = 8;  // parts whose sums are loaded before their weights are known
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWidth = 128;  // value elements a warp adds: four a lane
+constexpr int kJoinAhead = 8;    // parts in flight
 
-// Block (i, c) looks at the border between the shares of workers i and i + 1. Where it is the
-// first border inside a unit, the block adds the unit's partial results for the columns c,
-// c + grid, ... in the order of the workers, so the sums do not depend on timing:
+// Block (i, .) looks at the border between the shares of workers i and i + 1. Where it is the
+// first border inside a unit, its warps add the unit's partial results, each for one column and
+// kJoinWidth value elements, in the order of the workers, so the sums do not depend on timing:
 // m = max m_j, l = sum 2^(m_j - m) l_j, o = sum 2^(m_j - m) o_j / l.
-// Bound by latency: three dependent loads (the record, maxima and sums, the parts).
+// Bound by latency, so a warp waits for two loads only: the record, then references, sums and
+// the first parts together.
 __global__ void __launch_bounds__(kJoinThreads) gdn_attn_join_kernel(const AttnParams p) {
-  __shared__ float weight[kMaxAttnCtas];
-  __shared__ float total[2];
   griddep_launch_dependents();
   griddep_wait();
-  const int i = blockIdx.x + 1, tid = threadIdx.x;
+  const int i = blockIdx.x + 1, lane = threadIdx.x & 31;
   const uint32_t* rec = p.records + static_cast<size_t>(i) * kRecordInts;
   const uint4 r = *reinterpret_cast<const uint4*>(rec);
+  const int unit = static_cast<int>(rec[4]);
   const uint32_t tiles = r.x, unit_start = r.y, unit_end = r.z;
-  const int b = static_cast<int>(r.w), unit = static_cast<int>(rec[4]);
+  const int b = static_cast<int>(r.w);
   if (tiles == 0) return;
   const uint32_t before = share_start(tiles, p.workers, i - 1);
   // the unit begins with worker i, or an earlier border is inside it too
   if (share_start(tiles, p.workers, i) <= unit_start || before > unit_start) return;
   const int kv_head = unit / p.col_groups, col_base = (unit - kv_head * p.col_groups) * p.ncol;
   const int cols = min(p.ncol, p.cols - col_base);
+  const int widths = (p.dv + kJoinWidth - 1) / kJoinWidth;
+  const int task = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5);
+  const int c = task / widths, d = (task - c * widths) * kJoinWidth + lane * 4;
+  if (c >= cols) return;
   const int parts = static_cast<int>(worker_from(tiles, p.workers, unit_end)) - (i - 1);  // workers i - 1, i, ...
   // the unit is worker i - 1's last segment: its first one only where the share begins with it
   const int slot0 = before == unit_start ? 0 : 1;
-  auto part = [&](int j) { return partial_of(p, i - 1 + j, j == 0 ? slot0 : 0); };
-  for (int c = blockIdx.y; c < cols; c += gridDim.y) {
-    const int64_t row = row_of(p, b, kv_head, col_base + c);
-    float2 ahead[kJoinAhead];
+  const size_t floats = partial_floats(p);
+  const float* const first = partial_of(p, i - 1, slot0);
+  const float* const second = partial_of(p, i, 0);  // and so on, two apart
+  auto part = [&](int j) { return j == 0 ? first : second + (j - 1) * 2 * floats; };
+  const int64_t at = static_cast<int64_t>(c) * p.dv + d, ref = static_cast<int64_t>(p.ncol) * p.dv + c;
+  const bool mine = d < p.dv;
+
+  float4 ahead[kJoinAhead];
 #pragma unroll
-    for (int j = 0; j < kJoinAhead; ++j)
-      if (j < parts && 2 * tid < p.dv) ahead[j] = *reinterpret_cast<const float2*>(part(j) + c * p.dv + 2 * tid);
-    __syncthreads();  // the last column's weights are read
-    if (tid < 32) {
-      float m = -INFINITY;
-      for (int j = tid; j < parts; j += 32) {
-        weight[j] = part(j)[p.ncol * p.dv + c];
-        m = fmaxf(m, weight[j]);
-      }
+  for (int j = 0; j < kJoinAhead; ++j)
+    if (mine && j < parts) ahead[j] = *reinterpret_cast<const float4*>(part(j) + at);
+  float m = -INFINITY;
+  for (int j = lane; j < parts; j += 32) m = fmaxf(m, part(j)[ref]);
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-      const float ref = m == -INFINITY ? 0.0f : m;
-      float l = 0.0f;
-      for (int j = tid; j < parts; j += 32) {
-        const float f = exp2f(weight[j] - ref);
-        weight[j] = f;
-        l += f * part(j)[p.ncol * p.dv + p.ncol + c];
+  for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+  const float zero = m == -INFINITY ? 0.0f : m;
+  float l = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  auto add = [&](float w, const float4& x) {
+    o.x = fmaf(w, x.x, o.x);
+    o.y = fmaf(w, x.y, o.y);
+    o.z = fmaf(w, x.z, o.z);
+    o.w = fmaf(w, x.w, o.w);
+  };
+  for (int j0 = 0; j0 < parts; j0 += 32) {
+    const bool have = j0 + lane < parts;
+    const float w = have ? exp2f(part(j0 + lane)[ref] - zero) : 0.0f;
+    if (have) l = fmaf(w, part(j0 + lane)[ref + p.ncol], l);
+    const int count = min(32, parts - j0);
+    for (int j1 = 0; j1 < count; j1 += kJoinAhead) {
+      if (j0 + j1 > 0) {
+#pragma unroll
+        for (int j = 0; j < kJoinAhead; ++j)
+          if (mine && j1 + j < count) ahead[j] = *reinterpret_cast<const float4*>(part(j0 + j1 + j) + at);
       }
-      l = warp_sum(l);
-      if (tid == 0) {
-        total[0] = m;
-        total[1] = l;
-      }
-    }
-    __syncthreads();
-    const float l = total[1], inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
-    for (int d = 2 * tid; d < p.dv; d += 2 * kJoinThreads) {
-      float2 o = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int j = 0; j < kJoinAhead; ++j) {
-        if (j >= parts) break;
-        const float2 x = d == 2 * tid ? ahead[j] : *reinterpret_cast<const float2*>(part(j) + c * p.dv + d);
-        o.x = fmaf(weight[j], x.x, o.x);
-        o.y = fmaf(weight[j], x.y, o.y);
+        const float wj = __shfl_sync(0xffffffffu, w, (j1 + j) & 31);
+        if (mine && j1 + j < count) add(wj, ahead[j]);
       }
-#pragma unroll 8
-      for (int j = kJoinAhead; j < parts; ++j) {
-        const float2 x = *reinterpret_cast<const float2*>(part(j) + c * p.dv + d);
-        o.x = fmaf(weight[j], x.x, o.x);
-        o.y = fmaf(weight[j], x.y, o.y);
-      }
-      *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.o) + row * p.dv + d) =
-          __floats2bfloat162_rn(o.x * inv, o.y * inv);
     }
-    if (tid == 0 && p.lse != nullptr) p.lse[row] = lse_of(total[0], l);
   }
+  l = warp_sum(l);
+  const int64_t row = row_of(p, b, kv_head, col_base + c);
+  if (mine) {
+    const float inv = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);
+    __nv_bfloat162* const to = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.o) + row * p.dv + d);
+    to[0] = __floats2bfloat162_rn(o.x * inv, o.y * inv);
+    to[1] = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+  }
+  if (d == 0 && p.lse != nullptr) p.lse[row] = lse_of(m, l);
 }
 
 cudaError_t launch_overlapped(void (*kernel)(const AttnParams), const AttnParams& p, dim3 grid, unsigned threads,
@@ -320,8 +325,9 @@ cudaError_t launch_attn_general(AttnParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_attn_join(const AttnParams& p, cudaStream_t stream) {
-  const unsigned parts = static_cast<unsigned>(p.cols < p.ncol ? p.cols : p.ncol);
-  return launch_overlapped(gdn_attn_join_kernel, p, dim3(p.workers - 1, parts), kJoinThreads, 0, stream);
+  const unsigned cols = static_cast<unsigned>(p.cols < p.ncol ? p.cols : p.ncol);
+  const unsigned tasks = cols * ((p.dv + kJoinWidth - 1) / kJoinWidth), warps = kJoinThreads / 32;
+  return launch_overlapped(gdn_attn_join_kernel, p, dim3(p.workers - 1, (tasks + warps - 1) / warps), kJoinThreads, 0, stream);
 }
 
 cudaError_t launch_attn(const AttnPlan& plan, AttnParams& p, cudaStream_t stream) {
