@@ -252,7 +252,7 @@ int attend(const gdn_paged_kv* kv, const gdn_attn* a, void* workspace, size_t wo
     return fail(GDN_ERR_INVALID_ARG, "workspace of %zu bytes, %zu are needed (gdn_attn_workspace)", workspace_bytes, need);
   const int64_t col_groups = (a->num_tokens * group + plan.ncol - 1) / plan.ncol;
   const int64_t tiles = (static_cast<int64_t>(a->max_pages) * kv->page_size + gdn::kTile - 1) / gdn::kTile;
-  if (tiles * a->batch > 0x7fffffffLL / (kv->num_kv_heads * col_groups))
+  if ((tiles + plan.unit_cost) * a->batch > 0x7fffffffLL / (kv->num_kv_heads * col_groups))
     return fail(GDN_ERR_UNSUPPORTED, "the table could hold 2^31 tiles of %d positions or more", gdn::kTile);
   gdn::AttnParams p{};
   p.B = a->batch;

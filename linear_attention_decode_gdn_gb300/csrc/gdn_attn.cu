@@ -208,13 +208,15 @@ __global__ void __launch_bounds__(kJoinThreads) gdn_attn_join_kernel(const AttnP
   const int i = blockIdx.x + 1, lane = threadIdx.x & 31;
   const uint32_t* rec = p.records + static_cast<size_t>(i) * kRecordInts;
   const uint4 r = *reinterpret_cast<const uint4*>(rec);
-  const int unit = static_cast<int>(rec[4]);
+  const uint2 r2 = *reinterpret_cast<const uint2*>(rec + 4);
+  const int unit = static_cast<int>(r2.x);
   const uint32_t tiles = r.x, unit_start = r.y, unit_end = r.z;
   const int b = static_cast<int>(r.w);
   if (tiles == 0) return;
   const uint32_t before = share_start(tiles, p.workers, i - 1);
-  // the unit begins with worker i, or an earlier border is inside it too
-  if (share_start(tiles, p.workers, i) <= unit_start || before > unit_start) return;
+  // the unit's first tile is worker i's or a later one's, or an earlier border is inside it too
+  const uint32_t first_tile = unit_start + r2.y;
+  if (share_start(tiles, p.workers, i) <= first_tile || before > first_tile) return;
   const int kv_head = unit / p.col_groups, col_base = (unit - kv_head * p.col_groups) * p.ncol;
   const int cols = min(p.ncol, p.cols - col_base);
   const int widths = (p.dv + kJoinWidth - 1) / kJoinWidth;
@@ -223,7 +225,7 @@ __global__ void __launch_bounds__(kJoinThreads) gdn_attn_join_kernel(const AttnP
   if (c >= cols) return;
   const int parts = static_cast<int>(worker_from(tiles, p.workers, unit_end)) - (i - 1);  // workers i - 1, i, ...
   // the unit is worker i - 1's last segment: its first one only where the share begins with it
-  const int slot0 = before == unit_start ? 0 : 1;
+  const int slot0 = before >= unit_start ? 0 : 1;
   const size_t floats = partial_floats(p);
   const float* const first = partial_of(p, i - 1, slot0);
   const float* const second = partial_of(p, i, 0);  // and so on, two apart
@@ -308,9 +310,9 @@ AttnPlan attn_plan(const gdn_paged_kv& kv, int cols) {
       if (extent[i] > 1 && (s[i] <= 0 || s[i] >= (int64_t{1} << 39))) return false;
     return true;
   };
-  if (!heads || !pages || !strides(kv.k_strides) || (!latent && !strides(kv.v_strides))) return {false, kCols, kMaxAttnCtas};
+  if (!heads || !pages || !strides(kv.k_strides) || (!latent && !strides(kv.v_strides))) return {false, kCols, kMaxAttnCtas, 1};
   // a latent cache is read by pairs of CTAs
-  return {true, cols <= 16 ? 16 : cols <= 32 ? 32 : 64, latent ? kSms / 2 : kSms};
+  return {true, cols <= 16 ? 16 : cols <= 32 ? 32 : 64, latent ? kSms / 2 : kSms, latent || kv.dk == 256 ? 1 : kv.dk == 128 ? 2 : 3};
 }
 
 size_t attn_workspace_bytes(const AttnPlan& plan, int dv) {
@@ -332,6 +334,7 @@ cudaError_t launch_attn_join(const AttnParams& p, cudaStream_t stream) {
 
 cudaError_t launch_attn(const AttnPlan& plan, AttnParams& p, cudaStream_t stream) {
   p.ncol = plan.ncol;
+  p.unit_cost = plan.unit_cost;
   p.col_groups = (p.cols + p.ncol - 1) / p.ncol;
   // at most one worker a tile that there could be
   const int64_t positions = static_cast<int64_t>(p.max_pages) * p.page_size;

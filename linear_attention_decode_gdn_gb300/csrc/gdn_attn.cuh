@@ -8,7 +8,10 @@
 // them) takes an equal, unbroken share of the line, computed from kv_len on the device. So all
 // are busy equally long whatever the lengths are, one long request is spread over the GPU, and
 // a unit is cut only where two shares meet: of a worker's segments only the first and the last
-// can be part of a unit. Those leave unnormalised sums in the workspace, and gdn_attn_join_kernel adds them.
+// can be part of a unit. A unit also counts for p.unit_cost tiles that stand before its first
+// one (its queries, first maximum and result take that long), so that a share of many short
+// units is not the one that the others wait for; where a worker has only a few tiles anyway, an
+// even cut matters more and they count for none. The cut units' workers leave unnormalised sums in the workspace, and gdn_attn_join_kernel adds them.
 #pragma once
 
 #include "gdn_device.cuh"
@@ -41,7 +44,7 @@ __device__ __forceinline__ Tiles tiles_of(const AttnParams& p, int32_t n) {
   return {first, (n - 1) / kTile + 1 - first};
 }
 
-// Tiles of the line before worker w's share begins (a worker: a CTA, or a pair of them).
+// Line position where worker w's share begins (a worker: a CTA, or a pair of them).
 __device__ __forceinline__ uint32_t share_start(uint32_t total, uint32_t workers, uint32_t w) {
   const uint32_t q = total / workers, r = total - q * workers;
   return w * q + min(w, r);
@@ -54,11 +57,12 @@ __device__ __forceinline__ uint32_t worker_from(uint32_t total, uint32_t workers
 }
 
 // Where a worker's share begins: the request, the unit of it (kv head * col_groups + column
-// group) and the tile in the unit. The host keeps the tiles of a launch below 2^31.
+// group) and the position in the unit. The host keeps the line below 2^31.
 struct Share {
   uint32_t total, count;
-  uint32_t unit_start;  // line position of the first unit's first tile
-  int32_t b, unit, tile;
+  uint32_t unit_start;  // line position of the first unit
+  int32_t extra;        // what a unit counts for beyond its tiles
+  int32_t b, unit, at;
 };
 
 // Called by all lanes of a warp; every warp finds the same share for itself, which costs one
@@ -67,16 +71,23 @@ __device__ __forceinline__ Share find_share(const AttnParams& p, uint32_t worker
   const int lane = threadIdx.x & 31;
   const uint32_t units = static_cast<uint32_t>(p.heads_kv * p.col_groups);
   const int per = (p.B + 31) / 32, from = min(lane * per, p.B), to = min(from + per, p.B);
-  uint32_t mine = 0;
+  uint32_t tiles = 0, requests = 0;
 #pragma unroll 4
-  for (int b = from; b < to; ++b) mine += static_cast<uint32_t>(tiles_of(p, length_of(p, b)).count);
+  for (int b = from; b < to; ++b) {
+    const uint32_t count = static_cast<uint32_t>(tiles_of(p, length_of(p, b)).count);
+    tiles += count;
+    requests += count > 0 ? 1u : 0u;
+  }
+  Share s{};
+  const uint32_t all_tiles = __reduce_add_sync(0xffffffffu, tiles) * units;
+  s.extra = all_tiles >= 4u * p.workers ? p.unit_cost : 0;
+  const uint32_t mine = tiles + requests * s.extra;
   uint32_t upto = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const uint32_t y = __shfl_up_sync(0xffffffffu, upto, d);
     if (lane >= d) upto += y;
   }
-  Share s{};
   s.total = __shfl_sync(0xffffffffu, upto, 31) * units;
   const uint32_t start = share_start(s.total, p.workers, worker);
   s.count = share_start(s.total, p.workers, worker + 1) - start;
@@ -87,20 +98,22 @@ __device__ __forceinline__ Share find_share(const AttnParams& p, uint32_t worker
   if (here) {
     for (;; ++b) {
       const uint32_t count = static_cast<uint32_t>(tiles_of(p, length_of(p, b)).count);
-      if (start < (before + count) * units) {
+      if (count == 0) continue;
+      const uint32_t cost = count + s.extra;
+      if (start < (before + cost) * units) {
         const uint32_t in = start - before * units;
-        s.unit = static_cast<int32_t>(in / count);
-        s.tile = static_cast<int32_t>(in - s.unit * count);
+        s.unit = static_cast<int32_t>(in / cost);
+        s.at = static_cast<int32_t>(in - s.unit * cost);
         break;
       }
-      before += count;
+      before += cost;
     }
   }
   const int owner = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
   s.b = __shfl_sync(0xffffffffu, b, owner);
   s.unit = __shfl_sync(0xffffffffu, s.unit, owner);
-  s.tile = __shfl_sync(0xffffffffu, s.tile, owner);
-  s.unit_start = start - s.tile;
+  s.at = __shfl_sync(0xffffffffu, s.at, owner);
+  s.unit_start = start - s.at;
   return s;
 }
 
@@ -108,7 +121,7 @@ __device__ __forceinline__ Share find_share(const AttnParams& p, uint32_t worker
 struct Segment {
   int32_t b, unit, kv_head, col_base;
   int32_t n;           // cached positions
-  int32_t tile, tiles; // first tile (absolute) and how many
+  int32_t tile, tiles; // first tile (absolute) and how many, at least one
   int32_t index;       // 0 for the worker's first
   bool whole;          // covers the unit
 };
@@ -116,46 +129,51 @@ struct Segment {
 // Walks the segments of a share; every thread that walks sees the same ones.
 struct Walk {
   uint32_t left;
-  int32_t b, unit, tile, index;
+  int32_t extra, b, unit, at, index;
 
   __device__ __forceinline__ explicit Walk(const Share& s)
-      : left(s.count), b(s.b), unit(s.unit), tile(s.tile), index(0) {}
+      : left(s.count), extra(s.extra), b(s.b), unit(s.unit), at(s.at), index(0) {}
 
   __device__ __forceinline__ bool next(const AttnParams& p, Segment* seg) {
-    if (left == 0) return false;
     const int units = p.heads_kv * p.col_groups;
-    int32_t n = length_of(p, b);
-    Tiles t = tiles_of(p, n);
-    if (unit >= units) {
-      unit = 0;
-      do {  // a later request has tiles, because tiles are left
-        ++b;
-        n = length_of(p, b);
-        t = tiles_of(p, n);
-      } while (t.count == 0);
+    while (left > 0) {
+      int32_t n = length_of(p, b);
+      Tiles t = tiles_of(p, n);
+      if (unit >= units) {
+        unit = 0;
+        do {  // a later request has tiles, because some are left
+          ++b;
+          n = length_of(p, b);
+          t = tiles_of(p, n);
+        } while (t.count == 0);
+      }
+      const uint32_t rest = static_cast<uint32_t>(t.count + extra - at);
+      const int32_t take = static_cast<int32_t>(left < rest ? left : rest);
+      const int32_t first = max(at - extra, 0), end = max(at + take - extra, 0);
+      seg->b = b;
+      seg->unit = unit;
+      seg->n = n;
+      seg->tile = t.first + first;
+      seg->tiles = end - first;
+      seg->whole = end - first == t.count;
+      left -= take;
+      at = 0;
+      ++unit;
+      if (end == first) continue;  // the share ends before the unit's first tile
+      seg->kv_head = seg->unit / p.col_groups;
+      seg->col_base = (seg->unit - seg->kv_head * p.col_groups) * p.ncol;
+      seg->index = index++;
+      return true;
     }
-    const uint32_t rest = static_cast<uint32_t>(t.count - tile);
-    const int32_t take = static_cast<int32_t>(left < rest ? left : rest);
-    seg->b = b;
-    seg->unit = unit;
-    seg->kv_head = unit / p.col_groups;
-    seg->col_base = (unit - seg->kv_head * p.col_groups) * p.ncol;
-    seg->n = n;
-    seg->tile = t.first + tile;
-    seg->tiles = take;
-    seg->index = index++;
-    seg->whole = take == t.count;
-    left -= take;
-    tile = 0;
-    ++unit;
-    return true;
+    return false;
   }
 };
 
 // ---- the workspace ----------------------------------------------------------------------
-// Record of a worker: [tiles of the launch, or 0 without work; line positions of the first
-// segment's unit, begin and end; request; unit]. A partial result: dv x ncol sums (column by
-// column, fp32), then the columns' references (in the scaled log2 domain: sums are of 2^(s - m)) and sums.
+// Record of a worker: [length of the line, or 0 without work; line positions of the first
+// segment's unit, begin and end; request; unit; what a unit counts for beyond its tiles]. A
+// partial result: dv x ncol sums (column by column, fp32), then the columns' references (in the
+// scaled log2 domain: sums are of 2^(s - m)) and sums.
 __device__ __forceinline__ size_t partial_floats(const AttnParams& p) {
   return static_cast<size_t>(p.ncol) * (p.dv + 2);
 }
@@ -168,9 +186,10 @@ __device__ __forceinline__ void write_record(const AttnParams& p, const Share& s
   r[0] = s.count > 0 ? s.total : 0;
   if (s.count == 0) return;
   r[1] = s.unit_start;
-  r[2] = s.unit_start + tiles_of(p, length_of(p, s.b)).count;
+  r[2] = s.unit_start + s.extra + tiles_of(p, length_of(p, s.b)).count;
   r[3] = s.b;
   r[4] = s.unit;
+  r[5] = s.extra;
 }
 
 // Row of column c of a request and kv head: [B][T][H].

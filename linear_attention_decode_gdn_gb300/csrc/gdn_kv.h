@@ -71,6 +71,7 @@ struct AttnParams {
   int32_t ncol;       // of these, how many one CTA takes at a time
   int32_t col_groups; // ceil(cols / ncol)
   uint32_t workers;   // CTAs, or pairs of CTAs, that share the tiles
+  int32_t unit_cost;  // tiles that a unit counts for beyond its own
   float scale_log2;   // scale * log2(e)
   const void* q;
   int64_t q_b, q_t, q_h;
@@ -94,12 +95,12 @@ cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t stream);
 // Columns one worker takes at a time and workers at most for a shape, on the path that runs it.
 struct AttnPlan {
   bool tensor;  // the tensor-core kernel
-  int ncol, max_workers;
+  int ncol, max_workers, unit_cost;
 };
 AttnPlan attn_plan(const gdn_paged_kv& kv, int cols);
 size_t attn_workspace_bytes(const AttnPlan& plan, int dv);
 // records, then partials
-constexpr int kRecordInts = 8;  // five of them in use
+constexpr int kRecordInts = 8;  // six of them in use
 constexpr size_t kRecordBytes = static_cast<size_t>(kMaxAttnCtas) * kRecordInts * sizeof(uint32_t);
 static_assert(kRecordBytes % 16 == 0, "partials are read as vectors");
 
