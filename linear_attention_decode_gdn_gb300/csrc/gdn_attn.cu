@@ -312,7 +312,7 @@ AttnPlan attn_plan(const gdn_paged_kv& kv, int cols) {
   };
   if (!heads || !pages || !strides(kv.k_strides) || (!latent && !strides(kv.v_strides))) return {false, kCols, kMaxAttnCtas, 1};
   // a latent cache is read by pairs of CTAs
-  return {true, cols <= 16 ? 16 : cols <= 32 ? 32 : 64, latent ? kSms / 2 : kSms, latent || kv.dk == 256 ? 1 : kv.dk == 128 ? 2 : 3};
+  return {true, cols <= 16 ? 16 : cols <= 32 ? 32 : 64, latent ? kSms / 2 : kSms, latent ? 3 : kv.dk == 256 ? 1 : kv.dk == 128 ? 2 : 3};
 }
 
 size_t attn_workspace_bytes(const AttnPlan& plan, int dv) {

@@ -67,7 +67,10 @@ struct Cfg {
   static constexpr int PER = KS + VS;
   static constexpr int MB = VCOLS > 128 ? VCOLS / 128 : 1; // blocks of 128 rows of O^T
   static constexpr int NC = 16, G = N / NC;                // columns of a softmax group, groups
-  static constexpr int THREADS = 128 + 128 * G;
+  // Two softmax teams take turns at units, each with its own O^T: one ends a unit while the other
+  // begins the next. Wider blocks have their threads in column groups, latent units are long.
+  static constexpr int TEAMS = !LATENT && G == 1 ? 2 : 1;
+  static constexpr int THREADS = 128 + 128 * G * TEAMS;
   static constexpr int PB = LATENT ? 1 : 2;                // buffers of weights
   static constexpr int QB = !LATENT && DK < 256 && N <= 32 ? 2 : 1;  // and of queries
   static constexpr int TAIL = kTile * TCOLS * 2, TAILS = LATENT ? 1 : 0;
@@ -76,7 +79,7 @@ struct Cfg {
   static constexpr int FIT = (kSmemMost - FIXED) / SLOT < kMaxSlots ? (kSmemMost - FIXED) / SLOT : kMaxSlots;
   static constexpr int SLOTS = SLOTC == 1 ? FIT & ~1 : FIT;
   static constexpr int SMEM = FIXED + SLOTS * SLOT;
-  static constexpr int TMEM_USED = (2 + MB) * N;
+  static constexpr int TMEM_USED = (2 + MB * TEAMS) * N;
   static constexpr int TMEM = TMEM_USED <= 32 ? 32 : TMEM_USED <= 64 ? 64 : TMEM_USED <= 128 ? 128 : TMEM_USED <= 256 ? 256 : 512;
   // the scores of a tile are taken while the values of the one before still need their slots
   static_assert(SLOTS >= KS + (LATENT ? KS : VS), "the ring holds what both products need");
@@ -88,7 +91,8 @@ struct Misc {
   uint64_t tail_full[2], tail_empty[2];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], s_empty[2];
-  uint64_t p_full[2], pv_done[2];
+  uint64_t p_full[2], pv_done[2];  // by tile
+  uint64_t unit_begun[2], unit_done[2];  // by unit: its first scores, its O^T are complete
   uint64_t got[4], may_send[4];  // a group's scores received; the other CTA has read what was sent
   uint64_t drained;
   uint32_t tmem;
@@ -173,7 +177,7 @@ __device__ __forceinline__ void send16(uint32_t dst, float a, float b, float c, 
 __device__ __forceinline__ void arrive_there(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Barriers of one softmax group (four warps).
+// Barriers of four softmax warps.
 __device__ __forceinline__ void group_sync(int g) { asm volatile("bar.sync %0, 128;" ::"r"(g + 1) : "memory"); }
 __device__ __forceinline__ bool group_any(int g, bool pred) {
   uint32_t r;
@@ -301,6 +305,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
       mbar_init(&sm.s_empty[i], 4 * C::G);
       mbar_init(&sm.p_full[i], 4 * C::G);
       mbar_init(&sm.pv_done[i], 1);
+      mbar_init(&sm.unit_begun[i], 1);
+      mbar_init(&sm.unit_done[i], 1);
     }
     for (int i = 0; i < C::G; ++i) {
       mbar_init(&sm.got[i], 1);
@@ -429,7 +435,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
     const uint32_t ring_at = smem_addr(ring), tails_at = smem_addr(tails), w_at = smem_addr(weights);
     uint32_t i = 0, units = 0;   // tiles and units begun
     uint32_t k_slot = 0, k_round = 0, v_slot = 0, v_round = 0;  // next slots of keys and of values
-    uint32_t first_of_last = 0;  // whether the last tile with scores was its unit's first
+    // of the last tile with scores: whether it is its unit's first, its last, and that unit
+    uint32_t first_of_last = 0, last_of_last = 0, unit_of_last = 0;
     bool ok = true;
     auto skip = [](uint32_t& slot, uint32_t& round, uint32_t n) {
       slot += n;
@@ -470,9 +477,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
       skip(k_slot, k_round, C::VS);
       tc::commit(&sm.s_full[i & 1u]);
     };
-    // values of tile j; `first`: of its unit
-    auto values = [&](uint32_t j, uint32_t first) {
-      const uint32_t buf = j % C::PB;
+    // values of the last tile with scores, j
+    auto values = [&](uint32_t j) {
+      const uint32_t buf = j % C::PB, first = first_of_last;
+      const uint32_t d = tmem + 2 * N + (unit_of_last % C::TEAMS) * (C::MB * N);
       ok = warp_waited(&sm.p_full[buf], (j / C::PB) & 1u, sm);
       if (!ok) return;
       tc::fence_after_sync();
@@ -488,13 +496,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
         const uint32_t a = ring_at + (C::DV >= 128 ? v_slot : v_slot - 1) * C::SLOT, b = w_at + buf * C::PBYTES;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          mma_bf16(tmem + (2 + m) * N, desc_sw128(a + k * 2048, kChunk, 1024), tc::smem_desc(b + k * 256, 128, kTile * 16),
+          mma_bf16(d + m * N, desc_sw128(a + k * 2048, kChunk, 1024), tc::smem_desc(b + k * 256, 128, kTile * 16),
                    kValues, first == 0u || k > 0);
         tc::commit(&sm.empty[v_slot]);
         skip(v_slot, v_round, 1);
       }
       if (!C::LATENT) skip(v_slot, v_round, C::KS);
       tc::commit(&sm.pv_done[j & 1u]);
+      if (last_of_last != 0u) tc::commit(&sm.unit_done[unit_of_last & 1u]);
     };
 
     while (ok && walk.next(p, &seg)) {
@@ -511,7 +520,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
           const long long t0 = clock64();
           while (ok && !ready(&sm.full[k_slot], k_round)) {
             if (ready(&sm.p_full[j % C::PB], (j / C::PB) & 1u)) {
-              values(j, first_of_last);
+              values(j);
               due = false;
               break;
             }
@@ -521,14 +530,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
         }
         scores();
         if (!ok) break;
+        if (C::TEAMS > 1 && t == 0) tc::commit(&sm.unit_begun[units & 1u]);
         if (t == seg.tiles - 1) tc::commit(&sm.q_empty[qb]);
-        if (due) values(i - 1, first_of_last);
+        if (due) values(i - 1);
         first_of_last = t == 0;
+        last_of_last = t == seg.tiles - 1;
+        unit_of_last = units;
         ++i;
       }
       ++units;
     }
-    if (ok && i > 0) values(i - 1, first_of_last);
+    if (ok && i > 0) values(i - 1);
     // the last MMA has left TMEM and shared memory alone when this completes
     tc::commit(&sm.drained);
     if (!mbar_wait(&sm.drained, 0)) *static_cast<volatile uint32_t*>(&sm.timeout) = 1u;
@@ -559,17 +571,19 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
     write_empty<64>(p, tid - 64);
   } else {
     // ---- softmax ------------------------------------------------------------------------------
-    const int g = C::G > 1 ? (warp - 4) / 4 : 0, w = warp & 3;
+    const int quad = (warp - 4) / 4, g = C::TEAMS > 1 ? 0 : quad, w = warp & 3;  // its group of columns, its warp
+    const uint32_t team = C::TEAMS > 1 ? quad : 0;
     const int r = w * 32 + lane;      // this thread's position of the tile and TMEM lane
     const int c_base = g * NC;        // its group's first column
+    const int a_base = quad * NC;     // and its place in the arrays that are kept by column
     const uint32_t lanes = tc::lane_base(w);
-    const uint32_t s_at = tmem + lanes + c_base, o_at = tmem + lanes + 2 * N + c_base;
+    const uint32_t s_at = tmem + lanes + c_base, o_at = tmem + lanes + 2 * N + team * (C::MB * N) + c_base;
     // the group's part of what the CTAs send each other, and its barriers there
     const uint32_t mine = g * (NC * kTile * 4) + r * 16;
     const uint32_t there = C::LATENT ? in_cta(smem_addr(received), rank ^ 1u) + mine : 0u;
     const uint32_t got_there = C::LATENT ? in_cta(smem_addr(&sm.got[g]), rank ^ 1u) : 0u;
     const uint32_t may_send_there = C::LATENT ? in_cta(smem_addr(&sm.may_send[g]), rank ^ 1u) : 0u;
-    uint32_t i = 0;
+    uint32_t i = 0, units = 0;
     // After a wait that ran out the threads still go through every barrier together (no later
     // wait holds them up) and write nothing more.
     bool ok = true;
@@ -579,7 +593,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
 #pragma unroll
       for (int j = 0; j < 16; ++j) s[j] = x[j];
     };
-    while (walk.next(p, &seg)) {
+    for (; walk.next(p, &seg); ++units) {
+      if (C::TEAMS > 1 && (units & 1u) != team) {
+        i += seg.tiles;
+        continue;
+      }
       const int cols = min(N, p.cols - seg.col_base);
       const int t_first = seg.col_base / p.group, t_last = (seg.col_base + cols - 1) / p.group;
       const int32_t lower = lower_bound_of(p, seg.n, t_first);
@@ -591,12 +609,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
         return row[tp.box < kTile ? at >> tp.box_shift : tile / tp.page_tiles];
       };
       int32_t next = entry(seg.tile);
-      group_sync(g);  // the last unit's rows and maxima are read
+      group_sync(quad);  // the last unit's rows and maxima are read
       if (r < NC) {
-        const int c = c_base + r;
-        sm.m[c] = kNothing;
-        sm.last[c] = seg.n - p.T + (seg.col_base + c) / p.group;
-        sm.rows[c] = static_cast<int32_t>(row_of(p, seg.b, seg.kv_head, seg.col_base + c));
+        const int a = a_base + r, col = seg.col_base + c_base + r;
+        sm.m[a] = kNothing;
+        sm.last[a] = seg.n - p.T + col / p.group;
+        sm.rows[a] = static_cast<int32_t>(row_of(p, seg.b, seg.kv_head, col));
       }
       // Sums of weights, and references: in registers, but for the block of 640 threads, which has
       // 96 of them a thread and reads the references from shared memory.
@@ -609,9 +627,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
       }
       auto references = [&](int c) -> float4 {
         if (kKeep) return make_float4(kept[c], kept[c + 1], kept[c + 2], kept[c + 3]);
-        return *reinterpret_cast<const float4*>(&sm.m[c_base + c]);
+        return *reinterpret_cast<const float4*>(&sm.m[a_base + c]);
       };
-      group_sync(g);
+      group_sync(quad);
+      // A barrier's parity tells two rounds apart, so a team that has sat out a unit first waits for
+      // its own unit's turn: the barriers of that unit's tiles are then at their rounds.
+      if (C::TEAMS > 1) ok &= waited(&sm.unit_begun[units & 1u], (units >> 1) & 1u, sm);
       for (int t = 0; t < seg.tiles; ++t, ++i) {
         const int tile = seg.tile + t;
         const int32_t begin = tile * kTile, pos = begin + r;
@@ -648,7 +669,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
         } else {
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
-            const int32_t last = sm.last[c_base + c];
+            const int32_t last = sm.last[a_base + c];
             const bool seen = live && pos <= last && (p.window <= 0 || pos > last - p.window);
             s[c] = seen ? s[c] * p.scale_log2 : -INFINITY;
           }
@@ -659,16 +680,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
           const float4 m = references(c);
           raise |= s[c] > m.x || s[c + 1] > m.y || s[c + 2] > m.z || s[c + 3] > m.w;
         }
-        const bool any = group_any(g, raise);
+        const bool any = group_any(quad, raise);
         // every thread of the group has used what it received: the other CTA may send more
         if (C::LATENT && r == 0) arrive_there(may_send_there);
         if (any) {
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
             const float x = warp_max(s[c]);
-            if (lane == 0) sm.per_warp[w][c_base + c] = x;
+            if (lane == 0) sm.per_warp[w][a_base + c] = x;
           }
-          group_sync(g);
+          group_sync(quad);
           if (t > 0) {  // O^T is complete up to the last tile, and no MMA writes it until p_full
             ok &= waited(&sm.pv_done[(i - 1) & 1u], ((i - 1) >> 1) & 1u, sm);
             __syncwarp();
@@ -679,7 +700,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
             float f[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              const int c = c0 + j, a = c_base + c;
+              const int c = c0 + j, a = a_base + c;
               const float top = fmaxf(fmaxf(sm.per_warp[0][a], sm.per_warp[1][a]), fmaxf(sm.per_warp[2][a], sm.per_warp[3][a]));
               const float m = kKeep ? kept[c] : sm.m[a];
               const float to = top > m ? top + kHeadroom : m;
@@ -706,13 +727,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
             tc::fence_before_sync();
           }
           if (!kKeep) {
-            group_sync(g);  // the old references are read
+            group_sync(quad);  // the old references are read
             if (r < NC) {
-              const int a = c_base + r;
+              const int a = a_base + r;
               const float top = fmaxf(fmaxf(sm.per_warp[0][a], sm.per_warp[1][a]), fmaxf(sm.per_warp[2][a], sm.per_warp[3][a]));
               if (top > sm.m[a]) sm.m[a] = top + kHeadroom;
             }
-            group_sync(g);
+            group_sync(quad);
           }
         }
         // this tile's buffer of weights was last read by the products of tile i - PB
@@ -763,25 +784,25 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
 
       // ---- the unit's (or the share's) end: sums over the positions, then O^T ---------------
       column_sums(l, lane);
-      group_sync(g);  // maxima of the last raise are read
-      if (NC == 32 || (lane & 1) == 0) sm.per_warp[w][c_base + lane * NC / 32] = l[0];
-      group_sync(g);
+      group_sync(quad);  // maxima of the last raise are read
+      if (NC == 32 || (lane & 1) == 0) sm.per_warp[w][a_base + lane * NC / 32] = l[0];
+      group_sync(quad);
       float* const part = partial_of(p, worker, seg.index == 0 ? 0 : 1);
       if (r < NC) {
-        const int c = c_base + r;
-        const float sum = (sm.per_warp[0][c] + sm.per_warp[1][c]) + (sm.per_warp[2][c] + sm.per_warp[3][c]);
-        sm.inv[c] = !seg.whole ? 1.0f : sum > 0.0f ? 1.0f / sum : (sum == sum ? 0.0f : sum);
+        const int a = a_base + r, c = c_base + r;
+        const float sum = (sm.per_warp[0][a] + sm.per_warp[1][a]) + (sm.per_warp[2][a] + sm.per_warp[3][a]);
+        sm.inv[a] = !seg.whole ? 1.0f : sum > 0.0f ? 1.0f / sum : (sum == sum ? 0.0f : sum);
         if (ok && c < cols && rank == 0) {
           if (!seg.whole) {
-            part[N * C::DV + c] = sm.m[c];
+            part[N * C::DV + c] = sm.m[a];
             part[N * C::DV + N + c] = sum;
           } else if (p.lse != nullptr) {
-            p.lse[sm.rows[c]] = lse_of(sm.m[c], sum);
+            p.lse[sm.rows[a]] = lse_of(sm.m[a], sum);
           }
         }
       }
-      group_sync(g);
-      ok &= waited(&sm.pv_done[(i - 1) & 1u], ((i - 1) >> 1) & 1u, sm);
+      group_sync(quad);
+      ok &= waited(&sm.unit_done[units & 1u], (units >> 1) & 1u, sm);
       __syncwarp();
       tc::fence_after_sync();
 #pragma unroll 1
@@ -794,10 +815,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
           if (ok && d >= 0) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              const int c = c_base + c0 + j;
+              const int a = a_base + c0 + j, c = c_base + c0 + j;
               if (c >= cols) break;
               if (seg.whole)
-                static_cast<__nv_bfloat16*>(p.o)[static_cast<int64_t>(sm.rows[c]) * C::DV + d] = __float2bfloat16_rn(x[j] * sm.inv[c]);
+                static_cast<__nv_bfloat16*>(p.o)[static_cast<int64_t>(sm.rows[a]) * C::DV + d] = __float2bfloat16_rn(x[j] * sm.inv[a]);
               else
                 part[c * C::DV + d] = x[j];
             }
