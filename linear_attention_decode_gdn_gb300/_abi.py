@@ -77,6 +77,8 @@ class LogSizes(ctypes.Structure):
                 ("total", ctypes.c_size_t)]
 
 
+# The two structs of the paged cache's calls. The calls take their address as a plain pointer:
+# ctypes.byref() of these, or the same bytes packed by hand.
 class PagedKV(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_strides", ctypes.c_int64 * 3),
                 ("v_strides", ctypes.c_int64 * 3), ("num_pages", ctypes.c_int32),
@@ -126,13 +128,13 @@ def _declare(lib):
     lib.gdn_kv_release.restype = ctypes.c_int
     lib.gdn_kv_release.argtypes = [i32, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp]
     lib.gdn_kv_append.restype = ctypes.c_int
-    lib.gdn_kv_append.argtypes = [P(PagedKV), i32, vp, vp, vp, vp, vp, ctypes.c_uint32, vp, vp]
+    lib.gdn_kv_append.argtypes = [vp, i32, vp, vp, vp, vp, vp, ctypes.c_uint32, vp, vp]
     for name in ("gdn_attn_decode", "gdn_latent_decode"):
         fn = getattr(lib, name)
         fn.restype = ctypes.c_int
-        fn.argtypes = [P(PagedKV), P(Attn), vp, ctypes.c_size_t, vp, vp]
+        fn.argtypes = [vp, vp, vp, ctypes.c_size_t, vp, vp]
     lib.gdn_attn_workspace.restype = ctypes.c_int
-    lib.gdn_attn_workspace.argtypes = [P(PagedKV), i32, i32, i32, P(ctypes.c_size_t)]
+    lib.gdn_attn_workspace.argtypes = [vp, i32, i32, i32, vp]
     return lib
 
 

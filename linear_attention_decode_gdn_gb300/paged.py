@@ -8,19 +8,34 @@ launched; what libgdn refuses raises ``GDNError``.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
 from . import _abi
-from ._abi import Attn, PagedKV, check
-from .decode import _ptr
+from ._abi import GDN_OK, check
 
 # A decode step makes one call a layer, so what these functions spend before the launch counts:
-# conditions are written out (no helper call for each), and structs are filled in one go.
+# conditions are written out (no helper call for each), and the C structs are packed in one go.
+_pack_kv = struct.Struct("=QQ6q5i4x").pack       # gdn_paged_kv
+_pack_attn = struct.Struct("=5if4q4Q").pack      # gdn_attn
+_pack_strides = struct.Struct("=2q").pack
 _BF16, _FP32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
-_I2 = ctypes.c_int64 * 2
+
+
+class PagedKV:
+    """The cache of one layer, as make_paged_kv() describes it to the calls; it keeps its pages alive."""
+
+    __slots__ = ("packed", "dk", "dv", "heads", "latent", "k", "v")
+
+    def __init__(self, packed, dk, dv, heads, latent, k, v):
+        self.packed, self.dk, self.dv, self.heads, self.latent, self.k, self.v = packed, dk, dv, heads, latent, k, v
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream, beside):
@@ -30,16 +45,18 @@ def _stream(stream, beside):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _ints(t, n: int, what: str, dtype=_I32) -> None:
+def _ints(t, n: int, what: str, dtype=_I32) -> int:
     if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{what}: contiguous {dtype} on the GPU with {n} entries, got {t.dtype} {tuple(t.shape)} "
                          f"on {t.device}")
+    return t.data_ptr()
 
 
 def _table(t, batch: int) -> int:
-    if t.dtype is not _I32 or t.dim() != 2 or t.size(0) != batch or not t.is_contiguous() or not t.is_cuda:
+    shape = t.shape
+    if t.dtype is not _I32 or len(shape) != 2 or shape[0] != batch or not t.is_contiguous() or not t.is_cuda:
         raise ValueError("block_table: contiguous int32 [batch, max_pages] on the GPU")
-    return t.size(1)
+    return shape[1]
 
 
 def make_paged_kv(k, v=None, dv=None) -> PagedKV:
@@ -52,17 +69,16 @@ def make_paged_kv(k, v=None, dv=None) -> PagedKV:
     if v is None:
         if dv is None:
             raise ValueError("a latent cache needs dv, the part of a row that is the value")
-        kv = PagedKV(k.data_ptr(), None, (k0, k1, k2), (0, 0, 0), pages, page_size, heads, dk, dv)
-    else:
-        if v.dtype is not _BF16 or v.dim() != 4 or v.stride(3) != 1 or v.device != k.device:
-            raise ValueError("v: bf16 [pages, page_size, heads, dv] beside k, its last stride 1")
-        v_pages, v_size, v_heads, size = v.shape
-        if (v_pages, v_size, v_heads) != (pages, page_size, heads) or (dv is not None and dv != size):
-            raise ValueError("v: as many pages, positions and heads as k; dv is its last size")
-        v0, v1, v2, _ = v.stride()
-        kv = PagedKV(k.data_ptr(), v.data_ptr(), (k0, k1, k2), (v0, v1, v2), pages, page_size, heads, dk, size)
-    kv._keep = (k, v)  # the struct keeps the pages alive for as long as it holds their addresses
-    return kv
+        packed = _pack_kv(k.data_ptr(), 0, k0, k1, k2, 0, 0, 0, pages, page_size, heads, dk, dv)
+        return PagedKV(packed, dk, dv, heads, True, k, None)
+    if v.dtype is not _BF16 or v.dim() != 4 or v.stride(3) != 1 or v.device != k.device:
+        raise ValueError("v: bf16 [pages, page_size, heads, dv] beside k, its last stride 1")
+    v_pages, v_size, v_heads, size = v.shape
+    if v_pages != pages or v_size != page_size or v_heads != heads or (dv is not None and dv != size):
+        raise ValueError("v: as many pages, positions and heads as k; dv is its last size")
+    v0, v1, v2, _ = v.stride()
+    packed = _pack_kv(k.data_ptr(), v.data_ptr(), k0, k1, k2, v0, v1, v2, pages, page_size, heads, dk, size)
+    return PagedKV(packed, dk, size, heads, False, k, v)
 
 
 def kv_plan(cached_len, new_len, held, block_table, free_list, free_count, *, kv_len, cu_new, slot_map, held_out,
@@ -70,62 +86,53 @@ def kv_plan(cached_len, new_len, held, block_table, free_list, free_count, *, kv
     """Pages and slots for the new tokens of a step, from the requests' lengths (new_len None: one
     token each). Writes block_table, kv_len, cu_new, slot_map, held_out and free_count_out; the
     last three of kv_len / held_out / free_count_out may be the input arrays themselves."""
-    batch = cached_len.numel()
-    _ints(cached_len, batch, "cached_len")
-    if new_len is not None:
-        _ints(new_len, batch, "new_len")
-    _ints(held, batch, "held")
-    _ints(kv_len, batch, "kv_len")
-    _ints(held_out, batch, "held_out")
-    _ints(cu_new, batch + 1, "cu_new")
-    _ints(free_count, 1, "free_count")
-    _ints(free_count_out, 1, "free_count_out")
-    capacity = slot_map.numel()
-    _ints(slot_map, capacity, "slot_map", _I64)
-    _ints(free_list, free_list.numel(), "free_list")
-    if free_list.numel() > num_pages:
+    batch, capacity, free = cached_len.numel(), slot_map.numel(), free_list.numel()
+    if free > num_pages:
         raise ValueError("free_list: at most num_pages entries")
-    check(_abi.load().gdn_kv_plan(batch, _table(block_table, batch), page_size, num_pages, capacity,
-                                  _ptr(cached_len), _ptr(new_len), _ptr(held), _ptr(block_table), _ptr(free_list),
-                                  _ptr(free_count), _ptr(kv_len), _ptr(cu_new), _ptr(slot_map), _ptr(held_out),
-                                  _ptr(free_count_out), _ptr(status), _stream(stream, cached_len)), "gdn_kv_plan")
+    cached = _ints(cached_len, batch, "cached_len")
+    check(_abi.load().gdn_kv_plan(
+        batch, _table(block_table, batch), page_size, num_pages, capacity, cached,
+        None if new_len is None else _ints(new_len, batch, "new_len"), _ints(held, batch, "held"),
+        block_table.data_ptr(), _ints(free_list, free, "free_list"), _ints(free_count, 1, "free_count"),
+        _ints(kv_len, batch, "kv_len"), _ints(cu_new, batch + 1, "cu_new"), _ints(slot_map, capacity, "slot_map", _I64),
+        _ints(held_out, batch, "held_out"), _ints(free_count_out, 1, "free_count_out"), _ptr(status),
+        _stream(stream, cached_len)), "gdn_kv_plan")
 
 
 def kv_release(requests, held, block_table, free_list, free_count, *, status=None, stream=None):
     """Pushes the pages of the given requests (rows of block_table) on free_list, which has room for
     every page of the cache; held of those rows becomes 0 and free_count grows."""
-    batch = held.numel()
-    _ints(requests, requests.numel(), "requests")
-    _ints(held, batch, "held")
-    _ints(free_count, 1, "free_count")
-    _ints(free_list, free_list.numel(), "free_list")
-    check(_abi.load().gdn_kv_release(batch, _table(block_table, batch), free_list.numel(), _ptr(requests),
-                                     requests.numel(), _ptr(block_table), _ptr(held), _ptr(free_list),
-                                     _ptr(free_count), _ptr(status), _stream(stream, held)), "gdn_kv_release")
+    batch, n, free = held.numel(), requests.numel(), free_list.numel()
+    finished = _ints(requests, n, "requests")
+    check(_abi.load().gdn_kv_release(
+        batch, _table(block_table, batch), free, finished, n, block_table.data_ptr(),
+        _ints(held, batch, "held"), _ints(free_list, free, "free_list"), _ints(free_count, 1, "free_count"),
+        _ptr(status), _stream(stream, held)), "gdn_kv_release")
 
 
 def kv_append(kv: PagedKV, k, v, slot_map, *, status=None, stream=None):
     """Rows of new tokens to their slots: k [n, heads, dk] and v [n, heads, dv]; for a latent cache the
     latent part [n, 1, dv] and the tail [n, 1, dk - dv] (None if dk == dv). bf16 or fp32."""
-    n, heads, dv, dtype = slot_map.numel(), kv.num_kv_heads, kv.dv, k.dtype
-    width, tail = (dv, kv.dk - dv) if kv.v is None else (kv.dk, dv)
-    _ints(slot_map, n, "slot_map", _I64)
-    if (dtype is not _BF16 and dtype is not _FP32) or k.shape != (n, heads, width) or not k.is_cuda or k.stride(2) != 1:
+    n, heads, dv, dtype = slot_map.numel(), kv.heads, kv.dv, k.dtype
+    width, tail = (dv, kv.dk - dv) if kv.latent else (kv.dk, dv)
+    slots = _ints(slot_map, n, "slot_map", _I64)
+    k_row, k_head, k_last = k.stride() if k.dim() == 3 else (0, 0, 0)
+    if k_last != 1 or (dtype is not _BF16 and dtype is not _FP32) or k.shape != (n, heads, width) or not k.is_cuda:
         raise ValueError(f"k: bf16 or fp32 [{n}, {heads}, {width}] on the GPU, its last stride 1")
     v_ptr = v_strides = None
     if tail:
         if v is None or v.dtype is not dtype or v.shape != (n, heads, tail) or not v.is_cuda or v.stride(2) != 1:
             raise ValueError(f"v: of k's type [{n}, {heads}, {tail}] on the GPU, its last stride 1")
-        v_ptr, v_strides = v.data_ptr(), _I2(v.stride(0), v.stride(1))
-    check(_abi.load().gdn_kv_append(kv, n, k.data_ptr(), _I2(k.stride(0), k.stride(1)), v_ptr, v_strides,
-                                    slot_map.data_ptr(), _abi.QKV_BF16 if dtype is _BF16 else 0, _ptr(status),
-                                    _stream(stream, k)), "gdn_kv_append")
+        v_row, v_head, _ = v.stride()
+        v_ptr, v_strides = v.data_ptr(), _pack_strides(v_row, v_head)
+    check(_abi.load().gdn_kv_append(kv.packed, n, k.data_ptr(), _pack_strides(k_row, k_head), v_ptr, v_strides, slots,
+                                    1 if dtype is _BF16 else 0, _ptr(status), _stream(stream, k)), "gdn_kv_append")
 
 
 def attn_workspace_bytes(kv: PagedKV, batch: int, num_tokens: int, num_heads: int) -> int:
     """Bytes of workspace that attn_decode / latent_decode need."""
     out = ctypes.c_size_t()
-    check(_abi.load().gdn_attn_workspace(kv, batch, num_tokens, num_heads, out), "gdn_attn_workspace")
+    check(_abi.load().gdn_attn_workspace(kv.packed, batch, num_tokens, num_heads, ctypes.byref(out)), "gdn_attn_workspace")
     return out.value
 
 
@@ -143,11 +150,12 @@ def _attend(call, name, kv, q, block_table, kv_len, o, workspace, lse, scale, wi
         raise ValueError("lse: contiguous fp32 [batch, tokens, heads] on the GPU")
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace: contiguous, on the GPU")
-    _ints(kv_len, batch, "kv_len")
-    a = Attn(batch, tokens, heads, _table(block_table, batch), window, dk ** -0.5 if scale is None else scale, q.data_ptr(),
-             (s0, s1, s2), block_table.data_ptr(), kv_len.data_ptr(), o.data_ptr(),
-             None if lse is None else lse.data_ptr())
-    check(call(kv, a, workspace.data_ptr(), workspace.nbytes, _ptr(status), _stream(stream, q)), name)
+    a = _pack_attn(batch, tokens, heads, _table(block_table, batch), window, dk ** -0.5 if scale is None else scale,
+                   q.data_ptr(), s0, s1, s2, block_table.data_ptr(), _ints(kv_len, batch, "kv_len"), o.data_ptr(),
+                   0 if lse is None else lse.data_ptr())
+    rc = call(kv.packed, a, workspace.data_ptr(), workspace.nbytes, _ptr(status), _stream(stream, q))
+    if rc != GDN_OK:
+        check(rc, name)
 
 
 def attn_decode(kv: PagedKV, q, block_table, kv_len, o, workspace, *, lse=None, scale=None, window=0, status=None,

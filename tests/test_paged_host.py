@@ -41,7 +41,8 @@ def attn(gdn, **kw):
 
 
 def attend(gdn, kv, a, size=1 << 40, workspace=FAKE, name="gdn_attn_decode"):
-    return getattr(gdn._abi.load(), name)(kv, a, workspace, size, None, None)
+    by = lambda x: None if x is None else ctypes.byref(x)  # noqa: E731
+    return getattr(gdn._abi.load(), name)(by(kv), by(a), workspace, size, None, None)
 
 
 BAD, NO = 1, 2  # GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED
@@ -57,9 +58,9 @@ def test_cache_is_checked(gdn, kw, code):
     kv = cache(gdn, **kw)
     assert attend(gdn, kv, attn(gdn)) == code
     size = ctypes.c_size_t()
-    assert gdn._abi.load().gdn_attn_workspace(kv, 1, 1, 8, size) == code
+    assert gdn._abi.load().gdn_attn_workspace(ctypes.byref(kv), 1, 1, 8, ctypes.byref(size)) == code
     s2 = (ctypes.c_int64 * 2)(512, 128)
-    assert gdn._abi.load().gdn_kv_append(kv, 3, FAKE, s2, FAKE, s2, FAKE, gdn.QKV_BF16, None, None) == code
+    assert gdn._abi.load().gdn_kv_append(ctypes.byref(kv), 3, FAKE, s2, FAKE, s2, FAKE, gdn.QKV_BF16, None, None) == code
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -76,7 +77,7 @@ def test_attention_arguments_are_checked(gdn, kw, code):
 
 def test_attention_cache_kinds_and_workspace(gdn):
     lib = gdn._abi.load()
-    assert lib.gdn_attn_decode(None, attn(gdn), FAKE, 1 << 40, None, None) == BAD
+    assert attend(gdn, None, attn(gdn)) == BAD
     assert attend(gdn, cache(gdn), None) == BAD
     assert attend(gdn, cache(gdn), attn(gdn), workspace=None) == BAD
     assert attend(gdn, cache(gdn), attn(gdn), workspace=FAKE + 8) == NO
@@ -88,12 +89,12 @@ def test_attention_cache_kinds_and_workspace(gdn):
     # an empty batch is no call at all
     assert attend(gdn, cache(gdn), attn(gdn, batch=0)) == 0
     size = ctypes.c_size_t()
-    assert lib.gdn_attn_workspace(cache(gdn), 1, 1, 8, None) == BAD
-    assert lib.gdn_attn_workspace(cache(gdn), 1, 1, 6, size) == BAD
-    assert lib.gdn_attn_workspace(cache(gdn), 1, 4096, 8, size) == NO
+    assert lib.gdn_attn_workspace(ctypes.byref(cache(gdn)), 1, 1, 8, None) == BAD
+    assert lib.gdn_attn_workspace(ctypes.byref(cache(gdn)), 1, 1, 6, ctypes.byref(size)) == BAD
+    assert lib.gdn_attn_workspace(ctypes.byref(cache(gdn)), 1, 4096, 8, ctypes.byref(size)) == NO
     sizes = []
     for tokens in (1, 2, 16):
-        assert lib.gdn_attn_workspace(cache(gdn), 1, tokens, 8, size) == 0
+        assert lib.gdn_attn_workspace(ctypes.byref(cache(gdn)), 1, tokens, 8, ctypes.byref(size)) == 0
         sizes.append(size.value)
     assert 0 < sizes[0] <= sizes[1] <= sizes[2] < 1 << 27  # grows with the columns, never with the batch
 
@@ -101,7 +102,7 @@ def test_attention_cache_kinds_and_workspace(gdn):
 def test_append_arguments_are_checked(gdn):
     lib = gdn._abi.load()
     s2, odd = (ctypes.c_int64 * 2)(512, 128), (ctypes.c_int64 * 2)(510, 128)
-    kv, bf16 = cache(gdn), gdn.QKV_BF16
+    kv, bf16 = ctypes.byref(cache(gdn)), gdn.QKV_BF16
     assert lib.gdn_kv_append(None, 1, FAKE, s2, FAKE, s2, FAKE, bf16, None, None) == BAD
     assert lib.gdn_kv_append(kv, -1, FAKE, s2, FAKE, s2, FAKE, bf16, None, None) == BAD
     assert lib.gdn_kv_append(kv, 1, FAKE, s2, FAKE, s2, FAKE, gdn.FUSE_CONV, None, None) == BAD
@@ -113,7 +114,7 @@ def test_append_arguments_are_checked(gdn):
         assert lib.gdn_kv_append(kv, 1, *args, bf16, None, None) == NO
     assert lib.gdn_kv_append(kv, 1, FAKE, odd, FAKE, s2, FAKE, 0, None, None) == NO  # fp32: multiples of 4
     # a latent cache without a tail needs no second source
-    assert lib.gdn_kv_append(latent(gdn), 1, FAKE, s2, None, None, FAKE, bf16, None, None) == BAD
+    assert lib.gdn_kv_append(ctypes.byref(latent(gdn)), 1, FAKE, s2, None, None, FAKE, bf16, None, None) == BAD
 
 
 def test_plan_and_release_arguments_are_checked(gdn):
@@ -153,3 +154,14 @@ def test_tensors_on_the_host_are_refused(gdn):
                     held_out=ints, free_count_out=ints, page_size=16, num_pages=4)
     with pytest.raises(ValueError, match="requests"):
         gdn.kv_release(ints, ints, ints[None], ints, ints[:1])
+
+
+def test_packed_structs_are_the_c_structs(gdn):
+    """The binding packs the structs by hand: the same bytes as the ctypes layout of gdn.h."""
+    from linear_attention_decode_gdn_gb300 import paged
+    kv = cache(gdn, k=3 << 40, k_strides=(1 << 33, 16, 8), v_strides=(24, 1 << 34, 32))
+    assert bytes(kv) == paged._pack_kv(kv.k, kv.v, *kv.k_strides, *kv.v_strides, kv.num_pages, kv.page_size, kv.num_kv_heads,
+                                       kv.dk, kv.dv)
+    a = attn(gdn, window=7, scale=0.25, lse=5 << 40)
+    assert bytes(a) == paged._pack_attn(a.batch, a.num_tokens, a.num_heads, a.max_pages, a.window, a.scale, a.q, *a.q_strides,
+                                        a.block_table, a.kv_len, a.o, a.lse)
