@@ -196,9 +196,11 @@ int decode_common(int mode, const gdn_dims* dims, const gdn_inputs* in, float* p
 constexpr int kMaxCacheDk = 576, kMaxCacheDv = 512;
 constexpr int kMaxAttnCols = 4096;  // query rows per kv head in one call
 
-bool strides_ok(const int64_t* s, int n, int multiple) {
-  for (int i = 0; i < n; ++i)
-    if (s[i] < 0 || s[i] % multiple != 0) return false;
+// Strides of dimensions with `extents`; a dimension of one element may have any.
+template <int N>
+bool strides_ok(const int64_t* s, const int32_t (&extents)[N], int multiple) {
+  for (int i = 0; i < N; ++i)
+    if (extents[i] > 1 && (s[i] < 0 || s[i] % multiple != 0)) return false;
   return true;
 }
 
@@ -212,8 +214,9 @@ int check_kv(const gdn_paged_kv* kv) {
                 kv->dv, kMaxCacheDk, kMaxCacheDv);
   if (kv->v == nullptr && (kv->num_kv_heads != 1 || kv->dv > kv->dk))
     return fail(GDN_ERR_INVALID_ARG, "a latent cache (v NULL) has one head and dv <= dk");
-  if (!aligned16(kv->k) || !aligned16(kv->v) || !strides_ok(kv->k_strides, 3, 8) ||
-      (kv->v != nullptr && !strides_ok(kv->v_strides, 3, 8)))
+  const int32_t extents[3] = {kv->num_pages, kv->page_size, kv->num_kv_heads};
+  if (!aligned16(kv->k) || !aligned16(kv->v) || !strides_ok(kv->k_strides, extents, 8) ||
+      (kv->v != nullptr && !strides_ok(kv->v_strides, extents, 8)))
     return fail(GDN_ERR_UNSUPPORTED, "cache pages must be 16-byte aligned, with strides >= 0 that are multiples of 8");
   return GDN_OK;
 }
@@ -233,7 +236,8 @@ int check_attn(const gdn_paged_kv* kv, const gdn_attn* a, const void* workspace)
   if (a->batch == 0) return GDN_OK;
   if (a->q == nullptr || a->block_table == nullptr || a->kv_len == nullptr || a->o == nullptr || workspace == nullptr)
     return fail(GDN_ERR_INVALID_ARG, "q, block_table, kv_len, o and workspace are required");
-  if (!aligned16(a->q) || !aligned16(a->o) || !aligned16(workspace) || !strides_ok(a->q_strides, 3, 8))
+  const int32_t extents[3] = {a->batch, a->num_tokens, a->num_heads};
+  if (!aligned16(a->q) || !aligned16(a->o) || !aligned16(workspace) || !strides_ok(a->q_strides, extents, 8))
     return fail(GDN_ERR_UNSUPPORTED, "q, o and workspace must be 16-byte aligned, q strides >= 0 and multiples of 8");
   return GDN_OK;
 }
@@ -503,8 +507,9 @@ int gdn_kv_append(const gdn_paged_kv* kv, int32_t n, const void* k, const int64_
     return fail(GDN_ERR_INVALID_ARG, "k, v, their strides and slot_map are required");
   const bool bf16 = (flags & GDN_QKV_BF16) != 0u;
   const int multiple = bf16 ? 8 : 4;
-  if (!aligned16(k) || !strides_ok(k_strides, 2, multiple) ||
-      (tail > 0 && (!aligned16(v) || !strides_ok(v_strides, 2, multiple))))
+  const int32_t extents[2] = {n, kv->num_kv_heads};
+  if (!aligned16(k) || !strides_ok(k_strides, extents, multiple) ||
+      (tail > 0 && (!aligned16(v) || !strides_ok(v_strides, extents, multiple))))
     return fail(GDN_ERR_UNSUPPORTED, "k and v must be 16-byte aligned, with strides >= 0 that are multiples of 16 bytes");
   gdn::KvAppendParams p{};
   p.n = n;

@@ -469,3 +469,60 @@ def test_offsets_past_32_bits(gdn):
     torch.cuda.synchronize()
     assert p.status.item() == 0
     assert torch.equal(big_k[-1, -1], new[0, :heads_kv]) and torch.equal(big_v[shift, 0], new[1, heads_kv:])
+
+
+# ---- together ---------------------------------------------------------------------------------
+def load_example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "hybrid_decode.py")
+    spec = importlib.util.spec_from_file_location("hybrid_decode", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+def test_hybrid_steps_in_a_graph(gdn):
+    """The example's stack: replayed graphs give the eager steps' bits, pages are handed out as
+    lengths pass them, and both attention layers agree with 64-bit sums over what was appended."""
+    hybrid = load_example()
+    lens = [1, 63, 64, 200, 5]
+    eager, graph = (hybrid.HybridDecoder(len(lens), heads=8, heads_kv=2, layers=8, max_len=400, seed=3) for _ in range(2))
+    for m in (eager, graph):
+        m.admit(lens)
+    history = {i: [] for i, x in enumerate(eager.layers) if "kv" in x}
+    for step in range(4):
+        for m in (eager, graph):
+            m.step()
+        if step == 0:
+            graph.capture()
+        torch.cuda.synchronize()
+        assert torch.equal(eager.y, graph.y)
+        assert eager.length.tolist() == [n + step + 1 for n in lens]
+        assert eager.held.tolist() == [-(-(n + step + 1) // 64) for n in lens]
+        assert eager.free_count.item() == eager.num_pages - sum(eager.held.tolist())
+        for i in history:
+            rows = eager.layers[i]["k"].flatten(0, 1)[eager.slots]
+            history[i].append(rows.clone())
+            assert torch.equal(rows, graph.layers[i]["k"].flatten(0, 1)[graph.slots])
+    assert eager.status.item() == 0 and graph.status.item() == 0
+    for i, rows in history.items():
+        layer = eager.layers[i]
+        latent = layer["kind"] == "latent"
+        for b, n in enumerate(lens):
+            total = n + 4
+            pages = eager.table[b, :eager.held[b]].long()
+            k = layer["k"][pages].flatten(0, 1)[:total]
+            assert torch.equal(k[n:], torch.stack([r[b] for r in rows]))  # the appended rows, in order
+            v = k[..., :512] if latent else layer["v"][pages].flatten(0, 1)[:total]
+            for h in range(8):
+                kh = 0 if latent else h // 4
+                q = layer["q"][b, 0, h].double()
+                scale = q.numel() ** -0.5
+                s = k[:, kh].double() @ q * scale
+                w = torch.softmax(s, 0)
+                want, size = w @ v[:, kh].double(), w @ v[:, kh].double().abs()
+                # output and weights rounded to bf16; scores summed in fp32 (see Problem.expected)
+                off = (q.numel() + 4) * 2.0 ** -24 * float((k[:, kh].double().abs() @ q.abs()).max()) * scale + 2.0 ** -21
+                tolerance = want.abs() * 2.0 ** -8 + size * (2.0 ** -8 + 2 * off + (total + 64) * 2.0 ** -24) * 1.01
+                assert bool(((layer["o"][b, 0, h].double() - want).abs() <= tolerance).all()), (i, b, h)

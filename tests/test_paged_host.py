@@ -111,8 +111,8 @@ def test_append_arguments_are_checked(gdn):
                  (FAKE, s2, FAKE, None, FAKE), (FAKE, s2, FAKE, s2, None)):
         assert lib.gdn_kv_append(kv, 1, *args, bf16, None, None) == BAD
     for args in ((FAKE + 8, s2, FAKE, s2, FAKE), (FAKE, odd, FAKE, s2, FAKE), (FAKE, s2, FAKE, odd, FAKE)):
-        assert lib.gdn_kv_append(kv, 1, *args, bf16, None, None) == NO
-    assert lib.gdn_kv_append(kv, 1, FAKE, odd, FAKE, s2, FAKE, 0, None, None) == NO  # fp32: multiples of 4
+        assert lib.gdn_kv_append(kv, 2, *args, bf16, None, None) == NO
+    assert lib.gdn_kv_append(kv, 2, FAKE, odd, FAKE, s2, FAKE, 0, None, None) == NO  # fp32: multiples of 4
     # a latent cache without a tail needs no second source
     assert lib.gdn_kv_append(ctypes.byref(latent(gdn)), 1, FAKE, s2, None, None, FAKE, bf16, None, None) == BAD
 
