@@ -257,61 +257,61 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-// A row of 8-element vectors is copied by a warp (or by 2^k lanes of one, where it is that short),
-// kFlight vectors a lane in flight: the slot and its page are looked up once a row, and
-// neighbouring lanes move neighbouring 16 bytes.
-template <bool BF16>
-__device__ __forceinline__ void copy_rows(const KvAppendParams& p, const KvRows& s, int64_t r, int64_t page, int64_t pos,
-                                          int lane, int lanes) {
-  constexpr int kFlight = 4;
-  const uint32_t all = s.vecs * s.heads;
-  const unsigned char* const src = static_cast<const unsigned char*>(s.src) + r * s.src_row * (BF16 ? 2 : 4);
-  uint16_t* const dst = static_cast<uint16_t*>(s.dst) + page * s.dst_page + pos * s.dst_pos;
-  for (uint32_t v0 = lane; v0 < all; v0 += lanes * kFlight) {
-    uint4 x[kFlight];
-    int64_t to[kFlight];
-#pragma unroll
-    for (int k = 0; k < kFlight; ++k) {
-      const uint32_t v = v0 + k * lanes;
-      if (v >= all) break;
-      const uint32_t head = s.heads == 1 ? 0u : v / s.vecs, e = (v - head * s.vecs) * 8;
-      const int64_t from = head * s.src_head + e;
-      to[k] = head * s.dst_head + e;
-      if (BF16) {
-        x[k] = *reinterpret_cast<const uint4*>(src + from * 2);
-      } else {
-        const float4* f = reinterpret_cast<const float4*>(src + from * 4);
-        const float4 lo = f[0], hi = f[1];
-        x[k] = make_uint4(pack_bf16(lo.x, lo.y), pack_bf16(lo.z, lo.w), pack_bf16(hi.x, hi.y), pack_bf16(hi.z, hi.w));
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kFlight; ++k) {
-      if (v0 + k * lanes >= all) break;
-      *reinterpret_cast<uint4*>(dst + to[k]) = x[k];
-    }
-  }
-}
-
+// A token's 8-element vectors (of both sources) are copied by a warp, or by 2^k lanes of one where
+// they are that few, with kFlight of them a lane in flight: the slot and its page are looked up
+// once a token, neighbouring lanes move neighbouring 16 bytes, and a lane's loads are all under
+// way before its first store.
 template <bool BF16>
 __global__ void __launch_bounds__(kAppendThreads) gdn_kv_append_kernel(const KvAppendParams p) {
+  constexpr int kFlight = BF16 ? 8 : 4;
   griddep_launch_dependents();
   griddep_wait();
   const int lanes = p.lanes, lane = threadIdx.x & (lanes - 1);
+  const uint32_t va = p.a.vecs * p.a.heads, all = va + p.b.vecs * p.b.heads;
   const int64_t rows_at_once = static_cast<int64_t>(gridDim.x) * (kAppendThreads / lanes);
   for (int64_t r = static_cast<int64_t>(blockIdx.x) * (kAppendThreads / lanes) + threadIdx.x / lanes; r < p.n; r += rows_at_once) {
     const int64_t slot = p.slot_map[r];
-    if (slot < 0) continue;
-    if (slot >= p.num_slots) {
-      if (lane == 0) atomic_status(p.status, GDN_STATUS_BAD_SLOT);
-      continue;
+    for (uint32_t v0 = lane; v0 < all; v0 += lanes * kFlight) {
+      uint4 x[kFlight], y[kFlight];  // y: the second half of fp32 vectors
+      int64_t to[kFlight];
+#pragma unroll
+      for (int k = 0; k < kFlight; ++k) {
+        uint32_t v = v0 + k * lanes;
+        if (v >= all) break;
+        const bool second = v >= va;
+        if (second) v -= va;
+        const KvRows& s = second ? p.b : p.a;
+        const uint32_t head = s.heads == 1 ? 0u : v / s.vecs, e = (v - head * s.vecs) * 8;
+        const int64_t from = r * s.src_row + head * s.src_head + e;
+        to[k] = head * s.dst_head + e;
+        const uint4* f = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(s.src) + from * (BF16 ? 2 : 4));
+        x[k] = f[0];
+        if (!BF16) y[k] = f[1];
+      }
+      // what was read is dropped where the token has no slot: the loads need not wait for it
+      if (slot < 0) break;
+      if (slot >= p.num_slots) {
+        if (v0 == 0) atomic_status(p.status, GDN_STATUS_BAD_SLOT);
+        break;
+      }
+      // 32 bits hold most slots, and their division is several times shorter
+      const int64_t page = slot <= 0x7fffffff ? static_cast<int64_t>(static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.page_size))
+                                              : slot / p.page_size;
+      const int64_t pos = slot - page * p.page_size;
+#pragma unroll
+      for (int k = 0; k < kFlight; ++k) {
+        const uint32_t v = v0 + k * lanes;
+        if (v >= all) break;
+        const KvRows& s = v >= va ? p.b : p.a;
+        uint4 z = x[k];
+        if (!BF16) {
+          auto f = [](uint32_t bits) { return __uint_as_float(bits); };
+          z = make_uint4(pack_bf16(f(x[k].x), f(x[k].y)), pack_bf16(f(x[k].z), f(x[k].w)), pack_bf16(f(y[k].x), f(y[k].y)),
+                         pack_bf16(f(y[k].z), f(y[k].w)));
+        }
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(s.dst) + page * s.dst_page + pos * s.dst_pos + to[k]) = z;
+      }
     }
-    // 32 bits hold most slots, and their division is several times shorter
-    const int64_t page = slot <= 0x7fffffff ? static_cast<int64_t>(static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.page_size))
-                                            : slot / p.page_size;
-    const int64_t pos = slot - page * p.page_size;
-    copy_rows<BF16>(p, p.a, r, page, pos, lane, lanes);
-    if (p.b.vecs > 0) copy_rows<BF16>(p, p.b, r, page, pos, lane, lanes);
   }
 }
 
@@ -368,19 +368,18 @@ cudaError_t launch_kv_release(const KvReleaseParams& p, cudaStream_t stream) {
 
 cudaError_t launch_kv_append(const KvAppendParams& given, cudaStream_t stream) {
   KvAppendParams p = given;
-  uint32_t longest = 0;
+  uint32_t all = 0;
   for (KvRows* s : {&p.a, &p.b}) {
     if (s->heads > 1 && s->src_head == s->vecs * 8 && s->dst_head == s->vecs * 8) {  // heads in one piece
       s->vecs *= s->heads;
       s->heads = 1;
     }
-    const uint32_t all = s->vecs * s->heads;
-    longest = all > longest ? all : longest;
+    all += s->vecs * s->heads;
   }
   p.lanes = 1;
-  while (p.lanes < 32 && static_cast<uint32_t>(p.lanes) < longest) p.lanes *= 2;
+  while (p.lanes < 32 && static_cast<uint32_t>(p.lanes) < all) p.lanes *= 2;
   const int64_t rows = kAppendThreads / p.lanes, blocks = (p.n + rows - 1) / rows;
-  const unsigned grid = static_cast<unsigned>(blocks < kSms * 8 ? blocks : kSms * 8);
+  const unsigned grid = static_cast<unsigned>(blocks < kSms * 32 ? blocks : kSms * 32);
   return launch_overlapped(p.bf16 ? gdn_kv_append_kernel<true> : gdn_kv_append_kernel<false>, p, grid, kAppendThreads, 0, 1u,
                            stream);
 }
