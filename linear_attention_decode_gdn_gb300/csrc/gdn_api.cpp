@@ -231,7 +231,7 @@ int check_attn(const gdn_paged_kv* kv, const gdn_attn* a, const void* workspace)
   if (static_cast<long long>(a->num_tokens) * (a->num_heads / kv->num_kv_heads) > kMaxAttnCols)
     return fail(GDN_ERR_UNSUPPORTED, "num_tokens * num_heads / num_kv_heads must be at most %d", kMaxAttnCols);
   if (static_cast<long long>(a->batch) * a->num_tokens * a->num_heads > 0x7fffffffLL ||
-      static_cast<long long>(a->max_pages) * kv->page_size > 0x7fffffffLL)
+      static_cast<long long>(a->max_pages) * kv->page_size > 0x7fffff00LL)  // a tile past the last fits 32 bits
     return fail(GDN_ERR_INVALID_ARG, "batch * num_tokens * num_heads or max_pages * page_size too large");
   if (a->batch == 0) return GDN_OK;
   if (a->q == nullptr || a->block_table == nullptr || a->kv_len == nullptr || a->o == nullptr || workspace == nullptr)

@@ -206,26 +206,15 @@ __global__ void __launch_bounds__(kJoinThreads) gdn_attn_join_kernel(const AttnP
   griddep_launch_dependents();
   griddep_wait();
   const int i = blockIdx.x + 1, lane = threadIdx.x & 31;
-  const uint32_t* rec = p.records + static_cast<size_t>(i) * kRecordInts;
-  const uint4 r = *reinterpret_cast<const uint4*>(rec);
-  const uint2 r2 = *reinterpret_cast<const uint2*>(rec + 4);
-  const int unit = static_cast<int>(r2.x);
-  const uint32_t tiles = r.x, unit_start = r.y, unit_end = r.z;
-  const int b = static_cast<int>(r.w);
-  if (tiles == 0) return;
-  const uint32_t before = share_start(tiles, p.workers, i - 1);
-  // the unit's first tile is worker i's or a later one's, or an earlier border is inside it too
-  const uint32_t first_tile = unit_start + r2.y;
-  if (share_start(tiles, p.workers, i) <= first_tile || before > first_tile) return;
+  const uint4 r = *reinterpret_cast<const uint4*>(p.records + static_cast<size_t>(i) * kRecordInts);
+  if (r.x == 0) return;
+  const int parts = static_cast<int>(r.x), slot0 = static_cast<int>(r.y), b = static_cast<int>(r.z), unit = static_cast<int>(r.w);
   const int kv_head = unit / p.col_groups, col_base = (unit - kv_head * p.col_groups) * p.ncol;
   const int cols = min(p.ncol, p.cols - col_base);
   const int widths = (p.dv + kJoinWidth - 1) / kJoinWidth;
   const int task = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5);
   const int c = task / widths, d = (task - c * widths) * kJoinWidth + lane * 4;
   if (c >= cols) return;
-  const int parts = static_cast<int>(worker_from(tiles, p.workers, unit_end)) - (i - 1);  // workers i - 1, i, ...
-  // the unit is worker i - 1's last segment: its first one only where the share begins with it
-  const int slot0 = before >= unit_start ? 0 : 1;
   const size_t floats = partial_floats(p);
   const float* const first = partial_of(p, i - 1, slot0);
   const float* const second = partial_of(p, i, 0);  // and so on, two apart

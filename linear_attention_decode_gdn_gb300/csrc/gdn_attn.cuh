@@ -170,10 +170,10 @@ struct Walk {
 };
 
 // ---- the workspace ----------------------------------------------------------------------
-// Record of a worker: [length of the line, or 0 without work; line positions of the first
-// segment's unit, begin and end; request; unit; what a unit counts for beyond its tiles]. A
-// partial result: dv x ncol sums (column by column, fp32), then the columns' references (in the
-// scaled log2 domain: sums are of 2^(s - m)) and sums.
+// Record of a worker: what is to be joined at the border where its share begins: [parts, or 0 where
+// that is not the first border inside a unit; the slot of the first part (the worker before's);
+// request; unit]. A partial result: dv x ncol sums (column by column, fp32), then the columns'
+// references (in the scaled log2 domain: sums are of 2^(s - m)) and sums.
 __device__ __forceinline__ size_t partial_floats(const AttnParams& p) {
   return static_cast<size_t>(p.ncol) * (p.dv + 2);
 }
@@ -182,14 +182,18 @@ __device__ __forceinline__ float* partial_of(const AttnParams& p, int worker, in
 }
 
 __device__ __forceinline__ void write_record(const AttnParams& p, const Share& s, uint32_t worker) {
-  uint32_t* r = p.records + static_cast<size_t>(worker) * kRecordInts;
-  r[0] = s.count > 0 ? s.total : 0;
-  if (s.count == 0) return;
-  r[1] = s.unit_start;
-  r[2] = s.unit_start + s.extra + tiles_of(p, length_of(p, s.b)).count;
-  r[3] = s.b;
-  r[4] = s.unit;
-  r[5] = s.extra;
+  uint4 r = make_uint4(0u, 0u, static_cast<uint32_t>(s.b), static_cast<uint32_t>(s.unit));
+  if (s.count > 0 && worker > 0) {
+    const uint32_t start = s.unit_start + s.at, before = share_start(s.total, p.workers, worker - 1);
+    const uint32_t first_tile = s.unit_start + s.extra;
+    const uint32_t end = first_tile + tiles_of(p, length_of(p, s.b)).count;
+    if (start > first_tile && before <= first_tile) {
+      r.x = worker_from(s.total, p.workers, end) - (worker - 1);  // workers worker - 1, worker, ...
+      // the unit is that worker's last segment: its first one only where its share begins with it
+      r.y = before >= s.unit_start ? 0u : 1u;
+    }
+  }
+  *reinterpret_cast<uint4*>(p.records + static_cast<size_t>(worker) * kRecordInts) = r;
 }
 
 // Row of column c of a request and kv head: [B][T][H].

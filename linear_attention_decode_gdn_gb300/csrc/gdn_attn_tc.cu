@@ -334,7 +334,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
 
   if (warp == 0) {
     // ---- pages into the ring --------------------------------------------------------------
-    if (lane == 0 && rank == 0) write_record(p, share, worker);
     uint32_t slot = 0, round = 1, tile_no = 0;  // next slot, the parity its barrier has when free
     uint32_t put = 0;
     bool bad = false, ok = true;
@@ -568,6 +567,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
       arrive(&sm.q_full[qb], lane);
       ++units;
     }
+    if (tid == 64 && rank == 0) write_record(p, share, worker);
     write_empty<64>(p, tid - 64);
   } else {
     // ---- softmax ------------------------------------------------------------------------------

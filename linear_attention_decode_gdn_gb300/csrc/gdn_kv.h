@@ -100,7 +100,7 @@ struct AttnPlan {
 AttnPlan attn_plan(const gdn_paged_kv& kv, int cols);
 size_t attn_workspace_bytes(const AttnPlan& plan, int dv);
 // records, then partials
-constexpr int kRecordInts = 8;  // six of them in use
+constexpr int kRecordInts = 4;
 constexpr size_t kRecordBytes = static_cast<size_t>(kMaxAttnCtas) * kRecordInts * sizeof(uint32_t);
 static_assert(kRecordBytes % 16 == 0, "partials are read as vectors");
 
