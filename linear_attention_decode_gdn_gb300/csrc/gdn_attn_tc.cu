@@ -698,17 +698,40 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
 #pragma unroll
           for (int c0 = 0; c0 < NC; c0 += 16) {
             float f[16];
+            if constexpr (kKeep) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int c = c0 + j, a = a_base + c;
-              const float top = fmaxf(fmaxf(sm.per_warp[0][a], sm.per_warp[1][a]), fmaxf(sm.per_warp[2][a], sm.per_warp[3][a]));
-              const float m = kKeep ? kept[c] : sm.m[a];
-              const float to = top > m ? top + kHeadroom : m;
-              f[j] = ex2(m - to);
-              l[c] *= f[j];
-              if (kKeep) {
-                kept[c] = to;
-                if (r == c) sm.m[a] = to;
+              for (int j = 0; j < 16; j += 4) {
+                const int c = c0 + j, a = a_base + c;
+                float top[4], x[4];
+                auto load = [](float (&to)[4], const float* from) {
+                  const float4 v = *reinterpret_cast<const float4*>(from);
+                  to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
+                };
+                load(top, &sm.per_warp[0][a]);
+#pragma unroll
+                for (int v = 1; v < 4; ++v) {
+                  load(x, &sm.per_warp[v][a]);
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], x[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const float to = top[k] > kept[c + k] ? top[k] + kHeadroom : kept[c + k];
+                  f[j + k] = ex2(kept[c + k] - to);
+                  l[c + k] *= f[j + k];
+                  kept[c + k] = to;
+                  if (r == c + k) sm.m[a + k] = to;
+                }
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const int c = c0 + j, a = a_base + c;
+                const float top = fmaxf(fmaxf(sm.per_warp[0][a], sm.per_warp[1][a]), fmaxf(sm.per_warp[2][a], sm.per_warp[3][a]));
+                const float m = sm.m[a];
+                const float to = top > m ? top + kHeadroom : m;
+                f[j] = ex2(m - to);
+                l[c] *= f[j];
               }
             }
             if (t > 0) {
@@ -812,16 +835,19 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
         for (int c0 = 0; c0 < NC; c0 += 16) {
           float x[16];
           tc::ld16(o_at + block * N + c0, x);
-          if (ok && d >= 0) {
+          const int left = cols - (c_base + c0);  // columns that are rows of o
+          if (ok && d >= 0 && seg.whole) {
+            __nv_bfloat16* const o = static_cast<__nv_bfloat16*>(p.o) + d;
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              const int a = a_base + c0 + j, c = c_base + c0 + j;
-              if (c >= cols) break;
-              if (seg.whole)
-                static_cast<__nv_bfloat16*>(p.o)[static_cast<int64_t>(sm.rows[a]) * C::DV + d] = __float2bfloat16_rn(x[j] * sm.inv[a]);
-              else
-                part[c * C::DV + d] = x[j];
+              const int a = a_base + c0 + j;
+              if (j < left) o[static_cast<int64_t>(sm.rows[a]) * C::DV] = __float2bfloat16_rn(x[j] * sm.inv[a]);
             }
+          } else if (ok && d >= 0) {
+            float* const to = part + (c_base + c0) * C::DV + d;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (j < left) to[j * C::DV] = x[j];
           }
           __syncwarp();
         }
