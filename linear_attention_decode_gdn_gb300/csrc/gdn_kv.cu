@@ -62,8 +62,9 @@ __device__ __forceinline__ void cluster_sync_all() {
 // request and spares a second launch or a grid barrier. Then the CTAs share the tokens and the
 // pages. Where outputs are the inputs' own arrays (in_place), no CTA may write before all have
 // read: the grid is one cluster then, with its barrier in between.
-// Bound by instructions: a token costs a search over the sums and a division, so the tokens of
-// prompts want many SMs (131,000 tokens: 25 us on one cluster of 8 CTAs).
+// Bound by instructions for prompts: a token costs a search over the sums and a division, so
+// they want many SMs (512 requests, 114,000 tokens, pages of 16: 6.6 us; 25 us on one cluster of
+// 8 CTAs). Bound by latency for a decode step (256 requests: 3.8 us in one CTA).
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) gdn_kv_plan_kernel(const KvPlanParams p) {
   extern __shared__ int32_t sm[];
@@ -260,7 +261,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // A token's 8-element vectors (of both sources) are copied by a warp, or by 2^k lanes of one where
 // they are that few, with kFlight of them a lane in flight: the slot and its page are looked up
 // once a token, neighbouring lanes move neighbouring 16 bytes, and a lane's loads are all under
-// way before its first store.
+// way before its first store. Bound by HBM: 32,749 tokens of 8 + 8 heads of 128 (bf16) take 42 us,
+// 0.93 of the measured copy bandwidth.
 template <bool BF16>
 __global__ void __launch_bounds__(kAppendThreads) gdn_kv_append_kernel(const KvAppendParams p) {
   constexpr int kFlight = BF16 ? 8 : 4;
