@@ -374,8 +374,10 @@ typedef struct gdn_paged_kv {
  *   new_len [B]: new tokens of each request, or NULL (one each).
  *   held [B]: pages in each request's row; held_out receives the count after the step.
  *   block_table [B][max_pages]: entries held[b] .. held_out[b] - 1 are written.
- *   free_list, free_count [1]: the first *free_count entries are the free pages, handed out
- *       from the end; *free_count_out is what is left. The list itself is only read.
+ *   free_list [free_capacity], free_count [1]: the first *free_count entries are the free
+ *       pages, handed out from the end; *free_count_out is what is left. The list itself is
+ *       only read. A count outside [0, free_capacity] sets GDN_STATUS_BAD_LEN and is left as
+ *       it is; no page is handed out.
  *   kv_len [B]: cached_len + new_len. cu_new [B + 1]: running sums of new_len (where each
  *       request's tokens start among the packed new tokens; a sum past 2^31 - 1 stays there).
  *   slot_map [slot_capacity] int64: token cu_new[b] + i gets the slot page * page_size +
@@ -385,10 +387,10 @@ typedef struct gdn_paged_kv {
  * later request that needs one), or whose length passes max_pages pages, 2^31 - 1 or
  * slot_capacity, or is negative (GDN_STATUS_BAD_LEN) is skipped: kv_len = cached_len, no page, slots -1. An
  * entry outside [0, num_pages) (GDN_STATUS_BAD_PAGE) gives its positions the slot -1.
- * Requires batch <= 4096. free_list holds num_pages entries at most.
+ * Requires batch <= 4096.
  */
-int gdn_kv_plan(int32_t batch, int32_t max_pages, int32_t page_size, int32_t num_pages, int32_t slot_capacity,
-                const int32_t *cached_len, const int32_t *new_len, const int32_t *held, int32_t *block_table,
+int gdn_kv_plan(int32_t batch, int32_t max_pages, int32_t page_size, int32_t num_pages, int32_t free_capacity,
+                int32_t slot_capacity, const int32_t *cached_len, const int32_t *new_len, const int32_t *held, int32_t *block_table,
                 const int32_t *free_list, const int32_t *free_count, int32_t *kv_len, int32_t *cu_new,
                 int64_t *slot_map, int32_t *held_out, int32_t *free_count_out, int32_t *status, void *stream);
 
@@ -396,10 +398,10 @@ int gdn_kv_plan(int32_t batch, int32_t max_pages, int32_t page_size, int32_t num
  * gdn_kv_release -- gives the pages of n finished requests back: the first held[b] entries
  * of row b = requests[i] are pushed on the free list in order and held[b] becomes 0. Entries
  * of requests < 0 are ignored; >= batch sets GDN_STATUS_BAD_SLOT; a held count outside
- * [0, max_pages], or a list that would pass num_pages entries, sets GDN_STATUS_BAD_LEN and
- * leaves the request as it is. The requests of one call must be distinct.
+ * [0, max_pages], or a list that would pass free_capacity entries, sets GDN_STATUS_BAD_LEN
+ * and leaves the request as it is. The requests of one call must be distinct.
  */
-int gdn_kv_release(int32_t batch, int32_t max_pages, int32_t num_pages, const int32_t *requests, int32_t n,
+int gdn_kv_release(int32_t batch, int32_t max_pages, int32_t free_capacity, const int32_t *requests, int32_t n,
                    const int32_t *block_table, int32_t *held, int32_t *free_list, int32_t *free_count,
                    int32_t *status, void *stream);
 

@@ -124,7 +124,7 @@ def _declare(lib):
     lib.gdn_slot_reset.argtypes = [P(Dims), P(Log), vp, vp, vp, ctypes.c_int32, vp, vp]
     i32 = ctypes.c_int32
     lib.gdn_kv_plan.restype = ctypes.c_int
-    lib.gdn_kv_plan.argtypes = [i32] * 5 + [vp] * 13
+    lib.gdn_kv_plan.argtypes = [i32] * 6 + [vp] * 13
     lib.gdn_kv_release.restype = ctypes.c_int
     lib.gdn_kv_release.argtypes = [i32, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp]
     lib.gdn_kv_append.restype = ctypes.c_int

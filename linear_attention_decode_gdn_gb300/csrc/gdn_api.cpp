@@ -463,12 +463,13 @@ int gdn_slot_reset(const gdn_dims* dims, const gdn_log* log, void* conv_pool, fl
   return launched(gdn::launch_slot_reset(p, static_cast<cudaStream_t>(stream)), "gdn_slot_reset");
 }
 
-int gdn_kv_plan(int32_t batch, int32_t max_pages, int32_t page_size, int32_t num_pages, int32_t slot_capacity,
-                const int32_t* cached_len, const int32_t* new_len, const int32_t* held, int32_t* block_table,
+int gdn_kv_plan(int32_t batch, int32_t max_pages, int32_t page_size, int32_t num_pages, int32_t free_capacity,
+                int32_t slot_capacity, const int32_t* cached_len, const int32_t* new_len, const int32_t* held, int32_t* block_table,
                 const int32_t* free_list, const int32_t* free_count, int32_t* kv_len, int32_t* cu_new,
                 int64_t* slot_map, int32_t* held_out, int32_t* free_count_out, int32_t* status, void* stream) {
-  if (batch < 0 || max_pages <= 0 || page_size <= 0 || num_pages <= 0 || slot_capacity < 0)
-    return fail(GDN_ERR_INVALID_ARG, "batch and slot_capacity must be >= 0, max_pages, page_size and num_pages > 0");
+  if (batch < 0 || max_pages <= 0 || page_size <= 0 || num_pages <= 0 || free_capacity < 0 || slot_capacity < 0)
+    return fail(GDN_ERR_INVALID_ARG,
+                "batch, free_capacity and slot_capacity must be >= 0, max_pages, page_size and num_pages > 0");
   if (batch > gdn::kMaxPlanBatch)
     return fail(GDN_ERR_UNSUPPORTED, "batch %d > %d", batch, gdn::kMaxPlanBatch);
   if (batch == 0) return GDN_OK;
@@ -476,21 +477,37 @@ int gdn_kv_plan(int32_t batch, int32_t max_pages, int32_t page_size, int32_t num
       free_count == nullptr || kv_len == nullptr || cu_new == nullptr || held_out == nullptr ||
       free_count_out == nullptr || (slot_map == nullptr && slot_capacity > 0))
     return fail(GDN_ERR_INVALID_ARG, "every array but new_len and status is required");
-  gdn::KvPlanParams p{batch,   max_pages, page_size,  num_pages, slot_capacity, cached_len, new_len,        held,
-                      block_table, free_list, free_count, kv_len,    cu_new,        slot_map,   held_out, free_count_out,
-                      status, false};
+  gdn::KvPlanParams p{};
+  p.B = batch;
+  p.max_pages = max_pages;
+  p.page_size = page_size;
+  p.num_pages = num_pages;
+  p.free_capacity = free_capacity;
+  p.slot_capacity = slot_capacity;
+  p.cached = cached_len;
+  p.fresh = new_len;
+  p.held = held;
+  p.table = block_table;
+  p.free_list = free_list;
+  p.free_count = free_count;
+  p.kv_len = kv_len;
+  p.cu_new = cu_new;
+  p.slot_map = slot_map;
+  p.held_out = held_out;
+  p.free_count_out = free_count_out;
+  p.status = status;
   return launched(gdn::launch_kv_plan(p, static_cast<cudaStream_t>(stream)), "gdn_kv_plan");
 }
 
-int gdn_kv_release(int32_t batch, int32_t max_pages, int32_t num_pages, const int32_t* requests, int32_t n,
+int gdn_kv_release(int32_t batch, int32_t max_pages, int32_t free_capacity, const int32_t* requests, int32_t n,
                    const int32_t* block_table, int32_t* held, int32_t* free_list, int32_t* free_count,
                    int32_t* status, void* stream) {
-  if (batch < 0 || max_pages <= 0 || num_pages <= 0 || n < 0)
-    return fail(GDN_ERR_INVALID_ARG, "batch and n must be >= 0, max_pages and num_pages > 0");
+  if (batch < 0 || max_pages <= 0 || free_capacity <= 0 || n < 0)
+    return fail(GDN_ERR_INVALID_ARG, "batch and n must be >= 0, max_pages and free_capacity > 0");
   if (n == 0) return GDN_OK;
   if (requests == nullptr || block_table == nullptr || held == nullptr || free_list == nullptr || free_count == nullptr)
     return fail(GDN_ERR_INVALID_ARG, "requests, block_table, held, free_list and free_count are required");
-  gdn::KvReleaseParams p{batch, max_pages, num_pages, n, requests, block_table, held, free_list, free_count, status};
+  gdn::KvReleaseParams p{batch, max_pages, free_capacity, n, requests, block_table, held, free_list, free_count, status};
   return launched(gdn::launch_kv_release(p, static_cast<cudaStream_t>(stream)), "gdn_kv_release");
 }
 

@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(THREADS) gdn_kv_plan_kernel(const KvPlanParams
   uint32_t bad = 0;
   int32_t avail = p.free_count[0];
   const int32_t given = avail;
-  if (avail < 0 || avail > p.num_pages) {
+  if (avail < 0 || avail > p.free_capacity) {
     avail = 0;
     bad |= GDN_STATUS_BAD_LEN;
   }
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kReleaseThreads) gdn_kv_release_kernel(const K
   uint32_t bad = 0;
   int64_t top = p.free_count[0];
   __syncthreads();  // read by all before thread 0 writes it at the end
-  if (top < 0 || top > p.num_pages) {
+  if (top < 0 || top > p.free_capacity) {
     if (tid == 0) atomic_status(p.status, GDN_STATUS_BAD_LEN);
     return;
   }
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kReleaseThreads) gdn_kv_release_kernel(const K
     int64_t total;
     const int64_t upto = block_scan<kReleaseThreads>(h, warp_sums, &total);
     // past the list's end this request and the later ones of the chunk keep their pages
-    const bool fits = top + upto <= p.num_pages;
+    const bool fits = top + upto <= p.free_capacity;
     if (h > 0 && !fits) bad |= GDN_STATUS_BAD_LEN;
     at[tid] = static_cast<int32_t>(top + upto - h);
     row[tid] = b;

@@ -14,7 +14,7 @@ namespace gdn {
 constexpr int kMaxPlanBatch = 4096;  // requests of one plan (its running sums sit in shared memory)
 
 struct KvPlanParams {
-  int32_t B, max_pages, page_size, num_pages, slot_capacity;
+  int32_t B, max_pages, page_size, num_pages, free_capacity, slot_capacity;
   const int32_t* cached;
   const int32_t* fresh;  // new tokens, or NULL
   const int32_t* held;
@@ -31,7 +31,7 @@ struct KvPlanParams {
 };
 
 struct KvReleaseParams {
-  int32_t B, max_pages, num_pages, n;
+  int32_t B, max_pages, free_capacity, n;
   const int32_t* requests;
   const int32_t* table;
   int32_t* held;

@@ -87,11 +87,9 @@ def kv_plan(cached_len, new_len, held, block_table, free_list, free_count, *, kv
     token each). Writes block_table, kv_len, cu_new, slot_map, held_out and free_count_out; the
     last three of kv_len / held_out / free_count_out may be the input arrays themselves."""
     batch, capacity, free = cached_len.numel(), slot_map.numel(), free_list.numel()
-    if free > num_pages:
-        raise ValueError("free_list: at most num_pages entries")
     cached = _ints(cached_len, batch, "cached_len")
     check(_abi.load().gdn_kv_plan(
-        batch, _table(block_table, batch), page_size, num_pages, capacity, cached,
+        batch, _table(block_table, batch), page_size, num_pages, free, capacity, cached,
         None if new_len is None else _ints(new_len, batch, "new_len"), _ints(held, batch, "held"),
         block_table.data_ptr(), _ints(free_list, free, "free_list"), _ints(free_count, 1, "free_count"),
         _ints(kv_len, batch, "kv_len"), _ints(cu_new, batch + 1, "cu_new"), _ints(slot_map, capacity, "slot_map", _I64),

@@ -30,7 +30,7 @@ def plan_reference(cached, new, held, table, free, count, page, pages, capacity)
     """Request by request, as gdn.h says it. Returns what the call writes, and the status."""
     S = dict(NO_PAGES=0x10, BAD_LEN=4, BAD_PAGE=0x20)
     bad, avail, given = 0, count, count
-    if not 0 <= count <= pages:
+    if not 0 <= count <= len(free):  # the list's room
         bad, avail = S["BAD_LEN"], 0
     table, held, free = [list(r) for r in table], list(held), list(free)
     length, cu, slots, used, full = [], [0], [-1] * capacity, 0, False
@@ -115,7 +115,7 @@ def test_plan(gdn, batch, page, most, new_most, short, seed):
 
 @pytest.mark.parametrize("kw", [
     dict(new=[1, -2, 1]), dict(cached=[10, 3000, 4]), dict(held=[1, -1, 1]), dict(held=[1, 99, 1]),
-    dict(cached=[2 ** 31 - 1, 3, 4]), dict(new=[2 ** 30, 2 ** 30, 2 ** 30]), dict(count=-3), dict(count=99),
+    dict(cached=[2 ** 31 - 1, 3, 4]), dict(new=[2 ** 30, 2 ** 30, 2 ** 30]), dict(count=-3), dict(count=99), dict(count=5),
     dict(table=[[0, -1], [77, -1], [2, -1]]), dict(free=[8, -5, 7, 99], cached=[16, 16, 16]),
 ])
 def test_plan_reports_what_cannot_be(gdn, kw):

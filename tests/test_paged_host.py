@@ -120,13 +120,13 @@ def test_append_arguments_are_checked(gdn):
 def test_plan_and_release_arguments_are_checked(gdn):
     lib = gdn._abi.load()
 
-    def plan(batch=2, pages=4, size=16, total=8, capacity=2, **kw):
+    def plan(batch=2, pages=4, size=16, total=8, room=8, capacity=2, **kw):
         ptr = dict(cached=FAKE, new=None, held=FAKE, table=FAKE, free=FAKE, count=FAKE, kv=FAKE, cu=FAKE, slots=FAKE,
                    held_out=FAKE, count_out=FAKE)
         ptr.update(kw)
-        return lib.gdn_kv_plan(batch, pages, size, total, capacity, *ptr.values(), None, None)
+        return lib.gdn_kv_plan(batch, pages, size, total, room, capacity, *ptr.values(), None, None)
 
-    for kw in (dict(batch=-1), dict(pages=0), dict(size=0), dict(total=0), dict(capacity=-1)):
+    for kw in (dict(batch=-1), dict(pages=0), dict(size=0), dict(total=0), dict(room=-1), dict(capacity=-1)):
         assert plan(**kw) == BAD, kw
     assert plan(batch=4097) == NO
     assert plan(batch=0) == 0
