@@ -526,3 +526,24 @@ def test_hybrid_steps_in_a_graph(gdn):
                 off = (q.numel() + 4) * 2.0 ** -24 * float((k[:, kh].double().abs() @ q.abs()).max()) * scale + 2.0 ** -21
                 tolerance = want.abs() * 2.0 ** -8 + size * (2.0 ** -8 + 2 * off + (total + 64) * 2.0 ** -24) * 1.01
                 assert bool(((layer["o"][b, 0, h].double() - want).abs() <= tolerance).all()), (i, b, h)
+
+
+def test_two_streams_at_once(gdn):
+    """Calls that share the GPU, each with its workspace: the bits of the calls alone."""
+    problems = [Problem(gdn, [900, 30, 2000, 0, 129], heads=8, heads_kv=2, dk=128, page=32, seed=11),
+                Problem(gdn, [1500, 1, 700], heads=32, heads_kv=1, dk=576, dv=512, page=64, latent=True, seed=12),
+                Problem(gdn, [64, 3000], heads=4, heads_kv=2, dk=48, page=10, T=2, seed=13)]
+    alone = []
+    for p in problems:
+        p.call()
+        torch.cuda.synchronize()
+        alone.append((p.o.clone(), p.lse.clone()))
+        p.o.zero_(), p.lse.zero_()
+    streams = [torch.cuda.Stream() for _ in problems]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for p, s in zip(problems, streams):
+            p.call(stream=s)
+    torch.cuda.synchronize()
+    for p, (o, lse) in zip(problems, alone):
+        assert torch.equal(p.o, o) and torch.equal(p.lse, lse) and p.status.item() == 0
