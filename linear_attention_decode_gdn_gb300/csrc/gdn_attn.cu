@@ -319,8 +319,9 @@ size_t attn_workspace_bytes(const AttnPlan& plan, int dv) {
 }
 
 cudaError_t launch_attn_general(AttnParams& p, cudaStream_t stream) {
-  const cudaError_t err = cudaFuncSetAttribute(gdn_attn_general_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(sizeof(GeneralSmem)));
+  static std::atomic<bool> allowed[kDevices];
+  const cudaError_t err =
+      allow_shared(reinterpret_cast<const void*>(gdn_attn_general_kernel), static_cast<int>(sizeof(GeneralSmem)), allowed);
   if (err != cudaSuccess) return err;
   return launch_overlapped(gdn_attn_general_kernel, p, dim3(p.workers), kThreads, sizeof(GeneralSmem), stream);
 }

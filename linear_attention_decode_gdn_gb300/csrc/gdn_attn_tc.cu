@@ -879,7 +879,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
 
 template <class C>
 cudaError_t launch_one(const TcParams& tp, cudaStream_t stream) {
-  const cudaError_t err = cudaFuncSetAttribute(gdn_attn_tc_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static std::atomic<bool> allowed[kDevices];
+  const cudaError_t err = allow_shared(reinterpret_cast<const void*>(gdn_attn_tc_kernel<C>), C::SMEM, allowed);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(tp.a.workers * C::CL);

@@ -345,8 +345,9 @@ template <int THREADS>
 cudaError_t launch_plan(const KvPlanParams& p, unsigned ctas, cudaStream_t stream) {
   const size_t smem = (5u * p.B + 1u) * sizeof(int32_t);
   if (smem > 48 * 1024) {
-    const cudaError_t err = cudaFuncSetAttribute(gdn_kv_plan_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (5 * kMaxPlanBatch + 1) * static_cast<int>(sizeof(int32_t)));
+    static std::atomic<bool> allowed[kDevices];
+    const cudaError_t err = allow_shared(reinterpret_cast<const void*>(gdn_kv_plan_kernel<THREADS>),
+                                         (5 * kMaxPlanBatch + 1) * static_cast<int>(sizeof(int32_t)), allowed);
     if (err != cudaSuccess) return err;
   }
   return launch_overlapped(gdn_kv_plan_kernel<THREADS>, p, ctas, THREADS, smem, p.in_place ? ctas : 1u, stream);

@@ -2,6 +2,7 @@
 // kernels. Not part of the public interface (include/gdn.h is).
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -87,6 +88,19 @@ struct AttnParams {
   uint32_t* records;
   float* partials;
 };
+
+// Dynamic shared memory past 48 KB is allowed once a kernel and device; `done` is the kernel's own.
+constexpr int kDevices = 64;
+inline cudaError_t allow_shared(const void* kernel, int bytes, std::atomic<bool> (&done)[kDevices]) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+  if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (err == cudaSuccess) done[dev].store(true, std::memory_order_relaxed);
+  return err;
+}
 
 cudaError_t launch_kv_plan(const KvPlanParams& p, cudaStream_t stream);
 cudaError_t launch_kv_release(const KvReleaseParams& p, cudaStream_t stream);
