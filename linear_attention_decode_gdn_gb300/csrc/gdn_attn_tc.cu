@@ -15,8 +15,8 @@
 //
 // One CTA an SM. Warp 0 gathers pages by TMA into a ring of slots (128 positions x 64 or 128
 // elements, 128-byte swizzle; pages of 16 .. 128 positions are boxes of a slot). Warp 1 issues
-// the MMAs: scores of tile i + 1 before values of tile i, so the tensor core works while the
-// softmax does. Warps 2 and 3 lay out the next unit's queries. The other warps are the softmax,
+// the MMAs: scores of tile i + 1 before values of tile i (over latent rows, whichever is ready),
+// so the tensor core works while the softmax does. Warps 2 and 3 lay out the next unit's queries. The other warps are the softmax,
 // four for every 16 columns: one thread a position; sums of weights stay in the threads until
 // the unit ends. The reference is the maximum of the tile that set it, times 2^8; it is raised
 // (and O^T rescaled in TMEM) only where a score passes it, so most tiles need one barrier and no
@@ -24,11 +24,13 @@
 //
 // Latent rows: the value is the key's own row, so a tile's 147 KB would have to stay until the
 // values' product, and with them alone shared memory is full: loads, scores, softmax and values
-// would take turns. A pair of CTAs (one cluster) therefore splits the row: each CTA holds half
-// of the latent and of the tail, two tiles deep, forms its half of every score's sum, sends it
-// to the other CTA's shared memory (st.async, counted on an mbarrier), and adds what it is
-// sent. Both then take the same softmax (the sum of two is the same in either order) and each
-// its half of O^T. No byte of the cache and no product is taken twice.
+// would take turns (128 requests x 32 heads: 300 us). A pair of CTAs (one cluster) therefore
+// splits the row: each CTA holds half of the latent and of the tail, two to three tiles deep,
+// forms its half of every score's sum, sends it to the other CTA's shared memory (st.async,
+// counted on an mbarrier), and adds what it is sent. Both then take the same softmax (the sum of
+// two is the same in either order) and each its half of O^T. No byte of the cache and no product
+// is taken twice.
+//
 // What bounds it, and what it takes (bf16 cache, one GB300):
 //   full batch, 128 requests x 32 heads over 8 kv heads of 128, 2.17 GB: 321 us, 6.7 TB/s: HBM.
 //   one request of 131,071 positions, same heads, 0.54 GB: 86 us, 6.2 TB/s: HBM, start and join.
