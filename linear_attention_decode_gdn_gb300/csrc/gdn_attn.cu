@@ -196,7 +196,6 @@ __global__ void __launch_bounds__(kThreads) gdn_attn_general_kernel(const AttnPa
 
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWidth = 128;  // value elements a warp adds: four a lane
-constexpr int kJoinAhead = 8;    // parts in flight
 
 // Block (i, .) looks at the border between the shares of workers i and i + 1. Where it is the
 // first border inside a unit, its warps add the unit's partial results, each for one column and
@@ -204,7 +203,9 @@ constexpr int kJoinAhead = 8;    // parts in flight
 // m = max m_j, l = sum 2^(m_j - m) l_j, o = sum 2^(m_j - m) o_j / l.
 // Bound by latency, so a warp waits for two loads only: the record, then references, sums and
 // the first parts together (one request of 131,071 positions, 8 units in 19 parts: about 3 us of
-// 86 with the launch; a block a column that walked the records took 8).
+// 86 with the launch; a block a column that walked the records took 8). AHEAD parts are in
+// flight: more shorten long lists of parts, fewer leave registers for more blocks.
+template <int AHEAD>
 __global__ void __launch_bounds__(kJoinThreads) gdn_attn_join_kernel(const AttnParams p) {
   griddep_launch_dependents();
   griddep_wait();
@@ -225,9 +226,9 @@ __global__ void __launch_bounds__(kJoinThreads) gdn_attn_join_kernel(const AttnP
   const int64_t at = static_cast<int64_t>(c) * p.dv + d, ref = static_cast<int64_t>(p.ncol) * p.dv + c;
   const bool mine = d < p.dv;
 
-  float4 ahead[kJoinAhead];
+  float4 ahead[AHEAD];
 #pragma unroll
-  for (int j = 0; j < kJoinAhead; ++j)
+  for (int j = 0; j < AHEAD; ++j)
     if (mine && j < parts) ahead[j] = *reinterpret_cast<const float4*>(part(j) + at);
   float m = -INFINITY;
   for (int j = lane; j < parts; j += 32) m = fmaxf(m, part(j)[ref]);
@@ -247,14 +248,14 @@ __global__ void __launch_bounds__(kJoinThreads) gdn_attn_join_kernel(const AttnP
     const float w = have ? exp2f(part(j0 + lane)[ref] - zero) : 0.0f;
     if (have) l = fmaf(w, part(j0 + lane)[ref + p.ncol], l);
     const int count = min(32, parts - j0);
-    for (int j1 = 0; j1 < count; j1 += kJoinAhead) {
+    for (int j1 = 0; j1 < count; j1 += AHEAD) {
       if (j0 + j1 > 0) {
 #pragma unroll
-        for (int j = 0; j < kJoinAhead; ++j)
+        for (int j = 0; j < AHEAD; ++j)
           if (mine && j1 + j < count) ahead[j] = *reinterpret_cast<const float4*>(part(j0 + j1 + j) + at);
       }
 #pragma unroll
-      for (int j = 0; j < kJoinAhead; ++j) {
+      for (int j = 0; j < AHEAD; ++j) {
         const float wj = __shfl_sync(0xffffffffu, w, (j1 + j) & 31);
         if (mine && j1 + j < count) add(wj, ahead[j]);
       }
@@ -329,7 +330,14 @@ cudaError_t launch_attn_general(AttnParams& p, cudaStream_t stream) {
 cudaError_t launch_attn_join(const AttnParams& p, cudaStream_t stream) {
   const unsigned cols = static_cast<unsigned>(p.cols < p.ncol ? p.cols : p.ncol);
   const unsigned tasks = cols * ((p.dv + kJoinWidth - 1) / kJoinWidth), warps = kJoinThreads / 32;
-  return launch_overlapped(gdn_attn_join_kernel, p, dim3(p.workers - 1, (tasks + warps - 1) / warps), kJoinThreads, 0, stream);
+  const dim3 grid(p.workers - 1, (tasks + warps - 1) / warps);
+  // By the parts that units of equal length would have. One request on 2 kv heads (76 parts): 21.9,
+  // 17.1, 15.4 us for the whole call with 4, 8, 16 ahead; one on 2 kv heads in 8 parts: 9.3, 8.9,
+  // 9.3; 67 requests on latent rows: 25.7, 26.4, 29.4.
+  const int64_t units = static_cast<int64_t>(p.B) * p.heads_kv * p.col_groups;
+  auto kernel = p.workers >= 16 * units ? gdn_attn_join_kernel<16>
+                : p.workers >= 4 * units ? gdn_attn_join_kernel<8> : gdn_attn_join_kernel<4>;
+  return launch_overlapped(kernel, p, grid, kJoinThreads, 0, stream);
 }
 
 cudaError_t launch_attn(const AttnPlan& plan, AttnParams& p, cudaStream_t stream) {
