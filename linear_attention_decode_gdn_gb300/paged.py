@@ -21,7 +21,7 @@ _pack_kv = struct.Struct("=QQ6q5i4x").pack       # gdn_paged_kv
 _pack_attn = struct.Struct("=5if4q4Q").pack      # gdn_attn
 _pack_strides = struct.Struct("=2q").pack
 _BF16, _FP32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # absent where torch has no CUDA
 
 
 
