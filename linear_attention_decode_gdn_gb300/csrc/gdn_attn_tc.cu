@@ -777,6 +777,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
           const uint32_t j = i - C::PB;
           ok &= waited(&sm.pv_done[j & 1u], (j >> 1) & 1u, sm);
         }
+        // Weights are rounded to bf16 for the product with the values (2^-8 of a weight at most, as the
+        // values and the output are bf16 themselves); their sums l, and so lse, take them in fp32.
         unsigned char* const to = weights + (i % C::PB) * C::PBYTES + (c_base / 8) * (kTile * 16) + r * 16;
 #pragma unroll
         for (int c = 0; c < NC; c += 8) {
