@@ -95,6 +95,13 @@ struct Cfg {
   static constexpr int TMEM = TMEM_USED <= 32 ? 32 : TMEM_USED <= 64 ? 64 : TMEM_USED <= 128 ? 128 : TMEM_USED <= 256 ? 256 : 512;
   // the scores of a tile are taken while the values of the one before still need their slots
   static_assert(SLOTS >= KS + (LATENT ? KS : VS), "the ring holds what both products need");
+  // A slot's barrier tells its fills apart by parity alone, so waiting for a fill is sound only where the
+  // slot's fill before is known to have landed. With a tile's scores its keys have, and all fills before
+  // them but the values of the tile before. Latent values are the keys; elsewhere every value slot's fill
+  // before is among these where the ring holds a tile and its values, and where it does not (heads of 256
+  // with more than 16 columns) the softmax first waits for the products of the tile before.
+  static constexpr bool FILL_KNOWN = LATENT || SLOTS >= PER + VS;
+  static_assert(FILL_KNOWN || TEAMS == 1, "that wait is for a tile of the same threads");
   static_assert(N % 16 == 0 && N <= 64 && SMEM <= kSmemMost && TMEM_USED <= 512, "fits");
 };
 
@@ -801,6 +808,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
           // Positions outside the request share its pages: whatever their values are (another
           // request's, or never written), a weight of zero has to meet a zero.
           constexpr int kSlots = C::LATENT ? C::KS : C::VS;
+          if (!C::FILL_KNOWN && i > 0) ok &= waited(&sm.pv_done[(i - 1) & 1u], ((i - 1) >> 1) & 1u, sm);
 #pragma unroll 1
           for (int v = 0; v < kSlots; ++v) {
             const uint32_t n = i * C::PER + (C::LATENT ? 0 : C::KS) + v, slot = n % C::SLOTS;
