@@ -460,6 +460,18 @@ int gdn_attn_decode(const gdn_paged_kv *kv, const gdn_attn *attn, void *workspac
 int gdn_latent_decode(const gdn_paged_kv *kv, const gdn_attn *attn, void *workspace, size_t workspace_bytes,
                       int32_t *status, void *stream);
 
+/*
+ * gdn_attn_starve_wait -- test only: gdn_attn_decode, or gdn_latent_decode for a latent cache, in which
+ * one wait of the tensor-core kernel's first CTA is for an arrival that never comes, so that it runs
+ * out (about a second) and the call reports GDN_STATUS_TIMEOUT; exercises the timeout path
+ * without any fault. wait: GDN_STARVE_LOAD, the first page box; GDN_STARVE_WEIGHTS, the first
+ * tile's weights. GDN_ERR_UNSUPPORTED where the call would run on the CUDA cores.
+ */
+#define GDN_STARVE_LOAD 1
+#define GDN_STARVE_WEIGHTS 2
+int gdn_attn_starve_wait(const gdn_paged_kv *kv, const gdn_attn *attn, int32_t wait, void *workspace, size_t workspace_bytes,
+                         int32_t *status, void *stream);
+
 /* Bytes of workspace for a call of either with this cache, batch, T and H. Host only. */
 int gdn_attn_workspace(const gdn_paged_kv *kv, int32_t batch, int32_t num_tokens, int32_t num_heads, size_t *bytes);
 

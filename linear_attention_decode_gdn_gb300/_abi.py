@@ -42,11 +42,15 @@ OUT_NORM_GATE = 1 << 9
 SPLIT_DV = 1 << 10
 TEST_STARVE_WAIT = 1 << 31
 
+# waits of gdn_attn_starve_wait
+STARVE_LOAD = 1
+STARVE_WEIGHTS = 2
+
 # every symbol include/gdn.h declares
 EXPORTS = ("gdn_version", "gdn_strerror", "gdn_last_error", "gdn_conv_l2norm", "gdn_decode_dense",
            "gdn_decode_append", "gdn_decode_merge", "gdn_decode_step", "gdn_decode_verify",
            "gdn_prefill", "gdn_log_bytes", "gdn_slot_reset", "gdn_kv_plan", "gdn_kv_release",
-           "gdn_kv_append", "gdn_attn_decode", "gdn_latent_decode", "gdn_attn_workspace")
+           "gdn_kv_append", "gdn_attn_decode", "gdn_latent_decode", "gdn_attn_starve_wait", "gdn_attn_workspace")
 
 
 class Dims(ctypes.Structure):
@@ -133,6 +137,8 @@ def _declare(lib):
         fn = getattr(lib, name)
         fn.restype = ctypes.c_int
         fn.argtypes = [vp, vp, vp, ctypes.c_size_t, vp, vp]
+    lib.gdn_attn_starve_wait.restype = ctypes.c_int
+    lib.gdn_attn_starve_wait.argtypes = [vp, vp, i32, vp, ctypes.c_size_t, vp, vp]
     lib.gdn_attn_workspace.restype = ctypes.c_int
     lib.gdn_attn_workspace.argtypes = [vp, i32, i32, i32, vp]
     return lib

@@ -243,7 +243,7 @@ int check_attn(const gdn_paged_kv* kv, const gdn_attn* a, const void* workspace)
 }
 
 int attend(const gdn_paged_kv* kv, const gdn_attn* a, void* workspace, size_t workspace_bytes, int32_t* status,
-           void* stream, bool latent, const char* name) {
+           void* stream, bool latent, const char* name, int32_t starve = 0) {
   if (int rc = check_attn(kv, a, workspace)) return rc;
   if ((kv->v == nullptr) != latent)
     return fail(GDN_ERR_INVALID_ARG, latent ? "gdn_latent_decode reads a latent cache (kv->v NULL)"
@@ -258,7 +258,9 @@ int attend(const gdn_paged_kv* kv, const gdn_attn* a, void* workspace, size_t wo
   const int64_t tiles = (static_cast<int64_t>(a->max_pages) * kv->page_size + gdn::kTile - 1) / gdn::kTile;
   if ((tiles + plan.unit_cost) * a->batch > 0x7fffffffLL / (kv->num_kv_heads * col_groups))
     return fail(GDN_ERR_UNSUPPORTED, "the table could hold 2^31 tiles of %d positions or more", gdn::kTile);
+  if (starve != 0 && !plan.tensor) return fail(GDN_ERR_UNSUPPORTED, "this shape's kernel has no waits");
   gdn::AttnParams p{};
+  p.starve = starve;
   p.B = a->batch;
   p.T = a->num_tokens;
   p.H = a->num_heads;
@@ -553,6 +555,12 @@ int gdn_attn_decode(const gdn_paged_kv* kv, const gdn_attn* attn, void* workspac
 int gdn_latent_decode(const gdn_paged_kv* kv, const gdn_attn* attn, void* workspace, size_t workspace_bytes,
                       int32_t* status, void* stream) {
   return attend(kv, attn, workspace, workspace_bytes, status, stream, true, "gdn_latent_decode");
+}
+
+int gdn_attn_starve_wait(const gdn_paged_kv* kv, const gdn_attn* attn, int32_t wait, void* workspace, size_t workspace_bytes,
+                         int32_t* status, void* stream) {
+  if (wait != GDN_STARVE_LOAD && wait != GDN_STARVE_WEIGHTS) return fail(GDN_ERR_INVALID_ARG, "wait is one of GDN_STARVE_*");
+  return attend(kv, attn, workspace, workspace_bytes, status, stream, kv != nullptr && kv->v == nullptr, "gdn_attn_starve_wait", wait);
 }
 
 int gdn_attn_workspace(const gdn_paged_kv* kv, int32_t batch, int32_t num_tokens, int32_t num_heads, size_t* bytes) {

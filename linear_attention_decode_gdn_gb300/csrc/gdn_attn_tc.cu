@@ -262,7 +262,8 @@ __device__ __forceinline__ bool test_wait(uint64_t* bar, uint32_t parity) {
 }
 
 // A wait with a limit. The first one that runs out raises a flag that ends every other wait of
-// the CTA, so the kernel returns soon after (and reports GDN_STATUS_TIMEOUT).
+// the CTA, so the kernel returns soon after (and reports GDN_STATUS_TIMEOUT). The other CTA of a
+// pair is sent nothing more, so its own waits run out too.
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool waited(uint64_t* bar, uint32_t parity, Misc& sm) {
   auto done = [&] { return CLUSTER ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity); };
@@ -311,8 +312,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
 
   griddep_launch_dependents();
   if (tid == 0) {
+    // for tests, the first barrier of the first CTA counts on an arrival that never comes
+    const bool starve_load = p.starve == GDN_STARVE_LOAD && blockIdx.x == 0, starve_weights = p.starve == GDN_STARVE_WEIGHTS && blockIdx.x == 0;
     for (int i = 0; i < C::SLOTS; ++i) {
-      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.full[i], i == 0 && starve_load ? 2 : 1);
       mbar_init(&sm.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -322,7 +325,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
       mbar_init(&sm.q_empty[i], 1);
       mbar_init(&sm.s_full[i], 1);
       mbar_init(&sm.s_empty[i], 4 * C::G);
-      mbar_init(&sm.p_full[i], 4 * C::G);
+      mbar_init(&sm.p_full[i], 4 * C::G + (i == 0 && starve_weights ? 1 : 0));
       mbar_init(&sm.pv_done[i], 1);
       mbar_init(&sm.unit_begun[i], 1);
       mbar_init(&sm.unit_done[i], 1);
@@ -667,11 +670,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
         tc::fence_before_sync();
         arrive(&sm.s_empty[i & 1u], lane);
         if (C::LATENT) {
+          // After a wait that ran out nothing is sent, expected or freed any more: the bytes that a
+          // barrier counts would get ahead of the round that the other CTA is in. Its wait for them runs
+          // out instead, and it stops as well.
           if (i > 0) ok &= waited(&sm.may_send[g], (i - 1) & 1u, sm);
+          if (ok) {
 #pragma unroll
-          for (int c = 0; c < NC; c += 4) send16(there + (c / 4) * (kTile * 16), s[c], s[c + 1], s[c + 2], s[c + 3], got_there);
+            for (int c = 0; c < NC; c += 4) send16(there + (c / 4) * (kTile * 16), s[c], s[c + 1], s[c + 2], s[c + 3], got_there);
+          }
           ok &= waited<true>(&sm.got[g], i & 1u, sm);
-          if (r == 0) mbar_arrive_expect_tx(&sm.got[g], NC * kTile * 4);  // the next tile's
+          if (ok && r == 0) mbar_arrive_expect_tx(&sm.got[g], NC * kTile * 4);  // the next tile's
           const unsigned char* from = received + mine;
 #pragma unroll
           for (int c = 0; c < NC; c += 4) {
@@ -702,7 +710,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
         }
         const bool any = group_any(quad, raise);
         // every thread of the group has used what it received: the other CTA may send more
-        if (C::LATENT && r == 0) arrive_there(may_send_there);
+        if (C::LATENT && ok && r == 0) arrive_there(may_send_there);
         if (any) {
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
@@ -881,7 +889,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
 
   tc::fence_before_sync();
   __syncthreads();
-  if (C::CL > 1) cluster_sync_all();  // nothing more comes from, or goes to, the other CTA
+  if (C::CL > 1) {
+    // What a CTA that gave up had sent may still be on its way, and only the receiver counts it: it
+    // is given some 50 us, where it takes one.
+    if (sm.timeout != 0u) {
+      const long long t0 = clock64();
+      while (clock64() - t0 < 100000) {
+      }
+    }
+    cluster_sync_all();  // nothing more comes from, or goes to, the other CTA
+  }
   if (warp == 1) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, C::TMEM);

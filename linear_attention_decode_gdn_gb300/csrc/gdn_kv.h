@@ -73,6 +73,7 @@ struct AttnParams {
   int32_t col_groups; // ceil(cols / ncol)
   uint32_t workers;   // CTAs, or pairs of CTAs, that share the tiles
   int32_t unit_cost;  // tiles that a unit counts for beyond its own
+  int32_t starve;     // 0, or the wait that is to run out (GDN_STARVE_*)
   float scale_log2;   // scale * log2(e)
   const void* q;
   int64_t q_b, q_t, q_h;

@@ -1,5 +1,7 @@
 """Paged-cache calls at their edges: rings that hold one tile, waits that run out, padding over several
 steps, batches around the shared-memory limit, values that are no numbers among the newest positions."""
+import time
+
 import pytest
 import torch
 
@@ -30,3 +32,40 @@ def test_cold_requests_whose_last_tile_is_partial(gdn, shape):
             first = p.o.clone(), p.lse.clone()
         torch.cuda.synchronize()
         assert torch.equal(p.o, first[0]) and torch.equal(p.lse, first[1])
+
+
+# ---- waits that run out ---------------------------------------------------------------------------
+def starve(gdn, p, wait):
+    """Problem p's call with a wait that runs out; how long it took."""
+    from linear_attention_decode_gdn_gb300 import _abi, paged
+    call = lambda kv, a, *rest: _abi.load().gdn_attn_starve_wait(kv, a, wait, *rest)  # noqa: E731
+    torch.cuda.synchronize()
+    begin = time.perf_counter()
+    paged._attend(call, "gdn_attn_starve_wait", p.kv, p.q, p.table, p.kv_len, p.o, p.workspace, p.lse, p.scale, p.window, p.status, None)
+    torch.cuda.synchronize()
+    return time.perf_counter() - begin
+
+
+STARVED = [dict(dk=128, page=64, heads=8, heads_kv=1), dict(dk=128, page=16, heads=48, heads_kv=1), dict(dk=64, page=32, heads=8, heads_kv=1),
+           dict(dk=256, page=128, heads=40, heads_kv=1), dict(dk=576, dv=512, page=64, heads=16, heads_kv=1, latent=True),
+           dict(dk=576, dv=512, page=32, heads=64, heads_kv=1, latent=True)]
+
+
+@pytest.mark.parametrize("wait", [1, 2])
+@pytest.mark.parametrize("shape", STARVED, ids=name_of)
+def test_a_wait_that_runs_out_is_reported(gdn, shape, wait):
+    p = Problem(gdn, [20000, 20000], seed=15, **shape)
+    starve(gdn, p, wait)
+    assert p.status.item() == gdn.STATUS_TIMEOUT
+    p.status.zero_()
+    p.call()  # the next call finds everything as it should be
+    p.check()
+
+
+def test_the_test_switch_is_checked(gdn):
+    p = Problem(gdn, [30], dk=128, page=16)
+    with pytest.raises(gdn.GDNError):
+        starve(gdn, p, 3)
+    p = Problem(gdn, [30], dk=32, page=16)
+    with pytest.raises(gdn.GDNError):  # the kernel on the CUDA cores waits for nothing
+        starve(gdn, p, 1)
