@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
   if (warp == 0) {
     // ---- pages into the ring --------------------------------------------------------------
     uint32_t slot = 0, round = 1, tile_no = 0;  // next slot, the parity its barrier has when free
-    uint32_t put = 0;
+    uint32_t put = 0, tails_put = 0;  // loads begun
     bool bad = false, ok = true;
     // BOXES of a chunk; lane l looks up the page of box l
     auto produce = [&](auto boxes_of_a_chunk) {
@@ -411,6 +411,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
             ok = warp_waited(&sm.tail_empty[t], ((tile_no / kTails) & 1u) ^ 1u, sm);
             if (!ok) break;
             tc::expect_tx(&sm.tail_full[t], C::TAIL);
+            ++tails_put;
 #pragma unroll
             for (int b = 0; b < BOXES; ++b)
               tma_box(smem_addr(tails) + t * C::TAIL + b * BOX * (C::TCOLS * 2), &tp.v, C::DV + static_cast<int32_t>(rank) * C::TCOLS,
@@ -443,13 +444,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
       case 64: produce(std::integral_constant<int, 2>{}); break;
       default: produce(std::integral_constant<int, 1>{}); break;
     }
-    if (!ok) {  // nothing may still be on its way into this CTA's memory when it ends
-      for (uint32_t i = put > C::SLOTS ? put - C::SLOTS : 0; i < put; ++i)
-        mbar_wait(&sm.full[i % C::SLOTS], (i / C::SLOTS) & 1u);
-      if (C::LATENT)
-        for (uint32_t i = tile_no > kTails ? tile_no - kTails : 0; i < tile_no; ++i)
-          mbar_wait(&sm.tail_full[i % kTails], (i / kTails) & 1u);
-    }
+    // Nothing may still be on its way into this CTA's memory when it ends, whichever warp gave up.
+    for (uint32_t i = put > C::SLOTS ? put - C::SLOTS : 0; i < put; ++i)
+      mbar_wait(&sm.full[i % C::SLOTS], (i / C::SLOTS) & 1u);
+    if (C::LATENT)
+      for (uint32_t i = tails_put > kTails ? tails_put - kTails : 0; i < tails_put; ++i)
+        mbar_wait(&sm.tail_full[i % kTails], (i / kTails) & 1u);
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomic_status(p.status, GDN_STATUS_BAD_PAGE);
   } else if (warp == 1) {
     // ---- matrix products --------------------------------------------------------------------

@@ -69,3 +69,14 @@ def test_the_test_switch_is_checked(gdn):
     p = Problem(gdn, [30], dk=32, page=16)
     with pytest.raises(gdn.GDNError):  # the kernel on the CUDA cores waits for nothing
         starve(gdn, p, 1)
+
+
+def test_a_latent_call_that_gives_up_waits_for_its_own_loads_alone(gdn):
+    """One limit until the wait for the first weights runs out, and no other for loads that were never begun."""
+    took = []
+    for shape in (STARVED[1], STARVED[5]):
+        p = Problem(gdn, [20000, 20000], seed=16, **shape)
+        p.call()
+        took.append(min(starve(gdn, p, 2) for _ in range(2)))
+        assert p.status.item() == gdn.STATUS_TIMEOUT
+    assert took[1] < 1.4 * took[0], took
