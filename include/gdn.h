@@ -442,6 +442,8 @@ typedef struct gdn_attn {
  * pages skips the request (GDN_STATUS_BAD_LEN, rows unchanged). A page outside
  * [0, num_pages) is left out (GDN_STATUS_BAD_PAGE). What the pages hold in positions that
  * no query of the request sees has no influence, NaN included.
+ * After GDN_STATUS_TIMEOUT, elements of o and lse that were to come of the work that was given up
+ * are left as they were (of a latent row perhaps one half of o); all others are right.
  * Scores, softmax and sums are fp32; each weight is rounded to bf16 where it meets the
  * values (head sizes 64, 128 and 256 with page sizes 16, 32, 64 or a multiple of 128, on the
  * tensor cores); every other shape runs in fp32 on the CUDA cores.

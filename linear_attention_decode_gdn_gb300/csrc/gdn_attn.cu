@@ -231,7 +231,14 @@ __global__ void __launch_bounds__(kJoinThreads) gdn_attn_join_kernel(const AttnP
   for (int j = 0; j < AHEAD; ++j)
     if (mine && j < parts) ahead[j] = *reinterpret_cast<const float4*>(part(j) + at);
   float m = -INFINITY;
-  for (int j = lane; j < parts; j += 32) m = fmaxf(m, part(j)[ref]);
+  bool lost = false;
+  for (int j = lane; j < parts; j += 32) {
+    const float mj = part(j)[ref];
+    lost |= mj != mj;
+    m = fmaxf(m, mj);
+  }
+  // a worker that gave up left nothing to add: the row stays as it is, and the status tells
+  if (__any_sync(0xffffffffu, lost)) return;
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
   const float zero = m == -INFINITY ? 0.0f : m;

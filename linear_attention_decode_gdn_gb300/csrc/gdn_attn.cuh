@@ -184,6 +184,9 @@ __device__ __forceinline__ float* partial_of(const AttnParams& p, int worker, in
   return p.partials + (static_cast<size_t>(worker) * 2 + slot) * partial_floats(p);
 }
 
+// In place of the references of a worker that gave up; no column's reference is ever a NaN.
+__device__ __forceinline__ float lost_reference() { return __int_as_float(0x7fffffff); }
+
 __device__ __forceinline__ void write_record(const AttnParams& p, const Share& s, uint32_t worker) {
   uint4 r = make_uint4(0u, 0u, static_cast<uint32_t>(s.b), static_cast<uint32_t>(s.unit));
   if (s.count > 0 && worker > 0) {

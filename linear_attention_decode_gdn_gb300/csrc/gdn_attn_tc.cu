@@ -156,6 +156,10 @@ __device__ __forceinline__ void arrive(uint64_t* bar, int lane) {
   __syncwarp();
   if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
+// The same where all of the warp's threads are `ok`; a warp that gave up arrives nowhere.
+__device__ __forceinline__ void arrive_if(bool ok, uint64_t* bar, int lane) {
+  if (__all_sync(0xffffffffu, ok)) arrive(bar, lane);
+}
 // One page's box; called by a whole warp with uniform operands, one elected lane issues.
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t head, int32_t pos,
                                         int32_t page, uint64_t* bar) {
@@ -607,8 +611,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
     const uint32_t got_there = C::LATENT ? in_cta(smem_addr(&sm.got[g]), rank ^ 1u) : 0u;
     const uint32_t may_send_there = C::LATENT ? in_cta(smem_addr(&sm.may_send[g]), rank ^ 1u) : 0u;
     uint32_t i = 0, units = 0;
-    // After a wait that ran out the threads still go through every barrier together (no later
-    // wait holds them up) and write nothing more.
+    // After a wait that ran out the threads still go through the group's barriers together (no later
+    // wait holds them up), but arrive at no other and write nothing more. So what is complete, here or in
+    // the other CTA, was made of what all had waited for.
     bool ok = true;
     auto load16 = [](uint32_t at, float* s) {
       float x[16];
@@ -668,7 +673,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
 #pragma unroll
         for (int c = 0; c < NC; c += 16) load16(s_at + (i & 1u) * N + c, s + c);
         tc::fence_before_sync();
-        arrive(&sm.s_empty[i & 1u], lane);
+        arrive_if(ok, &sm.s_empty[i & 1u], lane);
         if (C::LATENT) {
           // After a wait that ran out nothing is sent, expected or freed any more: the bytes that a
           // barrier counts would get ahead of the round that the other CTA is in. Its wait for them runs
@@ -833,7 +838,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
         }
         tc::fence_smem_to_async();
         tc::fence_before_sync();
-        arrive(&sm.p_full[i % C::PB], lane);
+        arrive_if(ok, &sm.p_full[i % C::PB], lane);
       }
 
       // ---- the unit's (or the share's) end: sums over the positions, then O^T ---------------
@@ -841,6 +846,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
       group_sync(quad);  // maxima of the last raise are read
       if (NC == 32 || (lane & 1) == 0) sm.per_warp[w][a_base + lane * NC / 32] = l[0];
       group_sync(quad);
+      // Whoever of the group gave up raised the flag before its sum was exchanged above.
+      ok &= *const_cast<volatile uint32_t*>(&sm.timeout) == 0u;
       float* const part = partial_of(p, worker, seg.index == 0 ? 0 : 1);
       if (r < NC) {
         const int a = a_base + r, c = c_base + r;
@@ -903,7 +910,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, C::TMEM);
   }
-  if (tid == 0 && sm.timeout != 0u) atomic_status(p.status, GDN_STATUS_TIMEOUT);
+  if (sm.timeout != 0u) {
+    // what this worker leaves to be joined is not all there: the join writes no row of it
+    for (int c = tid; c < 2 * N; c += C::THREADS) partial_of(p, worker, c / N)[N * C::DV + c % N] = lost_reference();
+    if (tid == 0) atomic_status(p.status, GDN_STATUS_TIMEOUT);
+  }
 }
 
 template <class C>

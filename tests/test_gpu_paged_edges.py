@@ -80,3 +80,36 @@ def test_a_latent_call_that_gives_up_waits_for_its_own_loads_alone(gdn):
         took.append(min(starve(gdn, p, 2) for _ in range(2)))
         assert p.status.item() == gdn.STATUS_TIMEOUT
     assert took[1] < 1.4 * took[0], took
+
+
+@pytest.mark.parametrize("wait", [1, 2])
+@pytest.mark.parametrize("shape", STARVED, ids=name_of)
+def test_what_is_given_up_is_not_written(gdn, shape, wait):
+    """The first worker's share begins the first request, cut over several workers: its rows stay as they
+    were, whatever the workspace held before, and those of the other requests are right."""
+    p = Problem(gdn, [20000, 3000, 9000, 0, 15000], seed=17, **shape)
+    q = Problem(gdn, [20000, 3000, 9000, 0, 15000], seed=18, **shape)
+    q.workspace = p.workspace
+    q.call()  # another call's sums are in the workspace
+    starve(gdn, p, wait)
+    assert p.status.item() == gdn.STATUS_TIMEOUT
+    assert bool((p.o[0] == 7).all()) and bool((p.lse[0] == 7).all())
+    want = p.o.clone(), p.lse.clone()
+    p.status.zero_()
+    p.call()
+    p.check()
+    assert torch.equal(p.o[1:], want[0][1:]) and torch.equal(p.lse[1:], want[1][1:])
+
+
+@pytest.mark.parametrize("shape", [dict(dk=128, page=64, heads=8, heads_kv=2), dict(dk=64, page=16, heads=8, heads_kv=4, T=4),
+                                   dict(dk=576, dv=512, page=64, heads=32, heads_kv=1, latent=True)], ids=name_of)
+def test_rows_are_right_or_untouched_after_a_wait_ran_out(gdn, shape):
+    """Short requests, many of them to a worker: each element is the one of an undisturbed call or is not written."""
+    p = Problem(gdn, [3, 200, 129, 700] * 60, seed=19, **shape)
+    starve(gdn, p, 1)
+    assert p.status.item() == gdn.STATUS_TIMEOUT
+    o, lse = p.o.clone(), p.lse.clone()
+    p.call()
+    torch.cuda.synchronize()
+    assert bool(((o == p.o) | (o == 7)).all()) and bool(((lse == p.lse) | (lse == 7)).all())
+    assert bool((o[:1] == 7).all()) and bool((o[-1] == p.o[-1]).all())
