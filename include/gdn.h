@@ -464,8 +464,8 @@ int gdn_latent_decode(const gdn_paged_kv *kv, const gdn_attn *attn, void *worksp
 
 /*
  * gdn_attn_starve_wait -- test only: gdn_attn_decode, or gdn_latent_decode for a latent cache, in which
- * one wait of the tensor-core kernel's first CTA is for an arrival that never comes, so that it runs
- * out (about a second) and the call reports GDN_STATUS_TIMEOUT; exercises the timeout path
+ * one wait of the tensor-core kernel's first two workers is for an arrival that never comes, so that
+ * it runs out (about a second) and the call reports GDN_STATUS_TIMEOUT; exercises the timeout path
  * without any fault. wait: GDN_STARVE_LOAD, the first page box; GDN_STARVE_WEIGHTS, the first
  * tile's weights. GDN_ERR_UNSUPPORTED where the call would run on the CUDA cores.
  */

@@ -316,8 +316,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
 
   griddep_launch_dependents();
   if (tid == 0) {
-    // for tests, the first barrier of the first CTA counts on an arrival that never comes
-    const bool starve_load = p.starve == GDN_STARVE_LOAD && blockIdx.x == 0, starve_weights = p.starve == GDN_STARVE_WEIGHTS && blockIdx.x == 0;
+    // For tests, a barrier of the first two workers counts on an arrival that never comes (the first
+    // one's share may end before its unit's first tile).
+    const int32_t starve = worker < 2 && rank == 0 ? p.starve : 0;
+    const bool starve_load = starve == GDN_STARVE_LOAD, starve_weights = starve == GDN_STARVE_WEIGHTS;
     for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(&sm.full[i], i == 0 && starve_load ? 2 : 1);
       mbar_init(&sm.empty[i], 1);
