@@ -344,7 +344,8 @@ namespace {
 template <int THREADS>
 cudaError_t launch_plan(const KvPlanParams& p, unsigned ctas, cudaStream_t stream) {
   const size_t smem = (5u * p.B + 1u) * sizeof(int32_t);
-  if (smem > 48 * 1024) {
+  // static shared memory, up to 300 bytes of it here, counts towards the 48 KB too
+  if (smem > 47 * 1024) {
     static std::atomic<bool> allowed[kDevices];
     const cudaError_t err = allow_shared(reinterpret_cast<const void*>(gdn_kv_plan_kernel<THREADS>),
                                          (5 * kMaxPlanBatch + 1) * static_cast<int>(sizeof(int32_t)), allowed);

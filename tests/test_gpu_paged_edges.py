@@ -113,3 +113,35 @@ def test_rows_are_right_or_untouched_after_a_wait_ran_out(gdn, shape):
     torch.cuda.synchronize()
     assert bool(((o == p.o) | (o == 7)).all()) and bool(((lse == p.lse) | (lse == 7)).all())
     assert bool((o[:1] == 7).all()) and bool((o[-1] == p.o[-1]).all())
+
+
+# ---- the plan -------------------------------------------------------------------------------------
+PLANS = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import linear_attention_decode_gdn_gb300 as gdn
+from test_gpu_paged import plan_reference, run_plan
+for batch in (2030, 2036, 2037, 2038, 2042, 2045, 2047, 2048, 2444, 2445, 2450, 2454, 2455, 2457, 2458, 4096):
+    cached = [b % 40 for b in range(batch)]
+    held = [-(-c // 16) for c in cached]
+    table, ids = [[-1] * 3 for _ in cached], list(range(4 * batch))
+    for b, h in enumerate(held):
+        table[b][:h] = [ids.pop() for _ in range(h)]
+    args = (cached, None, held, table, ids, len(ids), 16, 4 * batch, batch)
+    want, bad = plan_reference(*args)
+    got, st = run_plan(gdn, *args, in_place={in_place})
+    assert got == want and st == bad == 0, batch
+print("planned")
+"""
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_batches_around_the_shared_memory_limit(in_place):
+    """Rising batches in a process of its own, so that no larger one has raised the kernel's limit before."""
+    import os
+    import subprocess
+    import sys
+    tests = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", PLANS.format(root=os.path.dirname(tests), tests=tests, in_place=in_place)],
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "planned" in r.stdout, r.stderr[-2000:]
