@@ -369,8 +369,11 @@ typedef struct gdn_paged_kv {
 /*
  * gdn_kv_plan -- pages and slots for the new tokens of a step, in request order.
  *   cached_len [B]: positions that request b holds before the step; < 0: padding (no tokens,
- *       kv_len 0, pages untouched). A length that shrank since the last step (rejected
- *       drafts) keeps its pages.
+ *       pages untouched). Below -1 (GDN_LEN_PADDING) its kv_len is cached_len, so the row stays
+ *       padding where kv_len is the cached_len array, step after step, and the attention calls
+ *       leave its output rows unchanged. -1 pads one step: kv_len 0, which is an empty request
+ *       (attention gives o = 0), a live one from the next step on where the arrays are one. A
+ *       length that shrank since the last step (rejected drafts) keeps its pages.
  *   new_len [B]: new tokens of each request, or NULL (one each).
  *   held [B]: pages in each request's row; held_out receives the count after the step.
  *   block_table [B][max_pages]: entries held[b] .. held_out[b] - 1 are written.
@@ -378,7 +381,7 @@ typedef struct gdn_paged_kv {
  *       pages, handed out from the end; *free_count_out is what is left. The list itself is
  *       only read. A count outside [0, free_capacity] sets GDN_STATUS_BAD_LEN and is left as
  *       it is; no page is handed out.
- *   kv_len [B]: cached_len + new_len. cu_new [B + 1]: running sums of new_len (where each
+ *   kv_len [B]: cached_len + new_len (padding: see there). cu_new [B + 1]: running sums of new_len (where each
  *       request's tokens start among the packed new tokens; a sum past 2^31 - 1 stays there).
  *   slot_map [slot_capacity] int64: token cu_new[b] + i gets the slot page * page_size +
  *       offset of position cached_len[b] + i; entries past the last token get -1.
@@ -389,6 +392,7 @@ typedef struct gdn_paged_kv {
  * entry outside [0, num_pages) (GDN_STATUS_BAD_PAGE) gives its positions the slot -1.
  * Requires batch <= 4096.
  */
+#define GDN_LEN_PADDING (-2)
 int gdn_kv_plan(int32_t batch, int32_t max_pages, int32_t page_size, int32_t num_pages, int32_t free_capacity,
                 int32_t slot_capacity, const int32_t *cached_len, const int32_t *new_len, const int32_t *held, int32_t *block_table,
                 const int32_t *free_list, const int32_t *free_count, int32_t *kv_len, int32_t *cu_new,

@@ -28,6 +28,9 @@ STATUS_TIMEOUT = 0x8
 STATUS_NO_PAGES = 0x10
 STATUS_BAD_PAGE = 0x20
 
+# cached_len of gdn_kv_plan: a row that stays padding
+LEN_PADDING = -2
+
 # flags
 QKV_BF16 = 1 << 0
 FUSE_CONV = 1 << 1

@@ -72,9 +72,10 @@ __global__ void __launch_bounds__(THREADS) gdn_kv_plan_kernel(const KvPlanParams
   __shared__ int32_t handed;            // free pages handed out
   int32_t* cu = sm;                     // [B + 1] tokens before request b
   int32_t* fresh_cu = cu + p.B + 1;     // [B] pages handed out before request b
-  int32_t* start = fresh_cu + p.B;      // [B] cached length c; ~c for a request without slots
+  int32_t* start = fresh_cu + p.B;      // [B] cached length; -1 for a request without slots
   int32_t* held = start + p.B;          // [B] pages the request had
   int32_t* held_new = held + p.B;       // [B] and has now
+  int32_t* len_new = held_new + p.B;    // [B] kv_len
   const int tid = threadIdx.x;
   griddep_launch_dependents();
   griddep_wait();
@@ -130,7 +131,8 @@ __global__ void __launch_bounds__(THREADS) gdn_kv_plan_kernel(const KvPlanParams
       cu[b] = static_cast<int32_t>(min(upto - n, kTop));
       if (b == p.B - 1) cu[p.B] = static_cast<int32_t>(min(upto, kTop));
       fresh_cu[b] = static_cast<int32_t>(min(pages_upto - want, kTop));
-      start[b] = skip ? ~max(c, 0) : c;
+      start[b] = skip ? -1 : c;
+      len_new[b] = !skip ? c + n : c == -1 ? 0 : c;
       held[b] = h;
       held_new[b] = fits ? h + static_cast<int32_t>(want) : h;
     }
@@ -146,8 +148,7 @@ __global__ void __launch_bounds__(THREADS) gdn_kv_plan_kernel(const KvPlanParams
       p.free_count_out[0] = given != avail ? given : avail - handed;
       break;
     }
-    const int32_t c = start[b];
-    p.kv_len[b] = c < 0 ? ~c : c + (cu[b + 1] - cu[b]);
+    p.kv_len[b] = len_new[b];
     p.held_out[b] = held_new[b];
   }
   uint32_t bad_page = 0;
@@ -343,12 +344,12 @@ namespace {
 
 template <int THREADS>
 cudaError_t launch_plan(const KvPlanParams& p, unsigned ctas, cudaStream_t stream) {
-  const size_t smem = (5u * p.B + 1u) * sizeof(int32_t);
+  const size_t smem = (6u * p.B + 1u) * sizeof(int32_t);
   // static shared memory, up to 300 bytes of it here, counts towards the 48 KB too
   if (smem > 47 * 1024) {
     static std::atomic<bool> allowed[kDevices];
     const cudaError_t err = allow_shared(reinterpret_cast<const void*>(gdn_kv_plan_kernel<THREADS>),
-                                         (5 * kMaxPlanBatch + 1) * static_cast<int>(sizeof(int32_t)), allowed);
+                                         (6 * kMaxPlanBatch + 1) * static_cast<int>(sizeof(int32_t)), allowed);
     if (err != cudaSuccess) return err;
   }
   return launch_overlapped(gdn_kv_plan_kernel<THREADS>, p, ctas, THREADS, smem, p.in_place ? ctas : 1u, stream);

@@ -84,8 +84,9 @@ def make_paged_kv(k, v=None, dv=None) -> PagedKV:
 def kv_plan(cached_len, new_len, held, block_table, free_list, free_count, *, kv_len, cu_new, slot_map, held_out,
             free_count_out, page_size: int, num_pages: int, status=None, stream=None):
     """Pages and slots for the new tokens of a step, from the requests' lengths (new_len None: one
-    token each). Writes block_table, kv_len, cu_new, slot_map, held_out and free_count_out; the
-    last three of kv_len / held_out / free_count_out may be the input arrays themselves."""
+    token each). Writes block_table, kv_len, cu_new, slot_map, held_out and free_count_out; kv_len,
+    held_out and free_count_out may be cached_len, held and free_count themselves. A cached length of
+    LEN_PADDING marks a row that takes no part and stays so; -1 does for one step only."""
     batch, capacity, free = cached_len.numel(), slot_map.numel(), free_list.numel()
     cached = _ints(cached_len, batch, "cached_len")
     check(_abi.load().gdn_kv_plan(

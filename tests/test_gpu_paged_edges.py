@@ -145,3 +145,59 @@ def test_batches_around_the_shared_memory_limit(in_place):
     r = subprocess.run([sys.executable, "-c", PLANS.format(root=os.path.dirname(tests), tests=tests, in_place=in_place)],
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "planned" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("batch", [6, 1500])
+@pytest.mark.parametrize("graph", [False, True])
+def test_padding_lasts_over_steps_in_place(gdn, batch, graph):
+    """Steps with kv_len, held_out and free_count_out in their inputs' arrays: rows retired with LEN_PADDING
+    take no page and no slot in any of them, the live rows' slots close up, and attention leaves the retired
+    rows of its output as they are. What -1 pads is an empty request after one step."""
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    page, width, heads, dk = 16, 4, 4, 64
+    start = [gdn.LEN_PADDING if b % 3 == 1 else -77 if b % 3 == 2 and b % 2 else 14 + b % 5 for b in range(batch)]
+    length, held = ints(start), ints([1 if n < 0 else -(-n // page) for n in start])
+    pages = 3 * batch + 5
+    table = [[-1] * width for _ in range(batch)]
+    ids = list(range(pages))
+    for b, h in enumerate(held.tolist()):
+        table[b][:h] = [ids.pop() for _ in range(h)]
+    free, count, cu = ints(ids), ints([len(ids)]), ints([0] * (batch + 1))
+    table, slots, status = ints(table), torch.zeros(batch, dtype=torch.int64, device="cuda"), ints([0])
+    k, v = (torch.randn(pages, page, 2, dk, device="cuda").bfloat16() for _ in range(2))
+    kv = gdn.make_paged_kv(k, v)
+    q = torch.randn(batch, 1, heads, dk, device="cuda").bfloat16()
+    o = torch.full((batch, 1, heads, dk), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(gdn.attn_workspace_bytes(kv, batch, 1, heads), dtype=torch.uint8, device="cuda")
+
+    def step():
+        gdn.kv_plan(length, None, held, table, free, count, kv_len=length, cu_new=cu, slot_map=slots, held_out=held,
+                    free_count_out=count, page_size=page, num_pages=pages, status=status)
+        gdn.attn_decode(kv, q, table, length, o, ws, status=status)
+
+    run = step
+    if graph:
+        captured = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(captured):
+            step()
+        run = captured.replay
+    live = [b for b, n in enumerate(start) if n >= 0]
+    for i in range(1, 5):
+        run()
+        torch.cuda.synchronize()
+        assert status.item() == 0
+        assert length.tolist() == [n + i if n >= 0 else n for n in start]
+        want = [-(-(n + i) // page) if n >= 0 else 1 for n in start]
+        assert held.tolist() == want and count.item() == pages - sum(want)
+        sums = [0]
+        for n in start:
+            sums.append(sums[-1] + (n >= 0))
+        assert cu.tolist() == sums
+        rows = table.tolist()
+        at = [rows[b][(start[b] + i - 1) // page] * page + (start[b] + i - 1) % page for b in live]
+        assert slots.tolist() == at + [-1] * (batch - len(live)) and len(set(at)) == len(at)
+        retired = torch.tensor([n < 0 for n in start], device="cuda")
+        assert bool((o[retired] == 7).all()) and not bool((o[~retired] == 7).flatten(1).all(1).any())
+    length[1] = -1
+    run()
+    assert length[1].item() == 0
