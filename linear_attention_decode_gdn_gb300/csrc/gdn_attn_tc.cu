@@ -297,6 +297,72 @@ __device__ __forceinline__ bool warp_waited(uint64_t* bar, uint32_t parity, Misc
   return __all_sync(0xffffffffu, waited(bar, parity, sm));
 }
 
+// A segment's sums of w v for the `left` columns of a softmax group from c_base on, and the value elements
+// d, d + 128, .. of each lane, on the CUDA cores: a weight of zero leaves a value out, whatever it holds,
+// where a product on the tensor cores makes a NaN of it. refs and lasts: the group's references and last
+// positions. Called by a whole warp, and only where a sum came out as no number; a lane scores one
+// position of 32, then all sum them.
+template <class C>
+__device__ __noinline__ void sums_of_seen(const AttnParams& p, const Segment& seg, const float* refs, const int32_t* lasts, int c_base,
+                                          int left, int d, float (&sums)[C::MB][16]) {
+  const int lane = threadIdx.x & 31;
+  const int32_t lower = lower_bound_of(p, seg.n, seg.col_base / p.group);
+  const int32_t end = min((seg.tile + seg.tiles) * kTile, seg.n);
+  const int32_t* const row = p.table + static_cast<int64_t>(seg.b) * p.max_pages;
+  const uint16_t* const k_at = static_cast<const uint16_t*>(p.k) + seg.kv_head * p.k_head;
+  const uint16_t* const v_at = static_cast<const uint16_t*>(p.v) + seg.kv_head * p.v_head + d;
+  float w[16];
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    w[c] = 0.0f;
+#pragma unroll
+    for (int b = 0; b < C::MB; ++b) sums[b][c] = 0.0f;
+  }
+  for (int32_t base = max(seg.tile * kTile, lower & ~31); base < end; base += 32) {
+    const int32_t pos = base + lane;
+    int32_t page = -1, in = 0;
+    if (pos < end && pos >= lower) {
+      page = row[pos / p.page_size];
+      in = pos % p.page_size;
+      if (page >= p.num_pages) page = -1;
+    }
+    const uint16_t* const k = k_at + page * p.k_page + in * p.k_pos;
+#pragma unroll 1
+    for (int c = 0; c < left; ++c) {
+      const int col = seg.col_base + c_base + c, t = col / p.group, h = seg.kv_head * p.group + (col - t * p.group);
+      const uint16_t* const q = static_cast<const uint16_t*>(p.q) + seg.b * p.q_b + t * p.q_t + h * p.q_h;
+      const bool seen = page >= 0 && pos <= lasts[c] && (p.window <= 0 || pos > lasts[c] - p.window);
+      float s = 0.0f;
+      for (int e = 0; seen && e < C::DK; e += 8) {
+        const uint4 x = *reinterpret_cast<const uint4*>(k + e), y = *reinterpret_cast<const uint4*>(q + e);
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s = fmaf(__uint_as_float(xs[j] << 16), __uint_as_float(ys[j] << 16), s);
+          s = fmaf(__uint_as_float(xs[j] & 0xffff0000u), __uint_as_float(ys[j] & 0xffff0000u), s);
+        }
+      }
+      w[c] = seen ? ex2(s * p.scale_log2 - refs[c]) : 0.0f;
+    }
+#pragma unroll 1
+    for (int j = 0; j < 32; ++j) {
+      const int32_t page_j = __shfl_sync(0xffffffffu, page, j), in_j = __shfl_sync(0xffffffffu, in, j);
+      if (page_j < 0) continue;
+      const uint16_t* const v = v_at + page_j * p.v_page + in_j * p.v_pos;
+      float x[C::MB];
+#pragma unroll
+      for (int b = 0; b < C::MB; ++b) x[b] = __uint_as_float(static_cast<uint32_t>(v[b * 128]) << 16);
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const float wj = __shfl_sync(0xffffffffu, w[c], j);
+        if (wj == 0.0f) continue;
+#pragma unroll
+        for (int b = 0; b < C::MB; ++b) sums[b][c] = fmaf(wj, x[b], sums[b][c]);
+      }
+    }
+  }
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid_constant__ TcParams tp) {
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -868,6 +934,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
       ok &= waited(&sm.unit_done[units & 1u], (units >> 1) & 1u, sm);
       __syncwarp();
       tc::fence_after_sync();
+      float again[C::MB][16];
+      bool have = false;
 #pragma unroll 1
       for (int block = 0; block < C::MB; ++block) {
         const int d = static_cast<int>(rank) * C::VCOLS + (C::DV >= 128 ? block * 128 + r : r - 64);
@@ -876,6 +944,22 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
           float x[16];
           tc::ld16(o_at + block * N + c0, x);
           const int left = cols - (c_base + c0);  // columns that are rows of o
+          // Among several positions a value that only some see meets the others' weights of zero: where it
+          // is no number, neither are their sums. (With one, what is not seen was zeroed above.)
+          if (p.T > 1) {
+            bool number = true;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) number &= j >= left || fabsf(x[j]) <= 3.4028235e38f;
+            if (__any_sync(0xffffffffu, ok && d >= 0 && !number)) {
+              if (!have) {
+                const Segment here = seg;  // a copy: what a call takes by address has no registers
+                sums_of_seen<C>(p, here, sm.m + a_base, sm.last + a_base, c_base, min(left, 16), d - block * 128, again);
+              }
+              have = true;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) x[j] = again[block][j];
+            }
+          }
           if (ok && d >= 0 && seg.whole) {
             __nv_bfloat16* const o = static_cast<__nv_bfloat16*>(p.o) + d;
 #pragma unroll

@@ -201,3 +201,48 @@ def test_padding_lasts_over_steps_in_place(gdn, batch, graph):
     length[1] = -1
     run()
     assert length[1].item() == 0
+
+
+# ---- values that are no numbers -------------------------------------------------------------------
+@pytest.mark.parametrize("lens", [[1, 5, 128, 131, 700, 40], [9000, 260]], ids=lambda x: f"{len(x)}x{max(x)}")
+@pytest.mark.parametrize("T,window", [(4, 0), (3, 130), (5, 2)])
+@pytest.mark.parametrize("shape", [dict(dk=32, page=6, heads=4, heads_kv=2), dict(dk=64, page=16, heads=8, heads_kv=2),
+                                   dict(dk=64, page=32, heads=20, heads_kv=1), dict(dk=128, page=64, heads=4, heads_kv=2),
+                                   dict(dk=128, page=128, heads=32, heads_kv=2), dict(dk=256, page=32, heads=4, heads_kv=4),
+                                   dict(dk=256, page=64, heads=24, heads_kv=2),
+                                   dict(dk=576, dv=512, page=64, heads=4, heads_kv=1, latent=True),
+                                   dict(dk=576, dv=512, page=32, heads=20, heads_kv=1, latent=True)], ids=name_of)
+def test_values_that_only_some_positions_see(gdn, shape, T, window, lens):
+    """The newest position's value holds NaN and infinities (of a latent row: the key too), and so does the oldest
+    one that the first query sees through its window. Queries that do not see them give what they give without."""
+    p = Problem(gdn, lens, T=T, window=window, seed=20, **shape)
+    bad = torch.tensor([float("nan"), float("inf"), float("-inf")], device="cuda").bfloat16()
+    rows = p.k if p.latent else p.v
+    first = {}  # by request: the oldest position, and the newest
+    for b, n in enumerate(lens):
+        spoiled = {n - 1}
+        if window and n - T - window + 1 >= 0:
+            spoiled.add(n - T - window + 1)
+        for j in spoiled:
+            rows[p.own_pages[b][j // p.page], j % p.page, :, 3::7] = bad[torch.arange(len(range(3, rows.shape[3], 7)), device="cuda") % 3]
+        first[b] = sorted(spoiled)
+    p.call()
+    torch.cuda.synchronize()
+    assert p.status.item() == 0
+    for b, n in enumerate(lens):
+        o, lse, to, tl = p.expected(b)
+        got, got_lse = p.o[b].double(), p.lse[b].double()
+        for t in range(T):
+            pos = n - T + t
+            sees = [j for j in first[b] if j <= pos and (not window or j > pos - window)]
+            if not sees:
+                assert bool(((got[t] - o[t]).abs() <= to[t]).all()), (b, n, t)
+                assert bool(((got_lse[t] == lse[t]) | ((got_lse[t] - lse[t]).abs() <= tl[t])).all()), (b, n, t)
+            elif p.latent:
+                assert bool(torch.isnan(got[t]).all()), (b, n, t)
+            else:
+                whole = torch.ones(p.dv, dtype=torch.bool, device="cuda")
+                whole[3::7] = False
+                assert bool(((got[t] - o[t]).abs() <= to[t])[:, whole].all()), (b, n, t)
+                assert not bool(torch.isfinite(got[t][:, ~whole]).any()), (b, n, t)
+                assert torch.equal(torch.isnan(got[t]), torch.isnan(o[t])) and torch.equal(got[t] == float("inf"), o[t] == float("inf"))
