@@ -78,7 +78,7 @@ struct Cfg {
   static constexpr int VS = LATENT ? 0 : VCOLS / 64 / SLOTC;
   static constexpr int PER = KS + VS;
   static constexpr int MB = VCOLS > 128 ? VCOLS / 128 : 1; // blocks of 128 rows of O^T
-  static constexpr int NC = 16, G = N / NC;                // columns of a softmax group, groups
+  static constexpr int NC = 16, G = N / NC;                // columns of a softmax group (one load of TMEM), groups
   // Two softmax teams take turns at units, each with its own O^T: one ends a unit while the other
   // begins the next. Wider blocks have their threads in column groups, latent units are long.
   static constexpr int TEAMS = !LATENT && G == 1 ? 2 : 1;
@@ -227,12 +227,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-// Sums of N (16 or 32) columns over the warp's lanes: afterwards a lane holds the sum of column
-// lane * N / 32.
-template <int N>
-__device__ __forceinline__ void column_sums(float (&v)[N], int lane) {
+// Sums of 16 columns over the warp's lanes: afterwards a lane holds the sum of column lane / 2.
+__device__ __forceinline__ void column_sums(float (&v)[16], int lane) {
 #pragma unroll
-  for (int half = N / 2, off = 16; half > 0; half >>= 1, off >>= 1) {
+  for (int half = 8, off = 16; half > 0; half >>= 1, off >>= 1) {
     const bool upper = (lane & off) != 0;
 #pragma unroll
     for (int j = 0; j < half; ++j) {
@@ -240,7 +238,7 @@ __device__ __forceinline__ void column_sums(float (&v)[N], int lane) {
       v[j] = keep + __shfl_xor_sync(0xffffffffu, send, off);
     }
   }
-  if (N == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+  v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
 // mbar_try_wait that also sees what another CTA of the cluster has written
@@ -683,12 +681,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
     // wait holds them up), but arrive at no other and write nothing more. So what is complete, here or in
     // the other CTA, was made of what all had waited for.
     bool ok = true;
-    auto load16 = [](uint32_t at, float* s) {
-      float x[16];
-      tc::ld16(at, x);
-#pragma unroll
-      for (int j = 0; j < 16; ++j) s[j] = x[j];
-    };
     for (; walk.next(p, &seg); ++units) {
       if (C::TEAMS > 1 && (units & 1u) != team) {
         i += seg.tiles;
@@ -738,8 +730,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
         ok &= waited(&sm.s_full[i & 1u], (i >> 1) & 1u, sm);
         __syncwarp();
         tc::fence_after_sync();
-#pragma unroll
-        for (int c = 0; c < NC; c += 16) load16(s_at + (i & 1u) * N + c, s + c);
+        tc::ld16(s_at + (i & 1u) * N, s);
         tc::fence_before_sync();
         arrive_if(ok, &sm.s_empty[i & 1u], lane);
         if (C::LATENT) {
@@ -796,54 +787,51 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
             __syncwarp();
             tc::fence_after_sync();
           }
+          float f[NC];
+          if constexpr (kKeep) {
 #pragma unroll
-          for (int c0 = 0; c0 < NC; c0 += 16) {
-            float f[16];
-            if constexpr (kKeep) {
+            for (int j = 0; j < NC; j += 4) {
+              const int a = a_base + j;
+              float top[4], x[4];
+              auto load = [](float (&to)[4], const float* from) {
+                const float4 v = *reinterpret_cast<const float4*>(from);
+                to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
+              };
+              load(top, &sm.per_warp[0][a]);
 #pragma unroll
-              for (int j = 0; j < 16; j += 4) {
-                const int c = c0 + j, a = a_base + c;
-                float top[4], x[4];
-                auto load = [](float (&to)[4], const float* from) {
-                  const float4 v = *reinterpret_cast<const float4*>(from);
-                  to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
-                };
-                load(top, &sm.per_warp[0][a]);
+              for (int v = 1; v < 4; ++v) {
+                load(x, &sm.per_warp[v][a]);
 #pragma unroll
-                for (int v = 1; v < 4; ++v) {
-                  load(x, &sm.per_warp[v][a]);
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], x[k]);
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const float to = top[k] > kept[c + k] ? top[k] + kHeadroom : kept[c + k];
-                  f[j + k] = ex2(kept[c + k] - to);
-                  l[c + k] *= f[j + k];
-                  kept[c + k] = to;
-                  if (r == c + k) sm.m[a + k] = to;
-                }
+                for (int k = 0; k < 4; ++k) top[k] = fmaxf(top[k], x[k]);
               }
-            } else {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const int c = c0 + j, a = a_base + c;
-                const float top = fmaxf(fmaxf(sm.per_warp[0][a], sm.per_warp[1][a]), fmaxf(sm.per_warp[2][a], sm.per_warp[3][a]));
-                const float m = sm.m[a];
-                const float to = top > m ? top + kHeadroom : m;
-                f[j] = ex2(m - to);
-                l[c] *= f[j];
+              for (int k = 0; k < 4; ++k) {
+                const float to = top[k] > kept[j + k] ? top[k] + kHeadroom : kept[j + k];
+                f[j + k] = ex2(kept[j + k] - to);
+                l[j + k] *= f[j + k];
+                kept[j + k] = to;
+                if (r == j + k) sm.m[a + k] = to;
               }
             }
-            if (t > 0) {
-#pragma unroll 1
-              for (int block = 0; block < C::MB; ++block) {
-                float x[16];
-                tc::ld16(o_at + block * N + c0, x);
+          } else {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] *= f[j];
-                tc::st16(o_at + block * N + c0, x);
-              }
+            for (int j = 0; j < NC; ++j) {
+              const int a = a_base + j;
+              const float top = fmaxf(fmaxf(sm.per_warp[0][a], sm.per_warp[1][a]), fmaxf(sm.per_warp[2][a], sm.per_warp[3][a]));
+              const float m = sm.m[a];
+              const float to = top > m ? top + kHeadroom : m;
+              f[j] = ex2(m - to);
+              l[j] *= f[j];
+            }
+          }
+          if (t > 0) {
+#pragma unroll 1
+            for (int block = 0; block < C::MB; ++block) {
+              float x[NC];
+              tc::ld16(o_at + block * N, x);
+#pragma unroll
+              for (int j = 0; j < NC; ++j) x[j] *= f[j];
+              tc::st16(o_at + block * N, x);
             }
           }
           if (t > 0) {
@@ -912,7 +900,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
       // ---- the unit's (or the share's) end: sums over the positions, then O^T ---------------
       column_sums(l, lane);
       group_sync(quad);  // maxima of the last raise are read
-      if (NC == 32 || (lane & 1) == 0) sm.per_warp[w][a_base + lane * NC / 32] = l[0];
+      if ((lane & 1) == 0) sm.per_warp[w][a_base + lane / 2] = l[0];
       group_sync(quad);
       // Whoever of the group gave up raised the flag before its sum was exchanged above.
       ok &= *const_cast<volatile uint32_t*>(&sm.timeout) == 0u;
@@ -934,47 +922,44 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
       ok &= waited(&sm.unit_done[units & 1u], (units >> 1) & 1u, sm);
       __syncwarp();
       tc::fence_after_sync();
-      float again[C::MB][16];
+      const int left = cols - c_base;  // columns that are rows of o
+      float again[C::MB][NC];
       bool have = false;
 #pragma unroll 1
       for (int block = 0; block < C::MB; ++block) {
         const int d = static_cast<int>(rank) * C::VCOLS + (C::DV >= 128 ? block * 128 + r : r - 64);
-#pragma unroll 1
-        for (int c0 = 0; c0 < NC; c0 += 16) {
-          float x[16];
-          tc::ld16(o_at + block * N + c0, x);
-          const int left = cols - (c_base + c0);  // columns that are rows of o
-          // Among several positions a value that only some see meets the others' weights of zero: where it
-          // is no number, neither are their sums. (With one, what is not seen was zeroed above.)
-          if (p.T > 1) {
-            bool number = true;
+        float x[NC];
+        tc::ld16(o_at + block * N, x);
+        // Among several positions a value that only some see meets the others' weights of zero: where it
+        // is no number, neither are their sums. (With one, what is not seen was zeroed above.)
+        if (p.T > 1) {
+          bool number = true;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) number &= j >= left || fabsf(x[j]) <= 3.4028235e38f;
-            if (__any_sync(0xffffffffu, ok && d >= 0 && !number)) {
-              if (!have) {
-                const Segment here = seg;  // a copy: what a call takes by address has no registers
-                sums_of_seen<C>(p, here, sm.m + a_base, sm.last + a_base, c_base, min(left, 16), d - block * 128, again);
-              }
-              have = true;
-#pragma unroll
-              for (int j = 0; j < 16; ++j) x[j] = again[block][j];
+          for (int j = 0; j < NC; ++j) number &= j >= left || fabsf(x[j]) <= 3.4028235e38f;
+          if (__any_sync(0xffffffffu, ok && d >= 0 && !number)) {
+            if (!have) {
+              const Segment here = seg;  // a copy: what a call takes by address has no registers
+              sums_of_seen<C>(p, here, sm.m + a_base, sm.last + a_base, c_base, min(left, NC), d - block * 128, again);
             }
-          }
-          if (ok && d >= 0 && seg.whole) {
-            __nv_bfloat16* const o = static_cast<__nv_bfloat16*>(p.o) + d;
+            have = true;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int a = a_base + c0 + j;
-              if (j < left) o[static_cast<int64_t>(sm.rows[a]) * C::DV] = __float2bfloat16_rn(x[j] * sm.inv[a]);
-            }
-          } else if (ok && d >= 0) {
-            float* const to = part + (c_base + c0) * C::DV + d;
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (j < left) to[j * C::DV] = x[j];
+            for (int j = 0; j < NC; ++j) x[j] = again[block][j];
           }
-          __syncwarp();
         }
+        if (ok && d >= 0 && seg.whole) {
+          __nv_bfloat16* const o = static_cast<__nv_bfloat16*>(p.o) + d;
+#pragma unroll
+          for (int j = 0; j < NC; ++j) {
+            const int a = a_base + j;
+            if (j < left) o[static_cast<int64_t>(sm.rows[a]) * C::DV] = __float2bfloat16_rn(x[j] * sm.inv[a]);
+          }
+        } else if (ok && d >= 0) {
+          float* const to = part + c_base * C::DV + d;
+#pragma unroll
+          for (int j = 0; j < NC; ++j)
+            if (j < left) to[j * C::DV] = x[j];
+        }
+        __syncwarp();
       }
       tc::fence_before_sync();  // read before the next unit's products write it (p_full)
     }
