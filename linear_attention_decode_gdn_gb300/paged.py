@@ -2,8 +2,9 @@
 
 As in ``decode``: each function checks what the pointers cannot show (types, shapes,
 strides, devices), gathers them, and calls the matching ``gdn_*`` function of libgdn on the
-current stream. Where a tensor is wrong the call raises ``ValueError`` before anything is
-launched; what libgdn refuses raises ``GDNError``.
+current stream. All tensors of a call live on the current device, on which libgdn launches. Where
+a tensor is wrong the call raises ``ValueError`` before anything is launched; what libgdn refuses
+raises ``GDNError``.
 """
 from __future__ import annotations
 
@@ -21,41 +22,55 @@ _pack_kv = struct.Struct("=QQ6q5i4x").pack       # gdn_paged_kv
 _pack_attn = struct.Struct("=5if4q4Q").pack      # gdn_attn
 _pack_strides = struct.Struct("=2q").pack
 _BF16, _FP32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # absent where torch has no CUDA
-
+# absent where torch has no CUDA
+_raw_stream, _current_device = (getattr(torch._C, name, None) for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
 
 
 class PagedKV:
     """The cache of one layer, as make_paged_kv() describes it to the calls; it keeps its pages alive."""
 
-    __slots__ = ("packed", "dk", "dv", "heads", "latent", "k", "v")
+    __slots__ = ("packed", "dk", "dv", "heads", "latent", "device", "k", "v")
 
     def __init__(self, packed, dk, dv, heads, latent, k, v):
         self.packed, self.dk, self.dv, self.heads, self.latent, self.k, self.v = packed, dk, dv, heads, latent, k, v
+        self.device = k.get_device()
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _here(device: int, what: str) -> int:
+    """The device of a call's tensors (get_device() is -1 on the host), which is the current one."""
+    if device < 0:
+        raise ValueError(f"{what}: on the GPU")
+    if device != _current_device():
+        raise ValueError(f"{what}: on the GPU that is the current device, got cuda:{device}")
+    return device
 
 
-def _stream(stream, beside):
-    """The given stream, or the current one of the device that tensor `beside` lives on."""
-    if stream is None:
-        return _raw_stream(beside.get_device())
-    return stream if isinstance(stream, int) else stream.cuda_stream
-
-
-def _ints(t, n: int, what: str, dtype=_I32) -> int:
-    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{what}: contiguous {dtype} on the GPU with {n} entries, got {t.dtype} {tuple(t.shape)} "
-                         f"on {t.device}")
+def _status(t, device: int):
+    if t is None:
+        return None
+    if t.dtype is not _I32 or t.numel() < 1 or t.get_device() != device:
+        raise ValueError(f"status: int32 on the GPU beside the others, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _table(t, batch: int) -> int:
+def _stream(stream, device: int):
+    """The given stream, or the current one."""
+    if stream is None:
+        return _raw_stream(device)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _ints(t, n: int, what: str, device: int, dtype=_I32) -> int:
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{what}: contiguous {dtype} on the GPU beside the others with {n} entries, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _table(t, batch: int, device: int) -> int:
     shape = t.shape
-    if t.dtype is not _I32 or len(shape) != 2 or shape[0] != batch or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError("block_table: contiguous int32 [batch, max_pages] on the GPU")
+    if t.dtype is not _I32 or len(shape) != 2 or shape[0] != batch or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError("block_table: contiguous int32 [batch, max_pages] on the GPU beside the others")
     return shape[1]
 
 
@@ -88,25 +103,27 @@ def kv_plan(cached_len, new_len, held, block_table, free_list, free_count, *, kv
     held_out and free_count_out may be cached_len, held and free_count themselves. A cached length of
     LEN_PADDING marks a row that takes no part and stays so; -1 does for one step only."""
     batch, capacity, free = cached_len.numel(), slot_map.numel(), free_list.numel()
-    cached = _ints(cached_len, batch, "cached_len")
+    at = _here(cached_len.get_device(), "cached_len")
+    cached = _ints(cached_len, batch, "cached_len", at)
     check(_abi.load().gdn_kv_plan(
-        batch, _table(block_table, batch), page_size, num_pages, free, capacity, cached,
-        None if new_len is None else _ints(new_len, batch, "new_len"), _ints(held, batch, "held"),
-        block_table.data_ptr(), _ints(free_list, free, "free_list"), _ints(free_count, 1, "free_count"),
-        _ints(kv_len, batch, "kv_len"), _ints(cu_new, batch + 1, "cu_new"), _ints(slot_map, capacity, "slot_map", _I64),
-        _ints(held_out, batch, "held_out"), _ints(free_count_out, 1, "free_count_out"), _ptr(status),
-        _stream(stream, cached_len)), "gdn_kv_plan")
+        batch, _table(block_table, batch, at), page_size, num_pages, free, capacity, cached,
+        None if new_len is None else _ints(new_len, batch, "new_len", at), _ints(held, batch, "held", at),
+        block_table.data_ptr(), _ints(free_list, free, "free_list", at), _ints(free_count, 1, "free_count", at),
+        _ints(kv_len, batch, "kv_len", at), _ints(cu_new, batch + 1, "cu_new", at),
+        _ints(slot_map, capacity, "slot_map", at, _I64), _ints(held_out, batch, "held_out", at),
+        _ints(free_count_out, 1, "free_count_out", at), _status(status, at), _stream(stream, at)), "gdn_kv_plan")
 
 
 def kv_release(requests, held, block_table, free_list, free_count, *, status=None, stream=None):
     """Pushes the pages of the given requests (rows of block_table) on free_list, which has room for
     every page of the cache; held of those rows becomes 0 and free_count grows."""
     batch, n, free = held.numel(), requests.numel(), free_list.numel()
-    finished = _ints(requests, n, "requests")
+    at = _here(requests.get_device(), "requests")
+    finished = _ints(requests, n, "requests", at)
     check(_abi.load().gdn_kv_release(
-        batch, _table(block_table, batch), free, finished, n, block_table.data_ptr(),
-        _ints(held, batch, "held"), _ints(free_list, free, "free_list"), _ints(free_count, 1, "free_count"),
-        _ptr(status), _stream(stream, held)), "gdn_kv_release")
+        batch, _table(block_table, batch, at), free, finished, n, block_table.data_ptr(),
+        _ints(held, batch, "held", at), _ints(free_list, free, "free_list", at), _ints(free_count, 1, "free_count", at),
+        _status(status, at), _stream(stream, at)), "gdn_kv_release")
 
 
 def kv_append(kv: PagedKV, k, v, slot_map, *, status=None, stream=None):
@@ -114,18 +131,19 @@ def kv_append(kv: PagedKV, k, v, slot_map, *, status=None, stream=None):
     latent part [n, 1, dv] and the tail [n, 1, dk - dv] (None if dk == dv). bf16 or fp32."""
     n, heads, dv, dtype = slot_map.numel(), kv.heads, kv.dv, k.dtype
     width, tail = (dv, kv.dk - dv) if kv.latent else (kv.dk, dv)
-    slots = _ints(slot_map, n, "slot_map", _I64)
+    at = _here(kv.device, "the pages")
+    slots = _ints(slot_map, n, "slot_map", at, _I64)
     k_row, k_head, k_last = k.stride() if k.dim() == 3 else (0, 0, 0)
-    if k_last != 1 or (dtype is not _BF16 and dtype is not _FP32) or k.shape != (n, heads, width) or not k.is_cuda:
-        raise ValueError(f"k: bf16 or fp32 [{n}, {heads}, {width}] on the GPU, its last stride 1")
+    if k_last != 1 or (dtype is not _BF16 and dtype is not _FP32) or k.shape != (n, heads, width) or k.get_device() != at:
+        raise ValueError(f"k: bf16 or fp32 [{n}, {heads}, {width}] on the GPU beside the pages, its last stride 1")
     v_ptr = v_strides = None
     if tail:
-        if v is None or v.dtype is not dtype or v.shape != (n, heads, tail) or not v.is_cuda or v.stride(2) != 1:
-            raise ValueError(f"v: of k's type [{n}, {heads}, {tail}] on the GPU, its last stride 1")
+        if v is None or v.dtype is not dtype or v.shape != (n, heads, tail) or v.get_device() != at or v.stride(2) != 1:
+            raise ValueError(f"v: of k's type [{n}, {heads}, {tail}] on the GPU beside the pages, its last stride 1")
         v_row, v_head, _ = v.stride()
         v_ptr, v_strides = v.data_ptr(), _pack_strides(v_row, v_head)
     check(_abi.load().gdn_kv_append(kv.packed, n, k.data_ptr(), _pack_strides(k_row, k_head), v_ptr, v_strides, slots,
-                                    1 if dtype is _BF16 else 0, _ptr(status), _stream(stream, k)), "gdn_kv_append")
+                                    1 if dtype is _BF16 else 0, _status(status, at), _stream(stream, at)), "gdn_kv_append")
 
 
 def attn_workspace_bytes(kv: PagedKV, batch: int, num_tokens: int, num_heads: int) -> int:
@@ -136,23 +154,24 @@ def attn_workspace_bytes(kv: PagedKV, batch: int, num_tokens: int, num_heads: in
 
 
 def _attend(call, name, kv, q, block_table, kv_len, o, workspace, lse, scale, window, status, stream):
-    if q.dtype is not _BF16 or q.dim() != 4 or not q.is_cuda:
-        raise ValueError("q: bf16 [batch, tokens, heads, dk] on the GPU")
+    at = _here(kv.device, "the pages")
+    if q.dtype is not _BF16 or q.dim() != 4 or q.get_device() != at:
+        raise ValueError("q: bf16 [batch, tokens, heads, dk] on the GPU beside the pages")
     batch, tokens, heads, dk = q.shape
     s0, s1, s2, s3 = q.stride()
     if dk != kv.dk or s3 != 1:
         raise ValueError("q: heads of dk elements, its last stride 1")
-    if o.dtype is not _BF16 or o.shape != (batch, tokens, heads, kv.dv) or not o.is_contiguous() or not o.is_cuda:
-        raise ValueError("o: contiguous bf16 [batch, tokens, heads, dv] on the GPU")
+    if o.dtype is not _BF16 or o.shape != (batch, tokens, heads, kv.dv) or not o.is_contiguous() or o.get_device() != at:
+        raise ValueError("o: contiguous bf16 [batch, tokens, heads, dv] on the GPU beside the pages")
     if lse is not None and (lse.dtype is not _FP32 or lse.shape != (batch, tokens, heads) or not lse.is_contiguous()
-                            or not lse.is_cuda):
-        raise ValueError("lse: contiguous fp32 [batch, tokens, heads] on the GPU")
-    if not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace: contiguous, on the GPU")
-    a = _pack_attn(batch, tokens, heads, _table(block_table, batch), window, dk ** -0.5 if scale is None else scale,
-                   q.data_ptr(), s0, s1, s2, block_table.data_ptr(), _ints(kv_len, batch, "kv_len"), o.data_ptr(),
+                            or lse.get_device() != at):
+        raise ValueError("lse: contiguous fp32 [batch, tokens, heads] on the GPU beside the pages")
+    if workspace.get_device() != at or not workspace.is_contiguous():
+        raise ValueError("workspace: contiguous, on the GPU beside the pages")
+    a = _pack_attn(batch, tokens, heads, _table(block_table, batch, at), window, dk ** -0.5 if scale is None else scale,
+                   q.data_ptr(), s0, s1, s2, block_table.data_ptr(), _ints(kv_len, batch, "kv_len", at), o.data_ptr(),
                    0 if lse is None else lse.data_ptr())
-    rc = call(kv.packed, a, workspace.data_ptr(), workspace.nbytes, _ptr(status), _stream(stream, q))
+    rc = call(kv.packed, a, workspace.data_ptr(), workspace.nbytes, _status(status, at), _stream(stream, at))
     if rc != GDN_OK:
         check(rc, name)
 
