@@ -390,7 +390,8 @@ typedef struct gdn_paged_kv {
  * later request that needs one), or whose length passes max_pages pages, 2^31 - 1 or
  * slot_capacity, or is negative (GDN_STATUS_BAD_LEN) is skipped: kv_len = cached_len, no page, slots -1. An
  * entry outside [0, num_pages) (GDN_STATUS_BAD_PAGE) gives its positions the slot -1.
- * Requires batch <= 4096.
+ * Requires batch <= 4096. An empty batch is no call: nothing is launched and nothing written, so
+ * slot_map, cu_new and free_count_out keep what they held, and the step has no tokens to append.
  */
 #define GDN_LEN_PADDING (-2)
 int gdn_kv_plan(int32_t batch, int32_t max_pages, int32_t page_size, int32_t num_pages, int32_t free_capacity,

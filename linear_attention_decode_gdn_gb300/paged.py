@@ -101,7 +101,8 @@ def kv_plan(cached_len, new_len, held, block_table, free_list, free_count, *, kv
     """Pages and slots for the new tokens of a step, from the requests' lengths (new_len None: one
     token each). Writes block_table, kv_len, cu_new, slot_map, held_out and free_count_out; kv_len,
     held_out and free_count_out may be cached_len, held and free_count themselves. A cached length of
-    LEN_PADDING marks a row that takes no part and stays so; -1 does for one step only."""
+    LEN_PADDING marks a row that takes no part and stays so; -1 does for one step only. An empty
+    batch is no call: nothing is written."""
     batch, capacity, free = cached_len.numel(), slot_map.numel(), free_list.numel()
     at = _here(cached_len.get_device(), "cached_len")
     cached = _ints(cached_len, batch, "cached_len", at)

@@ -112,3 +112,13 @@ def test_the_status_word_is_checked(paged):
             with pytest.raises(ValueError, match="status"):
                 call({**tensors, "status": bad})
         assert paged.lib.calls == 2
+
+
+def test_an_empty_batch_writes_nothing():
+    """The library itself, with arrays of the host behind the pointers: no call is launched, so none is touched."""
+    import ctypes
+    from linear_attention_decode_gdn_gb300 import _abi, build
+    build.build()
+    arrays = [(ctypes.c_int64 * 8)(*[77] * 8) for _ in range(11)]
+    assert _abi.load().gdn_kv_plan(0, 4, 16, 8, 8, 8, *arrays, None, None) == 0
+    assert all(list(a) == [77] * 8 for a in arrays)
