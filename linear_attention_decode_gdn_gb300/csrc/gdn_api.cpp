@@ -475,10 +475,10 @@ int gdn_kv_plan(int32_t batch, int32_t max_pages, int32_t page_size, int32_t num
   if (batch > gdn::kMaxPlanBatch)
     return fail(GDN_ERR_UNSUPPORTED, "batch %d > %d", batch, gdn::kMaxPlanBatch);
   if (batch == 0) return GDN_OK;
-  if (cached_len == nullptr || held == nullptr || block_table == nullptr || free_list == nullptr ||
+  if (cached_len == nullptr || held == nullptr || block_table == nullptr || (free_list == nullptr && free_capacity > 0) ||
       free_count == nullptr || kv_len == nullptr || cu_new == nullptr || held_out == nullptr ||
       free_count_out == nullptr || (slot_map == nullptr && slot_capacity > 0))
-    return fail(GDN_ERR_INVALID_ARG, "every array but new_len and status is required");
+    return fail(GDN_ERR_INVALID_ARG, "every array but new_len and status is required (free_list and slot_map where they have room)");
   gdn::KvPlanParams p{};
   p.B = batch;
   p.max_pages = max_pages;

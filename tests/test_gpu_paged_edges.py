@@ -5,7 +5,7 @@ import time
 import pytest
 import torch
 
-from test_gpu_paged import Problem, name_of
+from test_gpu_paged import Problem, name_of, plan_reference, run_plan
 
 pytestmark = pytest.mark.gpu
 
@@ -246,3 +246,11 @@ def test_values_that_only_some_positions_see(gdn, shape, T, window, lens):
                 assert bool(((got[t] - o[t]).abs() <= to[t])[:, whole].all()), (b, n, t)
                 assert not bool(torch.isfinite(got[t][:, ~whole]).any()), (b, n, t)
                 assert torch.equal(torch.isnan(got[t]), torch.isnan(o[t])) and torch.equal(got[t] == float("inf"), o[t] == float("inf"))
+
+
+def test_a_plan_without_a_free_list(gdn):
+    """A list of no room (an empty tensor has no address): requests that need no page go on, the others are told."""
+    args = ([3, 16, 7], None, [1, 1, 1], [[0, -1], [1, -1], [2, -1]], [], 0, 16, 3, 3)
+    want, bad = plan_reference(*args)
+    got, st = run_plan(gdn, *args)
+    assert got == want and st == bad == gdn.STATUS_NO_PAGES
