@@ -279,21 +279,6 @@ __global__ void __launch_bounds__(kJoinThreads) gdn_attn_join_kernel(const AttnP
   if (d == 0 && p.lse != nullptr) p.lse[row] = lse_of(m, l);
 }
 
-cudaError_t launch_overlapped(void (*kernel)(const AttnParams), const AttnParams& p, dim3 grid, unsigned threads,
-                              size_t smem, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1]{};
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
 }  // namespace
 
 // The tensor-core kernel needs rows made of whole 64-element chunks, pages that fill a tile in
@@ -331,7 +316,7 @@ cudaError_t launch_attn_general(AttnParams& p, cudaStream_t stream) {
   const cudaError_t err =
       allow_shared(reinterpret_cast<const void*>(gdn_attn_general_kernel), static_cast<int>(sizeof(GeneralSmem)), allowed);
   if (err != cudaSuccess) return err;
-  return launch_overlapped(gdn_attn_general_kernel, p, dim3(p.workers), kThreads, sizeof(GeneralSmem), stream);
+  return launch_overlapped(gdn_attn_general_kernel, p, dim3(p.workers), kThreads, sizeof(GeneralSmem), 1u, stream);
 }
 
 cudaError_t launch_attn_join(const AttnParams& p, cudaStream_t stream) {
@@ -344,7 +329,7 @@ cudaError_t launch_attn_join(const AttnParams& p, cudaStream_t stream) {
   const int64_t units = static_cast<int64_t>(p.B) * p.heads_kv * p.col_groups;
   auto kernel = p.workers >= 16 * units ? gdn_attn_join_kernel<16>
                 : p.workers >= 4 * units ? gdn_attn_join_kernel<8> : gdn_attn_join_kernel<4>;
-  return launch_overlapped(kernel, p, grid, kJoinThreads, 0, stream);
+  return launch_overlapped(kernel, p, grid, kJoinThreads, 0, 1u, stream);
 }
 
 cudaError_t launch_attn(const AttnPlan& plan, AttnParams& p, cudaStream_t stream) {

@@ -85,9 +85,9 @@ struct Cfg {
   static constexpr int THREADS = 128 + 128 * G * TEAMS;
   static constexpr int PB = LATENT ? 1 : 2;                // buffers of weights
   static constexpr int QB = !LATENT && DK < 256 && N <= 32 ? 2 : 1;  // and of queries
-  static constexpr int TAIL = kTile * TCOLS * 2, TAILS = LATENT ? 1 : 0;
+  static constexpr int TAIL = kTile * TCOLS * 2;            // bytes of a tile's tail; there is one buffer
   static constexpr int QBYTES = N * (KCOLS + TCOLS) * 2, PBYTES = N * kTile * 2, RBYTES = LATENT ? N * kTile * 4 : 0;
-  static constexpr int FIXED = kMiscBytes + QB * QBYTES + PB * PBYTES + RBYTES + TAILS * TAIL;
+  static constexpr int FIXED = kMiscBytes + QB * QBYTES + PB * PBYTES + RBYTES + TAIL;
   static constexpr int FIT = (kSmemMost - FIXED) / SLOT < kMaxSlots ? (kSmemMost - FIXED) / SLOT : kMaxSlots;
   static constexpr int SLOTS = SLOTC == 1 ? FIT & ~1 : FIT;
   static constexpr int SMEM = FIXED + SLOTS * SLOT;
@@ -107,7 +107,7 @@ struct Cfg {
 
 struct Misc {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
-  uint64_t tail_full[2], tail_empty[2];
+  uint64_t tail_full, tail_empty;
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], s_empty[2];
   uint64_t p_full[2], pv_done[2];  // by tile
@@ -186,9 +186,6 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t saddr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
-}
 // 16 bytes to another CTA's shared memory, counted on that CTA's mbarrier
 __device__ __forceinline__ void send16(uint32_t dst, float a, float b, float c, float d, uint32_t bar) {
   asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
@@ -219,11 +216,6 @@ __device__ __forceinline__ float warp_max(float x) {
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 
@@ -366,10 +358,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
   extern __shared__ __align__(1024) unsigned char smem[];
   const AttnParams& p = tp.a;
   constexpr int N = C::N, NC = C::NC;
-  constexpr uint32_t kTails = C::TAILS > 0 ? C::TAILS : 1;
   unsigned char* const ring = smem;
-  unsigned char* const tails = ring + C::SLOTS * C::SLOT;
-  unsigned char* const weights = tails + C::TAILS * C::TAIL;
+  unsigned char* const tail = ring + C::SLOTS * C::SLOT;
+  unsigned char* const weights = tail + C::TAIL;
   unsigned char* const received = weights + C::PB * C::PBYTES;
   unsigned char* const queries = received + C::RBYTES;
   Misc& sm = *reinterpret_cast<Misc*>(queries + C::QB * C::QBYTES);
@@ -389,8 +380,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
       mbar_init(&sm.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.tail_full[i], 1);
-      mbar_init(&sm.tail_empty[i], 1);
       mbar_init(&sm.q_full[i], 2);
       mbar_init(&sm.q_empty[i], 1);
       mbar_init(&sm.s_full[i], 1);
@@ -404,6 +393,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
       mbar_init(&sm.got[i], 1);
       mbar_init(&sm.may_send[i], 1);
     }
+    mbar_init(&sm.tail_full, 1);
+    mbar_init(&sm.tail_empty, 1);
     mbar_init(&sm.drained, 1);
     sm.timeout = 0u;
     fence_mbar_init();
@@ -477,15 +468,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
             }
           }
           if (C::LATENT && ok) {
-            const uint32_t t = tile_no % kTails;
-            ok = warp_waited(&sm.tail_empty[t], ((tile_no / kTails) & 1u) ^ 1u, sm);
+            ok = warp_waited(&sm.tail_empty, (tile_no & 1u) ^ 1u, sm);
             if (!ok) break;
-            tc::expect_tx(&sm.tail_full[t], C::TAIL);
+            tc::expect_tx(&sm.tail_full, C::TAIL);
             ++tails_put;
 #pragma unroll
             for (int b = 0; b < BOXES; ++b)
-              tma_box(smem_addr(tails) + t * C::TAIL + b * BOX * (C::TCOLS * 2), &tp.v, C::DV + static_cast<int32_t>(rank) * C::TCOLS,
-                      0, pos, pages[b], &sm.tail_full[t]);
+              tma_box(smem_addr(tail) + b * BOX * (C::TCOLS * 2), &tp.v, C::DV + static_cast<int32_t>(rank) * C::TCOLS,
+                      0, pos, pages[b], &sm.tail_full);
           }
           if (C::LATENT && ok && tile + kAhead < end) {
             // The ring holds little more than two tiles, so a tile's loads begin when the one two
@@ -517,14 +507,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
     // Nothing may still be on its way into this CTA's memory when it ends, whichever warp gave up.
     for (uint32_t i = put > C::SLOTS ? put - C::SLOTS : 0; i < put; ++i)
       mbar_wait(&sm.full[i % C::SLOTS], (i / C::SLOTS) & 1u);
-    if (C::LATENT)
-      for (uint32_t i = tails_put > kTails ? tails_put - kTails : 0; i < tails_put; ++i)
-        mbar_wait(&sm.tail_full[i % kTails], (i / kTails) & 1u);
+    if (C::LATENT && tails_put > 0) mbar_wait(&sm.tail_full, (tails_put - 1) & 1u);
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomic_status(p.status, GDN_STATUS_BAD_PAGE);
   } else if (warp == 1) {
     // ---- matrix products --------------------------------------------------------------------
     constexpr uint32_t kScores = idesc_bf16(128, N, false, false), kValues = idesc_bf16(128, N, true, true);
-    const uint32_t ring_at = smem_addr(ring), tails_at = smem_addr(tails), w_at = smem_addr(weights);
+    const uint32_t ring_at = smem_addr(ring), tail_at = smem_addr(tail), w_at = smem_addr(weights);
     uint32_t i = 0, units = 0;   // tiles and units begun
     uint32_t k_slot = 0, k_round = 0, v_slot = 0, v_round = 0;  // next slots of keys and of values
     // of the last tile with scores: whether it is its unit's first, its last, and that unit
@@ -556,15 +544,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
         skip(k_slot, k_round, 1);
       }
       if (C::LATENT) {
-        const uint32_t t = i % kTails;
-        ok = warp_waited(&sm.tail_full[t], (i / kTails) & 1u, sm);
+        ok = warp_waited(&sm.tail_full, i & 1u, sm);
         if (!ok) return;
         tc::fence_after_sync();
 #pragma unroll
         for (int k = 0; k < C::TCOLS / 16; ++k)
-          mma_bf16(d, desc_sw64(tails_at + t * C::TAIL + k * 32, 16, 512),
+          mma_bf16(d, desc_sw64(tail_at + k * 32, 16, 512),
                    tc::smem_desc(q_at + (C::KCOLS / 8 + 2 * k) * (N * 16), N * 16, 128), kScores, 1);
-        tc::commit(&sm.tail_empty[t]);
+        tc::commit(&sm.tail_empty);
       }
       skip(k_slot, k_round, C::VS);
       tc::commit(&sm.s_full[i & 1u]);
@@ -993,19 +980,7 @@ cudaError_t launch_one(const TcParams& tp, cudaStream_t stream) {
   static std::atomic<bool> allowed[kDevices];
   const cudaError_t err = allow_shared(reinterpret_cast<const void*>(gdn_attn_tc_kernel<C>), C::SMEM, allowed);
   if (err != cudaSuccess) return err;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(tp.a.workers * C::CL);
-  cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2]{};
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim = {static_cast<unsigned>(C::CL), 1u, 1u};
-  cfg.attrs = attr;
-  cfg.numAttrs = C::CL > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, gdn_attn_tc_kernel<C>, tp);
+  return launch_overlapped(gdn_attn_tc_kernel<C>, tp, dim3(tp.a.workers * C::CL), C::THREADS, C::SMEM, C::CL, stream);
 }
 
 template <int DK, int DV, bool LATENT>

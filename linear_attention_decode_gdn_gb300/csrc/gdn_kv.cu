@@ -54,10 +54,6 @@ __device__ __forceinline__ void find_rows(const int32_t* sums, int n, const int 
   }
 }
 
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
-}
-
 // Every CTA takes the whole batch's sums for itself, in shared memory: that is 12 bytes read a
 // request and spares a second launch or a grid barrier. Then the CTAs share the tokens and the
 // pages. Where outputs are the inputs' own arrays (in_place), no CTA may write before all have
@@ -253,12 +249,6 @@ __global__ void __launch_bounds__(kReleaseThreads) gdn_kv_release_kernel(const K
 // ---- rows to their slots ----------------------------------------------------------------
 constexpr int kAppendThreads = 256;
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 // A token's 8-element vectors (of both sources) are copied by a warp, or by 2^k lanes of one where
 // they are that few, with kFlight of them a lane in flight: the slot and its page are looked up
 // once a token, neighbouring lanes move neighbouring 16 bytes, and a lane's loads are all under
@@ -318,26 +308,6 @@ __global__ void __launch_bounds__(kAppendThreads) gdn_kv_append_kernel(const KvA
   }
 }
 
-// Launch with programmatic stream serialisation: the kernel waits itself (griddep_wait)
-// before its first read, so its launch overlaps the previous kernel's tail.
-template <class P>
-cudaError_t launch_overlapped(void (*kernel)(const P), const P& p, unsigned grid, unsigned threads, size_t smem,
-                              unsigned cluster, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2]{};
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim = {cluster, 1u, 1u};
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
 }  // namespace
 
 namespace {
@@ -352,7 +322,7 @@ cudaError_t launch_plan(const KvPlanParams& p, unsigned ctas, cudaStream_t strea
                                          (6 * kMaxPlanBatch + 1) * static_cast<int>(sizeof(int32_t)), allowed);
     if (err != cudaSuccess) return err;
   }
-  return launch_overlapped(gdn_kv_plan_kernel<THREADS>, p, ctas, THREADS, smem, p.in_place ? ctas : 1u, stream);
+  return launch_overlapped(gdn_kv_plan_kernel<THREADS>, p, dim3(ctas), THREADS, smem, p.in_place ? ctas : 1u, stream);
 }
 
 }  // namespace
@@ -368,7 +338,7 @@ cudaError_t launch_kv_plan(const KvPlanParams& given, cudaStream_t stream) {
 }
 
 cudaError_t launch_kv_release(const KvReleaseParams& p, cudaStream_t stream) {
-  return launch_overlapped(gdn_kv_release_kernel, p, 1u, kReleaseThreads, 0, 1u, stream);
+  return launch_overlapped(gdn_kv_release_kernel, p, dim3(1), kReleaseThreads, 0, 1u, stream);
 }
 
 cudaError_t launch_kv_append(const KvAppendParams& given, cudaStream_t stream) {
@@ -385,8 +355,8 @@ cudaError_t launch_kv_append(const KvAppendParams& given, cudaStream_t stream) {
   while (p.lanes < 32 && static_cast<uint32_t>(p.lanes) < all) p.lanes *= 2;
   const int64_t rows = kAppendThreads / p.lanes, blocks = (p.n + rows - 1) / rows;
   const unsigned grid = static_cast<unsigned>(blocks < kSms * 32 ? blocks : kSms * 32);
-  return launch_overlapped(p.bf16 ? gdn_kv_append_kernel<true> : gdn_kv_append_kernel<false>, p, grid, kAppendThreads, 0, 1u,
-                           stream);
+  return launch_overlapped(p.bf16 ? gdn_kv_append_kernel<true> : gdn_kv_append_kernel<false>, p, dim3(grid), kAppendThreads, 0,
+                           1u, stream);
 }
 
 }  // namespace gdn
