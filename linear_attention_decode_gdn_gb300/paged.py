@@ -36,18 +36,13 @@ class PagedKV:
         self.device = k.get_device()
 
 
-def _here(device: int, what: str) -> int:
-    """The device of a call's tensors (get_device() is -1 on the host), which is the current one."""
-    if device < 0:
-        raise ValueError(f"{what}: on the GPU")
-    if device != _current_device():
-        raise ValueError(f"{what}: on the GPU that is the current device, got cuda:{device}")
-    return device
+def _not_here(device: int, what: str):
+    """The error of tensors that are not on the current device (get_device() is -1 on the host)."""
+    got = "the host" if device < 0 else f"cuda:{device}"
+    return ValueError(f"{what}: on the GPU that is the current device, got {got}")
 
 
 def _status(t, device: int):
-    if t is None:
-        return None
     if t.dtype is not _I32 or t.numel() < 1 or t.get_device() != device:
         raise ValueError(f"status: int32 on the GPU beside the others, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
@@ -104,7 +99,9 @@ def kv_plan(cached_len, new_len, held, block_table, free_list, free_count, *, kv
     LEN_PADDING marks a row that takes no part and stays so; -1 does for one step only. An empty
     batch is no call: nothing is written."""
     batch, capacity, free = cached_len.numel(), slot_map.numel(), free_list.numel()
-    at = _here(cached_len.get_device(), "cached_len")
+    at = cached_len.get_device()
+    if at < 0 or at != _current_device():
+        raise _not_here(at, "cached_len")
     cached = _ints(cached_len, batch, "cached_len", at)
     check(_abi.load().gdn_kv_plan(
         batch, _table(block_table, batch, at), page_size, num_pages, free, capacity, cached,
@@ -112,19 +109,22 @@ def kv_plan(cached_len, new_len, held, block_table, free_list, free_count, *, kv
         block_table.data_ptr(), _ints(free_list, free, "free_list", at), _ints(free_count, 1, "free_count", at),
         _ints(kv_len, batch, "kv_len", at), _ints(cu_new, batch + 1, "cu_new", at),
         _ints(slot_map, capacity, "slot_map", at, _I64), _ints(held_out, batch, "held_out", at),
-        _ints(free_count_out, 1, "free_count_out", at), _status(status, at), _stream(stream, at)), "gdn_kv_plan")
+        _ints(free_count_out, 1, "free_count_out", at), None if status is None else _status(status, at),
+        _stream(stream, at)), "gdn_kv_plan")
 
 
 def kv_release(requests, held, block_table, free_list, free_count, *, status=None, stream=None):
     """Pushes the pages of the given requests (rows of block_table) on free_list, which has room for
     every page of the cache; held of those rows becomes 0 and free_count grows."""
     batch, n, free = held.numel(), requests.numel(), free_list.numel()
-    at = _here(requests.get_device(), "requests")
+    at = requests.get_device()
+    if at < 0 or at != _current_device():
+        raise _not_here(at, "requests")
     finished = _ints(requests, n, "requests", at)
     check(_abi.load().gdn_kv_release(
         batch, _table(block_table, batch, at), free, finished, n, block_table.data_ptr(),
         _ints(held, batch, "held", at), _ints(free_list, free, "free_list", at), _ints(free_count, 1, "free_count", at),
-        _status(status, at), _stream(stream, at)), "gdn_kv_release")
+        None if status is None else _status(status, at), _stream(stream, at)), "gdn_kv_release")
 
 
 def kv_append(kv: PagedKV, k, v, slot_map, *, status=None, stream=None):
@@ -132,7 +132,9 @@ def kv_append(kv: PagedKV, k, v, slot_map, *, status=None, stream=None):
     latent part [n, 1, dv] and the tail [n, 1, dk - dv] (None if dk == dv). bf16 or fp32."""
     n, heads, dv, dtype = slot_map.numel(), kv.heads, kv.dv, k.dtype
     width, tail = (dv, kv.dk - dv) if kv.latent else (kv.dk, dv)
-    at = _here(kv.device, "the pages")
+    at = kv.device
+    if at < 0 or at != _current_device():
+        raise _not_here(at, "the pages")
     slots = _ints(slot_map, n, "slot_map", at, _I64)
     k_row, k_head, k_last = k.stride() if k.dim() == 3 else (0, 0, 0)
     if k_last != 1 or (dtype is not _BF16 and dtype is not _FP32) or k.shape != (n, heads, width) or k.get_device() != at:
@@ -144,7 +146,8 @@ def kv_append(kv: PagedKV, k, v, slot_map, *, status=None, stream=None):
         v_row, v_head, _ = v.stride()
         v_ptr, v_strides = v.data_ptr(), _pack_strides(v_row, v_head)
     check(_abi.load().gdn_kv_append(kv.packed, n, k.data_ptr(), _pack_strides(k_row, k_head), v_ptr, v_strides, slots,
-                                    1 if dtype is _BF16 else 0, _status(status, at), _stream(stream, at)), "gdn_kv_append")
+                                    1 if dtype is _BF16 else 0, None if status is None else _status(status, at),
+                                    _stream(stream, at)), "gdn_kv_append")
 
 
 def attn_workspace_bytes(kv: PagedKV, batch: int, num_tokens: int, num_heads: int) -> int:
@@ -155,7 +158,9 @@ def attn_workspace_bytes(kv: PagedKV, batch: int, num_tokens: int, num_heads: in
 
 
 def _attend(call, name, kv, q, block_table, kv_len, o, workspace, lse, scale, window, status, stream):
-    at = _here(kv.device, "the pages")
+    at = kv.device
+    if at < 0 or at != _current_device():
+        raise _not_here(at, "the pages")
     if q.dtype is not _BF16 or q.dim() != 4 or q.get_device() != at:
         raise ValueError("q: bf16 [batch, tokens, heads, dk] on the GPU beside the pages")
     batch, tokens, heads, dk = q.shape
@@ -172,7 +177,8 @@ def _attend(call, name, kv, q, block_table, kv_len, o, workspace, lse, scale, wi
     a = _pack_attn(batch, tokens, heads, _table(block_table, batch, at), window, dk ** -0.5 if scale is None else scale,
                    q.data_ptr(), s0, s1, s2, block_table.data_ptr(), _ints(kv_len, batch, "kv_len", at), o.data_ptr(),
                    0 if lse is None else lse.data_ptr())
-    rc = call(kv.packed, a, workspace.data_ptr(), workspace.nbytes, _status(status, at), _stream(stream, at))
+    rc = call(kv.packed, a, workspace.data_ptr(), workspace.nbytes, None if status is None else _status(status, at),
+              _stream(stream, at))
     if rc != GDN_OK:
         check(rc, name)
 
