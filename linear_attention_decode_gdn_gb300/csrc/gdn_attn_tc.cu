@@ -116,9 +116,10 @@ struct Misc {
   uint64_t drained;
   uint32_t tmem;
   uint32_t timeout;
-  float m[64];
+  uint32_t cleaned[2];  // 1 + the unit of the share whose values held what is no number, by the unit's parity
+  alignas(16) float m[64];  // read as vectors, like per_warp
   float inv[64];
-  float per_warp[4][64];
+  alignas(16) float per_warp[4][64];
   int32_t last[64];  // the last position that each column sees
   int32_t rows[64];  // the column's row of o
 };
@@ -287,73 +288,82 @@ __device__ __forceinline__ bool warp_waited(uint64_t* bar, uint32_t parity, Misc
   return __all_sync(0xffffffffu, waited(bar, parity, sm));
 }
 
-// A segment's sums of w v for the `left` columns of a softmax group from c_base on, and the value elements
-// d, d + 128, .. of each lane, on the CUDA cores: a weight of zero leaves a value out, whatever it holds,
-// where a product on the tensor cores makes a NaN of it. refs and lasts: the group's references and last
-// positions. Called by a whole warp, and only where a sum came out as no number; a lane scores one
-// position of 32, then all sum them.
-template <class C>
-__device__ __noinline__ void sums_of_seen(const AttnParams& p, const Segment& seg, const float* refs, const int32_t* lasts, int c_base,
-                                          int left, int d, float (&sums)[C::MB][16]) {
-  const int lane = threadIdx.x & 31;
-  const int32_t lower = lower_bound_of(p, seg.n, seg.col_base / p.group);
-  const int32_t end = min((seg.tile + seg.tiles) * kTile, seg.n);
-  const int32_t* const row = p.table + static_cast<int64_t>(seg.b) * p.max_pages;
-  const uint16_t* const k_at = static_cast<const uint16_t*>(p.k) + seg.kv_head * p.k_head;
-  const uint16_t* const v_at = static_cast<const uint16_t*>(p.v) + seg.kv_head * p.v_head + d;
-  float w[16];
+__device__ __forceinline__ bool no_number(float x) { return !(fabsf(x) <= 3.4028235e38f); }
+
+// 16 bytes of a value's row (bf16) with zeros for what is no number; whether there was any.
+__device__ __forceinline__ bool clean16(uint4* at) {
+  uint4 x = *at;
+  uint32_t* const words[4] = {&x.x, &x.y, &x.z, &x.w};
+  bool found = false;
 #pragma unroll
-  for (int c = 0; c < 16; ++c) {
-    w[c] = 0.0f;
-#pragma unroll
-    for (int b = 0; b < C::MB; ++b) sums[b][c] = 0.0f;
+  for (int j = 0; j < 4; ++j) {
+    uint32_t& u = *words[j];
+    const bool lo = (u & 0x7f80u) == 0x7f80u, hi = (u & 0x7f800000u) == 0x7f800000u;
+    found |= lo || hi;
+    u &= (lo ? 0xffff0000u : 0xffffffffu) & (hi ? 0xffffu : 0xffffffffu);
   }
-  for (int32_t base = max(seg.tile * kTile, lower & ~31); base < end; base += 32) {
-    const int32_t pos = base + lane;
-    int32_t page = -1, in = 0;
-    if (pos < end && pos >= lower) {
-      page = row[pos / p.page_size];
-      in = pos % p.page_size;
-      if (page >= p.num_pages) page = -1;
+  if (found) *at = x;
+  return found;
+}
+
+// What clean16 took out of a segment's values, for the columns that see it: w v of every value that is
+// no number, for the `left` columns of a softmax group from c_base on and the elements d, d + 128, ..
+// of each lane. refs and lasts: the group's references and last positions. Called by a whole warp, and
+// only where something was found; looks at the positions that some columns of the unit see and others do not.
+template <class C>
+__device__ __noinline__ void sums_of_no_numbers(const AttnParams& p, const Segment& seg, const float* refs, const int32_t* lasts,
+                                                int c_base, int left, int d, float (&sums)[C::MB][16]) {
+  const int lane = threadIdx.x & 31;
+  const int t_first = seg.col_base / p.group, t_last = (min(seg.col_base + C::N, p.cols) - 1) / p.group;
+  const int32_t lower = lower_bound_of(p, seg.n, t_first), lower_last = lower_bound_of(p, seg.n, t_last);
+  const int32_t begin = max(seg.tile * kTile, lower), end = min((seg.tile + seg.tiles) * kTile, seg.n);
+  const int32_t all_see = max(seg.n - p.T + t_first, lower_last - 1);  // the last position that all columns see, if any does
+  const int32_t* const row = p.table + static_cast<int64_t>(seg.b) * p.max_pages;
+#pragma unroll
+  for (int b = 0; b < C::MB; ++b)
+#pragma unroll
+    for (int c = 0; c < 16; ++c) sums[b][c] = 0.0f;
+#pragma unroll 1
+  for (int32_t pos = begin; pos < end; ++pos) {
+    if (pos >= lower_last && pos <= all_see) {  // on to the first that is not seen by all
+      pos = all_see;
+      continue;
     }
-    const uint16_t* const k = k_at + page * p.k_page + in * p.k_pos;
+    const int32_t page = row[pos / p.page_size], in = pos % p.page_size;
+    if (page < 0 || page >= p.num_pages) continue;
+    const uint16_t* const v = static_cast<const uint16_t*>(p.v) + page * p.v_page + in * p.v_pos + seg.kv_head * p.v_head + d;
+    const uint16_t* const k = static_cast<const uint16_t*>(p.k) + page * p.k_page + in * p.k_pos + seg.kv_head * p.k_head;
+    float x[C::MB];
+    bool found = false;
+#pragma unroll
+    for (int b = 0; b < C::MB; ++b) {
+      x[b] = __uint_as_float(static_cast<uint32_t>(v[b * 128]) << 16);
+      found |= no_number(x[b]);
+    }
+    if (!__any_sync(0xffffffffu, found)) continue;
 #pragma unroll 1
     for (int c = 0; c < left; ++c) {
+      if (pos > lasts[c] || (p.window > 0 && pos <= lasts[c] - p.window)) continue;
       const int col = seg.col_base + c_base + c, t = col / p.group, h = seg.kv_head * p.group + (col - t * p.group);
       const uint16_t* const q = static_cast<const uint16_t*>(p.q) + seg.b * p.q_b + t * p.q_t + h * p.q_h;
-      const bool seen = page >= 0 && pos <= lasts[c] && (p.window <= 0 || pos > lasts[c] - p.window);
       float s = 0.0f;
-      for (int e = 0; seen && e < C::DK; e += 8) {
-        const uint4 x = *reinterpret_cast<const uint4*>(k + e), y = *reinterpret_cast<const uint4*>(q + e);
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s = fmaf(__uint_as_float(xs[j] << 16), __uint_as_float(ys[j] << 16), s);
-          s = fmaf(__uint_as_float(xs[j] & 0xffff0000u), __uint_as_float(ys[j] & 0xffff0000u), s);
-        }
-      }
-      w[c] = seen ? ex2(s * p.scale_log2 - refs[c]) : 0.0f;
-    }
 #pragma unroll 1
-    for (int j = 0; j < 32; ++j) {
-      const int32_t page_j = __shfl_sync(0xffffffffu, page, j), in_j = __shfl_sync(0xffffffffu, in, j);
-      if (page_j < 0) continue;
-      const uint16_t* const v = v_at + page_j * p.v_page + in_j * p.v_pos;
-      float x[C::MB];
-#pragma unroll
-      for (int b = 0; b < C::MB; ++b) x[b] = __uint_as_float(static_cast<uint32_t>(v[b * 128]) << 16);
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const float wj = __shfl_sync(0xffffffffu, w[c], j);
-        if (wj == 0.0f) continue;
-#pragma unroll
-        for (int b = 0; b < C::MB; ++b) sums[b][c] = fmaf(wj, x[b], sums[b][c]);
+      for (int e = lane * 2; e < C::DK; e += 64) {
+        const uint32_t a = *reinterpret_cast<const uint32_t*>(k + e), b = *reinterpret_cast<const uint32_t*>(q + e);
+        s = fmaf(__uint_as_float(a << 16), __uint_as_float(b << 16), s);
+        s = fmaf(__uint_as_float(a & 0xffff0000u), __uint_as_float(b & 0xffff0000u), s);
       }
+      const float w = ex2(warp_sum(s) * p.scale_log2 - refs[c]);
+      if (w == 0.0f) continue;
+#pragma unroll
+      for (int b = 0; b < C::MB; ++b)
+        if (no_number(x[b])) sums[b][c] = fmaf(w, x[b], sums[b][c]);
     }
   }
 }
 
-template <class C>
+// MULTI: several positions a request, so the columns of a unit may see different positions.
+template <class C, bool MULTI>
 __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid_constant__ TcParams tp) {
   extern __shared__ __align__(1024) unsigned char smem[];
   const AttnParams& p = tp.a;
@@ -396,7 +406,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
     mbar_init(&sm.tail_full, 1);
     mbar_init(&sm.tail_empty, 1);
     mbar_init(&sm.drained, 1);
-    sm.timeout = 0u;
+    sm.timeout = sm.cleaned[0] = sm.cleaned[1] = 0u;
     fence_mbar_init();
     if (C::LATENT)  // the first round of scores is expected from the start
       for (int i = 0; i < C::G; ++i) mbar_arrive_expect_tx(&sm.got[i], C::NC * kTile * 4);
@@ -742,7 +752,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
           }
         }
         // every column sees every position of the tile, but where it is not live
-        if (begin + kTile - 1 <= seg.n - p.T + t_first && begin >= lower_last) {
+        const bool all_see = begin + kTile - 1 <= seg.n - p.T + t_first && begin >= lower_last;
+        if (all_see) {
 #pragma unroll
           for (int c = 0; c < NC; ++c) s[c] = live ? s[c] * p.scale_log2 : -INFINITY;
         } else {
@@ -860,15 +871,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
           }
           *reinterpret_cast<uint4*>(to + (c / 8) * (kTile * 16)) = make_uint4(x[0], x[1], x[2], x[3]);
         }
-        if (begin + kTile > seg.n || begin < lower) {
+        if (begin + kTile > seg.n || begin < lower || (MULTI && !all_see)) {
           // Positions outside the request share its pages: whatever their values are (another
           // request's, or never written), a weight of zero has to meet a zero.
           constexpr int kSlots = C::LATENT ? C::KS : C::VS;
+          const uint32_t fill = i * C::PER + (C::LATENT ? 0 : C::KS);
           if (!C::FILL_KNOWN && i > 0) ok &= waited(&sm.pv_done[(i - 1) & 1u], ((i - 1) >> 1) & 1u, sm);
 #pragma unroll 1
           for (int v = 0; v < kSlots; ++v) {
-            const uint32_t n = i * C::PER + (C::LATENT ? 0 : C::KS) + v, slot = n % C::SLOTS;
-            ok &= waited(&sm.full[slot], (n / C::SLOTS) & 1u, sm);
+            const uint32_t slot = (fill + v) % C::SLOTS;
+            ok &= waited(&sm.full[slot], ((fill + v) / C::SLOTS) & 1u, sm);
             if (pos >= seg.n || pos < lower) {
 #pragma unroll
               for (int c = 0; c < C::SLOTC; ++c) {
@@ -877,6 +889,22 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
                 for (int j = 0; j < 8; ++j) to16[(j + r) & 7] = make_uint4(0u, 0u, 0u, 0u);
               }
             }
+          }
+          if (MULTI && !all_see) {
+            // Of the values that only some columns see (a window's oldest, the request's newest: rows
+            // old0 .. old1 - 1 and new0 .. new1 - 1) what is no number is taken out, a vector a thread,
+            // and comes back at the unit's end for those that see it.
+            constexpr int kVecs = C::VCOLS / 8;
+            const int old0 = max(lower - begin, 0), old1 = min(min(lower_last, seg.n) - begin, kTile);
+            const int new0 = max(max(seg.n - p.T + t_first + 1, lower_last) - begin, 0), new1 = min(seg.n - begin, kTile);
+            const int olds = max(old1 - old0, 0), items = (olds + max(new1 - new0, 0)) * kVecs;
+            bool found = false;
+            for (int item = g * 128 + r; item < items; item += 128 * C::G) {
+              const int at = item / kVecs, e = item - at * kVecs, to = at < olds ? old0 + at : new0 + at - olds;
+              const uint32_t slot = (fill + e / (8 * C::SLOTC)) % C::SLOTS;
+              found |= clean16(reinterpret_cast<uint4*>(ring + slot * C::SLOT + (e / 8) % C::SLOTC * kChunk + to * 128) + (e & 7));
+            }
+            if (found) *const_cast<volatile uint32_t*>(&sm.cleaned[units & 1u]) = units + 1;
           }
         }
         tc::fence_smem_to_async();
@@ -910,28 +938,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
       __syncwarp();
       tc::fence_after_sync();
       const int left = cols - c_base;  // columns that are rows of o
-      float again[C::MB][NC];
-      bool have = false;
+      float added[C::MB][NC];
+      const bool cleaned = MULTI && *const_cast<volatile uint32_t*>(&sm.cleaned[units & 1u]) == units + 1;
+      if (cleaned && (C::DV >= 128 || r >= 64)) {
+        const Segment here = seg;  // a copy: what a call takes by address has no registers
+        sums_of_no_numbers<C>(p, here, sm.m + a_base, sm.last + a_base, c_base, min(left, NC),
+                              static_cast<int>(rank) * C::VCOLS + (C::DV >= 128 ? r : r - 64), added);
+      }
 #pragma unroll 1
       for (int block = 0; block < C::MB; ++block) {
         const int d = static_cast<int>(rank) * C::VCOLS + (C::DV >= 128 ? block * 128 + r : r - 64);
         float x[NC];
         tc::ld16(o_at + block * N, x);
-        // Among several positions a value that only some see meets the others' weights of zero: where it
-        // is no number, neither are their sums. (With one, what is not seen was zeroed above.)
-        if (p.T > 1) {
-          bool number = true;
+        if (cleaned && d >= 0) {
 #pragma unroll
-          for (int j = 0; j < NC; ++j) number &= j >= left || fabsf(x[j]) <= 3.4028235e38f;
-          if (__any_sync(0xffffffffu, ok && d >= 0 && !number)) {
-            if (!have) {
-              const Segment here = seg;  // a copy: what a call takes by address has no registers
-              sums_of_seen<C>(p, here, sm.m + a_base, sm.last + a_base, c_base, min(left, NC), d - block * 128, again);
-            }
-            have = true;
-#pragma unroll
-            for (int j = 0; j < NC; ++j) x[j] = again[block][j];
-          }
+          for (int j = 0; j < NC; ++j) x[j] += added[block][j];
         }
         if (ok && d >= 0 && seg.whole) {
           __nv_bfloat16* const o = static_cast<__nv_bfloat16*>(p.o) + d;
@@ -975,12 +996,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) gdn_attn_tc_kernel(const __grid
   }
 }
 
+template <class C, bool MULTI>
+cudaError_t launch_form(const TcParams& tp, cudaStream_t stream) {
+  static std::atomic<bool> allowed[kDevices];
+  const cudaError_t err = allow_shared(reinterpret_cast<const void*>(gdn_attn_tc_kernel<C, MULTI>), C::SMEM, allowed);
+  if (err != cudaSuccess) return err;
+  return launch_overlapped(gdn_attn_tc_kernel<C, MULTI>, tp, dim3(tp.a.workers * C::CL), C::THREADS, C::SMEM, C::CL, stream);
+}
+
 template <class C>
 cudaError_t launch_one(const TcParams& tp, cudaStream_t stream) {
-  static std::atomic<bool> allowed[kDevices];
-  const cudaError_t err = allow_shared(reinterpret_cast<const void*>(gdn_attn_tc_kernel<C>), C::SMEM, allowed);
-  if (err != cudaSuccess) return err;
-  return launch_overlapped(gdn_attn_tc_kernel<C>, tp, dim3(tp.a.workers * C::CL), C::THREADS, C::SMEM, C::CL, stream);
+  return tp.a.T > 1 ? launch_form<C, true>(tp, stream) : launch_form<C, false>(tp, stream);
 }
 
 template <int DK, int DV, bool LATENT>

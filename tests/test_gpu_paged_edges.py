@@ -254,3 +254,47 @@ def test_a_plan_without_a_free_list(gdn):
     want, bad = plan_reference(*args)
     got, st = run_plan(gdn, *args)
     assert got == want and st == bad == gdn.STATUS_NO_PAGES
+
+
+@pytest.mark.parametrize("T,window,heads", [(4, 0, 8), (7, 5, 8), (70, 0, 4), (70, 200, 4), (150, 60, 2)])
+@pytest.mark.parametrize("shape", [dict(dk=64, page=32), dict(dk=128, page=16), dict(dk=256, page=64), dict(dk=128, page=128, permuted=True),
+                                   dict(dk=48, page=9)], ids=name_of)
+def test_values_of_every_newest_position(gdn, shape, T, window, heads):
+    """Each of the newest positions (and of the oldest that a window leaves) spoils two value elements of its own:
+    every query gives NaN and infinities where it sees them, and its sums everywhere else."""
+    lens = [1, 140, 260, 1000]
+    p = Problem(gdn, lens, T=T, window=window, heads=heads, heads_kv=2, seed=21, **shape)
+    kinds = torch.tensor([float("nan"), float("inf"), float("-inf")], device="cuda").bfloat16()
+    for b, n in enumerate(lens):
+        for j in range(max(0, n - T - window + 1 if window else n - T), n):
+            row = p.v[p.own_pages[b][j // p.page], j % p.page]
+            row[:, (5 * j) % p.dv], row[:, (5 * j + 11) % p.dv] = kinds[j % 3], kinds[(j // 3) % 3]
+    p.call()
+    torch.cuda.synchronize()
+    assert p.status.item() == 0
+    for b in range(len(lens)):
+        o, lse, to, tl = p.expected(b)
+        got, got_lse = p.o[b].double(), p.lse[b].double()
+        number = torch.isfinite(o)
+        assert torch.equal(torch.isnan(got), torch.isnan(o)) and torch.equal(got[~number].nan_to_num(0, 1, -1), o[~number].nan_to_num(0, 1, -1))
+        assert bool(((got - o).abs() <= to)[number].all())
+        assert bool(((got_lse == lse) | ((got_lse - lse).abs() <= tl)).all())
+
+
+def test_a_spoiled_value_costs_little(gdn):
+    """A request of 40,000 positions with NaN in its newest value takes no more than a few times what it takes without."""
+    took = []
+    for spoiled in (False, True):
+        p = Problem(gdn, [40000, 30000], T=4, heads=16, heads_kv=1, dk=576, dv=512, page=64, latent=True, seed=22)
+        if spoiled:
+            p.k[p.own_pages[0][39999 // 64], 39999 % 64, 0, 100] = float("nan")
+        p.call()
+        torch.cuda.synchronize()
+        begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        begin.record()
+        for _ in range(20):
+            p.call()
+        end.record()
+        torch.cuda.synchronize()
+        took.append(begin.elapsed_time(end))
+    assert took[1] < 4 * took[0], took
