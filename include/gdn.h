@@ -445,8 +445,8 @@ typedef struct gdn_attn {
  * A query that sees nothing (p < 0, or no page of it is usable) gets o = 0 and
  * lse = -inf. kv_len < 0 is padding: its rows are left unchanged. A length past max_pages
  * pages skips the request (GDN_STATUS_BAD_LEN, rows unchanged). A page outside
- * [0, num_pages) is left out (GDN_STATUS_BAD_PAGE). What the pages hold in positions that
- * no query of the request sees has no influence, NaN included.
+ * [0, num_pages) is left out (GDN_STATUS_BAD_PAGE). What the pages hold in positions that a
+ * query does not see has no influence on it, NaN included, whatever its other positions see.
  * After GDN_STATUS_TIMEOUT, elements of o and lse that were to come of the work that was given up
  * are left as they were (of a latent row perhaps one half of o); all others are right.
  * Scores, softmax and sums are fp32; each weight is rounded to bf16 where it meets the

@@ -10,15 +10,16 @@
 //   O^T [dv x N] += V^T [dv x 128] P^T [128 x N]                 A = V as it lies in memory (its
 //                                                                rows run along dv), B from shared
 //
-// So neither K nor V is transposed or padded, the accumulators take (2 + dv / 128) N columns of
-// TMEM, and a query group of 4 or 16 costs the same as it streams by.
+// So neither K nor V is transposed or padded, and a query group of 4 or 16 costs the same as it
+// streams by. The accumulators take 2 N columns of TMEM for two tiles' scores, and N for every 128
+// value elements of this CTA (64 count as 128) and every softmax team.
 //
 // One CTA an SM. Warp 0 gathers pages by TMA into a ring of slots (128 positions x 64 or 128
 // elements, 128-byte swizzle; pages of 16 .. 128 positions are boxes of a slot). Warp 1 issues
 // the MMAs: scores of tile i + 1 before values of tile i (over latent rows, whichever is ready),
-// so the tensor core works while the softmax does. Warps 2 and 3 lay out the next unit's queries. The other warps are the softmax,
-// four for every 16 columns: one thread a position; sums of weights stay in the threads until
-// the unit ends. The reference is the maximum of the tile that set it, times 2^8; it is raised
+// so the tensor core works while the softmax does. Warps 2 and 3 lay out the next unit's queries.
+// The other warps are the softmax, four for every 16 columns: one thread a position; sums of
+// weights stay in the threads until the unit ends. The reference is the maximum of the tile that set it, times 2^8; it is raised
 // (and O^T rescaled in TMEM) only where a score passes it, so most tiles need one barrier and no
 // reduction, and no weight is above 1.
 //
@@ -31,14 +32,23 @@
 // two is the same in either order) and each its half of O^T. No byte of the cache and no product
 // is taken twice.
 //
+// Values that a product must not meet: the tensor core multiplies a weight of zero too, and 0 x NaN is
+// NaN. Positions that no column sees are zeroed in shared memory; of those that some columns see and
+// others do not (several positions a request: MULTI, a kernel of its own) NaN and infinities are
+// taken out, and added at the unit's end for the columns that see them. 32 requests x 4 positions x 16
+// heads on latent rows: 38.5 us, 115 where every request's newest value holds NaN.
+//
 // What bounds it, and what it takes (bf16 cache, one GB300):
-//   full batch, 128 requests x 32 heads over 8 kv heads of 128, 2.17 GB: 321 us, 6.7 TB/s: HBM.
+//   full batch, 128 requests x 32 heads over 8 kv heads of 128, 2.17 GB: 315 to 327 us by the box,
+//     6.6 to 6.9 TB/s: HBM. The same on 2 kv heads of 256, 1.08 GB: 169 us, 6.4 TB/s.
 //   one request of 131,071 positions, same heads, 0.54 GB: 86 us, 6.2 TB/s: HBM, start and join.
-//   128 requests x 32 heads on latent rows, 0.62 GB: 114 us, 5.4 TB/s: a tile's chain of load,
+//   128 requests x 32 heads on latent rows, 0.62 GB: 112 us, 5.5 TB/s: a tile's chain of load,
 //     scores, exchange, softmax and values over a ring of two and a half tiles.
-//   4 requests x 128 heads on latent rows, 65,535 positions: 144 us for two passes of 64 columns
+//   4 requests x 128 heads on latent rows, 65,535 positions: 141 us for two passes of 64 columns
 //     (0.5 PFLOP/s): the same chain, 1850 cycles of it the exchange of 32 KB a tile.
-//   one request, 16 heads over 2 kv heads of 256, 1021 positions: 8.9 us with the join: latency.
+//   one request, 16 heads over 2 kv heads of 256, 1021 positions: 9.1 us with the join: latency.
+//   64 requests x 4 positions, 16 heads over 2 kv heads of 256, 0.28 GB: 55 us, 5.0 TB/s: 64 columns
+//     leave a ring of one tile, so loads, scores and values of neighbouring tiles hardly overlap.
 // The MMAs themselves take 34 to 42 cycles each at 16 to 64 columns, in every operand layout
 // tried, and are not what bounds any of these.
 #include "gdn_attn.cuh"

@@ -59,8 +59,8 @@ __device__ __forceinline__ void find_rows(const int32_t* sums, int n, const int 
 // pages. Where outputs are the inputs' own arrays (in_place), no CTA may write before all have
 // read: the grid is one cluster then, with its barrier in between.
 // Bound by instructions for prompts: a token costs a search over the sums and a division, so
-// they want many SMs (512 requests, 131,000 tokens, pages of 16: 6.6 us; 25 us on one cluster of
-// 8 CTAs). Bound by latency for a decode step (256 requests: 3.8 us in one CTA).
+// they want many SMs (512 requests, 131,000 tokens, pages of 16: 6.5 us; 21 us in place, on one
+// cluster of 8 CTAs). Bound by latency for a decode step (256 requests: 3.8 us in one CTA).
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) gdn_kv_plan_kernel(const KvPlanParams p) {
   extern __shared__ int32_t sm[];
