@@ -120,6 +120,8 @@ extern "C" {
                                       wait that runs out skips the slice that saw it: the other slice
                                       of the head may still commit. Same results as without the flag
                                       up to the order of the column sums */
+#define GDN_DT_SOFTPLUS (1u << 11) /* gdn_ssm: the step is softplus(dt + dt_bias); else dt + dt_bias itself */
+#define GDN_CONV_SILU (1u << 12)   /* gdn_conv: SiLU after the convolution */
 #define GDN_TEST_STARVE_WAIT (1u << 31) /* test only: the decode kernels expect 16 bytes more than
                                            the first tile copy delivers, so that bounded wait runs
                                            out (about a second) and the call reports
@@ -481,6 +483,121 @@ int gdn_attn_starve_wait(const gdn_paged_kv *kv, const gdn_attn *attn, int32_t w
 
 /* Bytes of workspace for a call of either with this cache, batch, T and H. Host only. */
 int gdn_attn_workspace(const gdn_paged_kv *kv, int32_t batch, int32_t num_tokens, int32_t num_heads, size_t *bytes);
+
+/* ---- selective state space layers ------------------------------------------------------
+ *
+ * The other recurrent layer of hybrid stacks: every channel d of a token keeps a state
+ * h[d][0..N) of its own, with a diagonal decay whose step depends on the token. Around the
+ * layer's matrix products it runs
+ *
+ *   gdn_add_rms_norm   residual and norm in front of a projection (of any layer), in 8 bits if wanted;
+ *   gdn_causal_conv    the short convolution of the projected channels u, prompts and single tokens;
+ *                      b, c and dt are projections of its output, so it stands on its own;
+ *   gdn_ssm_scan       prompts: the state over T positions, and every position's readout;
+ *   gdn_ssm_step       one new token of every request.
+ *
+ * The conventions at the top of this file hold: slot-indexed pools, padding, status bits, streams,
+ * no allocation. Outputs overlap no input of their call, but for the pools and the residual, which
+ * are updated in place. All sums, states, steps and norms are fp32.
+ */
+#define GDN_TYPE_BF16 0
+#define GDN_TYPE_FP32 1
+#define GDN_TYPE_E4M3 2
+typedef struct gdn_norm {
+  int32_t rows, width;     /* width: a multiple of 8, at most 16384 */
+  int32_t x_type;          /* GDN_TYPE_BF16 or GDN_TYPE_FP32 */
+  int32_t residual_type;   /* the same two */
+  int32_t o_type;          /* any of the three */
+  int32_t group;           /* GDN_TYPE_E4M3: channels that share a scale, 128, or 0: the whole row */
+  float eps;
+  const void *x;           /* [rows][width], rows x_stride elements apart */
+  int64_t x_stride;        /* rows start on 16-byte boundaries, here and in residual */
+  void *residual;          /* [rows][width], rows residual_stride apart, updated in place; NULL: none */
+  int64_t residual_stride;
+  const float *weight;     /* [width] or NULL: 1 */
+  void *o;                 /* [rows][width] */
+  float *scales;           /* GDN_TYPE_E4M3: [rows][ceil(width / group)], or [rows] */
+} gdn_norm;
+
+/*
+ * gdn_add_rms_norm -- r = x + residual (x alone without one), residual = r rounded to its type,
+ *   o = r / sqrt(mean r^2 + eps) * weight, of the r that is not rounded yet.
+ * In 8 bits each scale is s = max(m, 1e-30) / 448, m the largest |o| of its channels, and o holds
+ * the e4m3 value next to o / s: o is about s times what is stored. A NaN makes its row NaN, an
+ * infinity makes itself NaN and the rest of its row 0, as the formula says, and a scale whose
+ * channels hold NaN is NaN. Squares are summed in fp32: a sum past its range (values above about
+ * 1e19) counts as infinite.
+ */
+int gdn_add_rms_norm(const gdn_norm *norm, void *stream);
+
+typedef struct gdn_conv {
+  int32_t batch, num_tokens; /* B, T */
+  int32_t channels;          /* a multiple of 8 */
+  int32_t num_slots;
+  uint32_t flags;            /* GDN_QKV_BF16: x, pool and o are bf16, else fp32; GDN_CONV_SILU */
+  const void *x;             /* [B][T][channels] in x_strides; rows on 16-byte boundaries */
+  int64_t x_strides[2];      /* elements between requests, tokens */
+  const float *w;            /* [channels][4]; column 3 multiplies the current token; 16-byte aligned, like bias */
+  const float *bias;         /* [channels] or NULL */
+  void *pool;                /* [num_slots][channels][3], column 0 oldest, as gdn_inputs.conv_pool; in place */
+  const int32_t *slot;       /* [B]; < 0: padding */
+  const int32_t *seq_lens;   /* [B] in [0, T], or NULL: all T */
+  void *o;                   /* [B][T][channels] */
+} gdn_conv;
+
+/*
+ * gdn_causal_conv -- o_t = f(bias + sum_j w[.][j] x_{t - 3 + j}) with f = SiLU or nothing, for prompts
+ * (T positions) and single tokens (T = 1). The inputs before position 0 are the slot's row of
+ * the pool, which afterwards holds the last three inputs of (old row, prompt), copied bit for bit:
+ * what the next call, or a fused-conv decode with the same channels, continues from. Positions past
+ * seq_lens are not read and their rows of o are left unchanged; a request of length 0 changes nothing.
+ * A length outside [0, T] skips the request with GDN_STATUS_BAD_LEN.
+ */
+int gdn_causal_conv(const gdn_conv *conv, int32_t *status, void *stream);
+
+typedef struct gdn_ssm {
+  int32_t batch, num_tokens; /* B, T (gdn_ssm_step: 1) */
+  int32_t channels;          /* D, a multiple of 8 * num_groups */
+  int32_t state_size;        /* N: 8, 16, 32 or 64 */
+  int32_t num_groups;        /* G: channel d reads row d / (D / G) of b and c */
+  int32_t num_slots;
+  uint32_t flags;            /* GDN_QKV_BF16: u, dt, b, c, z and y are bf16, else fp32; GDN_DT_SOFTPLUS */
+  const void *u;             /* [B][T][D]: strides in elements between requests and tokens; every row of */
+  int64_t u_strides[2];      /* u, dt, b, c and z starts on a 16-byte boundary */
+  const void *dt;            /* [B][T][D] */
+  int64_t dt_strides[2];
+  const void *b;             /* [B][T][G][N]: strides between requests, tokens and groups */
+  int64_t b_strides[3];
+  const void *c;
+  int64_t c_strides[3];
+  const void *z;             /* [B][T][D] or NULL: no gate */
+  int64_t z_strides[2];
+  const float *a;            /* [D][N], finite, <= 0 for a state that decays; 16-byte aligned like skip and dt_bias */
+  const float *skip;         /* [D] or NULL: 0 */
+  const float *dt_bias;      /* [D] or NULL: 0 */
+  float *state;              /* [num_slots][D][N], in place */
+  const int32_t *slot;       /* [B]; < 0: padding */
+  const int32_t *seq_lens;   /* [B] in [0, T], or NULL: all T */
+  void *y;                   /* [B][T][D] */
+} gdn_ssm;
+
+/*
+ * gdn_ssm_scan -- the recurrence over the prompts, in place on the requests' rows of state:
+ *   s_t = softplus(dt_t + dt_bias)                            (GDN_DT_SOFTPLUS)
+ *   h_t[d][n] = exp(s_t[d] a[d][n]) h_{t-1}[d][n] + s_t[d] u_t[d] b_t[g][n]
+ *   y_t[d] = (sum_n c_t[g][n] h_t[d][n] + skip[d] u_t[d]) silu(z_t[d])
+ * Positions past seq_lens are not read and their rows of y are left unchanged; a request of length
+ * 0 changes nothing. A length outside [0, T] skips the request with GDN_STATUS_BAD_LEN.
+ * workspace: gdn_ssm_workspace() bytes, 16-byte aligned (NULL where that is 0); its contents need
+ * no care, but two calls that may run at the same time need one each.
+ */
+int gdn_ssm_scan(const gdn_ssm *ssm, void *workspace, size_t workspace_bytes, int32_t *status, void *stream);
+
+/* gdn_ssm_step -- the same for one token of every request (num_tokens = 1, seq_lens NULL). */
+int gdn_ssm_step(const gdn_ssm *ssm, int32_t *status, void *stream);
+
+/* Bytes of workspace for a gdn_ssm_scan of these sizes (0 is an answer). Host only. */
+int gdn_ssm_workspace(int32_t batch, int32_t num_tokens, int32_t channels, int32_t state_size, size_t *bytes);
 
 #ifdef __cplusplus
 }

@@ -43,17 +43,25 @@ ULOG_BF16 = 1 << 7
 GATE_KDA = 1 << 8
 OUT_NORM_GATE = 1 << 9
 SPLIT_DV = 1 << 10
+DT_SOFTPLUS = 1 << 11
+CONV_SILU = 1 << 12
 TEST_STARVE_WAIT = 1 << 31
 
 # waits of gdn_attn_starve_wait
 STARVE_LOAD = 1
 STARVE_WEIGHTS = 2
 
+# types of gdn_add_rms_norm
+TYPE_BF16 = 0
+TYPE_FP32 = 1
+TYPE_E4M3 = 2
+
 # every symbol include/gdn.h declares
 EXPORTS = ("gdn_version", "gdn_strerror", "gdn_last_error", "gdn_conv_l2norm", "gdn_decode_dense",
            "gdn_decode_append", "gdn_decode_merge", "gdn_decode_step", "gdn_decode_verify",
            "gdn_prefill", "gdn_log_bytes", "gdn_slot_reset", "gdn_kv_plan", "gdn_kv_release",
-           "gdn_kv_append", "gdn_attn_decode", "gdn_latent_decode", "gdn_attn_starve_wait", "gdn_attn_workspace")
+           "gdn_kv_append", "gdn_attn_decode", "gdn_latent_decode", "gdn_attn_starve_wait", "gdn_attn_workspace",
+           "gdn_add_rms_norm", "gdn_causal_conv", "gdn_ssm_scan", "gdn_ssm_step", "gdn_ssm_workspace")
 
 
 class Dims(ctypes.Structure):
@@ -100,6 +108,34 @@ class Attn(ctypes.Structure):
                 ("kv_len", ctypes.c_void_p), ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p)]
 
 
+# The structs of the selective state space layers' calls, passed in the same way.
+class Norm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("width", ctypes.c_int32), ("x_type", ctypes.c_int32),
+                ("residual_type", ctypes.c_int32), ("o_type", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_int64), ("weight", ctypes.c_void_p),
+                ("o", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class Conv(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("num_tokens", ctypes.c_int32), ("channels", ctypes.c_int32),
+                ("num_slots", ctypes.c_int32), ("flags", ctypes.c_uint32), ("x", ctypes.c_void_p),
+                ("x_strides", ctypes.c_int64 * 2), ("w", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("pool", ctypes.c_void_p), ("slot", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("o", ctypes.c_void_p)]
+
+
+class Ssm(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("num_tokens", ctypes.c_int32), ("channels", ctypes.c_int32),
+                ("state_size", ctypes.c_int32), ("num_groups", ctypes.c_int32), ("num_slots", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("u", ctypes.c_void_p), ("u_strides", ctypes.c_int64 * 2),
+                ("dt", ctypes.c_void_p), ("dt_strides", ctypes.c_int64 * 2), ("b", ctypes.c_void_p),
+                ("b_strides", ctypes.c_int64 * 3), ("c", ctypes.c_void_p), ("c_strides", ctypes.c_int64 * 3),
+                ("z", ctypes.c_void_p), ("z_strides", ctypes.c_int64 * 2), ("a", ctypes.c_void_p),
+                ("skip", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p), ("state", ctypes.c_void_p),
+                ("slot", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("y", ctypes.c_void_p)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -144,6 +180,16 @@ def _declare(lib):
     lib.gdn_attn_starve_wait.argtypes = [vp, vp, i32, vp, ctypes.c_size_t, vp, vp]
     lib.gdn_attn_workspace.restype = ctypes.c_int
     lib.gdn_attn_workspace.argtypes = [vp, i32, i32, i32, vp]
+    lib.gdn_add_rms_norm.restype = ctypes.c_int
+    lib.gdn_add_rms_norm.argtypes = [vp, vp]
+    lib.gdn_causal_conv.restype = ctypes.c_int
+    lib.gdn_causal_conv.argtypes = [vp, vp, vp]
+    lib.gdn_ssm_scan.restype = ctypes.c_int
+    lib.gdn_ssm_scan.argtypes = [vp, vp, ctypes.c_size_t, vp, vp]
+    lib.gdn_ssm_step.restype = ctypes.c_int
+    lib.gdn_ssm_step.argtypes = [vp, vp, vp]
+    lib.gdn_ssm_workspace.restype = ctypes.c_int
+    lib.gdn_ssm_workspace.argtypes = [i32, i32, i32, i32, vp]
     return lib
 
 

@@ -9,6 +9,7 @@
 #include "gdn.h"
 #include "gdn_internal.h"
 #include "gdn_kv.h"
+#include "gdn_ssm.h"
 
 namespace {
 
@@ -297,6 +298,42 @@ int attend(const gdn_paged_kv* kv, const gdn_attn* a, void* workspace, size_t wo
   return launched(gdn::launch_attn(plan, p, static_cast<cudaStream_t>(stream)), name);
 }
 
+// ---- selective state space layers ----------------------------------------------------------
+// Rows of a [B][T][..] operand: 16-byte aligned, with strides that keep its rows so.
+template <int N>
+bool rows_ok(const void* p, const int64_t* strides, const int32_t (&extents)[N], bool bf16) {
+  return aligned16(p) && strides_ok(strides, extents, bf16 ? 8 : 4);
+}
+
+int check_ssm(const gdn_ssm* s) {
+  if (s == nullptr) return fail(GDN_ERR_INVALID_ARG, "ssm is NULL");
+  if (s->batch < 0 || s->num_tokens < 0 || s->channels <= 0 || s->num_groups <= 0 || s->num_slots <= 0)
+    return fail(GDN_ERR_INVALID_ARG, "batch and num_tokens must be >= 0, channels, num_groups and num_slots > 0");
+  if ((s->flags & ~(GDN_QKV_BF16 | GDN_DT_SOFTPLUS)) != 0u)
+    return fail(GDN_ERR_INVALID_ARG, "a gdn_ssm knows GDN_QKV_BF16 and GDN_DT_SOFTPLUS only");
+  if (s->state_size != 8 && s->state_size != 16 && s->state_size != 32 && s->state_size != 64)
+    return fail(GDN_ERR_UNSUPPORTED, "state_size %d not built (8, 16, 32, 64)", s->state_size);
+  if (s->num_groups > s->channels / 8 || s->channels % (8 * s->num_groups) != 0)
+    return fail(GDN_ERR_UNSUPPORTED, "channels %d: not a multiple of 8 in each of %d groups", s->channels, s->num_groups);
+  if (static_cast<long long>(s->batch) * s->num_tokens > 0x7fffffffLL ||
+      static_cast<long long>(s->batch) * s->channels * s->state_size > 0x7fffffffLL * 32)
+    return fail(GDN_ERR_UNSUPPORTED, "batch * num_tokens must stay below 2^31, batch * channels * state_size below 2^36");
+  if (s->batch == 0 || s->num_tokens == 0) return GDN_OK;
+  if (s->u == nullptr || s->dt == nullptr || s->b == nullptr || s->c == nullptr || s->a == nullptr || s->state == nullptr ||
+      s->slot == nullptr || s->y == nullptr)
+    return fail(GDN_ERR_INVALID_ARG, "u, dt, a, b, c, state, slot and y are required");
+  const bool bf16 = (s->flags & GDN_QKV_BF16) != 0u;
+  const int32_t two[2] = {s->batch, s->num_tokens}, three[3] = {s->batch, s->num_tokens, s->num_groups};
+  if (!rows_ok(s->u, s->u_strides, two, bf16) || !rows_ok(s->dt, s->dt_strides, two, bf16) ||
+      !rows_ok(s->b, s->b_strides, three, bf16) || !rows_ok(s->c, s->c_strides, three, bf16) ||
+      (s->z != nullptr && !rows_ok(s->z, s->z_strides, two, bf16)))
+    return fail(GDN_ERR_UNSUPPORTED,
+                "u, dt, b, c and z must be 16-byte aligned, with strides >= 0 that are multiples of 16 bytes");
+  if (!aligned16(s->a) || !aligned16(s->skip) || !aligned16(s->dt_bias) || !aligned16(s->state) || !aligned16(s->y))
+    return fail(GDN_ERR_UNSUPPORTED, "a, skip, dt_bias, state and y must be 16-byte aligned");
+  return GDN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -572,6 +609,81 @@ int gdn_attn_workspace(const gdn_paged_kv* kv, int32_t batch, int32_t num_tokens
   if (cols > kMaxAttnCols)
     return fail(GDN_ERR_UNSUPPORTED, "num_tokens * num_heads / num_kv_heads must be at most %d", kMaxAttnCols);
   *bytes = gdn::attn_workspace_bytes(gdn::attn_plan(*kv, static_cast<int>(cols)), kv->dv);
+  return GDN_OK;
+}
+
+int gdn_add_rms_norm(const gdn_norm* norm, void* stream) {
+  if (norm == nullptr) return fail(GDN_ERR_INVALID_ARG, "norm is NULL");
+  const gdn_norm& n = *norm;
+  if (n.rows < 0 || n.width <= 0) return fail(GDN_ERR_INVALID_ARG, "rows must be >= 0 and width > 0");
+  auto wide = [](int type) { return type == GDN_TYPE_BF16 || type == GDN_TYPE_FP32; };
+  if (!wide(n.x_type) || !wide(n.residual_type) || !(wide(n.o_type) || n.o_type == GDN_TYPE_E4M3))
+    return fail(GDN_ERR_INVALID_ARG, "x_type and residual_type are bf16 or fp32, o_type one of these or e4m3");
+  if (n.group != 0 && (n.group != gdn::kNormGroup || n.o_type != GDN_TYPE_E4M3))
+    return fail(GDN_ERR_UNSUPPORTED, "group is 0, or %d with an e4m3 output", gdn::kNormGroup);
+  if (n.width % 8 != 0 || n.width > gdn::kMaxNormWidth)
+    return fail(GDN_ERR_UNSUPPORTED, "width %d not built (a multiple of 8, at most %d)", n.width, gdn::kMaxNormWidth);
+  if (n.rows == 0) return GDN_OK;
+  if (n.x == nullptr || n.o == nullptr || (n.o_type == GDN_TYPE_E4M3 && n.scales == nullptr))
+    return fail(GDN_ERR_INVALID_ARG, "x, o and, with an e4m3 output, scales are required");
+  const int32_t rows[1] = {n.rows};
+  if (!rows_ok(n.x, &n.x_stride, rows, n.x_type == GDN_TYPE_BF16) ||
+      (n.residual != nullptr && !rows_ok(n.residual, &n.residual_stride, rows, n.residual_type == GDN_TYPE_BF16)) ||
+      !aligned16(n.weight) || !aligned16(n.o))
+    return fail(GDN_ERR_UNSUPPORTED, "x, residual, weight and o must be 16-byte aligned, with row strides >= 0 that are multiples of 16 bytes");
+  if (n.residual != nullptr && n.rows > 1 && n.residual_stride < n.width)
+    return fail(GDN_ERR_INVALID_ARG, "rows of residual overlap");
+  return launched(gdn::launch_add_rms_norm(n, static_cast<cudaStream_t>(stream)), "gdn_add_rms_norm");
+}
+
+int gdn_causal_conv(const gdn_conv* conv, int32_t* status, void* stream) {
+  if (conv == nullptr) return fail(GDN_ERR_INVALID_ARG, "conv is NULL");
+  const gdn_conv& c = *conv;
+  if (c.batch < 0 || c.num_tokens < 0 || c.channels <= 0 || c.num_slots <= 0)
+    return fail(GDN_ERR_INVALID_ARG, "batch and num_tokens must be >= 0, channels and num_slots > 0");
+  if ((c.flags & ~(GDN_QKV_BF16 | GDN_CONV_SILU)) != 0u)
+    return fail(GDN_ERR_INVALID_ARG, "a gdn_conv knows GDN_QKV_BF16 and GDN_CONV_SILU only");
+  if (c.channels % 8 != 0) return fail(GDN_ERR_UNSUPPORTED, "channels %d: not a multiple of 8", c.channels);
+  if (static_cast<long long>(c.batch) * c.num_tokens > 0x7fffffffLL ||
+      static_cast<long long>(c.batch) * c.num_tokens > (1LL << 38) / c.channels)
+    return fail(GDN_ERR_UNSUPPORTED, "batch * num_tokens must stay below 2^31, times channels at most 2^38");
+  if (c.batch == 0 || c.num_tokens == 0) return GDN_OK;
+  if (c.x == nullptr || c.w == nullptr || c.pool == nullptr || c.slot == nullptr || c.o == nullptr)
+    return fail(GDN_ERR_INVALID_ARG, "x, w, pool, slot and o are required");
+  const int32_t two[2] = {c.batch, c.num_tokens};
+  if (!rows_ok(c.x, c.x_strides, two, (c.flags & GDN_QKV_BF16) != 0u))
+    return fail(GDN_ERR_UNSUPPORTED, "x must be 16-byte aligned, with strides >= 0 that are multiples of 16 bytes");
+  if (!aligned16(c.w) || !aligned16(c.bias) || !aligned16(c.pool) || !aligned16(c.o))
+    return fail(GDN_ERR_UNSUPPORTED, "w, bias, pool and o must be 16-byte aligned");
+  if (c.o == c.x) return fail(GDN_ERR_INVALID_ARG, "o overlaps x");
+  return launched(gdn::launch_causal_conv({c, status}, static_cast<cudaStream_t>(stream)), "gdn_causal_conv");
+}
+
+int gdn_ssm_scan(const gdn_ssm* ssm, void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
+  if (int rc = check_ssm(ssm)) return rc;
+  if (ssm->batch == 0 || ssm->num_tokens == 0) return GDN_OK;
+  const size_t need = gdn::ssm_workspace_bytes(ssm->batch, ssm->num_tokens, ssm->channels, ssm->state_size);
+  if (workspace_bytes < need || (need > 0 && workspace == nullptr))
+    return fail(GDN_ERR_INVALID_ARG, "workspace of %zu bytes, %zu are needed (gdn_ssm_workspace)", workspace == nullptr ? 0 : workspace_bytes, need);
+  if (need > 0 && !aligned16(workspace)) return fail(GDN_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");
+  return launched(gdn::launch_ssm_scan({*ssm, status}, workspace, static_cast<cudaStream_t>(stream)), "gdn_ssm_scan");
+}
+
+int gdn_ssm_step(const gdn_ssm* ssm, int32_t* status, void* stream) {
+  if (int rc = check_ssm(ssm)) return rc;
+  if (ssm->num_tokens != 1 || ssm->seq_lens != nullptr)
+    return fail(GDN_ERR_INVALID_ARG, "gdn_ssm_step takes one token of every request: num_tokens 1, seq_lens NULL");
+  if (ssm->batch == 0) return GDN_OK;
+  return launched(gdn::launch_ssm_step({*ssm, status}, static_cast<cudaStream_t>(stream)), "gdn_ssm_step");
+}
+
+int gdn_ssm_workspace(int32_t batch, int32_t num_tokens, int32_t channels, int32_t state_size, size_t* bytes) {
+  if (bytes == nullptr) return fail(GDN_ERR_INVALID_ARG, "bytes is NULL");
+  if (batch < 0 || num_tokens < 0 || channels <= 0)
+    return fail(GDN_ERR_INVALID_ARG, "batch and num_tokens must be >= 0, channels > 0");
+  if (state_size != 8 && state_size != 16 && state_size != 32 && state_size != 64)
+    return fail(GDN_ERR_UNSUPPORTED, "state_size %d not built (8, 16, 32, 64)", state_size);
+  *bytes = gdn::ssm_workspace_bytes(batch, num_tokens, channels, state_size);
   return GDN_OK;
 }
 

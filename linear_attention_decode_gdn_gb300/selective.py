@@ -1,0 +1,165 @@
+"""Python entry points of selective state space layers, with the C-ABI's names.
+
+As in ``paged``: each function checks what the pointers cannot show (types, shapes, strides,
+devices), packs them into the C struct and calls the matching ``gdn_*`` function of libgdn on the
+current stream. All tensors of a call live on the current device. Where a tensor is wrong the call
+raises ``ValueError`` before anything is launched; what libgdn refuses raises ``GDNError``.
+"""
+from __future__ import annotations
+
+import ctypes
+import struct
+
+import torch
+
+from . import _abi
+from ._abi import GDN_OK, check
+from .paged import _current_device, _ints, _not_here, _status, _stream
+
+_pack_norm = struct.Struct("=6if4xQqQqQQQ").pack        # gdn_norm
+_pack_conv = struct.Struct("=4iI4xQ2q6Q").pack          # gdn_conv
+_pack_ssm = struct.Struct("=6iI4xQ2qQ2qQ3qQ3qQ2q7Q").pack  # gdn_ssm
+_BF16, _FP32, _E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+_TYPES = {_BF16: _abi.TYPE_BF16, _FP32: _abi.TYPE_FP32, _E4M3: _abi.TYPE_E4M3}
+
+
+def _rows(t, shape, dtype, what: str, device: int):
+    """Address and leading strides of an operand whose last dimension is contiguous."""
+    strides = t.stride()
+    if t.dtype is not dtype or t.shape != shape or strides[-1] != 1 or t.get_device() != device:
+        raise ValueError(f"{what}: {dtype} {tuple(shape)} on the GPU beside the others, its last stride 1, got {t.dtype} "
+                         f"{tuple(t.shape)} in strides {tuple(strides)} on {t.device}")
+    return t.data_ptr(), *strides[:-1]
+
+
+def _whole(t, shape, dtype, what: str, device: int) -> int:
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{what}: contiguous {dtype} {tuple(shape)} on the GPU beside the others, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _input(t, dims, what: str):
+    """Type, shape and device of a call's first operand."""
+    at = t.get_device()
+    if at < 0 or at != _current_device():
+        raise _not_here(at, what)
+    if (t.dtype is not _BF16 and t.dtype is not _FP32) or t.dim() not in dims:
+        raise ValueError(f"{what}: bf16 or fp32, with {' or '.join(map(str, dims))} dimensions, got {t.dtype} {tuple(t.shape)}")
+    return t.dtype, t.shape, at
+
+
+def add_rms_norm(x, o, *, residual=None, weight=None, eps=1e-6, scales=None, group=0, stream=None):
+    """residual += x, and o = RMSNorm of that sum (of x without a residual) times weight [width]. x, residual
+    [rows, width] bf16 or fp32, in rows of any distance; o [rows, width] bf16, fp32 or float8_e4m3fn, which needs
+    scales: fp32 [rows, ceil(width / 128)] with group=128, [rows, 1] or [rows] with group=0."""
+    dtype, shape, at = _input(x, (2,), "x")
+    rows, width = shape
+    out = o.dtype
+    if out not in _TYPES:
+        raise ValueError(f"o: bf16, fp32 or float8_e4m3fn, got {out}")
+    r_type, r_ptr, r_row = dtype, 0, 0
+    if residual is not None:
+        r_type = residual.dtype
+        if r_type is not _BF16 and r_type is not _FP32:
+            raise ValueError(f"residual: bf16 or fp32, got {r_type}")
+        r_ptr, r_row = _rows(residual, shape, r_type, "residual", at)
+    scale_ptr = 0
+    if out is _E4M3:
+        if scales is None:
+            raise ValueError("o in 8 bits needs scales")
+        want = (rows, -(-width // group)) if group else (rows, 1)
+        scale_ptr = _whole(scales, (rows,) if not group and scales.dim() == 1 else want, _FP32, "scales", at)
+    elif scales is not None or group:
+        raise ValueError("scales and group belong to an output in 8 bits")
+    x_ptr, x_row = _rows(x, shape, dtype, "x", at)
+    rc = _abi.load().gdn_add_rms_norm(
+        _pack_norm(rows, width, _TYPES[dtype], _TYPES[r_type], _TYPES[out], group, eps, x_ptr, x_row, r_ptr, r_row,
+                   0 if weight is None else _whole(weight, (width,), _FP32, "weight", at), _whole(o, shape, out, "o", at), scale_ptr),
+        _stream(stream, at))
+    if rc != GDN_OK:
+        check(rc, "gdn_add_rms_norm")
+
+
+def causal_conv(x, weight, pool, slot, o, *, bias=None, silu=True, seq_lens=None, status=None, stream=None):
+    """o = the causal convolution of x [batch, T, channels] (or [batch, channels]: one token each) with weight
+    [channels, 4], plus bias [channels], through SiLU. pool [slots, channels, 3], of x's type, holds the three inputs
+    before each request's first position in row slot[b] and is left with the last three."""
+    dtype, shape, at = _input(x, (2, 3), "x")
+    x_ptr, *strides = _rows(x, shape, dtype, "x", at)
+    if len(shape) == 2:
+        (batch, channels), tokens = shape, 1
+        strides.append(0)
+    else:
+        batch, tokens, channels = shape
+    slots = pool.shape[0]
+    rc = _abi.load().gdn_causal_conv(
+        _pack_conv(batch, tokens, channels, slots, (_abi.QKV_BF16 if dtype is _BF16 else 0) | (_abi.CONV_SILU if silu else 0),
+                   x_ptr, *strides, _whole(weight, (channels, 4), _FP32, "weight", at),
+                   0 if bias is None else _whole(bias, (channels,), _FP32, "bias", at),
+                   _whole(pool, (slots, channels, 3), dtype, "pool", at), _ints(slot, batch, "slot", at),
+                   0 if seq_lens is None else _ints(seq_lens, batch, "seq_lens", at), _whole(o, shape, dtype, "o", at)),
+        None if status is None else _status(status, at), _stream(stream, at))
+    if rc != GDN_OK:
+        check(rc, "gdn_causal_conv")
+
+
+def ssm_workspace_bytes(batch: int, num_tokens: int, channels: int, state_size: int) -> int:
+    """Bytes of workspace that ssm_scan needs."""
+    out = ctypes.c_size_t()
+    check(_abi.load().gdn_ssm_workspace(batch, num_tokens, channels, state_size, ctypes.byref(out)), "gdn_ssm_workspace")
+    return out.value
+
+
+def _pack(dims, u, dt, a, b, c, state, slot, y, z, skip, dt_bias, softplus, seq_lens):
+    """The C struct of a scan (dims 3) or a step (dims 2), and the device."""
+    dtype, shape, at = _input(u, (dims,), "u")
+    channels, batch = shape[-1], shape[0]
+    if b.dim() != dims + 1 or state.dim() != 3:
+        raise ValueError(f"b: {dims + 1} dimensions [.., groups, state size]; state: [slots, channels, state size]")
+    groups, n = b.shape[-2:]
+    narrow = (*shape[:-1], groups, n)
+    u_at = _rows(u, shape, dtype, "u", at)
+    dt_at = _rows(dt, shape, dtype, "dt", at)
+    b_at = _rows(b, narrow, dtype, "b", at)
+    c_at = _rows(c, narrow, dtype, "c", at)
+    z_at = (0, 0, 0) if z is None else _rows(z, shape, dtype, "z", at)
+    tokens = 1
+    if dims == 2:  # no stride between the tokens of one
+        b_at, c_at = (*b_at[:2], 0, b_at[2]), (*c_at[:2], 0, c_at[2])
+        u_at, dt_at, z_at = (*u_at, 0), (*dt_at, 0), (*z_at[:2], 0)
+    else:
+        tokens = shape[1]
+    slots = state.shape[0]
+    return _pack_ssm(
+        batch, tokens, channels, n, groups, slots, (_abi.QKV_BF16 if dtype is _BF16 else 0) | (_abi.DT_SOFTPLUS if softplus else 0),
+        *u_at, *dt_at, *b_at, *c_at, *z_at, _whole(a, (channels, n), _FP32, "a", at),
+        0 if skip is None else _whole(skip, (channels,), _FP32, "skip", at),
+        0 if dt_bias is None else _whole(dt_bias, (channels,), _FP32, "dt_bias", at),
+        _whole(state, (slots, channels, n), _FP32, "state", at), _ints(slot, batch, "slot", at),
+        0 if seq_lens is None else _ints(seq_lens, batch, "seq_lens", at), _whole(y, shape, dtype, "y", at)), at
+
+
+def ssm_scan(u, dt, a, b, c, state, slot, y, workspace=None, *, z=None, skip=None, dt_bias=None, softplus=True, seq_lens=None,
+             status=None, stream=None):
+    """The selective recurrence over prompts: u, dt, z, y [batch, T, channels], b, c [batch, T, groups, N], a [channels, N],
+    skip, dt_bias [channels]; state [slots, channels, N] fp32 advances in place in the rows slot. workspace: a tensor
+    of ssm_workspace_bytes() or more."""
+    s, at = _pack(3, u, dt, a, b, c, state, slot, y, z, skip, dt_bias, softplus, seq_lens)
+    room = 0
+    if workspace is not None:
+        if workspace.get_device() != at or not workspace.is_contiguous():
+            raise ValueError("workspace: contiguous, on the GPU beside the others")
+        room = workspace.nbytes
+    rc = _abi.load().gdn_ssm_scan(s, workspace.data_ptr() if room else None, room, None if status is None else _status(status, at),
+                                  _stream(stream, at))
+    if rc != GDN_OK:
+        check(rc, "gdn_ssm_scan")
+
+
+def ssm_step(u, dt, a, b, c, state, slot, y, *, z=None, skip=None, dt_bias=None, softplus=True, status=None, stream=None):
+    """One token of every request: as ssm_scan, without the dimension of the positions."""
+    s, at = _pack(2, u, dt, a, b, c, state, slot, y, z, skip, dt_bias, softplus, None)
+    rc = _abi.load().gdn_ssm_step(s, None if status is None else _status(status, at), _stream(stream, at))
+    if rc != GDN_OK:
+        check(rc, "gdn_ssm_step")
