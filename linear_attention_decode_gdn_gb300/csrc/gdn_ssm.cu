@@ -82,10 +82,6 @@ cudaError_t launch_type(const SsmParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-size_t ssm_workspace_bytes(int32_t, int32_t, int32_t, int32_t) { return 0; }
-
-cudaError_t launch_ssm_scan(const SsmParams& p, void*, cudaStream_t stream) { return launch_ssm_step(p, stream); }
-
 cudaError_t launch_ssm_step(const SsmParams& p, cudaStream_t stream) {
   return (p.s.flags & GDN_QKV_BF16) != 0u ? launch_type<true>(p, stream) : launch_type<false>(p, stream);
 }

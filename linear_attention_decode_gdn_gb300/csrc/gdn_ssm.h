@@ -8,6 +8,7 @@
 #include <cuda_runtime_api.h>
 
 #include "gdn.h"
+#include "gdn_kv.h"
 
 namespace gdn {
 
