@@ -299,6 +299,8 @@ int attend(const gdn_paged_kv* kv, const gdn_attn* a, void* workspace, size_t wo
 }
 
 // ---- selective state space layers ----------------------------------------------------------
+constexpr long long kMaxPositions = 1LL << 30;  // of a call: a tile past the last fits 32 bits
+
 // Rows of a [B][T][..] operand: 16-byte aligned, with strides that keep its rows so.
 template <int N>
 bool rows_ok(const void* p, const int64_t* strides, const int32_t (&extents)[N], bool bf16) {
@@ -315,9 +317,9 @@ int check_ssm(const gdn_ssm* s) {
     return fail(GDN_ERR_UNSUPPORTED, "state_size %d not built (8, 16, 32, 64)", s->state_size);
   if (s->num_groups > s->channels / 8 || s->channels % (8 * s->num_groups) != 0)
     return fail(GDN_ERR_UNSUPPORTED, "channels %d: not a multiple of 8 in each of %d groups", s->channels, s->num_groups);
-  if (static_cast<long long>(s->batch) * s->num_tokens > 0x7fffffffLL ||
+  if (static_cast<long long>(s->batch) * s->num_tokens > kMaxPositions ||
       static_cast<long long>(s->batch) * s->channels * s->state_size > 0x7fffffffLL * 32)
-    return fail(GDN_ERR_UNSUPPORTED, "batch * num_tokens must stay below 2^31, batch * channels * state_size below 2^36");
+    return fail(GDN_ERR_UNSUPPORTED, "batch * num_tokens must be at most 2^30, batch * channels * state_size below 2^36");
   if (s->batch == 0 || s->num_tokens == 0) return GDN_OK;
   if (s->u == nullptr || s->dt == nullptr || s->b == nullptr || s->c == nullptr || s->a == nullptr || s->state == nullptr ||
       s->slot == nullptr || s->y == nullptr)
@@ -644,9 +646,9 @@ int gdn_causal_conv(const gdn_conv* conv, int32_t* status, void* stream) {
   if ((c.flags & ~(GDN_QKV_BF16 | GDN_CONV_SILU)) != 0u)
     return fail(GDN_ERR_INVALID_ARG, "a gdn_conv knows GDN_QKV_BF16 and GDN_CONV_SILU only");
   if (c.channels % 8 != 0) return fail(GDN_ERR_UNSUPPORTED, "channels %d: not a multiple of 8", c.channels);
-  if (static_cast<long long>(c.batch) * c.num_tokens > 0x7fffffffLL ||
+  if (static_cast<long long>(c.batch) * c.num_tokens > kMaxPositions ||
       static_cast<long long>(c.batch) * c.num_tokens > (1LL << 38) / c.channels)
-    return fail(GDN_ERR_UNSUPPORTED, "batch * num_tokens must stay below 2^31, times channels at most 2^38");
+    return fail(GDN_ERR_UNSUPPORTED, "batch * num_tokens must be at most 2^30, times channels at most 2^38");
   if (c.batch == 0 || c.num_tokens == 0) return GDN_OK;
   if (c.x == nullptr || c.w == nullptr || c.pool == nullptr || c.slot == nullptr || c.o == nullptr)
     return fail(GDN_ERR_INVALID_ARG, "x, w, pool, slot and o are required");

@@ -6,105 +6,104 @@
 #include "gdn_ssm.h"
 #include "gdn_vec.cuh"
 
+#include <type_traits>
+
 namespace gdn {
 
 namespace {
 
 constexpr int kWarps = 4;            // of a CTA; they have nothing in common
-constexpr float kLog2e = 1.44269504088896340736f;
-
-// ---- pairs of fp32, one instruction each ----------------------------------------------------
-using f32x2 = unsigned long long;
-__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
+// Two elements as they lie in memory.
+template <bool BF16>
+using Raw2 = typename std::conditional<BF16, uint32_t, float2>::type;
+template <bool BF16>
+__device__ __forceinline__ f32x2 pair_of(const Raw2<BF16>& r) {
+  if constexpr (BF16) return pack2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
+  else return pack2(r.x, r.y);
 }
-__device__ __forceinline__ float2 unpack2(f32x2 x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-  return r;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ f32x2 ex2_2(f32x2 x) {
+template <bool BF16>
+__device__ __forceinline__ Raw2<BF16> raw_of(f32x2 x) {
   const float2 v = unpack2(x);
-  return pack2(ex2(v.x), ex2(v.y));
+  if constexpr (BF16) return pack_bf16(v.x, v.y);
+  else return v;
 }
 
-// log(1 + e^x) = max(x, 0) + log(1 + e), e = e^-|x| in (0, 1]. log(1 + e) = 2 artanh(q) with
-// q = e / (2 + e) <= 1/3: the odd series to q^13 is off by less than 2^-26 of it, for any e.
-__device__ __forceinline__ float softplus_series(float x) {
-  const float e = expf(-fabsf(x)), q = __fdividef(e, 2.0f + e), q2 = q * q;
-  float r = fmaf(q2, 2.0f / 13, 2.0f / 11);
-  r = fmaf(r, q2, 2.0f / 9);
-  r = fmaf(r, q2, 2.0f / 7);
-  r = fmaf(r, q2, 2.0f / 5);
-  r = fmaf(r, q2, 2.0f / 3);
-  r = fmaf(r, q2, 2.0f);
-  return fmaf(r, q, fmaxf(x, 0.0f));
+// Eight elements of shared memory as pairs.
+template <bool BF16>
+__device__ __forceinline__ void pairs8(const unsigned char* from, f32x2 (&x)[4]) {
+  if constexpr (BF16) {
+    const uint4 v = *reinterpret_cast<const uint4*>(from);
+    x[0] = pair_of<true>(v.x), x[1] = pair_of<true>(v.y), x[2] = pair_of<true>(v.z), x[3] = pair_of<true>(v.w);
+  } else {
+    const ulonglong2 lo = reinterpret_cast<const ulonglong2*>(from)[0], hi = reinterpret_cast<const ulonglong2*>(from)[1];
+    x[0] = lo.x, x[1] = lo.y, x[2] = hi.x, x[3] = hi.y;
+  }
 }
-__device__ __forceinline__ float silu_fast(float z) { return __fdividef(z, 1.0f + expf(-z)); }
 
-// A thread owns four states of four channels: LANES neighbouring lanes a set of four channels, CH
-// channels a warp. STEPS positions are staged in shared memory at a time.
+// 16 bytes to shared memory, zeros where `there` is false (then nothing is read)
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+
+// A thread owns eight states of two channels, the states in pairs: LANES neighbouring lanes a pair of
+// channels, CH channels a warp, STEPS positions at a time in shared memory. Item i of a tile is the
+// pair of channels i % ROW of position i / ROW.
 template <int N_, bool BF16_>
 struct Cfg {
   static constexpr int N = N_;
   static constexpr bool BF16 = BF16_;
-  static constexpr int LANES = N / 4, CH = 4 * (32 / LANES);
-  static constexpr int STEPS = BF16 && N > 8 ? 16 : 8;
-  static constexpr int ROW = CH / 8, ITEMS = STEPS * ROW, U = (ITEMS + 31) / 32;            // vectors of u, dt, z
-  static constexpr int NROW = N / 8, NITEMS = 2 * STEPS * NROW, V = (NITEMS + 31) / 32;     // and of b and c
+  static constexpr int LANES = N / 8, CH = 2 * (32 / LANES), ROW = CH / 2, STEPS = 8;
+  static constexpr int ITEMS = STEPS * ROW, U = ITEMS / 32;  // of u, dt, z, y; a lane's
+  static constexpr int ELEM = BF16 ? 2 : 4;
+  // b and c in fp32 in shared memory; else every thread makes its own of bf16. A position's 2 N values
+  // are converted by the warp for 512 / N channels: 582 against 612 us at N = 16 (scan of 32 x 512
+  // positions, 8192 channels), but 740 against 670 at N = 32 and 461 against 346 at 64.
+  static constexpr bool WIDEN = BF16 && N <= 16;
+  static constexpr int COPY = STEPS * CH * ELEM / 16, NCOPY = STEPS * N * ELEM / 16;  // 16-byte copies of u, dt or z, and of b or c
+  static_assert(ITEMS % 32 == 0, "every lane has as many");
 };
 
-// A warp's part of shared memory. b and c are held twice each, next to one another, so that a pair
-// of channels meets them as a pair.
+// A warp's part of shared memory: two tiles as they lie in memory, one of which is being loaded,
+// and of the other, the tile at work, the items (the pair's steps, and steps times inputs) and the readout.
 template <class C>
 struct WarpSmem {
-  float dt[C::STEPS][C::CH], du[C::STEPS][C::CH], y[C::STEPS][C::CH];
-  float bc[2][C::STEPS][2 * C::N];
-  float bias[C::CH], skip[C::CH];
+  struct Tile {
+    alignas(16) unsigned char u[C::COPY * 16], dt[C::COPY * 16], z[C::COPY * 16], b[C::NCOPY * 16], c[C::NCOPY * 16];
+  } raw[2];
+  ulonglong2 in[C::ITEMS];
+  float y[C::STEPS][C::CH];
+  float b[C::WIDEN ? C::STEPS : 1][C::N], c[C::WIDEN ? C::STEPS : 1][C::N];
+  float bias[2][C::CH], skip[C::CH];  // bias: with softplus its product with log2(e), as the sum of two
 };
 
+// Where the prompts' channels are too few for the GPU, prompts are cut into parts of `part` positions
+// that are scanned side by side. A first kernel (SUMMARY) takes every part but the last from a state
+// of zero: end[j], and sum[j], the sum of its steps. A part then begins with the prompt's state
+// taken through the parts before it, h <- exp(sum[j] a) h + end[j].
 struct ScanParams {
   gdn_ssm s;
   int32_t* status;
   int32_t per_group, blocks;  // channels of a group, and blocks of them
-  uint32_t warps;             // tasks: (request, channel block)
+  int32_t parts, part;        // parts of a prompt at most, and positions of one
+  uint32_t tasks;             // (request, part, channel block)
+  float* init;                // [B][D][N]: the states before the prompts
+  float* end;                 // [B][parts - 1][D][N]
+  float* sum;                 // [B][parts - 1][D]
 };
 
-template <class C>
-__global__ void __launch_bounds__(kWarps * 32) gdn_ssm_scan_kernel(const ScanParams p) {
+template <class C, bool SUMMARY>
+__global__ void __launch_bounds__(kWarps * 32, 4) gdn_ssm_scan_kernel(const ScanParams p) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  constexpr bool BF16 = C::BF16;
   const gdn_ssm& s = p.s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   WarpSmem<C>& sm = reinterpret_cast<WarpSmem<C>*>(smem_raw)[warp];
   griddep_launch_dependents();
   griddep_wait();
   const uint32_t task = blockIdx.x * kWarps + warp;
-  if (task >= p.warps) return;
-  const int all_blocks = p.blocks * s.num_groups;
-  const int b = static_cast<int>(task / all_blocks), block = static_cast<int>(task - b * static_cast<uint32_t>(all_blocks));
+  if (task >= p.tasks) return;
+  const uint32_t all_blocks = static_cast<uint32_t>(p.blocks * s.num_groups), parts = SUMMARY ? p.parts - 1 : p.parts;
+  const uint32_t row = task / all_blocks;
+  const int block = static_cast<int>(task - row * all_blocks), b = static_cast<int>(row / parts), part_no = static_cast<int>(row - b * parts);
   const int group = block / p.blocks, in_group = (block - group * p.blocks) * C::CH;
   const int c0 = group * p.per_group + in_group, count = min(C::CH, p.per_group - in_group);
   const int slot = s.slot[b];
@@ -112,219 +111,283 @@ __global__ void __launch_bounds__(kWarps * 32) gdn_ssm_scan_kernel(const ScanPar
   const int len = s.seq_lens != nullptr ? s.seq_lens[b] : s.num_tokens;
   const bool bad_slot = slot >= s.num_slots, bad_len = len < 0 || len > s.num_tokens;
   if (bad_slot || bad_len) {
-    if (block == 0 && lane == 0) atomic_status(p.status, bad_slot ? GDN_STATUS_BAD_SLOT : GDN_STATUS_BAD_LEN);
+    if (block == 0 && part_no == 0 && lane == 0) atomic_status(p.status, bad_slot ? GDN_STATUS_BAD_SLOT : GDN_STATUS_BAD_LEN);
     return;
   }
-  if (len == 0) return;
-  const int begin = 0, end = len;
+  const int begin = part_no * p.part, end = min(len - begin, p.part) + begin;
+  if (begin >= len) return;
+  const bool last = end == len;
+  if (SUMMARY && last && part_no > 0) return;  // nothing comes after it
 
   // ---- this thread's states -----------------------------------------------------------------
   const int set = lane / C::LANES, part = lane % C::LANES;
-  float* const state = s.state + (static_cast<int64_t>(slot) * s.channels + c0 + set * 4) * C::N + part * 4;
-  const float* const a_at = s.a + static_cast<int64_t>(c0 + set * 4) * C::N + part * 4;
-  f32x2 h[2][4], a[2][4];
+  const bool mine_live = set * 2 < count;
+  float* const state = s.state + (static_cast<int64_t>(slot) * s.channels + c0 + set * 2) * C::N + part * 8;
+  f32x2 h[2][4], a[2][4];  // [channel][pair of states]
   auto load_states = [&](const float* from, f32x2 (&to)[2][4]) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-      if (set * 4 < count) {
-        x = *reinterpret_cast<const float4*>(from + (2 * i) * C::N);
-        y = *reinterpret_cast<const float4*>(from + (2 * i + 1) * C::N);
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        ulonglong2 x = make_ulonglong2(0, 0);
+        if (mine_live) x = *reinterpret_cast<const ulonglong2*>(from + i * C::N + j * 2);
+        to[i][j] = x.x, to[i][j + 1] = x.y;
       }
-      to[i][0] = pack2(x.x, y.x);
-      to[i][1] = pack2(x.y, y.y);
-      to[i][2] = pack2(x.z, y.z);
-      to[i][3] = pack2(x.w, y.w);
     }
   };
-  load_states(state, h);
-  load_states(a_at, a);
-  const f32x2 log2e = pack2(kLog2e, kLog2e);
+  auto store_states = [&](float* to, const f32x2 (&from)[2][4]) {
+    if (!mine_live) return;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) *reinterpret_cast<ulonglong2*>(to + i * C::N + j * 2) = make_ulonglong2(from[i][j], from[i][j + 1]);
+  };
+  load_states(s.a + static_cast<int64_t>(c0 + set * 2) * C::N + part * 8, a);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) a[i][j] = mul2(a[i][j], log2e);
+    for (int j = 0; j < 4; ++j) a[i][j] = mul2(a[i][j], both(kLog2e));
+  // this thread's place in init, and in end and sum of part j
+  const int64_t mine = static_cast<int64_t>(c0 + set * 2) * C::N + part * 8, per_request = static_cast<int64_t>(s.channels) * C::N;
+  auto end_of = [&](int j) { return p.end + (static_cast<int64_t>(b) * (p.parts - 1) + j) * per_request + mine; };
+  auto sum_of = [&](int j) { return p.sum + (static_cast<int64_t>(b) * (p.parts - 1) + j) * s.channels + c0 + set * 2; };
+  load_states(p.parts == 1 || (SUMMARY && part_no == 0) ? state : p.init + b * per_request + mine, h);
+  f32x2 steps_sum[2] = {0, 0};  // both halves alike
+  if (SUMMARY) {
+    // the last part's scan overwrites the slot's state while others still begin
+    if (part_no == 0) store_states(p.init + b * per_request + mine, h);
+    if (last) return;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[i][j] = 0;
+  } else {
+#pragma unroll 2
+    for (int j = 0; j < part_no; ++j) {
+      f32x2 e[2][4];
+      load_states(end_of(j), e);
+      float2 sum = make_float2(0.0f, 0.0f);
+      if (mine_live) sum = *reinterpret_cast<const float2*>(sum_of(j));
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[i][k] = fma2(ex2_2(mul2(both(i == 0 ? sum.x : sum.y), a[i][k])), h[i][k], e[i][k]);
+    }
+  }
+  const bool softplus = (s.flags & GDN_DT_SOFTPLUS) != 0u;
   for (int c = lane; c < C::CH; c += 32) {
-    sm.bias[c] = s.dt_bias != nullptr && c < count ? s.dt_bias[c0 + c] : 0.0f;
+    const float bias = s.dt_bias != nullptr && c < count ? s.dt_bias[c0 + c] : 0.0f;
+    sm.bias[0][c] = softplus ? bias * kLog2e : bias;
+    sm.bias[1][c] = softplus ? fmaf(bias, kLog2e, -(bias * kLog2e)) : 0.0f;
     sm.skip[c] = s.skip != nullptr && c < count ? s.skip[c0 + c] : 0.0f;
   }
-  __syncwarp();
 
-  // ---- rows of the inputs: item i of a tile is vector i % ROW of position i / ROW ------------------
-  const int vec = lane % C::ROW * 8;
-  const bool vec_live = vec < count;
-  const int64_t u_at = b * s.u_strides[0] + c0 + vec, dt_at = b * s.dt_strides[0] + c0 + vec, z_at = b * s.z_strides[0] + c0 + vec;
-  const int64_t b_at = b * s.b_strides[0] + group * s.b_strides[2], c_at = b * s.c_strides[0] + group * s.c_strides[2];
-  const int64_t y_at = static_cast<int64_t>(b) * s.num_tokens * s.channels + c0 + vec;
-  const bool softplus = (s.flags & GDN_DT_SOFTPLUS) != 0u;
-  Raw8<BF16> next_u[C::U], next_dt[C::U], next_bc[C::V];
-  auto item_t = [&](int k) { return (lane + 32 * k) / C::ROW; };
-  auto item_live = [&](int k, int t0) {
-    return vec_live && (C::ITEMS % 32 == 0 || lane + 32 * k < C::ITEMS) && t0 + item_t(k) < end;
+  // ---- tiles of the inputs ----------------------------------------------------------------------
+  constexpr int kE = C::ELEM, kPer = 16 / kE;  // elements of a copy
+  constexpr int kRow = C::CH / kPer, kNRow = C::N / kPer;  // copies of a row
+  const int col = lane % kRow * kPer, ncol = lane % kNRow * kPer;
+  auto row_at = [&](const void* base, const int64_t* strides, int64_t first, int per) {
+    return static_cast<const unsigned char*>(base) + (b * strides[0] + (begin + lane / per) * strides[1] + first) * kE;
   };
+  // this lane's first copies of the next tile
+  const unsigned char* u_at = row_at(s.u, s.u_strides, c0 + col, kRow);
+  const unsigned char* dt_at = row_at(s.dt, s.dt_strides, c0 + col, kRow);
+  const unsigned char* z_at = row_at(s.z, s.z_strides, c0 + col, kRow);
+  const unsigned char* b_at = row_at(s.b, s.b_strides, group * s.b_strides[2] + ncol, kNRow);
+  const unsigned char* c_at = row_at(s.c, s.c_strides, group * s.c_strides[2] + ncol, kNRow);
+  const bool gated = !SUMMARY && s.z != nullptr, col_live = col < count;
   auto fetch = [&](int t0) {
+    typename WarpSmem<C>::Tile& to = sm.raw[t0 / C::STEPS & 1];
+    auto copies = [&](unsigned char* dst, const unsigned char*& src, int64_t stride, int per, int all, bool live) {
 #pragma unroll
-    for (int k = 0; k < C::U; ++k) {
-      next_u[k] = next_dt[k] = zero8<BF16>();
-      if (!item_live(k, t0)) continue;
-      const int64_t t = t0 + item_t(k);
-      next_u[k] = load8<BF16>(s.u, u_at + t * s.u_strides[1]);
-      next_dt[k] = load8<BF16>(s.dt, dt_at + t * s.dt_strides[1]);
-    }
-#pragma unroll
-    for (int k = 0; k < C::V; ++k) {
-      next_bc[k] = zero8<BF16>();
-      const int item = lane + 32 * k, which = item / (C::STEPS * C::NROW), in = item % (C::STEPS * C::NROW);
-      const int64_t t = t0 + in / C::NROW;
-      if (item >= C::NITEMS || t >= end) continue;
-      next_bc[k] = which == 0 ? load8<BF16>(s.b, b_at + t * s.b_strides[1] + in % C::NROW * 8)
-                              : load8<BF16>(s.c, c_at + t * s.c_strides[1] + in % C::NROW * 8);
-    }
+      for (int k = 0; k < (all + 31) / 32; ++k) {
+        const int row = lane / per + 32 / per * k;
+        if (all % 32 != 0 && lane + 32 * k >= all) continue;
+        copy16(dst + (lane + 32 * k) * 16, src + (32 / per * k) * stride * kE, live && t0 + row < end);
+      }
+      src += C::STEPS * stride * kE;
+    };
+    copies(to.u, u_at, s.u_strides[1], kRow, C::COPY, col_live);
+    copies(to.dt, dt_at, s.dt_strides[1], kRow, C::COPY, col_live);
+    if (gated) copies(to.z, z_at, s.z_strides[1], kRow, C::COPY, col_live);
+    copies(to.b, b_at, s.b_strides[1], kNRow, C::NCOPY, true);
+    if (!SUMMARY) copies(to.c, c_at, s.c_strides[1], kNRow, C::NCOPY, true);
   };
 
+  const int pair = lane % C::ROW;  // of all items of this lane: ROW divides 32
+  const bool pair_live = pair * 2 < count;
+  const int64_t y_row = static_cast<int64_t>(s.channels) * kE;
+  unsigned char* y_at = static_cast<unsigned char*>(s.y) +
+                        ((static_cast<int64_t>(b) * s.num_tokens + begin + lane / C::ROW) * s.channels + c0 + pair * 2) * kE;
   fetch(begin);
   for (int t0 = begin; t0 < end; t0 += C::STEPS) {
-    // ---- steps, inputs, b and c of the tile into shared memory -----------------------------------
-    Raw8<BF16> u[C::U], z[C::U];
+    const typename WarpSmem<C>::Tile& raw = sm.raw[t0 / C::STEPS & 1];
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();  // the tile is there, and the last one is done with
+    if (t0 + C::STEPS < end) fetch(t0 + C::STEPS);
+
+    // ---- steps, inputs, b and c of the tile, in fp32 -----------------------------------------------
+    const f32x2 bias = *reinterpret_cast<const f32x2*>(&sm.bias[0][pair * 2]), rest = *reinterpret_cast<const f32x2*>(&sm.bias[1][pair * 2]);
 #pragma unroll
     for (int k = 0; k < C::U; ++k) {
-      u[k] = next_u[k];
-      float x[8], dt[8];
-      floats8<BF16>(next_u[k], x);
-      floats8<BF16>(next_dt[k], dt);
-      const bool live = item_live(k, t0);
+      const int i = lane + 32 * k;
+      f32x2 dt = pair_of<C::BF16>(reinterpret_cast<const Raw2<C::BF16>*>(raw.dt)[i]);
+      if (softplus)
+        dt = softplus_2(add2(fma2(dt, both(kLog2e), rest), bias));
+      else
+        dt = add2(dt, bias);
+      if (t0 + i / C::ROW >= end) dt = 0;  // the state passes a position of no prompt unchanged
+      const f32x2 x = mul2(pair_of<C::BF16>(reinterpret_cast<const Raw2<C::BF16>*>(raw.u)[i]), dt);
+      sm.in[i] = make_ulonglong2(dt, x);
+    }
+    if constexpr (C::WIDEN) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        dt[e] += sm.bias[vec + e];
-        if (softplus) dt[e] = softplus_series(dt[e]);
-        if (!live) dt[e] = 0.0f;  // the state passes a position of no prompt unchanged
-        x[e] *= dt[e];
+      for (int k = 0; k < C::STEPS * C::N / 64; ++k) {
+        const int i = lane + 32 * k;
+        reinterpret_cast<f32x2*>(sm.b)[i] = pair_of<C::BF16>(reinterpret_cast<const Raw2<C::BF16>*>(raw.b)[i]);
+        if (!SUMMARY) reinterpret_cast<f32x2*>(sm.c)[i] = pair_of<C::BF16>(reinterpret_cast<const Raw2<C::BF16>*>(raw.c)[i]);
       }
-      if (C::ITEMS % 32 == 0 || lane + 32 * k < C::ITEMS) {
-        store8<false>(&sm.dt[item_t(k)][vec], 0, raw8<false>(dt));
-        store8<false>(&sm.du[item_t(k)][vec], 0, raw8<false>(x));
-      }
     }
-#pragma unroll
-    for (int k = 0; k < C::V; ++k) {
-      const int item = lane + 32 * k, which = item / (C::STEPS * C::NROW), in = item % (C::STEPS * C::NROW);
-      if (C::NITEMS % 32 != 0 && item >= C::NITEMS) continue;
-      float x[8];
-      floats8<BF16>(next_bc[k], x);
-      float4* const to = reinterpret_cast<float4*>(&sm.bc[which][in / C::NROW][in % C::NROW * 16]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) to[e] = make_float4(x[2 * e], x[2 * e], x[2 * e + 1], x[2 * e + 1]);
-    }
-    if (s.z != nullptr) {
-#pragma unroll
-      for (int k = 0; k < C::U; ++k)
-        if (item_live(k, t0)) z[k] = load8<BF16>(s.z, z_at + (t0 + static_cast<int64_t>(item_t(k))) * s.z_strides[1]);
-    }
-    if (t0 + C::STEPS < end) fetch(t0 + C::STEPS);
     __syncwarp();
 
     // ---- the recurrence ----------------------------------------------------------------------------
-    const int steps = min(C::STEPS, (end - t0 + 3) & ~3);
-#pragma unroll 4
-    for (int t = 0; t < steps; ++t) {
-      const ulonglong2 dt = *reinterpret_cast<const ulonglong2*>(&sm.dt[t][set * 4]);
-      const ulonglong2 du = *reinterpret_cast<const ulonglong2*>(&sm.du[t][set * 4]);
-      const ulonglong2* const bt = reinterpret_cast<const ulonglong2*>(&sm.bc[0][t][part * 8]);
-      const ulonglong2* const ct = reinterpret_cast<const ulonglong2*>(&sm.bc[1][t][part * 8]);
-      const ulonglong2 b01 = bt[0], b23 = bt[1], c01 = ct[0], c23 = ct[1];
-      const f32x2 bb[4] = {b01.x, b01.y, b23.x, b23.y}, cc[4] = {c01.x, c01.y, c23.x, c23.y};
-      const f32x2 dts[2] = {dt.x, dt.y}, dus[2] = {du.x, du.y};
-      f32x2 sum[2];
+#pragma unroll
+    for (int t = 0; t < C::STEPS; ++t) {
+      const ulonglong2 in = sm.in[t * C::ROW + set];
+      const float2 dt = unpack2(in.x), du = unpack2(in.y);
+      const f32x2 dts[2] = {both(dt.x), both(dt.y)}, dus[2] = {both(du.x), both(du.y)};
+      f32x2 bb[4], cc[4] = {0, 0, 0, 0};
+      if constexpr (C::WIDEN) {
+        pairs8<false>(reinterpret_cast<const unsigned char*>(&sm.b[t][part * 8]), bb);
+        if (!SUMMARY) pairs8<false>(reinterpret_cast<const unsigned char*>(&sm.c[t][part * 8]), cc);
+      } else {
+        pairs8<C::BF16>(raw.b + (t * C::N + part * 8) * kE, bb);
+        if (!SUMMARY) pairs8<C::BF16>(raw.c + (t * C::N + part * 8) * kE, cc);
+      }
+      float sum[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
+        f32x2 acc = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           h[i][j] = fma2(ex2_2(mul2(dts[i], a[i][j])), h[i][j], mul2(dus[i], bb[j]));
-          sum[i] = j == 0 ? mul2(h[i][j], cc[j]) : fma2(h[i][j], cc[j], sum[i]);
+          if (!SUMMARY) acc = j == 0 ? mul2(h[i][j], cc[j]) : fma2(h[i][j], cc[j], acc);
         }
+        const float2 v = unpack2(acc);
+        sum[i] = v.x + v.y;
+        if (SUMMARY) steps_sum[i] = add2(steps_sum[i], dts[i]);
       }
-      // Sums over the set's lanes: a lane keeps half of its channels and gives the other half away,
-      // twice; further lanes add what is left.
-      f32x2 keep = sum[0];
-      {
-        const bool upper = (part & (C::LANES / 2)) != 0;
-        const f32x2 give = upper ? sum[0] : sum[1];
-        keep = upper ? sum[1] : sum[0];
-        keep = add2(keep, __shfl_xor_sync(0xffffffffu, give, C::LANES / 2));
-      }
-      const float2 two = unpack2(keep);
-      if constexpr (C::LANES == 2) {
-        *reinterpret_cast<float2*>(&sm.y[t][set * 4 + part * 2]) = two;
-      } else {
-        const bool upper = (part & (C::LANES / 4)) != 0;
-        float one = upper ? two.y : two.x;
-        one += __shfl_xor_sync(0xffffffffu, upper ? two.x : two.y, C::LANES / 4);
+      if constexpr (!SUMMARY) {
+        // Sums over the lanes of a pair of channels: a lane keeps one channel and gives the other
+        // away; further lanes add what is left.
+        if constexpr (C::LANES == 1) {
+          *reinterpret_cast<float2*>(&sm.y[t][set * 2]) = make_float2(sum[0], sum[1]);
+        } else {
+          constexpr int kOwn = C::LANES / 2;
+          const bool second = (part & kOwn) != 0;
+          float one = (second ? sum[1] : sum[0]) + __shfl_xor_sync(0xffffffffu, second ? sum[0] : sum[1], kOwn);
 #pragma unroll
-        for (int off = C::LANES / 8; off > 0; off >>= 1) one += __shfl_xor_sync(0xffffffffu, one, off);
-        if (part % (C::LANES / 4) == 0) sm.y[t][set * 4 + part / (C::LANES / 4)] = one;
+          for (int off = kOwn / 2; off > 0; off >>= 1) one += __shfl_xor_sync(0xffffffffu, one, off);
+          if (part % kOwn == 0) sm.y[t][set * 2 + part / kOwn] = one;
+        }
       }
     }
     __syncwarp();
 
     // ---- readout ----------------------------------------------------------------------------------
+    if constexpr (!SUMMARY) {
+      const f32x2 skip = *reinterpret_cast<const f32x2*>(&sm.skip[pair * 2]);
 #pragma unroll
-    for (int k = 0; k < C::U; ++k) {
-      if (!item_live(k, t0)) continue;
-      float x[8], y[8], g[8];
-      floats8<BF16>(u[k], x);
-      floats8<false>(load8<false>(&sm.y[item_t(k)][vec], 0), y);
-      if (s.z != nullptr) floats8<BF16>(z[k], g);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        y[e] = fmaf(sm.skip[vec + e], x[e], y[e]);
-        if (s.z != nullptr) y[e] *= silu_fast(g[e]);
+      for (int k = 0; k < C::U; ++k) {
+        const int i = lane + 32 * k, t = i / C::ROW;
+        if (!pair_live || t0 + t >= end) continue;
+        f32x2 y = fma2(skip, pair_of<C::BF16>(reinterpret_cast<const Raw2<C::BF16>*>(raw.u)[i]), reinterpret_cast<const f32x2*>(sm.y)[i]);
+        if (gated) y = mul2(y, silu_2<!C::BF16>(pair_of<C::BF16>(reinterpret_cast<const Raw2<C::BF16>*>(raw.z)[i])));
+        *reinterpret_cast<Raw2<C::BF16>*>(y_at + 32 / C::ROW * k * y_row) = raw_of<C::BF16>(y);
       }
-      store8<BF16>(s.y, y_at + (t0 + static_cast<int64_t>(item_t(k))) * s.channels, raw8<BF16>(y));
+      y_at += C::STEPS * y_row;
     }
   }
 
-  if (set * 4 < count) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float2 x[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = unpack2(h[i][j]);
-      *reinterpret_cast<float4*>(state + (2 * i) * C::N) = make_float4(x[0].x, x[1].x, x[2].x, x[3].x);
-      *reinterpret_cast<float4*>(state + (2 * i + 1) * C::N) = make_float4(x[0].y, x[1].y, x[2].y, x[3].y);
-    }
+  if (SUMMARY) {
+    store_states(end_of(part_no), h);
+    if (mine_live && part == 0) *reinterpret_cast<float2*>(sum_of(part_no)) = make_float2(unpack2(steps_sum[0]).x, unpack2(steps_sum[1]).x);
+  } else if (last) {
+    store_states(state, h);
   }
+}
+
+// How prompts are cut: by the warps that whole prompts would give. The GPU holds 2432 of them; from
+// 1536 on prompts stay whole (16 x 1024 positions of 4096 channels, 2048 warps: 342 us, 417 in two
+// parts), below that about 8192 are made: parts that are short beside the whole even out prompts of
+// several lengths (8 ragged prompts, 1024 warps: 457 us whole, 303 in 4 parts, 265 in 8; 16384
+// positions, 256 warps: 2906 us whole, 1331 in 5, 976 in 32). A part begins by going through the
+// ends of all parts before it, so there are at most sqrt(T) of them.
+struct Cut {
+  int32_t parts, part;
+};
+Cut cut_of(int32_t batch, int32_t tokens, int32_t channels, int32_t state_size) {
+  constexpr int64_t kEnough = 1536, kWanted = 8192;
+  constexpr int32_t kShortest = 64, kRound = 16;
+  const int32_t of_warp = 512 / state_size;  // channels
+  const int64_t warps = static_cast<int64_t>(batch) * ((channels + of_warp - 1) / of_warp);
+  int32_t parts = warps >= kEnough ? 1 : static_cast<int32_t>(kWanted / warps);
+  while (static_cast<int64_t>(parts) * parts > tokens) parts = parts > 256 ? parts / 2 : parts - 1;
+  if (parts < 1) parts = 1;
+  int32_t part = static_cast<int32_t>((static_cast<int64_t>(tokens) + parts - 1) / parts);
+  part = part > kShortest ? (part > 0x7fffffff - kRound ? part : (part + kRound - 1) / kRound * kRound) : kShortest;
+  return {static_cast<int32_t>((static_cast<int64_t>(tokens) + part - 1) / part), part};
+}
+
+template <class C, bool SUMMARY>
+cudaError_t launch_parts(ScanParams p, cudaStream_t stream) {
+  const int64_t tasks = static_cast<int64_t>(p.blocks) * p.s.num_groups * p.s.batch * (SUMMARY ? p.parts - 1 : p.parts);
+  p.tasks = static_cast<uint32_t>(tasks);
+  constexpr int kBytes = kWarps * static_cast<int>(sizeof(WarpSmem<C>));
+  static std::atomic<bool> allowed[kDevices];
+  const cudaError_t err = allow_shared(reinterpret_cast<const void*>(gdn_ssm_scan_kernel<C, SUMMARY>), kBytes, allowed);
+  if (err != cudaSuccess) return err;
+  return launch_overlapped(gdn_ssm_scan_kernel<C, SUMMARY>, p, dim3((p.tasks + kWarps - 1) / kWarps), kWarps * 32, kBytes, 1u, stream);
 }
 
 template <class C>
-cudaError_t launch_scan(const SsmParams& given, cudaStream_t stream) {
-  ScanParams p{given.s, given.status, given.s.channels / given.s.num_groups, 0, 0};
+cudaError_t launch_scan(const SsmParams& given, void* workspace, cudaStream_t stream) {
+  const gdn_ssm& s = given.s;
+  const Cut cut = cut_of(s.batch, s.num_tokens, s.channels, s.state_size);
+  ScanParams p{s, given.status, s.channels / s.num_groups, 0, cut.parts, cut.part, 0, nullptr, nullptr, nullptr};
   p.blocks = (p.per_group + C::CH - 1) / C::CH;
-  const int64_t warps = static_cast<int64_t>(p.blocks) * p.s.num_groups * p.s.batch;
-  if (warps > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  p.warps = static_cast<uint32_t>(warps);
-  constexpr int kBytes = kWarps * static_cast<int>(sizeof(WarpSmem<C>));
-  static std::atomic<bool> allowed[kDevices];
-  const cudaError_t err = allow_shared(reinterpret_cast<const void*>(gdn_ssm_scan_kernel<C>), kBytes, allowed);
-  if (err != cudaSuccess) return err;
-  return launch_overlapped(gdn_ssm_scan_kernel<C>, p, dim3((p.warps + kWarps - 1) / kWarps), kWarps * 32, kBytes, 1u, stream);
+  if (cut.parts > 1) {
+    const int64_t states = static_cast<int64_t>(s.batch) * s.channels * s.state_size;
+    p.init = static_cast<float*>(workspace);
+    p.end = p.init + states;
+    p.sum = p.end + states * (cut.parts - 1);
+    const cudaError_t err = launch_parts<C, true>(p, stream);
+    if (err != cudaSuccess) return err;
+  }
+  return launch_parts<C, false>(p, stream);
 }
 
 template <bool BF16>
-cudaError_t launch_type(const SsmParams& p, cudaStream_t stream) {
+cudaError_t launch_type(const SsmParams& p, void* workspace, cudaStream_t stream) {
   switch (p.s.state_size) {
-    case 8: return launch_scan<Cfg<8, BF16>>(p, stream);
-    case 16: return launch_scan<Cfg<16, BF16>>(p, stream);
-    case 32: return launch_scan<Cfg<32, BF16>>(p, stream);
-    default: return launch_scan<Cfg<64, BF16>>(p, stream);
+    case 8: return launch_scan<Cfg<8, BF16>>(p, workspace, stream);
+    case 16: return launch_scan<Cfg<16, BF16>>(p, workspace, stream);
+    case 32: return launch_scan<Cfg<32, BF16>>(p, workspace, stream);
+    default: return launch_scan<Cfg<64, BF16>>(p, workspace, stream);
   }
 }
 
 }  // namespace
 
-size_t ssm_workspace_bytes(int32_t, int32_t, int32_t, int32_t) { return 0; }
+size_t ssm_workspace_bytes(int32_t batch, int32_t tokens, int32_t channels, int32_t state_size) {
+  if (batch == 0 || tokens == 0) return 0;
+  const Cut cut = cut_of(batch, tokens, channels, state_size);
+  if (cut.parts == 1) return 0;
+  return static_cast<size_t>(batch) * channels * (static_cast<size_t>(cut.parts) * state_size + cut.parts - 1) * sizeof(float);
+}
 
-cudaError_t launch_ssm_scan(const SsmParams& p, void*, cudaStream_t stream) {
-  return (p.s.flags & GDN_QKV_BF16) != 0u ? launch_type<true>(p, stream) : launch_type<false>(p, stream);
+cudaError_t launch_ssm_scan(const SsmParams& p, void* workspace, cudaStream_t stream) {
+  return (p.s.flags & GDN_QKV_BF16) != 0u ? launch_type<true>(p, workspace, stream) : launch_type<false>(p, workspace, stream);
 }
 
 }  // namespace gdn
