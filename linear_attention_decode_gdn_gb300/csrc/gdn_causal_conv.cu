@@ -9,6 +9,7 @@ namespace {
 
 constexpr int kConvThreads = 128;
 constexpr int kSteps = 32;  // positions a thread takes
+constexpr int kAhead = 4;   // of them in flight
 
 // The three inputs before position `at` (oldest first) of eight channels: of the prompt, or of the
 // slot's row where they lie before it.
@@ -103,26 +104,52 @@ __global__ void __launch_bounds__(kConvThreads) gdn_causal_conv_kernel(const Con
     inputs_before<BF16>(c, row, x, len, d, last);
     write_row<BF16>(row, d, last);
   }
-  float w[8][4], bias[8], past[3][8];
+  // pairs of channels from here on
+  f32x2 w[4][4], bias[4], past[3][4];  // [tap][pair]
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const float4 v = reinterpret_cast<const float4*>(c.w)[d + k];
-    w[k][0] = v.x, w[k][1] = v.y, w[k][2] = v.z, w[k][3] = v.w;
-    bias[k] = c.bias != nullptr ? c.bias[d + k] : 0.0f;
+  for (int k = 0; k < 4; ++k) {
+    const float4 lo = reinterpret_cast<const float4*>(c.w)[d + 2 * k], hi = reinterpret_cast<const float4*>(c.w)[d + 2 * k + 1];
+    w[0][k] = pack2(lo.x, hi.x), w[1][k] = pack2(lo.y, hi.y), w[2][k] = pack2(lo.z, hi.z), w[3][k] = pack2(lo.w, hi.w);
+    bias[k] = c.bias != nullptr ? *reinterpret_cast<const f32x2*>(c.bias + d + 2 * k) : 0;
   }
+  auto pairs = [](const Raw8<BF16>& r, f32x2 (&x)[4]) {
+    float f[8];
+    floats8<BF16>(r, f);
 #pragma unroll
-  for (int j = 0; j < 3; ++j) floats8<BF16>(before[j], past[j]);
+    for (int k = 0; k < 4; ++k) x[k] = pack2(f[2 * k], f[2 * k + 1]);
+  };
+#pragma unroll
+  for (int j = 0; j < 3; ++j) pairs(before[j], past[j]);
   const bool silu = (c.flags & GDN_CONV_SILU) != 0u;
-  for (int t = begin; t < end; ++t) {
-    float now[8], o[8];
-    floats8<BF16>(load8<BF16>(c.x, x + t * c.x_strides[1]), now);
+  Raw8<BF16> next[kAhead];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      o[k] = fmaf(now[k], w[k][3], fmaf(past[2][k], w[k][2], fmaf(past[1][k], w[k][1], fmaf(past[0][k], w[k][0], bias[k]))));
-      if (silu) o[k] = siluf_(o[k]);
-      past[0][k] = past[1][k], past[1][k] = past[2][k], past[2][k] = now[k];
+  for (int j = 0; j < kAhead; ++j)
+    if (begin + j < end) next[j] = load8<BF16>(c.x, x + (begin + j) * c.x_strides[1]);
+  int64_t to = (static_cast<int64_t>(b) * c.num_tokens + begin) * c.channels + d;
+  for (int t0 = begin; t0 < end; t0 += kAhead) {
+    Raw8<BF16> now[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      now[j] = next[j];
+      if (t0 + kAhead + j < end) next[j] = load8<BF16>(c.x, x + (t0 + kAhead + j) * c.x_strides[1]);
     }
-    store8<BF16>(c.o, (static_cast<int64_t>(b) * c.num_tokens + t) * c.channels + d, raw8<BF16>(o));
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (t0 + j >= end) break;
+      f32x2 in[4];
+      float o[8];
+      pairs(now[j], in);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        f32x2 sum = fma2(in[k], w[3][k], fma2(past[2][k], w[2][k], fma2(past[1][k], w[1][k], fma2(past[0][k], w[0][k], bias[k]))));
+        if (silu) sum = silu_2<!BF16>(sum);
+        const float2 v = unpack2(sum);
+        o[2 * k] = v.x, o[2 * k + 1] = v.y;
+        past[0][k] = past[1][k], past[1][k] = past[2][k], past[2][k] = in[k];
+      }
+      store8<BF16>(c.o, to, raw8<BF16>(o));
+      to += c.channels;
+    }
   }
 }
 
