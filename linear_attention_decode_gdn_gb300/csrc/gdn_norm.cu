@@ -8,6 +8,8 @@ namespace gdn {
 namespace {
 
 constexpr int kMaxThreads = 1024;
+constexpr int kRowWarps = 4;   // rows of a CTA where a warp takes one
+constexpr int kFewRows = 608;  // up to here a thread takes one vector
 constexpr float kTop = 448.0f;    // the largest e4m3 value
 constexpr float kLeast = 1e-30f;  // scales are made as if the largest value were at least this
 
@@ -24,26 +26,58 @@ __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
   return r;
 }
 
-// A row a CTA, in registers between its two passes: V vectors of 8 elements a thread.
-template <bool XB, bool RB, int OT, int V>
-__global__ void __launch_bounds__(kMaxThreads) gdn_norm_kernel(const gdn_norm p) {
-  __shared__ float sums[32], tops[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+// A row stays in registers between the passes over it, V vectors of 8 elements a thread. It belongs to
+// a CTA, or (WARP) to a warp of one.
+template <bool XB, bool RB, int OT, int V, bool WARP>
+__global__ void __launch_bounds__(V > 2 ? 512 : kMaxThreads) gdn_norm_kernel(const gdn_norm p) {
+  __shared__ float sums[WARP ? 1 : 32], tops[WARP ? 1 : 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tid = WARP ? lane : threadIdx.x, threads = WARP ? 32 : blockDim.x, warps = threads >> 5;
   griddep_launch_dependents();
   griddep_wait();
-  const int64_t row = blockIdx.x;
+  const int64_t row = WARP ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp : blockIdx.x;
+  if (WARP && row >= p.rows) return;
+  // over the row's threads, every one of which gets the result
+  auto whole_sum = [&](float x) {
+    x = warp_sum(x);
+    if (WARP) return x;
+    if (lane == 0) sums[warp] = x;
+    __syncthreads();
+    return warp_sum(lane < warps ? sums[lane] : 0.0f);
+  };
+  auto warp_top = [](float x, int lanes) {
+    for (int off = lanes / 2; off > 0; off >>= 1) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, off));
+    return x;
+  };
+  auto whole_top = [&](float x) {
+    x = warp_top(x, 32);
+    if (WARP) return x;
+    if (lane == 0) tops[warp] = x;
+    __syncthreads();
+    return warp_top(lane < warps ? tops[lane] : 0.0f, 32);
+  };
+
+  Raw8<XB> in[V];
+  Raw8<RB> old[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int e = (j * threads + tid) * 8;
+    if (e >= p.width) continue;
+    in[j] = load8<XB>(p.x, row * p.x_stride + e);
+    if (p.residual != nullptr) old[j] = load8<RB>(p.residual, row * p.residual_stride + e);
+  }
   float y[V][8];
   float sum = 0.0f;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int e = (j * blockDim.x + tid) * 8;
+    const int e = (j * threads + tid) * 8;
 #pragma unroll
     for (int k = 0; k < 8; ++k) y[j][k] = 0.0f;
     if (e >= p.width) continue;
-    floats8<XB>(load8<XB>(p.x, row * p.x_stride + e), y[j]);
+    floats8<XB>(in[j], y[j]);
     if (p.residual != nullptr) {
       float r[8];
-      floats8<RB>(load8<RB>(p.residual, row * p.residual_stride + e), r);
+      floats8<RB>(old[j], r);
 #pragma unroll
       for (int k = 0; k < 8; ++k) y[j][k] += r[k];
       store8<RB>(p.residual, row * p.residual_stride + e, raw8<RB>(y[j]));
@@ -51,62 +85,46 @@ __global__ void __launch_bounds__(kMaxThreads) gdn_norm_kernel(const gdn_norm p)
 #pragma unroll
     for (int k = 0; k < 8; ++k) sum = fmaf(y[j][k], y[j][k], sum);
   }
-  sum = warp_sum(sum);
-  if (lane == 0) sums[warp] = sum;
-  __syncthreads();
-  sum = warp_sum(lane < warps ? sums[lane] : 0.0f);
-  const float inv = 1.0f / sqrtf(sum / static_cast<float>(p.width) + p.eps);
+  const float inv = 1.0f / sqrtf(whole_sum(sum) / static_cast<float>(p.width) + p.eps);
+
+  auto store_e4m3 = [&](int e, const float (&v)[8], float to) {
+    uint32_t q[2];
+#pragma unroll
+    for (int k = 0; k < 8; k += 4) q[k / 4] = pack_e4m3(v[k] * to, v[k + 1] * to) | pack_e4m3(v[k + 2] * to, v[k + 3] * to) << 16;
+    *reinterpret_cast<uint2*>(static_cast<unsigned char*>(p.o) + row * p.width + e) = make_uint2(q[0], q[1]);
+  };
   float top = 0.0f;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int e = (j * blockDim.x + tid) * 8;
-    float w[8];
-    if (p.weight != nullptr && e < p.width) floats8<false>(load8<false>(p.weight, e), w);
-    float group_top = 0.0f;
+    const int e = (j * threads + tid) * 8;
+    float w[8], group_top = 0.0f;
+    const bool weighed = p.weight != nullptr && e < p.width;
+    if (weighed) floats8<false>(load8<false>(p.weight, e), w);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       y[j][k] *= inv;
-      if (p.weight != nullptr && e < p.width) y[j][k] *= w[k];
-      group_top = max_nan(group_top, fabsf(y[j][k]));
+      if (weighed) y[j][k] *= w[k];
+      if (OT == GDN_TYPE_E4M3) group_top = max_nan(group_top, fabsf(y[j][k]));
     }
     if (OT != GDN_TYPE_E4M3) {
       if (e < p.width) store8<OT == GDN_TYPE_BF16>(p.o, row * p.width + e, raw8<OT == GDN_TYPE_BF16>(y[j]));
     } else if (p.group != 0) {
-      // 16 neighbouring lanes hold a group's 128 channels
-#pragma unroll
-      for (int off = 8; off > 0; off >>= 1) group_top = max_nan(group_top, __shfl_xor_sync(0xffffffffu, group_top, off));
-      const float s = max_nan(group_top, kLeast) / kTop, to = 1.0f / s;
+      const float s = max_nan(warp_top(group_top, kNormGroup / 8), kLeast) / kTop;  // 16 neighbouring lanes hold a group
       if (e < p.width) {
         if ((lane & 15) == 0) p.scales[row * ((p.width + kNormGroup - 1) / kNormGroup) + e / kNormGroup] = s;
-        uint32_t q[2];
-#pragma unroll
-        for (int k = 0; k < 8; k += 4)
-          q[k / 4] = pack_e4m3(y[j][k] * to, y[j][k + 1] * to) | pack_e4m3(y[j][k + 2] * to, y[j][k + 3] * to) << 16;
-        *reinterpret_cast<uint2*>(static_cast<unsigned char*>(p.o) + row * p.width + e) = make_uint2(q[0], q[1]);
+        store_e4m3(e, y[j], 1.0f / s);
       }
     } else {
       top = max_nan(top, group_top);
     }
   }
   if (OT == GDN_TYPE_E4M3 && p.group == 0) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, off));
-    if (lane == 0) tops[warp] = top;
-    __syncthreads();
-    top = lane < warps ? tops[lane] : 0.0f;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, off));
-    const float s = max_nan(top, kLeast) / kTop, to = 1.0f / s;
+    const float s = max_nan(whole_top(top), kLeast) / kTop;
     if (tid == 0) p.scales[row] = s;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int e = (j * blockDim.x + tid) * 8;
-      if (e >= p.width) continue;
-      uint32_t q[2];
-#pragma unroll
-      for (int k = 0; k < 8; k += 4)
-        q[k / 4] = pack_e4m3(y[j][k] * to, y[j][k + 1] * to) | pack_e4m3(y[j][k + 2] * to, y[j][k + 3] * to) << 16;
-      *reinterpret_cast<uint2*>(static_cast<unsigned char*>(p.o) + row * p.width + e) = make_uint2(q[0], q[1]);
+      const int e = (j * threads + tid) * 8;
+      if (e < p.width) store_e4m3(e, y[j], 1.0f / s);
     }
   }
 }
@@ -114,9 +132,15 @@ __global__ void __launch_bounds__(kMaxThreads) gdn_norm_kernel(const gdn_norm p)
 template <bool XB, bool RB, int OT>
 cudaError_t launch_row(const gdn_norm& p, cudaStream_t stream) {
   const int vecs = p.width / 8;
-  const unsigned one = static_cast<unsigned>((vecs + 31) / 32 * 32), two = static_cast<unsigned>(((vecs + 1) / 2 + 31) / 32 * 32);
-  if (one <= kMaxThreads) return launch_overlapped(gdn_norm_kernel<XB, RB, OT, 1>, p, dim3(p.rows), one, 0, 1u, stream);
-  return launch_overlapped(gdn_norm_kernel<XB, RB, OT, 2>, p, dim3(p.rows), two, 0, 1u, stream);
+  auto threads = [&](int v) { return static_cast<unsigned>(((vecs + v - 1) / v + 31) / 32 * 32); };
+  if (p.rows > kFewRows) {
+    const unsigned grid = static_cast<unsigned>((p.rows + kRowWarps - 1) / kRowWarps);
+    if (vecs <= 32) return launch_overlapped(gdn_norm_kernel<XB, RB, OT, 1, true>, p, dim3(grid), kRowWarps * 32, 0, 1u, stream);
+    if (vecs <= 128) return launch_overlapped(gdn_norm_kernel<XB, RB, OT, 4, true>, p, dim3(grid), kRowWarps * 32, 0, 1u, stream);
+    return launch_overlapped(gdn_norm_kernel<XB, RB, OT, 4, false>, p, dim3(p.rows), threads(4), 0, 1u, stream);
+  }
+  if (vecs <= kMaxThreads) return launch_overlapped(gdn_norm_kernel<XB, RB, OT, 1, false>, p, dim3(p.rows), threads(1), 0, 1u, stream);
+  return launch_overlapped(gdn_norm_kernel<XB, RB, OT, 4, false>, p, dim3(p.rows), threads(4), 0, 1u, stream);
 }
 
 template <bool XB, bool RB>
