@@ -8,84 +8,204 @@ namespace gdn {
 namespace {
 
 constexpr int kConvThreads = 128;
-constexpr int kSteps = 32;  // positions a thread takes
-constexpr int kAhead = 4;   // of them in flight
+constexpr int kGroup = 4, kGroups = 4;  // positions that are loaded together, and groups of them that a thread has room for
+constexpr int kMinSteps = 8, kMaxSteps = 128;  // positions a thread takes
+constexpr int64_t kEnough = 40000;              // threads
+constexpr int kTokenRows = 4;                   // requests that a thread takes one token of
+
+struct ConvTask {
+  ConvParams p;
+  int32_t steps;
+};
+
+// Eight channels of a slot's row: [8][3] elements, which start on a 16-byte boundary.
+template <bool BF16>
+struct Row {
+  uint32_t w[BF16 ? 12 : 24];
+};
+template <bool BF16>
+__device__ __forceinline__ void* row_at(const gdn_conv& c, int slot, int d) {
+  return static_cast<unsigned char*>(c.pool) + (static_cast<int64_t>(slot) * c.channels + d) * (3 * (BF16 ? 2 : 4));
+}
+template <bool BF16>
+__device__ __forceinline__ Row<BF16> load_row(const void* at) {
+  Row<BF16> r;
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 3 : 6); ++i) {
+    const uint4 v = static_cast<const uint4*>(at)[i];
+    r.w[4 * i] = v.x, r.w[4 * i + 1] = v.y, r.w[4 * i + 2] = v.z, r.w[4 * i + 3] = v.w;
+  }
+  return r;
+}
+// Column `col` as a vector of the eight channels.
+template <bool BF16>
+__device__ __forceinline__ Raw8<BF16> column(const Row<BF16>& r, int col) {
+  Raw8<BF16> x;
+  uint32_t out[BF16 ? 4 : 8];
+  if constexpr (BF16) {
+    auto e = [&](int i) { return (r.w[i / 2] >> (16 * (i & 1))) & 0xffffu; };
+#pragma unroll
+    for (int k = 0; k < 4; ++k) out[k] = e(6 * k + col) | e(6 * k + 3 + col) << 16;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) out[k] = r.w[3 * k + col];
+  }
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 1 : 2); ++i) x.v[i] = make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
+  return x;
+}
+// The row of three columns.
+template <bool BF16>
+__device__ __forceinline__ void store_row(void* at, const Raw8<BF16> (&col)[3]) {
+  uint32_t words[3][BF16 ? 4 : 8], out[BF16 ? 12 : 24];
+#pragma unroll
+  for (int j = 0; j < 3; ++j)
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 1 : 2); ++i)
+      words[j][4 * i] = col[j].v[i].x, words[j][4 * i + 1] = col[j].v[i].y, words[j][4 * i + 2] = col[j].v[i].z, words[j][4 * i + 3] = col[j].v[i].w;
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 12 : 24); ++i) {
+    if constexpr (BF16) {
+      auto e = [&](int j) { return (words[j % 3][j / 6] >> (16 * (j / 3 & 1))) & 0xffffu; };
+      out[i] = e(2 * i) | e(2 * i + 1) << 16;
+    } else {
+      out[i] = words[i % 3][i / 3];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 3 : 6); ++i) static_cast<uint4*>(at)[i] = make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
+}
+
+// a / b of what is not negative; most fit 32 bits, whose division is several times shorter.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+
+// Taps and bias of eight channels, as pairs of channels.
+struct Weights {
+  f32x2 w[4][4], bias[4];  // [tap][pair]
+};
+// Called by a whole warp, whose lanes hold consecutive vectors (those of lane 0's row and, past its
+// last, again from the first on). A lane's taps are 128 bytes in a row, so that loads of its own
+// would touch 32 lines each; the warp loads the 4 KB in order and hands them over in shared memory,
+// with places exchanged so that eight lanes meet all banks both ways.
+constexpr int kTapVecs = 256;
+__device__ __forceinline__ Weights load_weights(const gdn_conv& c, int d, float4* taps) {
+  const int lane = threadIdx.x & 31, first = __shfl_sync(0xffffffffu, d, 0);
+#pragma unroll
+  for (int j = 0; j < kTapVecs / 32; ++j) {
+    const int i = 32 * j + lane;
+    taps[i ^ (i >> 3 & 7)] = reinterpret_cast<const float4*>(c.w)[(first + i) % c.channels];
+  }
+  __syncwarp();
+  Weights r;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float4 lo = taps[8 * lane + ((2 * k) ^ (lane & 7))], hi = taps[8 * lane + ((2 * k + 1) ^ (lane & 7))];
+    r.w[0][k] = pack2(lo.x, hi.x), r.w[1][k] = pack2(lo.y, hi.y), r.w[2][k] = pack2(lo.z, hi.z), r.w[3][k] = pack2(lo.w, hi.w);
+    r.bias[k] = c.bias != nullptr ? *reinterpret_cast<const f32x2*>(c.bias + d + 2 * k) : 0;
+  }
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ void pairs8(const Raw8<BF16>& r, f32x2 (&x)[4]) {
+  float f[8];
+  floats8<BF16>(r, f);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x[k] = pack2(f[2 * k], f[2 * k + 1]);
+}
+// The output of eight channels at a position, of the inputs there and at the three before.
+template <bool BF16>
+__device__ __forceinline__ Raw8<BF16> output(const Weights& s, const f32x2 (&past)[3][4], const f32x2 (&in)[4], bool silu) {
+  float o[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    f32x2 sum = fma2(in[k], s.w[3][k], fma2(past[2][k], s.w[2][k], fma2(past[1][k], s.w[1][k], fma2(past[0][k], s.w[0][k], s.bias[k]))));
+    if (silu) sum = silu_2<!BF16>(sum);
+    const float2 v = unpack2(sum);
+    o[2 * k] = v.x, o[2 * k + 1] = v.y;
+  }
+  return raw8<BF16>(o);
+}
 
 // The three inputs before position `at` (oldest first) of eight channels: of the prompt, or of the
 // slot's row where they lie before it.
 template <bool BF16>
-__device__ __forceinline__ void inputs_before(const gdn_conv& c, const void* row, int64_t x, int at, int d, Raw8<BF16> (&w)[3]) {
-  // [8 channels][3]: 24 elements that start on a 16-byte boundary
-  uint4 old[BF16 ? 3 : 6];
+__device__ __forceinline__ void inputs_before(const gdn_conv& c, const void* row, int64_t x, int at, Raw8<BF16> (&to)[3]) {
   if (at < 3) {
+    const Row<BF16> old = load_row<BF16>(row);
 #pragma unroll
-    for (int i = 0; i < (BF16 ? 3 : 6); ++i)
-      old[i] = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(row) + d * 3 * (BF16 ? 2 : 4))[i];
-  }
-#pragma unroll
-  for (int j = 0; j < 3; ++j) {
-    const int from = at - 3 + j;  // position of the input; -3..-1: the row's columns 0..2
-    if (from >= 0) {
-      w[j] = load8<BF16>(c.x, x + from * c.x_strides[1]);
-      continue;
+    for (int j = 0; j < 3; ++j) {
+      if (at + j < 3)
+        to[j] = at == 0 ? column<BF16>(old, j) : at == 1 ? column<BF16>(old, j < 2 ? j + 1 : 2) : column<BF16>(old, 2);
+      else
+        to[j] = load8<BF16>(c.x, x + (at - 3 + j) * c.x_strides[1]);
     }
-#pragma unroll
-    for (int col = 0; col < 3; ++col) {
-      if (from + 3 != col) continue;
-      if constexpr (BF16) {
-        uint32_t e[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) e[k] = (reinterpret_cast<const uint32_t*>(old)[(k * 3 + col) / 2] >> (16 * ((k * 3 + col) & 1))) & 0xffffu;
-        w[j].v[0] = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
-      } else {
-        const uint32_t* o = reinterpret_cast<const uint32_t*>(old);
-        w[j].v[0] = make_uint4(o[col], o[3 + col], o[6 + col], o[9 + col]);
-        w[j].v[1] = make_uint4(o[12 + col], o[15 + col], o[18 + col], o[21 + col]);
-      }
-    }
-  }
-}
-
-// The slot's row of eight channels.
-template <bool BF16>
-__device__ __forceinline__ void write_row(void* row, int d, const Raw8<BF16> (&w)[3]) {
-  uint32_t* to = reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(row) + d * 3 * (BF16 ? 2 : 4));
-  uint32_t out[BF16 ? 12 : 24];
-  if constexpr (BF16) {
-    auto e = [&](int i) {  // element i of [8][3]
-      const uint4& v = w[i % 3].v[0];
-      const uint32_t words[4] = {v.x, v.y, v.z, v.w};
-      return (words[i / 3 / 2] >> (16 * (i / 3 & 1))) & 0xffffu;
-    };
-#pragma unroll
-    for (int i = 0; i < 12; ++i) out[i] = e(2 * i) | e(2 * i + 1) << 16;
   } else {
 #pragma unroll
-    for (int i = 0; i < 24; ++i) {
-      const uint4& v = w[i % 3].v[i / 3 / 4];
-      const uint32_t words[4] = {v.x, v.y, v.z, v.w};
-      out[i] = words[i / 3 % 4];
-    }
+    for (int j = 0; j < 3; ++j) to[j] = load8<BF16>(c.x, x + (at - 3 + j) * c.x_strides[1]);
   }
-#pragma unroll
-  for (int i = 0; i < (BF16 ? 3 : 6); ++i)
-    reinterpret_cast<uint4*>(to)[i] = make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
 }
 
-// A thread runs over kSteps positions of eight channels with the last three inputs in registers. The
+// One token of every request. A thread takes eight channels of `rows` requests, for which it loads the
+// taps once.
+struct TokenTask {
+  ConvParams p;
+  int32_t rows;
+};
+template <bool BF16>
+__global__ void __launch_bounds__(kConvThreads) gdn_causal_conv_token_kernel(const TokenTask task) {
+  const gdn_conv& c = task.p.c;
+  __shared__ float4 taps[kConvThreads / 32][kTapVecs];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int vecs = c.channels / 8;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * kConvThreads + threadIdx.x;
+  const int first = static_cast<int>(quotient(item, vecs)), d = static_cast<int>(item - static_cast<int64_t>(first) * vecs) * 8;
+  const Weights weights = load_weights(c, d, taps[threadIdx.x >> 5]);
+  const bool silu = (c.flags & GDN_CONV_SILU) != 0u;
+  for (int r = 0; r < task.rows; ++r) {
+    const int b = first * task.rows + r;
+    if (b >= c.batch) return;
+    const int slot = c.slot[b];
+    const Raw8<BF16> now = load8<BF16>(c.x, b * c.x_strides[0] + d);
+    const int len = c.seq_lens != nullptr ? c.seq_lens[b] : 1;
+    if (slot < 0) continue;
+    const bool bad_slot = slot >= c.num_slots, bad_len = len < 0 || len > 1;
+    if (bad_slot || bad_len) {
+      if (d == 0) atomic_status(task.p.status, bad_slot ? GDN_STATUS_BAD_SLOT : GDN_STATUS_BAD_LEN);
+      continue;
+    }
+    if (len == 0) continue;
+    void* const row = row_at<BF16>(c, slot, d);
+    const Row<BF16> old = load_row<BF16>(row);
+    const Raw8<BF16> cols[3] = {column<BF16>(old, 1), column<BF16>(old, 2), now};
+    store_row<BF16>(row, cols);
+    f32x2 past[3][4], in[4];
+    pairs8<BF16>(column<BF16>(old, 0), past[0]);
+    pairs8<BF16>(cols[0], past[1]);
+    pairs8<BF16>(cols[1], past[2]);
+    pairs8<BF16>(now, in);
+    store8<BF16>(c.o, static_cast<int64_t>(b) * c.channels + d, output<BF16>(weights, past, in, silu));
+  }
+}
+
+// A thread runs over `steps` positions of eight channels with the last three inputs in registers. The
 // thread of a request's first positions is the only one that reads the slot's row, so it also
 // writes it, from the prompt's end.
 template <bool BF16>
-__global__ void __launch_bounds__(kConvThreads) gdn_causal_conv_kernel(const ConvParams p) {
+__global__ void __launch_bounds__(kConvThreads, 4) gdn_causal_conv_kernel(const ConvTask task) {
+  const ConvParams& p = task.p;
   const gdn_conv& c = p.c;
+  __shared__ float4 taps[kConvThreads / 32][kTapVecs];
   griddep_launch_dependents();
   griddep_wait();
-  const int vecs = c.channels / 8, chunks = (c.num_tokens + kSteps - 1) / kSteps;
+  const int vecs = c.channels / 8, chunks = (c.num_tokens + task.steps - 1) / task.steps;
   const int64_t per = static_cast<int64_t>(vecs) * chunks, item = static_cast<int64_t>(blockIdx.x) * kConvThreads + threadIdx.x;
-  if (item >= per * c.batch) return;
-  const int b = static_cast<int>(item / per), in = static_cast<int>(item - b * per);
+  const int b = static_cast<int>(quotient(item, per)), in = static_cast<int>(item - b * per);
   const int chunk = in / vecs, vec = in - chunk * vecs, d = vec * 8;
-  const int slot = c.slot[b];
+  const int slot = b < c.batch ? c.slot[b] : -1;
+  const Weights weights = load_weights(c, d, taps[threadIdx.x >> 5]);  // while the slot is looked up
   if (slot < 0) return;
   const int len = c.seq_lens != nullptr ? c.seq_lens[b] : c.num_tokens;
   const bool bad_slot = slot >= c.num_slots, bad_len = len < 0 || len > c.num_tokens;
@@ -93,73 +213,87 @@ __global__ void __launch_bounds__(kConvThreads) gdn_causal_conv_kernel(const Con
     if (in == 0) atomic_status(p.status, bad_slot ? GDN_STATUS_BAD_SLOT : GDN_STATUS_BAD_LEN);
     return;
   }
-  const int begin = chunk * kSteps, end = min(begin + kSteps, len);
+  const int begin = chunk * task.steps, end = min(begin + task.steps, len);
   if (begin >= end) return;
   const int64_t x = b * c.x_strides[0] + d;
-  void* const row = static_cast<unsigned char*>(c.pool) + static_cast<int64_t>(slot) * c.channels * (3 * (BF16 ? 2 : 4));
+  void* const row = row_at<BF16>(c, slot, d);
   Raw8<BF16> before[3];
-  inputs_before<BF16>(c, row, x, begin, d, before);
+  inputs_before<BF16>(c, row, x, begin, before);
   if (chunk == 0) {
     Raw8<BF16> last[3];
-    inputs_before<BF16>(c, row, x, len, d, last);
-    write_row<BF16>(row, d, last);
+    inputs_before<BF16>(c, row, x, len, last);
+    store_row<BF16>(row, last);
   }
-  // pairs of channels from here on
-  f32x2 w[4][4], bias[4], past[3][4];  // [tap][pair]
+  f32x2 past[3][4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float4 lo = reinterpret_cast<const float4*>(c.w)[d + 2 * k], hi = reinterpret_cast<const float4*>(c.w)[d + 2 * k + 1];
-    w[0][k] = pack2(lo.x, hi.x), w[1][k] = pack2(lo.y, hi.y), w[2][k] = pack2(lo.z, hi.z), w[3][k] = pack2(lo.w, hi.w);
-    bias[k] = c.bias != nullptr ? *reinterpret_cast<const f32x2*>(c.bias + d + 2 * k) : 0;
-  }
-  auto pairs = [](const Raw8<BF16>& r, f32x2 (&x)[4]) {
-    float f[8];
-    floats8<BF16>(r, f);
+  for (int j = 0; j < 3; ++j) pairs8<BF16>(before[j], past[j]);
+  const bool silu = (c.flags & GDN_CONV_SILU) != 0u;
+  // Loads go through shared memory, where a thread reads what it has asked for itself: more of them
+  // are in flight than registers would hold.
+  extern __shared__ __align__(16) unsigned char ring[];
+  constexpr int kVec = BF16 ? 16 : 32;
+  unsigned char* const mine = ring + threadIdx.x * 16;
+  auto place = [&](int t, int half) { return mine + ((t & (kGroup * kGroups - 1)) * (kVec / 16) + half) * (kConvThreads * 16); };
+  const unsigned char* const from = static_cast<const unsigned char*>(c.x) + x * (kVec / 8);
+  const int64_t stride = c.x_strides[1] * (kVec / 8);
+  auto fetch = [&](int t0) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] = pack2(f[2 * k], f[2 * k + 1]);
+    for (int j = 0; j < kGroup; ++j)
+      if (t0 + j < end)
+#pragma unroll
+        for (int half = 0; half < kVec / 16; ++half) cp_async16(place(t0 + j - begin, half), from + (t0 + j) * stride + half * 16);
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
-  for (int j = 0; j < 3; ++j) pairs(before[j], past[j]);
-  const bool silu = (c.flags & GDN_CONV_SILU) != 0u;
-  Raw8<BF16> next[kAhead];
-#pragma unroll
-  for (int j = 0; j < kAhead; ++j)
-    if (begin + j < end) next[j] = load8<BF16>(c.x, x + (begin + j) * c.x_strides[1]);
+  for (int i = 0; i < kGroups - 1; ++i) fetch(begin + i * kGroup);
   int64_t to = (static_cast<int64_t>(b) * c.num_tokens + begin) * c.channels + d;
-  for (int t0 = begin; t0 < end; t0 += kAhead) {
-    Raw8<BF16> now[kAhead];
+  for (int t0 = begin; t0 < end; t0 += kGroup) {
+    fetch(t0 + (kGroups - 1) * kGroup);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kGroups - 1) : "memory");
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      now[j] = next[j];
-      if (t0 + kAhead + j < end) next[j] = load8<BF16>(c.x, x + (t0 + kAhead + j) * c.x_strides[1]);
-    }
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
+    for (int j = 0; j < kGroup; ++j) {
       if (t0 + j >= end) break;
-      f32x2 in[4];
-      float o[8];
-      pairs(now[j], in);
+      Raw8<BF16> now;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        f32x2 sum = fma2(in[k], w[3][k], fma2(past[2][k], w[2][k], fma2(past[1][k], w[1][k], fma2(past[0][k], w[0][k], bias[k]))));
-        if (silu) sum = silu_2<!BF16>(sum);
-        const float2 v = unpack2(sum);
-        o[2 * k] = v.x, o[2 * k + 1] = v.y;
-        past[0][k] = past[1][k], past[1][k] = past[2][k], past[2][k] = in[k];
-      }
-      store8<BF16>(c.o, to, raw8<BF16>(o));
+      for (int half = 0; half < kVec / 16; ++half) now.v[half] = *reinterpret_cast<const uint4*>(place(t0 + j - begin, half));
+      f32x2 in[4];
+      pairs8<BF16>(now, in);
+      store8<BF16>(c.o, to, output<BF16>(weights, past, in, silu));
+#pragma unroll
+      for (int k = 0; k < 4; ++k) past[0][k] = past[1][k], past[1][k] = past[2][k], past[2][k] = in[k];
       to += c.channels;
     }
   }
 }
 
+template <bool BF16>
+cudaError_t launch_conv(const ConvTask& task, int64_t items, cudaStream_t stream) {
+  constexpr int kBytes = kGroup * kGroups * (BF16 ? 16 : 32) * kConvThreads;
+  static std::atomic<bool> allowed[kDevices];
+  const cudaError_t err = allow_shared(reinterpret_cast<const void*>(gdn_causal_conv_kernel<BF16>), kBytes, allowed);
+  if (err != cudaSuccess) return err;
+  const unsigned grid = static_cast<unsigned>((items + kConvThreads - 1) / kConvThreads);
+  return launch_overlapped(gdn_causal_conv_kernel<BF16>, task, dim3(grid), kConvThreads, kBytes, 1u, stream);
+}
+
+template <bool BF16>
+cudaError_t launch_token(const ConvParams& p, cudaStream_t stream) {
+  const int64_t vecs = p.c.channels / 8;
+  TokenTask task{p, vecs * p.c.batch >= 4 * kEnough ? kTokenRows : 1};
+  const int64_t items = vecs * ((p.c.batch + task.rows - 1) / task.rows);
+  const unsigned grid = static_cast<unsigned>((items + kConvThreads - 1) / kConvThreads);
+  return launch_overlapped(gdn_causal_conv_token_kernel<BF16>, task, dim3(grid), kConvThreads, 0, 1u, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_causal_conv(const ConvParams& p, cudaStream_t stream) {
-  const int64_t chunks = (p.c.num_tokens + kSteps - 1) / kSteps, items = chunks * p.c.batch * (p.c.channels / 8);
-  const unsigned grid = static_cast<unsigned>((items + kConvThreads - 1) / kConvThreads);
-  return launch_overlapped((p.c.flags & GDN_QKV_BF16) != 0u ? gdn_causal_conv_kernel<true> : gdn_causal_conv_kernel<false>, p,
-                           dim3(grid), kConvThreads, 0, 1u, stream);
+  if (p.c.num_tokens == 1) return (p.c.flags & GDN_QKV_BF16) != 0u ? launch_token<true>(p, stream) : launch_token<false>(p, stream);
+  ConvTask task{p, kMaxSteps};
+  const int64_t vecs = static_cast<int64_t>(p.c.batch) * (p.c.channels / 8);
+  auto items = [&] { return (p.c.num_tokens + task.steps - 1) / task.steps * vecs; };
+  while (task.steps > kMinSteps && items() < kEnough) task.steps /= 2;
+  return (p.c.flags & GDN_QKV_BF16) != 0u ? launch_conv<true>(task, items(), stream) : launch_conv<false>(task, items(), stream);
 }
 
 }  // namespace gdn
