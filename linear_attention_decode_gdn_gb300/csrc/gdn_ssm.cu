@@ -26,7 +26,7 @@ struct StepParams {
 // takes once (steps, gate, readout) is done by the lane that the sums over the states end up in,
 // and comes to the others by shuffles.
 template <int N, bool BF16>
-__global__ void __launch_bounds__(kStepWarps * 32) gdn_ssm_step_kernel(const StepParams p) {
+__global__ void __launch_bounds__(kStepWarps * 32, 8) gdn_ssm_step_kernel(const StepParams p) {
   constexpr int LANES = N / 4, PASSES = LANES < 4 ? LANES : 4, WIDTH = 32 / LANES, CH = PASSES * WIDTH, SHARE = LANES / PASSES;
   const gdn_ssm& s = p.s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -124,7 +124,7 @@ cudaError_t launch_step(const SsmParams& given, cudaStream_t stream) {
   p.blocks = (p.per_group + CH - 1) / CH;
   p.columns = p.blocks * p.s.num_groups;
   const int64_t all = static_cast<int64_t>(p.columns) * p.s.batch;
-  p.rows = all >= 65536 ? 4 : 1;
+    p.rows = all >= 32768 ? 2 : 1;
   const int64_t warps = static_cast<int64_t>(p.columns) * ((p.s.batch + p.rows - 1) / p.rows);
   return launch_overlapped(gdn_ssm_step_kernel<N, BF16>, p, dim3(static_cast<unsigned>((warps + kStepWarps - 1) / kStepWarps)),
                            kStepWarps * 32, 0, 1u, stream);
