@@ -78,8 +78,10 @@ struct WarpSmem {
 
 // Where the prompts' channels are too few for the GPU, prompts are cut into parts of `part` positions
 // that are scanned side by side. A first kernel (SUMMARY) takes every part but the last from a state
-// of zero: end[j], and sum[j], the sum of its steps. A part then begins with the prompt's state
-// taken through the parts before it, h <- exp(sum[j] a) h + end[j].
+// of zero: end[j], and sum[j], the sum of its steps. A second one goes through the parts with the
+// prompt's state, h <- exp(sum[j] a) h + end[j], and leaves in end[j] the state after part j. (Every
+// part's warps doing that for themselves read O(parts^2) states: 45 MB for one prompt of 1021
+// positions and 2048 channels.)
 struct ScanParams {
   gdn_ssm s;
   int32_t* status;
@@ -151,7 +153,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) gdn_ssm_scan_kernel(const Scan
   const int64_t mine = static_cast<int64_t>(c0 + set * 2) * C::N + part * 8, per_request = static_cast<int64_t>(s.channels) * C::N;
   auto end_of = [&](int j) { return p.end + (static_cast<int64_t>(b) * (p.parts - 1) + j) * per_request + mine; };
   auto sum_of = [&](int j) { return p.sum + (static_cast<int64_t>(b) * (p.parts - 1) + j) * s.channels + c0 + set * 2; };
-  load_states(p.parts == 1 || (SUMMARY && part_no == 0) ? state : p.init + b * per_request + mine, h);
+  load_states(p.parts == 1 || (SUMMARY && part_no == 0) ? state : part_no == 0 ? p.init + b * per_request + mine : end_of(part_no - 1), h);
   f32x2 steps_sum[2] = {0, 0};  // both halves alike
   if (SUMMARY) {
     // the last part's scan overwrites the slot's state while others still begin
@@ -161,18 +163,6 @@ __global__ void __launch_bounds__(kWarps * 32, 4) gdn_ssm_scan_kernel(const Scan
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) h[i][j] = 0;
-  } else {
-#pragma unroll 2
-    for (int j = 0; j < part_no; ++j) {
-      f32x2 e[2][4];
-      load_states(end_of(j), e);
-      float2 sum = make_float2(0.0f, 0.0f);
-      if (mine_live) sum = *reinterpret_cast<const float2*>(sum_of(j));
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) h[i][k] = fma2(ex2_2(mul2(both(i == 0 ? sum.x : sum.y), a[i][k])), h[i][k], e[i][k]);
-    }
   }
   const bool softplus = (s.flags & GDN_DT_SOFTPLUS) != 0u;
   for (int c = lane; c < C::CH; c += 32) {
@@ -317,18 +307,55 @@ __global__ void __launch_bounds__(kWarps * 32, 4) gdn_ssm_scan_kernel(const Scan
   }
 }
 
+// Four states a thread, several parts' loads in flight.
+constexpr int kJoinThreads = 128, kJoinAhead = 8;
+__global__ void __launch_bounds__(kJoinThreads) gdn_ssm_join_kernel(const ScanParams p) {
+  const gdn_ssm& s = p.s;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t states = static_cast<int64_t>(s.channels) * s.state_size;
+  const uint32_t blocks = static_cast<uint32_t>((states / 4 + kJoinThreads - 1) / kJoinThreads);
+  const int b = static_cast<int>(blockIdx.x / blocks);
+  const int64_t at = (static_cast<int64_t>(blockIdx.x - b * blocks) * kJoinThreads + threadIdx.x) * 4;
+  const int slot = s.slot[b], len = s.seq_lens != nullptr ? s.seq_lens[b] : s.num_tokens;
+  if (at >= states || slot < 0 || slot >= s.num_slots || len <= p.part || len > s.num_tokens) return;
+  const int parts = (len - 1) / p.part;  // that another one comes after
+  const float4 a = *reinterpret_cast<const float4*>(s.a + at);
+  float4 h = *reinterpret_cast<const float4*>(p.init + b * states + at);
+  float* const end = p.end + b * (p.parts - 1) * states + at;
+  const float* const sum = p.sum + static_cast<int64_t>(b) * (p.parts - 1) * s.channels + at / s.state_size;
+  for (int j0 = 0; j0 < parts; j0 += kJoinAhead) {
+    float4 e[kJoinAhead];
+    float t[kJoinAhead];
+#pragma unroll
+    for (int j = 0; j < kJoinAhead; ++j) {
+      if (j0 + j >= parts) break;
+      e[j] = *reinterpret_cast<const float4*>(end + (j0 + j) * states);
+      t[j] = sum[static_cast<int64_t>(j0 + j) * s.channels] * kLog2e;
+    }
+#pragma unroll
+    for (int j = 0; j < kJoinAhead; ++j) {
+      if (j0 + j >= parts) break;
+      h = make_float4(fmaf(ex2(t[j] * a.x), h.x, e[j].x), fmaf(ex2(t[j] * a.y), h.y, e[j].y), fmaf(ex2(t[j] * a.z), h.z, e[j].z),
+                      fmaf(ex2(t[j] * a.w), h.w, e[j].w));
+      *reinterpret_cast<float4*>(end + (j0 + j) * states) = h;
+    }
+  }
+}
+
 // How prompts are cut: by the warps that whole prompts would give. The GPU holds 2432 of them; from
 // 1536 on prompts stay whole (16 x 1024 positions of 4096 channels, 2048 warps: 342 us, 417 in two
 // parts), below that about 8192 are made: parts that are short beside the whole even out prompts of
-// several lengths (8 ragged prompts, 1024 warps: 457 us whole, 303 in 4 parts, 265 in 8; 16384
-// positions, 256 warps: 2906 us whole, 1331 in 5, 976 in 32). A part begins by going through the
-// ends of all parts before it, so there are at most sqrt(T) of them.
+// several lengths (8 ragged prompts, 1024 warps: 457 us whole, 303 in 4 parts, 267 in 8; 16384
+// positions, 256 warps: 2906 us whole, 1331 in 5 parts, 942 in 19, 970 in 32). A join goes through
+// all parts in turn, so there are at most sqrt(T) of them, of 32 positions at least (128 positions of
+// 2048 channels: 16 us in parts of 32, 25 in parts of 64; 300 of 4096: 26 and 30).
 struct Cut {
   int32_t parts, part;
 };
 Cut cut_of(int32_t batch, int32_t tokens, int32_t channels, int32_t state_size) {
   constexpr int64_t kEnough = 1536, kWanted = 8192;
-  constexpr int32_t kShortest = 64, kRound = 16;
+    constexpr int32_t kShortest = 32, kRound = 8;
   const int32_t of_warp = 512 / state_size;  // channels
   const int64_t warps = static_cast<int64_t>(batch) * ((channels + of_warp - 1) / of_warp);
   int32_t parts = warps >= kEnough ? 1 : static_cast<int32_t>(kWanted / warps);
@@ -361,7 +388,10 @@ cudaError_t launch_scan(const SsmParams& given, void* workspace, cudaStream_t st
     p.init = static_cast<float*>(workspace);
     p.end = p.init + states;
     p.sum = p.end + states * (cut.parts - 1);
-    const cudaError_t err = launch_parts<C, true>(p, stream);
+    cudaError_t err = launch_parts<C, true>(p, stream);
+    if (err != cudaSuccess) return err;
+    const int64_t blocks = (static_cast<int64_t>(s.channels) * s.state_size / 4 + kJoinThreads - 1) / kJoinThreads;
+    err = launch_overlapped(gdn_ssm_join_kernel, p, dim3(static_cast<unsigned>(blocks * s.batch)), kJoinThreads, 0, 1u, stream);
     if (err != cudaSuccess) return err;
   }
   return launch_parts<C, false>(p, stream);

@@ -155,17 +155,18 @@ __device__ __forceinline__ f32x2 softplus_2(f32x2 x2) {
   p = fma2(p, e, both(0.9999999404f));
   return fma2(pack2(fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f)), both(kLn2), mul2(p, e));
 }
+
 // z / (1 + e^-z). 2^-t, t = z log2(e), is off by |z| roundings, which EXACT takes out again (the
 // factor 1 + r ln 2, r what the rounding of t lost): without it the result keeps 2^-20, bf16 has 2^-8.
 template <bool EXACT>
 __device__ __forceinline__ f32x2 silu_2(f32x2 z) {
-  const f32x2 t = mul2(z, both(-kLog2e));
-  f32x2 e = ex2_2(t);
+  f32x2 e = ex2_2(mul2(z, both(-kLog2e)));
   if (EXACT) {
-    const float2 v = unpack2(z);
-    // (of z between -80 and 80: past that e is 0 or so large that nothing changes)
+    const float2 v = unpack2(z), big = unpack2(e);
+    // past 80 either way e is next to 0 or so large that r does not count; finite, as r may be 0
     const f32x2 near = pack2(fminf(fmaxf(v.x, -80.0f), 80.0f), fminf(fmaxf(v.y, -80.0f), 80.0f));
     const f32x2 r = fma2(near, both(-kLog2e), mul2(near, both(kLog2e)));
+    e = pack2(fminf(big.x, 3e38f), fminf(big.y, 3e38f));
     e = fma2(e, mul2(r, both(kLn2)), e);
   }
   return mul2(z, rcp_2(add2(e, both(1.0f))));

@@ -111,33 +111,69 @@ def ssm_workspace_bytes(batch: int, num_tokens: int, channels: int, state_size: 
     return out.value
 
 
-def _pack(dims, u, dt, a, b, c, state, slot, y, z, skip, dt_bias, softplus, seq_lens):
-    """The C struct of a scan (dims 3) or a step (dims 2), and the device."""
-    dtype, shape, at = _input(u, (dims,), "u")
-    channels, batch = shape[-1], shape[0]
+def _wrong(u, dt, a, b, c, state, y, z, skip, dt_bias, at):
+    """Raises the error of what _pack found wrong."""
+    dims, dtype, shape = u.dim(), u.dtype, u.shape
     if b.dim() != dims + 1 or state.dim() != 3:
         raise ValueError(f"b: {dims + 1} dimensions [.., groups, state size]; state: [slots, channels, state size]")
-    groups, n = b.shape[-2:]
-    narrow = (*shape[:-1], groups, n)
-    u_at = _rows(u, shape, dtype, "u", at)
-    dt_at = _rows(dt, shape, dtype, "dt", at)
-    b_at = _rows(b, narrow, dtype, "b", at)
-    c_at = _rows(c, narrow, dtype, "c", at)
-    z_at = (0, 0, 0) if z is None else _rows(z, shape, dtype, "z", at)
-    tokens = 1
+    channels, groups, n = shape[-1], *b.shape[-2:]
+    for t, what in ((u, "u"), (dt, "dt"), (z, "z")):
+        if t is not None:
+            _rows(t, shape, dtype, what, at)
+    for t, what in ((b, "b"), (c, "c")):
+        _rows(t, (*shape[:-1], groups, n), dtype, what, at)
+    for t, size, what in ((a, (channels, n), "a"), (skip, (channels,), "skip"), (dt_bias, (channels,), "dt_bias"),
+                          (state, (state.shape[0], channels, n), "state")):
+        if t is not None:
+            _whole(t, size, _FP32, what, at)
+    _whole(y, shape, dtype, "y", at)
+    raise ValueError("tensors of other types, shapes, strides or devices than the call takes")
+
+
+# A decode step makes one call a layer: the conditions are written out, as in ``paged``.
+def _pack(dims, u, dt, a, b, c, state, slot, y, z, skip, dt_bias, softplus, seq_lens):
+    """The C struct of a scan (dims 3) or a step (dims 2), and the device."""
+    at = u.get_device()
+    if at < 0 or at != _current_device():
+        raise _not_here(at, "u")
+    dtype, shape, narrow, pool = u.dtype, u.shape, b.shape, state.shape
+    if (dtype is not _BF16 and dtype is not _FP32) or len(shape) != dims:
+        raise ValueError(f"u: bf16 or fp32, with {dims} dimensions, got {dtype} {tuple(shape)}")
+    if len(narrow) != dims + 1 or len(pool) != 3:
+        _wrong(u, dt, a, b, c, state, y, z, skip, dt_bias, at)
+    batch, channels, groups, n = shape[0], shape[-1], narrow[-2], narrow[-1]
+    z_ptr = z0 = z1 = 0
     if dims == 2:  # no stride between the tokens of one
-        b_at, c_at = (*b_at[:2], 0, b_at[2]), (*c_at[:2], 0, c_at[2])
-        u_at, dt_at, z_at = (*u_at, 0), (*dt_at, 0), (*z_at[:2], 0)
+        tokens = 1
+        (u0, ul), (t0, tl), (b0, b2, bl), (c0, c2, cl) = u.stride(), dt.stride(), b.stride(), c.stride()
+        u1 = t1 = b1 = c1 = 0
+        ok = narrow[0] == batch
+        if z is not None:
+            z0, zl = z.stride()
     else:
         tokens = shape[1]
-    slots = state.shape[0]
+        (u0, u1, ul), (t0, t1, tl), (b0, b1, b2, bl), (c0, c1, c2, cl) = u.stride(), dt.stride(), b.stride(), c.stride()
+        ok = narrow[0] == batch and narrow[1] == tokens
+        if z is not None:
+            z0, z1, zl = z.stride()
+    ok = (ok and ul == tl == bl == cl == 1 and dt.dtype is dtype and b.dtype is dtype and c.dtype is dtype and y.dtype is dtype
+          and dt.shape == shape and c.shape == narrow and y.shape == shape and a.shape == pool[1:] and pool[1] == channels and pool[2] == n
+          and a.dtype is _FP32 and state.dtype is _FP32 and y.is_contiguous() and a.is_contiguous() and state.is_contiguous()
+          and dt.get_device() == b.get_device() == c.get_device() == a.get_device() == state.get_device() == y.get_device() == at)
+    if ok and z is not None:
+        ok = zl == 1 and z.dtype is dtype and z.shape == shape and z.get_device() == at
+        z_ptr = z.data_ptr()
+    if ok and skip is not None:
+        ok = skip.dtype is _FP32 and skip.dim() == 1 and skip.numel() == channels and skip.is_contiguous() and skip.get_device() == at
+    if ok and dt_bias is not None:
+        ok = dt_bias.dtype is _FP32 and dt_bias.dim() == 1 and dt_bias.numel() == channels and dt_bias.is_contiguous() and dt_bias.get_device() == at
+    if not ok:
+        _wrong(u, dt, a, b, c, state, y, z, skip, dt_bias, at)
     return _pack_ssm(
-        batch, tokens, channels, n, groups, slots, (_abi.QKV_BF16 if dtype is _BF16 else 0) | (_abi.DT_SOFTPLUS if softplus else 0),
-        *u_at, *dt_at, *b_at, *c_at, *z_at, _whole(a, (channels, n), _FP32, "a", at),
-        0 if skip is None else _whole(skip, (channels,), _FP32, "skip", at),
-        0 if dt_bias is None else _whole(dt_bias, (channels,), _FP32, "dt_bias", at),
-        _whole(state, (slots, channels, n), _FP32, "state", at), _ints(slot, batch, "slot", at),
-        0 if seq_lens is None else _ints(seq_lens, batch, "seq_lens", at), _whole(y, shape, dtype, "y", at)), at
+        batch, tokens, channels, n, groups, pool[0], (_abi.QKV_BF16 if dtype is _BF16 else 0) | (_abi.DT_SOFTPLUS if softplus else 0),
+        u.data_ptr(), u0, u1, dt.data_ptr(), t0, t1, b.data_ptr(), b0, b1, b2, c.data_ptr(), c0, c1, c2, z_ptr, z0, z1, a.data_ptr(),
+        0 if skip is None else skip.data_ptr(), 0 if dt_bias is None else dt_bias.data_ptr(), state.data_ptr(), _ints(slot, batch, "slot", at),
+        0 if seq_lens is None else _ints(seq_lens, batch, "seq_lens", at), y.data_ptr()), at
 
 
 def ssm_scan(u, dt, a, b, c, state, slot, y, workspace=None, *, z=None, skip=None, dt_bias=None, softplus=True, seq_lens=None,

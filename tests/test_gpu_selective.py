@@ -72,7 +72,8 @@ def check_norm(gdn, x, residual, weight, out, group=0, eps=1e-6):
     close(o.float(), want, (want.abs() * 2.0 ** -4).clamp(min=2.0 ** -10) + want.abs() * (off + 4 * E) * 1.01)
 
 
-@pytest.mark.parametrize("rows,width", [(1, 8), (3, 24), (5, 128), (2, 136), (257, 1024), (3, 2056), (66, 4096), (700, 4104), (9, 6144), (2, 8192), (3, 12008), (2, 16384)])
+@pytest.mark.parametrize("rows,width", [(1, 8), (3, 24), (5, 128), (2, 136), (257, 1024), (3, 2056), (66, 4096), (700, 4104), (9, 6144), (2, 8192), (3, 12008), (2, 16384),
+                                        (609, 8), (700, 256), (700, 264), (613, 1024), (610, 1032), (640, 16384)])
 @pytest.mark.parametrize("kind,res", [(BF16, BF16), (BF16, FP32), (FP32, FP32), (FP32, BF16), (BF16, None), (FP32, None)])
 def test_norm(gdn, rows, width, kind, res):
     g = gen(rows * 31 + width)
@@ -165,6 +166,7 @@ def check_conv(gdn, B, T, D, kind, lens=None, slot=None, seed=1, silu=True, bias
 @pytest.mark.parametrize("kind", [BF16, FP32])
 @pytest.mark.parametrize("B,T,D,lens", [
     (1, 1, 8, None), (5, 1, 6144, None), (300, 1, 264, None), (3, 2, 64, None), (2, 3, 40, None), (4, 31, 264, None), (2, 33, 2048, None), (3, 517, 72, None),
+    (60, 300, 2048, [0, 1, 2, 3, 126, 127, 128, 129, 130, 131, 255, 256, 257, 259, 299] * 4), (320, 1, 4096, [1, 0, 1, 1, 0] * 64), (320, 1, 4096, None),
     (7, 9, 64, [0, 1, 2, 3, 4, 8, 9]), (6, 130, 136, [0, 1, 32, 33, 65, 130]), (3, 1, 64, [0, 1, 1]), (1, 4099, 512, None)])
 def test_conv(gdn, kind, B, T, D, lens):
     assert check_conv(gdn, B, T, D, kind, lens) == 0
@@ -177,6 +179,27 @@ def test_conv_skips_padding_and_what_is_wrong(gdn):
     assert check_conv(gdn, 3, 40, 64, BF16, [3, -1, 40], slot=[1, 2, 0]) == gdn.STATUS_BAD_LEN
     assert check_conv(gdn, 3, 40, 64, BF16, [3, 41, 40], slot=[1, 2, 0]) == gdn.STATUS_BAD_LEN
     assert check_conv(gdn, 3, 40, 64, BF16, [3, 41, 40], slot=[1, -1, 0]) == 0
+
+
+@pytest.mark.parametrize("kind", [BF16, FP32])
+def test_conv_of_large_values(gdn, kind):
+    """SiLU far from zero on either side, and infinities, which reach four positions."""
+    g = gen(4)
+    x, w = (300 * randn(g, 2, 40, 64)).to(kind), randn(g, 64, 4)
+    for silu in (True, False):
+        pool = randn(g, 3, 64, 3, dtype=kind)
+        want, size, rows = conv_want(x, w, None, pool, [2, 0], [40, 40], silu, 3)
+        o = torch.empty_like(x)
+        gdn.causal_conv(x, w, pool, ints([2, 0]), o, silu=silu)
+        close(o, want, want.abs() * (HALF[kind] + 8 * E) * 1.01 + 5.5 * E * size * 1.01 + 1e-35)
+        assert torch.equal(pool, rows)
+    x[0, 20, 5], x[1, 3, 7] = INF, NAN
+    o = torch.empty_like(x)
+    gdn.causal_conv(x, w, torch.zeros(3, 64, 3, dtype=kind, device="cuda"), ints([2, 0]), o, silu=False)
+    bad = ~torch.isfinite(o)
+    where = torch.zeros_like(bad)
+    where[0, 20:24, 5], where[1, 3:7, 7] = True, True
+    assert torch.equal(bad, where)
 
 
 @pytest.mark.parametrize("kind", [BF16, FP32])
@@ -302,7 +325,8 @@ class Layer:
 @pytest.mark.parametrize("B,T,D,N,G,lens", [
     (1, 1, 8, 8, 1, None), (2, 2, 64, 16, 1, None), (3, 17, 40, 16, 1, None), (2, 33, 264, 8, 1, None), (2, 40, 72, 32, 3, None), (1, 64, 64, 64, 4, None),
     (2, 100, 128, 16, 16, None), (9, 70, 64, 16, 2, [0, 1, 2, 15, 16, 17, 31, 32, 70]), (1, 1021, 2048, 16, 1, None), (2, 700, 136, 64, 1, [700, 513]),
-    (1, 2500, 96, 8, 1, None), (3, 1300, 64, 32, 2, [1300, 1, 0])])
+    (1, 2500, 96, 8, 1, None), (3, 1300, 64, 32, 2, [1300, 1, 0]), (12, 200, 64, 16, 1, [0, 1, 8, 31, 32, 33, 40, 63, 64, 65, 199, 200]),
+    (25, 21, 2048, 16, 1, None), (24, 40, 512, 64, 4, [40, 3, 39, 8, 9, 0] * 4), (50, 70, 4096, 8, 1, None)])
 def test_scan(gdn, kind, B, T, D, N, G, lens):
     assert Layer(gdn, B, T, D, N, G, kind, lens).check() == 0
 
@@ -318,6 +342,13 @@ def test_scan_with_long_and_short_memories(gdn):
     assert Layer(gdn, 2, 300, 64, 16, kind=FP32, seed=5, step=(0.5, 20.0)).check() == 0
     layer = Layer(gdn, 1, 50, 64, 16, kind=FP32, seed=6)
     layer.dt[0, 7], layer.dt[0, 8], layer.dt[0, 9] = 60.0, -60.0, -200.0
+    assert layer.check() == 0
+
+
+@pytest.mark.parametrize("kind", [BF16, FP32])
+def test_scan_with_far_gates(gdn, kind):
+    layer = Layer(gdn, 1, 60, 64, 16, kind=kind, seed=7)
+    layer.z[0, :8] = torch.tensor([-20.0, -87, -89, -100, -1000, 50, 100, 3e4], device="cuda").to(kind)[:, None]
     assert layer.check() == 0
 
 
@@ -341,6 +372,7 @@ def test_scan_gives_the_same_bits_again(gdn):
 
 @pytest.mark.parametrize("kind", [BF16, FP32])
 @pytest.mark.parametrize("B,D,N,G,slot", [(1, 8, 8, 1, None), (1, 2048, 16, 1, None), (5, 264, 16, 3, None), (3, 72, 32, 1, None), (33, 64, 64, 4, None),
+                                          (261, 4096, 16, 1, [i if i % 7 else -1 for i in range(260)] + [9999]),
                                           (6, 136, 16, 1, [0, -1, 3, 7, -2, 1]), (7, 64, 8, 2, [5, 4, 3, 99, 1, 0, -1])])
 def test_step(gdn, kind, B, D, N, G, slot):
     for z in (True, False):
@@ -354,6 +386,36 @@ def test_step(gdn, kind, B, D, N, G, slot):
                          skip=layer.skip, dt_bias=layer.bias, status=layer.status)
             layer.y = y[:, None]
         assert layer.check(call) == (gdn.STATUS_BAD_SLOT if bad else 0)
+
+
+def test_far_slots_and_rows(gdn):
+    """Offsets past 32 bits: the last slots of large pools, and requests far from one another."""
+    g = gen(12)
+    B, T, D, N, far = 2, 70, 8192, 32, 8300  # 2.2e9 states
+    small = Layer(gdn, B, T, D, N, seed=3, slot=[1, 0])
+    big = Layer(gdn, B, T, D, N, seed=3, slot=[far - 1, 0])
+    big.num_slots = far
+    big.state = torch.zeros(far, D, N, device="cuda")
+    big.state[far - 1], big.state[0] = small.state[1], small.state[0]
+    room = torch.empty(2 ** 31 + 8 + T * D, dtype=BF16, device="cuda")
+    u = room.as_strided((B, T, D), (2 ** 31 + 8, D, 1))
+    u.copy_(big.u)
+    big.u = u
+    small.call(), big.call()
+    assert torch.equal(small.y, big.y) and torch.equal(small.state[:2], big.state[[0, far - 1]])
+    for x in (small, big):
+        gdn.ssm_step(x.u[:, 5], x.dt[:, 5], x.a, x.b[:, 5], x.c[:, 5], x.state, ints(x.slot), x.y[:, 5].contiguous(), skip=x.skip)
+    assert torch.equal(small.state[:2], big.state[[0, far - 1]])
+    del big.state
+    w, slots = 0.5 * randn(g, D, 4), 90000  # 2.2e9 elements
+    pool = torch.zeros(slots, D, 3, dtype=BF16, device="cuda")
+    near = randn(g, 2, D, 3, dtype=BF16)
+    pool[slots - 1], pool[0] = near[1], near[0]
+    for x_small, x_big in ((small.u, u), (small.u[:, 3], u[:, 3])):
+        o = [torch.empty(x_small.shape, dtype=BF16, device="cuda") for _ in range(2)]
+        gdn.causal_conv(x_small, w, near, ints([1, 0]), o[0])
+        gdn.causal_conv(x_big, w, pool, ints([slots - 1, 0]), o[1])
+        assert torch.equal(o[0], o[1]) and torch.equal(near, pool[[0, slots - 1]])
 
 
 # ---- together -----------------------------------------------------------------------------------
