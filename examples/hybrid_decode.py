@@ -1,9 +1,10 @@
-"""Decode steps of a hybrid stack: recurrent layers (Gated DeltaNet) with an attention layer after
-every third, one grouped-query and one over a latent cache in turn.
+"""Decode steps of a hybrid stack: recurrent layers (Gated DeltaNet, and a selective state space in
+every second of three) with an attention layer after them, one grouped-query and one over a latent
+cache in turn. A norm that adds the layer before to the residual stands in front of each.
 
 One step is one CUDA graph: kv_plan hands out the pages and slots of the step's tokens for all
 attention layers, each of those appends its keys and values (or latent rows) and attends over its
-pages, and the recurrent layers advance their states. Lengths, page counts and the free list stay
+pages, and the recurrent layers advance their states and convolution inputs. Lengths, page counts and the free list stay
 on the GPU and are updated in place, so the same graph is replayed step after step.
 
     python examples/hybrid_decode.py [--batch 64] [--prompt 1000] [--steps 200] [--layers 8]
@@ -23,6 +24,7 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import linear_attention_decode_gdn_gb300 as gdn  # noqa: E402
 
 HEAD, LATENT, TAIL = 128, 512, 64
+STATES, RANK = 16, 64  # of a selective layer: states of a channel, width its steps are projected through
 
 
 class HybridDecoder:
@@ -33,7 +35,8 @@ class HybridDecoder:
         weight = lambda rows, cols: torch.randn(rows, cols, generator=g, device=device).mul_(rows ** -0.5).bfloat16()  # noqa: E731
         ints = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=device)  # noqa: E731
         empty = lambda *shape, dtype=torch.bfloat16: torch.empty(shape, dtype=dtype, device=device)  # noqa: E731
-        self.kinds = [("attn" if i % 8 == 3 else "latent") if i % 4 == 3 else "gdn" for i in range(layers)]
+        recurrent = ("gdn", "ssm", "gdn")
+        self.kinds = [("attn" if i % 8 == 3 else "latent") if i % 4 == 3 else recurrent[i % 4] for i in range(layers)]
 
         # the cache's bookkeeping, one for all attention layers
         max_pages = -(-max_len // page_size)
@@ -47,6 +50,7 @@ class HybridDecoder:
 
         self.x, self.y = empty(batch, width), empty(batch, width)  # a step's input and output
         self.x.normal_(generator=g)
+        self.residual, self.normed = empty(batch, width), empty(batch, width)
         self.dims = gdn.make_dims(batch, heads, HEAD, flags=gdn.QKV_BF16 | gdn.GATE_RAW, q_scale=HEAD ** -0.5)
         self.row = torch.arange(batch, dtype=torch.int32, device=device)
         self.layers = []
@@ -57,6 +61,15 @@ class HybridDecoder:
                 layer["out"] = weight(width, width)
                 layer["state"] = gdn.Pools.allocate(self.dims).state
                 layer["o"] = empty(batch, heads, HEAD, dtype=torch.float32)
+            elif kind == "ssm":
+                layer["in"], layer["out"] = weight(width, 2 * width), weight(width, width)
+                layer["narrow"], layer["dt"] = weight(width, RANK + 2 * STATES), weight(RANK, width)
+                layer["conv"] = torch.randn(width, 4, generator=g, device=device) / 2
+                layer["a"] = -torch.arange(1, STATES + 1, device=device).float().repeat(width, 1)
+                layer["skip"], layer["dt_bias"] = torch.ones(width, device=device), torch.full((width,), -4.0, device=device)
+                layer["pool"] = torch.zeros(batch, width, 3, dtype=torch.bfloat16, device=device)
+                layer["state"] = torch.zeros(batch, width, STATES, device=device)
+                layer["u"], layer["o"] = empty(batch, width), empty(batch, width)
             elif kind == "attn":
                 layer["in"] = weight(width, (heads + 2 * heads_kv) * HEAD)
                 layer["out"] = weight(width, width)
@@ -96,6 +109,16 @@ class HybridDecoder:
         gdn.decode_dense(self.dims, inputs, layer["state"], layer["o"], self.status)
         return layer["o"].flatten(1).bfloat16()
 
+    def _selective(self, layer, x):
+        W = x.shape[1]
+        mixed = x @ layer["in"]  # the convolution's channels and the gate's
+        gdn.causal_conv(mixed[:, :W], layer["conv"], layer["pool"], self.row, layer["u"], status=self.status)
+        narrow = layer["u"] @ layer["narrow"]
+        b, c = narrow[:, None, RANK:RANK + STATES], narrow[:, None, RANK + STATES:]
+        gdn.ssm_step(layer["u"], narrow[:, :RANK] @ layer["dt"], layer["a"], b, c, layer["state"], self.row, layer["o"], z=mixed[:, W:],
+                     skip=layer["skip"], dt_bias=layer["dt_bias"], status=self.status)
+        return layer["o"]
+
     def _attention(self, layer, x):
         B, H, KV = self.batch, self.heads, self.heads_kv
         mixed = (x @ layer["in"]).view(B, H + 2 * KV, HEAD)
@@ -115,13 +138,15 @@ class HybridDecoder:
 
     def eager(self):
         """One step: x -> y, every cache and state one token further."""
-        run = {"gdn": self._recurrent, "attn": self._attention, "latent": self._latent}
+        run = {"gdn": self._recurrent, "ssm": self._selective, "attn": self._attention, "latent": self._latent}
         self._plan(None, self.slots)
-        x = self.x
-        for layer in self.layers:
-            normed = (x.float() * torch.rsqrt(x.float().square().mean(1, keepdim=True) + 1e-6)).bfloat16()
-            x = x + run[layer["kind"]](layer, normed) @ layer["out"]
-        self.y.copy_(x)
+        self.residual.copy_(self.x)
+        gdn.add_rms_norm(self.x, self.normed)
+        for i, layer in enumerate(self.layers):
+            added = run[layer["kind"]](layer, self.normed) @ layer["out"]
+            if i + 1 < len(self.layers):
+                gdn.add_rms_norm(added, self.normed, residual=self.residual)
+        torch.add(self.residual, added, out=self.y)
 
     def capture(self):
         """Captures eager() (which has to have run once) for step()."""
