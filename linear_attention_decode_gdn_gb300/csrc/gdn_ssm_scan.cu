@@ -6,13 +6,15 @@
 #include "gdn_ssm.h"
 #include "gdn_vec.cuh"
 
+#include <cmath>
 #include <type_traits>
 
 namespace gdn {
 
 namespace {
 
-constexpr int kWarps = 4;            // of a CTA; they have nothing in common
+constexpr int kWarps = 4;  // of a CTA; they have nothing in common
+constexpr int kCtas = 4;   // of an SM
 // Two elements as they lie in memory.
 template <bool BF16>
 using Raw2 = typename std::conditional<BF16, uint32_t, float2>::type;
@@ -94,7 +96,7 @@ struct ScanParams {
 };
 
 template <class C, bool SUMMARY>
-__global__ void __launch_bounds__(kWarps * 32, 4) gdn_ssm_scan_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(kWarps * 32, kCtas) gdn_ssm_scan_kernel(const ScanParams p) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   const gdn_ssm& s = p.s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -343,27 +345,36 @@ __global__ void __launch_bounds__(kJoinThreads) gdn_ssm_join_kernel(const ScanPa
   }
 }
 
-// How prompts are cut: by the warps that whole prompts would give. The GPU holds 2432 of them; from
+// How prompts are cut: by the warps that whole prompts would give. The GPU holds kResident of them; from
 // 1536 on prompts stay whole (16 x 1024 positions of 4096 channels, 2048 warps: 342 us, 417 in two
-// parts), below that about 8192 are made: parts that are short beside the whole even out prompts of
-// several lengths (8 ragged prompts, 1024 warps: 457 us whole, 303 in 4 parts, 267 in 8; 16384
-// positions, 256 warps: 2906 us whole, 1331 in 5 parts, 942 in 19, 970 in 32). A join goes through
-// all parts in turn, so there are at most sqrt(T) of them, of 32 positions at least (128 positions of
-// 2048 channels: 16 us in parts of 32, 25 in parts of 64; 300 of 4096: 26 and 30).
+// parts). Below that they are cut so that the parts fill it a whole number of times, as often as
+// need be for at least 0.97 of its places to be taken (16384 positions, 256 warps: 2906 us whole,
+// 1009 in 9 parts, which fill 0.95 of it, 943 in 19, 1126 in 10, which leave half of the second round empty;
+// 4096 positions, 8 states, 128 warps: 169 us in 19 parts, 189 in 20). A join goes through all parts
+// in turn, so there are at most sqrt(T) of them, of 32 positions at least (128 positions of 2048
+// channels: 16 us in parts of 32, 25 in parts of 64; 300 of 4096: 26 and 30).
 struct Cut {
   int32_t parts, part;
 };
 Cut cut_of(int32_t batch, int32_t tokens, int32_t channels, int32_t state_size) {
-  constexpr int64_t kEnough = 1536, kWanted = 8192;
-    constexpr int32_t kShortest = 32, kRound = 8;
+  constexpr int64_t kEnough = 1536, kResident = kSms * kCtas * kWarps;
+  constexpr int32_t kShortest = 32, kRound = 8;
   const int32_t of_warp = 512 / state_size;  // channels
   const int64_t warps = static_cast<int64_t>(batch) * ((channels + of_warp - 1) / of_warp);
-  int32_t parts = warps >= kEnough ? 1 : static_cast<int32_t>(kWanted / warps);
-  while (static_cast<int64_t>(parts) * parts > tokens) parts = parts > 256 ? parts / 2 : parts - 1;
-  if (parts < 1) parts = 1;
-  int32_t part = static_cast<int32_t>((static_cast<int64_t>(tokens) + parts - 1) / parts);
-  part = part > kShortest ? (part > 0x7fffffff - kRound ? part : (part + kRound - 1) / kRound * kRound) : kShortest;
-  return {static_cast<int32_t>((static_cast<int64_t>(tokens) + part - 1) / part), part};
+  int64_t parts = 1;
+  if (warps < kEnough) {
+    double best = 0.0;
+    for (int rounds = 1; rounds <= 4 && best < 0.97; ++rounds) {
+      const int64_t fit = kResident * rounds / warps;
+      const double taken = static_cast<double>(fit * warps) / static_cast<double>(kResident * rounds);
+      if (taken > best) best = taken, parts = fit;
+    }
+  }
+  const int64_t most = static_cast<int64_t>(std::sqrt(static_cast<double>(tokens)));
+  if (parts > most) parts = most > 0 ? most : 1;
+  int64_t part = (static_cast<int64_t>(tokens) + parts - 1) / parts;
+  part = part > kShortest ? (part + kRound - 1) / kRound * kRound : kShortest;
+  return {static_cast<int32_t>((tokens + part - 1) / part), static_cast<int32_t>(part)};
 }
 
 template <class C, bool SUMMARY>
