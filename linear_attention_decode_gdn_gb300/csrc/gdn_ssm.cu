@@ -2,7 +2,10 @@
 //
 //   s = softplus(dt + dt_bias),  h <- exp(s a) h + s u b,  y = (c . h + skip u) silu(z)
 //
-// for every channel, with a state of N values.
+// for every channel, with a state of N values. Its bytes are the states', read and written: HBM.
+//   512 requests x 4096 channels x 16 states (bf16 inputs): 47 us, 6.1 TB/s (0.89 of the measured copy
+//     bandwidth); 112 us with lanes that load every scalar for themselves.
+//   64 requests: 7.2 us. One request x 2048 channels: 3.1 us, two dependent loads.
 #include "gdn_ssm.h"
 #include "gdn_vec.cuh"
 
@@ -10,7 +13,7 @@ namespace gdn {
 
 namespace {
 
-constexpr int kStepWarps = 4;  // of a CTA; they have nothing in common
+constexpr int kStepWarps = 4;  // of a CTA; they have nothing in common. Eight CTAs an SM: 47.7 us, 57 without that limit, 55 with ten
 
 struct StepParams {
   gdn_ssm s;
@@ -124,7 +127,7 @@ cudaError_t launch_step(const SsmParams& given, cudaStream_t stream) {
   p.blocks = (p.per_group + CH - 1) / CH;
   p.columns = p.blocks * p.s.num_groups;
   const int64_t all = static_cast<int64_t>(p.columns) * p.s.batch;
-    p.rows = all >= 32768 ? 2 : 1;
+    p.rows = all >= 32768 ? 2 : 1;  // a is loaded once for both: 47.7 us at 2, 48.3 at 4, 50.3 at 1 (512 x 4096 channels)
   const int64_t warps = static_cast<int64_t>(p.columns) * ((p.s.batch + p.rows - 1) / p.rows);
   return launch_overlapped(gdn_ssm_step_kernel<N, BF16>, p, dim3(static_cast<unsigned>((warps + kStepWarps - 1) / kStepWarps)),
                            kStepWarps * 32, 0, 1u, stream);
