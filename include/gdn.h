@@ -498,7 +498,8 @@ int gdn_attn_workspace(const gdn_paged_kv *kv, int32_t batch, int32_t num_tokens
  *
  * The conventions at the top of this file hold: slot-indexed pools, padding, status bits, streams,
  * no allocation. Outputs overlap no input of their call, but for the pools and the residual, which
- * are updated in place. All sums, states, steps and norms are fp32.
+ * are updated in place. A new request begins with zeros in its rows of the pools. All sums, states,
+ * steps and norms are fp32. A call has at most 2^24 channels and 2^30 positions (batch * num_tokens).
  */
 #define GDN_TYPE_BF16 0
 #define GDN_TYPE_FP32 1

@@ -300,6 +300,8 @@ int attend(const gdn_paged_kv* kv, const gdn_attn* a, void* workspace, size_t wo
 
 // ---- selective state space layers ----------------------------------------------------------
 constexpr long long kMaxPositions = 1LL << 30;  // of a call: a tile past the last fits 32 bits
+constexpr int kMaxChannels = 1 << 24;
+constexpr long long kMaxStates = 1LL << 36;     // of a call's requests
 
 // Rows of a [B][T][..] operand: 16-byte aligned, with strides that keep its rows so.
 template <int N>
@@ -307,19 +309,25 @@ bool rows_ok(const void* p, const int64_t* strides, const int32_t (&extents)[N],
   return aligned16(p) && strides_ok(strides, extents, bf16 ? 8 : 4);
 }
 
+int check_ssm_sizes(int32_t batch, int32_t num_tokens, int32_t channels, int32_t state_size) {
+  if (batch < 0 || num_tokens < 0 || channels <= 0)
+    return fail(GDN_ERR_INVALID_ARG, "batch and num_tokens must be >= 0, channels > 0");
+  if (state_size != 8 && state_size != 16 && state_size != 32 && state_size != 64)
+    return fail(GDN_ERR_UNSUPPORTED, "state_size %d not built (8, 16, 32, 64)", state_size);
+  if (channels > kMaxChannels || static_cast<long long>(batch) * num_tokens > kMaxPositions ||
+      static_cast<long long>(batch) * channels > kMaxStates / state_size)
+    return fail(GDN_ERR_UNSUPPORTED, "channels must be at most 2^24, batch * num_tokens 2^30, batch * channels * state_size 2^36");
+  return GDN_OK;
+}
+
 int check_ssm(const gdn_ssm* s) {
   if (s == nullptr) return fail(GDN_ERR_INVALID_ARG, "ssm is NULL");
-  if (s->batch < 0 || s->num_tokens < 0 || s->channels <= 0 || s->num_groups <= 0 || s->num_slots <= 0)
-    return fail(GDN_ERR_INVALID_ARG, "batch and num_tokens must be >= 0, channels, num_groups and num_slots > 0");
+  if (int rc = check_ssm_sizes(s->batch, s->num_tokens, s->channels, s->state_size)) return rc;
+  if (s->num_groups <= 0 || s->num_slots <= 0) return fail(GDN_ERR_INVALID_ARG, "num_groups and num_slots must be > 0");
   if ((s->flags & ~(GDN_QKV_BF16 | GDN_DT_SOFTPLUS)) != 0u)
     return fail(GDN_ERR_INVALID_ARG, "a gdn_ssm knows GDN_QKV_BF16 and GDN_DT_SOFTPLUS only");
-  if (s->state_size != 8 && s->state_size != 16 && s->state_size != 32 && s->state_size != 64)
-    return fail(GDN_ERR_UNSUPPORTED, "state_size %d not built (8, 16, 32, 64)", s->state_size);
   if (s->num_groups > s->channels / 8 || s->channels % (8 * s->num_groups) != 0)
     return fail(GDN_ERR_UNSUPPORTED, "channels %d: not a multiple of 8 in each of %d groups", s->channels, s->num_groups);
-  if (static_cast<long long>(s->batch) * s->num_tokens > kMaxPositions ||
-      static_cast<long long>(s->batch) * s->channels * s->state_size > 0x7fffffffLL * 32)
-    return fail(GDN_ERR_UNSUPPORTED, "batch * num_tokens must be at most 2^30, batch * channels * state_size below 2^36");
   if (s->batch == 0 || s->num_tokens == 0) return GDN_OK;
   if (s->u == nullptr || s->dt == nullptr || s->b == nullptr || s->c == nullptr || s->a == nullptr || s->state == nullptr ||
       s->slot == nullptr || s->y == nullptr)
@@ -646,9 +654,9 @@ int gdn_causal_conv(const gdn_conv* conv, int32_t* status, void* stream) {
   if ((c.flags & ~(GDN_QKV_BF16 | GDN_CONV_SILU)) != 0u)
     return fail(GDN_ERR_INVALID_ARG, "a gdn_conv knows GDN_QKV_BF16 and GDN_CONV_SILU only");
   if (c.channels % 8 != 0) return fail(GDN_ERR_UNSUPPORTED, "channels %d: not a multiple of 8", c.channels);
-  if (static_cast<long long>(c.batch) * c.num_tokens > kMaxPositions ||
+  if (c.channels > kMaxChannels || static_cast<long long>(c.batch) * c.num_tokens > kMaxPositions ||
       static_cast<long long>(c.batch) * c.num_tokens > (1LL << 38) / c.channels)
-    return fail(GDN_ERR_UNSUPPORTED, "batch * num_tokens must be at most 2^30, times channels at most 2^38");
+    return fail(GDN_ERR_UNSUPPORTED, "channels must be at most 2^24, batch * num_tokens 2^30, times channels 2^38");
   if (c.batch == 0 || c.num_tokens == 0) return GDN_OK;
   if (c.x == nullptr || c.w == nullptr || c.pool == nullptr || c.slot == nullptr || c.o == nullptr)
     return fail(GDN_ERR_INVALID_ARG, "x, w, pool, slot and o are required");
@@ -681,10 +689,7 @@ int gdn_ssm_step(const gdn_ssm* ssm, int32_t* status, void* stream) {
 
 int gdn_ssm_workspace(int32_t batch, int32_t num_tokens, int32_t channels, int32_t state_size, size_t* bytes) {
   if (bytes == nullptr) return fail(GDN_ERR_INVALID_ARG, "bytes is NULL");
-  if (batch < 0 || num_tokens < 0 || channels <= 0)
-    return fail(GDN_ERR_INVALID_ARG, "batch and num_tokens must be >= 0, channels > 0");
-  if (state_size != 8 && state_size != 16 && state_size != 32 && state_size != 64)
-    return fail(GDN_ERR_UNSUPPORTED, "state_size %d not built (8, 16, 32, 64)", state_size);
+  if (int rc = check_ssm_sizes(batch, num_tokens, channels, state_size)) return rc;
   *bytes = gdn::ssm_workspace_bytes(batch, num_tokens, channels, state_size);
   return GDN_OK;
 }

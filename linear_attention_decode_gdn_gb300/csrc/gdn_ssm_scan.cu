@@ -446,7 +446,11 @@ size_t ssm_workspace_bytes(int32_t batch, int32_t tokens, int32_t channels, int3
   return static_cast<size_t>(batch) * channels * (static_cast<size_t>(cut.parts) * state_size + cut.parts - 1) * sizeof(float);
 }
 
-cudaError_t launch_ssm_scan(const SsmParams& p, void* workspace, cudaStream_t stream) {
+cudaError_t launch_ssm_scan(const SsmParams& given, void* workspace, cudaStream_t stream) {
+  SsmParams p = given;
+  // The stride of a single token may be any, but copies of the positions past it, which read nothing,
+  // still want an aligned address.
+  if (p.s.num_tokens == 1) p.s.u_strides[1] = p.s.dt_strides[1] = p.s.z_strides[1] = p.s.b_strides[1] = p.s.c_strides[1] = 0;
   return (p.s.flags & GDN_QKV_BF16) != 0u ? launch_type<true>(p, workspace, stream) : launch_type<false>(p, workspace, stream);
 }
 

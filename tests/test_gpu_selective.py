@@ -360,6 +360,22 @@ def test_scan_skips_padding_and_what_is_wrong(gdn):
     assert Layer(gdn, 3, 1200, 64, 16, lens=[3, 1201, 1200], slot=[1, -1, 7]).check() == gdn.STATUS_BAD_SLOT
 
 
+@pytest.mark.parametrize("kind", [BF16, FP32])
+def test_scan_of_one_token_in_any_stride(gdn, kind):
+    """The distance to a next token, where there is none, need not be a multiple of anything."""
+    layer = Layer(gdn, 3, 1, 64, 16, 2, kind, seed=11)
+
+    def apart(x):
+        wide = x[0].numel() + 66
+        strides = (4 * wide, wide, 1) if x.dim() == 3 else (4 * wide, wide, x.shape[3], 1)
+        return torch.zeros(12 * wide, dtype=kind, device="cuda").as_strided(x.shape, strides, 32).copy_(x)
+
+    for name in ("u", "dt", "z", "b", "c"):
+        setattr(layer, name, apart(getattr(layer, name)))
+    assert layer.u.stride(1) % 8 == 2 and layer.b.stride(1) % 8 == 2
+    assert layer.check() == 0
+
+
 def test_scan_gives_the_same_bits_again(gdn):
     runs = []
     for _ in range(3):

@@ -70,6 +70,7 @@ def test_empty_calls_launch_nothing(gdn):
 @pytest.mark.parametrize("kw,code", [
     (dict(batch=-1), BAD), (dict(num_tokens=-1), BAD), (dict(channels=0), BAD), (dict(num_slots=0), BAD), (dict(flags=1 << 11), BAD),
     (dict(flags=1 << 1), BAD), (dict(channels=60), NO), (dict(batch=1 << 20, num_tokens=1 << 12), NO), (dict(batch=1 << 14, num_tokens=1 << 16, channels=512), NO),
+    (dict(channels=(1 << 24) + 8), NO), (dict(batch=(1 << 31) - 1, num_tokens=(1 << 31) - 1, channels=(1 << 31) - 8), NO),
     (dict(x=None), BAD), (dict(w=None), BAD), (dict(pool=None), BAD), (dict(slot=None), BAD), (dict(o=None), BAD), (dict(x=FAKE + 8), NO),
     (dict(x_strides=(256, 60)), NO), (dict(x_strides=(-256, 64)), NO), (dict(w=FAKE + 4), NO), (dict(bias=FAKE + 4), NO), (dict(pool=FAKE + 2), NO),
     (dict(o=FAKE + 8), NO), (dict(o=FAKE), BAD)])
@@ -81,7 +82,8 @@ def test_conv_is_checked(gdn, kw, code):
     (dict(batch=-1), BAD), (dict(num_tokens=-1), BAD), (dict(channels=0), BAD), (dict(num_groups=0), BAD), (dict(num_slots=0), BAD),
     (dict(flags=1 << 12), BAD), (dict(state_size=0), NO), (dict(state_size=24), NO), (dict(state_size=128), NO), (dict(channels=72), NO),
     (dict(num_groups=16), NO), (dict(num_groups=1 << 29), NO), (dict(batch=1 << 20, num_tokens=1 << 12), NO),
-    (dict(batch=1 << 22, num_tokens=1, channels=1 << 12), NO), (dict(u=None), BAD), (dict(dt=None), BAD), (dict(b=None), BAD), (dict(c=None), BAD),
+    (dict(batch=1 << 22, num_tokens=1, channels=1 << 16), NO), (dict(channels=(1 << 24) + 16), NO),
+    (dict(batch=(1 << 31) - 1, num_tokens=(1 << 31) - 1, channels=(1 << 31) - 16, state_size=64), NO), (dict(u=None), BAD), (dict(dt=None), BAD), (dict(b=None), BAD), (dict(c=None), BAD),
     (dict(a=None), BAD), (dict(state=None), BAD), (dict(slot=None), BAD), (dict(y=None), BAD), (dict(u=FAKE + 8), NO), (dict(dt=FAKE + 8), NO),
     (dict(b=FAKE + 2), NO), (dict(c=FAKE + 2), NO), (dict(z=FAKE + 2), NO), (dict(u_strides=(256, 60)), NO), (dict(dt_strides=(-8, 64)), NO),
     (dict(b_strides=(128, 36, 16)), NO), (dict(c_strides=(128, 32, 4)), NO), (dict(z_strides=(516, 128)), NO), (dict(a=FAKE + 4), NO),
@@ -106,7 +108,8 @@ def test_workspace_sizes(gdn):
     assert lib.gdn_ssm_workspace(1, 1, 64, 16, None) == BAD
     for args in ((-1, 1, 64, 16), (1, -1, 64, 16), (1, 1, 0, 16)):
         assert lib.gdn_ssm_workspace(*args, ctypes.byref(size)) == BAD
-    assert lib.gdn_ssm_workspace(1, 1, 64, 24, ctypes.byref(size)) == NO
+    for args in ((1, 1, 64, 24), (1, 1, (1 << 24) + 8, 16), (1 << 20, 1 << 20, 64, 16), ((1 << 31) - 1, 1, 1 << 24, 64)):
+        assert lib.gdn_ssm_workspace(*args, ctypes.byref(size)) == NO
     assert gdn.ssm_workspace_bytes(0, 1000, 64, 16) == 0 == gdn.ssm_workspace_bytes(8, 0, 64, 16)
     need = gdn.ssm_workspace_bytes(1, 8192, 2048, 16)
     if need:  # a scan in parts
