@@ -39,32 +39,52 @@ def _whole(t, shape, dtype, what: str, device: int) -> int:
     return t.data_ptr()
 
 
-def _input(t, dims, what: str):
-    """Type, shape and device of a call's first operand."""
-    at = t.get_device()
+# A decode step makes one call a layer: conditions are written out, as in ``paged``, and gone through
+# again one by one only for the error of a call that they refuse.
+def _refuse(at, x, what, dims, wide, whole):
+    """Raises the error of what a call found wrong: x is its first operand, `wide` the others of its kind,
+    `whole` those that are contiguous."""
     if at < 0 or at != _current_device():
         raise _not_here(at, what)
-    if (t.dtype is not _BF16 and t.dtype is not _FP32) or t.dim() not in dims:
-        raise ValueError(f"{what}: bf16 or fp32, with {' or '.join(map(str, dims))} dimensions, got {t.dtype} {tuple(t.shape)}")
-    return t.dtype, t.shape, at
+    if (x.dtype is not _BF16 and x.dtype is not _FP32) or x.dim() not in dims:
+        raise ValueError(f"{what}: bf16 or fp32, with {' or '.join(map(str, dims))} dimensions, got {x.dtype} {tuple(x.shape)}")
+    for t, shape, dtype, name in ((x, x.shape, x.dtype, what), *wide):
+        if t is not None:
+            _rows(t, shape, dtype, name, at)
+    for t, shape, dtype, name in whole:
+        if t is not None:
+            _whole(t, shape, dtype, name, at)
+    raise ValueError("tensors of other types, shapes, strides or devices than the call takes")
 
 
 def add_rms_norm(x, o, *, residual=None, weight=None, eps=1e-6, scales=None, group=0, stream=None):
     """residual += x, and o = RMSNorm of that sum (of x without a residual) times weight [width]. x, residual
     [rows, width] bf16 or fp32, in rows of any distance; o [rows, width] bf16, fp32 or float8_e4m3fn, which needs
     scales: fp32 [rows, ceil(width / 128)] with group=128, [rows, 1] or [rows] with group=0."""
-    dtype, shape, at = _input(x, (2,), "x")
-    rows, width = shape
-    out = o.dtype
-    if out not in _TYPES:
-        raise ValueError(f"o: bf16, fp32 or float8_e4m3fn, got {out}")
-    r_type, r_ptr, r_row = dtype, 0, 0
-    if residual is not None:
-        r_type = residual.dtype
-        if r_type is not _BF16 and r_type is not _FP32:
-            raise ValueError(f"residual: bf16 or fp32, got {r_type}")
-        r_ptr, r_row = _rows(residual, shape, r_type, "residual", at)
-    scale_ptr = 0
+    at, dtype, shape, out = x.get_device(), x.dtype, x.shape, o.dtype
+    x_type, o_type = _TYPES.get(dtype), _TYPES.get(out)
+    ok = at >= 0 and at == _current_device() and len(shape) == 2 and x_type is not None and x_type != _abi.TYPE_E4M3 and o_type is not None
+    if ok:
+        rows, width = shape
+        x_row, x_last = x.stride()
+        ok = x_last == 1 and o.shape == shape and o.is_contiguous() and o.get_device() == at
+    r_type, r_ptr, r_row, w_ptr, scale_ptr = x_type, 0, 0, 0, 0
+    if ok and residual is not None:
+        r_type = _TYPES.get(residual.dtype)
+        ok = r_type is not None and r_type != _abi.TYPE_E4M3 and residual.shape == shape and residual.get_device() == at
+        if ok:
+            r_row, r_last = residual.stride()
+            ok, r_ptr = r_last == 1, residual.data_ptr()
+    if ok and weight is not None:
+        ok = weight.dtype is _FP32 and weight.dim() == 1 and weight.numel() == width and weight.is_contiguous() and weight.get_device() == at
+        w_ptr = weight.data_ptr()
+    if not ok:
+        if out not in _TYPES:
+            raise ValueError(f"o: bf16, fp32 or float8_e4m3fn, got {out}")
+        if residual is not None and residual.dtype is not _BF16 and residual.dtype is not _FP32:
+            raise ValueError(f"residual: bf16 or fp32, got {residual.dtype}")
+        _refuse(at, x, "x", (2,), () if residual is None else ((residual, shape, residual.dtype, "residual"),),
+                ((weight, shape[-1:], _FP32, "weight"), (o, shape, out, "o")))
     if out is _E4M3:
         if scales is None:
             raise ValueError("o in 8 bits needs scales")
@@ -72,11 +92,8 @@ def add_rms_norm(x, o, *, residual=None, weight=None, eps=1e-6, scales=None, gro
         scale_ptr = _whole(scales, (rows,) if not group and scales.dim() == 1 else want, _FP32, "scales", at)
     elif scales is not None or group:
         raise ValueError("scales and group belong to an output in 8 bits")
-    x_ptr, x_row = _rows(x, shape, dtype, "x", at)
-    rc = _abi.load().gdn_add_rms_norm(
-        _pack_norm(rows, width, _TYPES[dtype], _TYPES[r_type], _TYPES[out], group, eps, x_ptr, x_row, r_ptr, r_row,
-                   0 if weight is None else _whole(weight, (width,), _FP32, "weight", at), _whole(o, shape, out, "o", at), scale_ptr),
-        _stream(stream, at))
+    rc = _abi.load().gdn_add_rms_norm(_pack_norm(rows, width, x_type, r_type, o_type, group, eps, x.data_ptr(), x_row, r_ptr, r_row, w_ptr,
+                                                 o.data_ptr(), scale_ptr), _stream(stream, at))
     if rc != GDN_OK:
         check(rc, "gdn_add_rms_norm")
 
@@ -85,20 +102,31 @@ def causal_conv(x, weight, pool, slot, o, *, bias=None, silu=True, seq_lens=None
     """o = the causal convolution of x [batch, T, channels] (or [batch, channels]: one token each) with weight
     [channels, 4], plus bias [channels], through SiLU. pool [slots, channels, 3], of x's type, holds the three inputs
     before each request's first position in row slot[b] and is left with the last three."""
-    dtype, shape, at = _input(x, (2, 3), "x")
-    x_ptr, *strides = _rows(x, shape, dtype, "x", at)
-    if len(shape) == 2:
-        (batch, channels), tokens = shape, 1
-        strides.append(0)
-    else:
-        batch, tokens, channels = shape
-    slots = pool.shape[0]
+    at, dtype, shape, rows = x.get_device(), x.dtype, x.shape, pool.shape
+    ok = at >= 0 and at == _current_device() and (dtype is _BF16 or dtype is _FP32)
+    if ok:
+        if len(shape) == 2:
+            (batch, channels), tokens, (x0, last), x1 = shape, 1, x.stride(), 0
+        elif len(shape) == 3:
+            (batch, tokens, channels), (x0, x1, last) = shape, x.stride()
+        else:
+            ok = False
+    ok = (ok and last == 1 and len(rows) == 3 and rows[1] == channels and rows[2] == 3 and pool.dtype is dtype and o.dtype is dtype
+          and weight.dtype is _FP32 and weight.shape == (channels, 4) and o.shape == shape
+          and weight.is_contiguous() and pool.is_contiguous() and o.is_contiguous()
+          and weight.get_device() == pool.get_device() == o.get_device() == at)
+    bias_ptr = 0
+    if ok and bias is not None:
+        ok = bias.dtype is _FP32 and bias.dim() == 1 and bias.numel() == channels and bias.is_contiguous() and bias.get_device() == at
+        bias_ptr = bias.data_ptr()
+    if not ok:
+        channels = shape[-1]
+        _refuse(at, x, "x", (2, 3), (), ((weight, (channels, 4), _FP32, "weight"), (bias, (channels,), _FP32, "bias"),
+                                         (pool, (*rows[:1], channels, 3), dtype, "pool"), (o, shape, dtype, "o")))
     rc = _abi.load().gdn_causal_conv(
-        _pack_conv(batch, tokens, channels, slots, (_abi.QKV_BF16 if dtype is _BF16 else 0) | (_abi.CONV_SILU if silu else 0),
-                   x_ptr, *strides, _whole(weight, (channels, 4), _FP32, "weight", at),
-                   0 if bias is None else _whole(bias, (channels,), _FP32, "bias", at),
-                   _whole(pool, (slots, channels, 3), dtype, "pool", at), _ints(slot, batch, "slot", at),
-                   0 if seq_lens is None else _ints(seq_lens, batch, "seq_lens", at), _whole(o, shape, dtype, "o", at)),
+        _pack_conv(batch, tokens, channels, rows[0], (_abi.QKV_BF16 if dtype is _BF16 else 0) | (_abi.CONV_SILU if silu else 0), x.data_ptr(),
+                   x0, x1, weight.data_ptr(), bias_ptr, pool.data_ptr(), _ints(slot, batch, "slot", at),
+                   0 if seq_lens is None else _ints(seq_lens, batch, "seq_lens", at), o.data_ptr()),
         None if status is None else _status(status, at), _stream(stream, at))
     if rc != GDN_OK:
         check(rc, "gdn_causal_conv")
@@ -111,36 +139,22 @@ def ssm_workspace_bytes(batch: int, num_tokens: int, channels: int, state_size: 
     return out.value
 
 
-def _wrong(u, dt, a, b, c, state, y, z, skip, dt_bias, at):
-    """Raises the error of what _pack found wrong."""
-    dims, dtype, shape = u.dim(), u.dtype, u.shape
-    if b.dim() != dims + 1 or state.dim() != 3:
-        raise ValueError(f"b: {dims + 1} dimensions [.., groups, state size]; state: [slots, channels, state size]")
-    channels, groups, n = shape[-1], *b.shape[-2:]
-    for t, what in ((u, "u"), (dt, "dt"), (z, "z")):
-        if t is not None:
-            _rows(t, shape, dtype, what, at)
-    for t, what in ((b, "b"), (c, "c")):
-        _rows(t, (*shape[:-1], groups, n), dtype, what, at)
-    for t, size, what in ((a, (channels, n), "a"), (skip, (channels,), "skip"), (dt_bias, (channels,), "dt_bias"),
-                          (state, (state.shape[0], channels, n), "state")):
-        if t is not None:
-            _whole(t, size, _FP32, what, at)
-    _whole(y, shape, dtype, "y", at)
-    raise ValueError("tensors of other types, shapes, strides or devices than the call takes")
+def _refuse_ssm(dims, at, u, dt, a, b, c, state, y, z, skip, dt_bias):
+    dtype, shape, narrow, pool = u.dtype, u.shape, b.shape, state.shape
+    if len(narrow) != len(shape) + 1 or len(pool) != 3:
+        raise ValueError(f"b: {len(shape) + 1} dimensions [.., groups, state size]; state: [slots, channels, state size]")
+    few, channels, n = (*shape[:-1], *narrow[-2:]), shape[-1], narrow[-1]
+    _refuse(at, u, "u", (dims,), ((dt, shape, dtype, "dt"), (z, shape, dtype, "z"), (b, few, dtype, "b"), (c, few, dtype, "c")),
+            ((a, (channels, n), _FP32, "a"), (skip, (channels,), _FP32, "skip"), (dt_bias, (channels,), _FP32, "dt_bias"),
+             (state, (pool[0], channels, n), _FP32, "state"), (y, shape, dtype, "y")))
 
 
-# A decode step makes one call a layer: the conditions are written out, as in ``paged``.
 def _pack(dims, u, dt, a, b, c, state, slot, y, z, skip, dt_bias, softplus, seq_lens):
     """The C struct of a scan (dims 3) or a step (dims 2), and the device."""
-    at = u.get_device()
-    if at < 0 or at != _current_device():
-        raise _not_here(at, "u")
-    dtype, shape, narrow, pool = u.dtype, u.shape, b.shape, state.shape
-    if (dtype is not _BF16 and dtype is not _FP32) or len(shape) != dims:
-        raise ValueError(f"u: bf16 or fp32, with {dims} dimensions, got {dtype} {tuple(shape)}")
-    if len(narrow) != dims + 1 or len(pool) != 3:
-        _wrong(u, dt, a, b, c, state, y, z, skip, dt_bias, at)
+    at, dtype, shape, narrow, pool = u.get_device(), u.dtype, u.shape, b.shape, state.shape
+    if (at < 0 or at != _current_device() or (dtype is not _BF16 and dtype is not _FP32) or len(shape) != dims or len(narrow) != dims + 1
+            or len(pool) != 3):
+        _refuse_ssm(dims, at, u, dt, a, b, c, state, y, z, skip, dt_bias)
     batch, channels, groups, n = shape[0], shape[-1], narrow[-2], narrow[-1]
     z_ptr = z0 = z1 = 0
     if dims == 2:  # no stride between the tokens of one
@@ -157,7 +171,7 @@ def _pack(dims, u, dt, a, b, c, state, slot, y, z, skip, dt_bias, softplus, seq_
         if z is not None:
             z0, z1, zl = z.stride()
     ok = (ok and ul == tl == bl == cl == 1 and dt.dtype is dtype and b.dtype is dtype and c.dtype is dtype and y.dtype is dtype
-          and dt.shape == shape and c.shape == narrow and y.shape == shape and a.shape == pool[1:] and pool[1] == channels and pool[2] == n
+          and dt.shape == shape and c.shape == narrow and y.shape == shape and a.shape == (channels, n) and pool[1] == channels and pool[2] == n
           and a.dtype is _FP32 and state.dtype is _FP32 and y.is_contiguous() and a.is_contiguous() and state.is_contiguous()
           and dt.get_device() == b.get_device() == c.get_device() == a.get_device() == state.get_device() == y.get_device() == at)
     if ok and z is not None:
@@ -168,7 +182,7 @@ def _pack(dims, u, dt, a, b, c, state, slot, y, z, skip, dt_bias, softplus, seq_
     if ok and dt_bias is not None:
         ok = dt_bias.dtype is _FP32 and dt_bias.dim() == 1 and dt_bias.numel() == channels and dt_bias.is_contiguous() and dt_bias.get_device() == at
     if not ok:
-        _wrong(u, dt, a, b, c, state, y, z, skip, dt_bias, at)
+        _refuse_ssm(dims, at, u, dt, a, b, c, state, y, z, skip, dt_bias)
     return _pack_ssm(
         batch, tokens, channels, n, groups, pool[0], (_abi.QKV_BF16 if dtype is _BF16 else 0) | (_abi.DT_SOFTPLUS if softplus else 0),
         u.data_ptr(), u0, u1, dt.data_ptr(), t0, t1, b.data_ptr(), b0, b1, b2, c.data_ptr(), c0, c1, c2, z_ptr, z0, z1, a.data_ptr(),
