@@ -364,36 +364,46 @@ __global__ void __launch_bounds__(kJoinThreads) gdn_ssm_join_kernel(const ScanPa
   }
 }
 
-// How prompts are cut: by the warps that whole prompts would give. The GPU holds kResident of them; from
-// 1536 on prompts stay whole (16 x 1024 positions of 4096 channels, 2048 warps: 342 us, 417 in two
-// parts). Below that they are cut so that the parts fill it a whole number of times, as often as
-// need be for at least 0.97 of its places to be taken (16384 positions, 256 warps: 2906 us whole,
-// 1009 in 9 parts, which fill 0.95 of it, 943 in 19, 1126 in 10, which leave half of the second round empty;
-// 4096 positions, 8 states, 128 warps: 169 us in 19 parts, 189 in 20). A join goes through all parts
-// in turn, so there are at most sqrt(T) of them, of 32 positions at least (128 positions of 2048
-// channels: 16 us in parts of 32, 25 in parts of 64; 300 of 4096: 26 and 30).
+// How prompts are cut: as a rough model of the times says, whose constants are measured. A position
+// takes 0.18 us where a warp has its quarter of an SM to itself, 0.225 where two share one, and 0.09
+// for each of more, up to the four that fit and in rounds beyond. Parts take two thirds more of it
+// for their ends, two launches, and 6 us a further round to begin (3 prompts of 509 positions of 64
+// states, 768 warps: 103 us in 3 parts, 113 in 11). Cuts that fill the GPU 1 to 4 times are compared with none:
+//   whole wins where there are enough warps (16 x 1024 positions of 4096 channels, 2048 warps: 342 us,
+//   417 in two parts) or few positions (2048 channels: 64 positions 14.5 us, 15.9 in two parts, but 96
+//   20.1 and 16.0; 768 warps: 200 positions 47.5 and 49.7);
+//   parts elsewhere (16384 positions, 256 warps: 2906 us whole, 1009 in 9 parts, which fill 0.95 of the
+//   GPU, 943 in 19, which fill it twice, 1126 in 10, which leave half of the second round empty), and
+//   where prompts have lengths of their own, of which a whole one holds up the end (8 ragged prompts,
+//   1024 warps: 457 us whole, 292 in 7 parts; of equal length 477 and 471): parts without
+//   positions cost next to nothing, so 0.6 of the time is reckoned there.
+// A join goes through all parts in turn, so there are at most sqrt(T) of them, of 32 positions at least.
 struct Cut {
   int32_t parts, part;
 };
-Cut cut_of(int32_t batch, int32_t tokens, int32_t channels, int32_t state_size) {
-  constexpr int64_t kEnough = 1536, kResident = kSms * kCtas * kWarps;
-  constexpr int32_t kShortest = 32, kRound = 8;
+Cut cut_of(int32_t batch, int32_t tokens, int32_t channels, int32_t state_size, bool ragged) {
+  constexpr int32_t kShortest = 32, kRound = 8, kQuarters = kSms * 4, kRounds = 4;
   const int32_t of_warp = 512 / state_size;  // channels
   const int64_t warps = static_cast<int64_t>(batch) * ((channels + of_warp - 1) / of_warp);
-  int64_t parts = 1;
-  if (warps < kEnough) {
-    double best = 0.0;
-    for (int rounds = 1; rounds <= 4 && best < 0.97; ++rounds) {
-      const int64_t fit = kResident * rounds / warps;
-      const double taken = static_cast<double>(fit * warps) / static_cast<double>(kResident * rounds);
-      if (taken > best) best = taken, parts = fit;
-    }
-  }
+  auto position = [](int64_t all_warps) {  // us
+    const int64_t shared = (all_warps + kQuarters - 1) / kQuarters;
+    return shared <= 1 ? 0.18 : shared <= 2 ? 0.225 : 0.09 * static_cast<double>(shared);
+  };
+  Cut best{1, tokens};
+  double least = 2.5 + tokens * position(warps);
   const int64_t most = static_cast<int64_t>(std::sqrt(static_cast<double>(tokens)));
-  if (parts > most) parts = most > 0 ? most : 1;
-  int64_t part = (static_cast<int64_t>(tokens) + parts - 1) / parts;
-  part = part > kShortest ? (part + kRound - 1) / kRound * kRound : kShortest;
-  return {static_cast<int32_t>((tokens + part - 1) / part), static_cast<int32_t>(part)};
+  for (int rounds = 1; rounds <= kRounds; ++rounds) {
+    int64_t parts = static_cast<int64_t>(kSms) * kCtas * kWarps * rounds / warps;
+    if (parts > most) parts = most;
+    if (parts < 2) continue;
+    int64_t part = (tokens + parts - 1) / parts;
+    part = part > kShortest ? (part + kRound - 1) / kRound * kRound : kShortest;
+    parts = (tokens + part - 1) / part;
+    const double all = static_cast<double>(part) * (5.0 / 3.0) * position(warps * parts);
+    const double took = ragged ? 5.0 + 0.6 * all : 6.0 * rounds - 1.0 + all;
+    if (parts > 1 && took < least) least = took, best = {static_cast<int32_t>(parts), static_cast<int32_t>(part)};
+  }
+  return best;
 }
 
 template <class C, bool SUMMARY>
@@ -410,7 +420,7 @@ cudaError_t launch_parts(ScanParams p, cudaStream_t stream) {
 template <class C>
 cudaError_t launch_scan(const SsmParams& given, void* workspace, cudaStream_t stream) {
   const gdn_ssm& s = given.s;
-  const Cut cut = cut_of(s.batch, s.num_tokens, s.channels, s.state_size);
+  const Cut cut = cut_of(s.batch, s.num_tokens, s.channels, s.state_size, s.seq_lens != nullptr);
   ScanParams p{s, given.status, s.channels / s.num_groups, 0, cut.parts, cut.part, 0, nullptr, nullptr, nullptr};
   p.blocks = (p.per_group + C::CH - 1) / C::CH;
   if (cut.parts > 1) {
@@ -441,9 +451,13 @@ cudaError_t launch_type(const SsmParams& p, void* workspace, cudaStream_t stream
 
 size_t ssm_workspace_bytes(int32_t batch, int32_t tokens, int32_t channels, int32_t state_size) {
   if (batch == 0 || tokens == 0) return 0;
-  const Cut cut = cut_of(batch, tokens, channels, state_size);
-  if (cut.parts == 1) return 0;
-  return static_cast<size_t>(batch) * channels * (static_cast<size_t>(cut.parts) * state_size + cut.parts - 1) * sizeof(float);
+  size_t most = 0;
+  for (bool ragged : {false, true}) {
+    const size_t parts = static_cast<size_t>(cut_of(batch, tokens, channels, state_size, ragged).parts);
+    const size_t bytes = parts > 1 ? static_cast<size_t>(batch) * channels * (parts * state_size + parts - 1) * sizeof(float) : 0;
+    if (bytes > most) most = bytes;
+  }
+  return most;
 }
 
 cudaError_t launch_ssm_scan(const SsmParams& given, void* workspace, cudaStream_t stream) {

@@ -38,14 +38,6 @@ __device__ __forceinline__ void store8(void* base, int64_t at, const Raw8<BF16>&
 }
 
 template <bool BF16>
-__device__ __forceinline__ Raw8<BF16> zero8() {
-  Raw8<BF16> r;
-#pragma unroll
-  for (int i = 0; i < (BF16 ? 1 : 2); ++i) r.v[i] = make_uint4(0u, 0u, 0u, 0u);
-  return r;
-}
-
-template <bool BF16>
 __device__ __forceinline__ void floats8(const Raw8<BF16>& r, float (&x)[8]) {
   if constexpr (BF16) {
     unpack8(r.v[0], x);
