@@ -14,14 +14,14 @@
 // exponentials (32 a cycle and SM: 260 us) but operands: the packed fp32 instructions read up to six
 // registers, of which the SM's quarter supplies two a cycle (measured: a packed multiply-add of three
 // different operands takes 3 cycles, a product 2). A position of 16 states and 32 channels is 102
-// instructions and about 290 operands, and takes 171 cycles of a quarter; issue slots are 60% busy,
-// the exponentials' unit 46%, shared memory 50%. Measured at 32 x 512 positions of 8192 channels:
+// instructions with, by count, some 290 operands, and takes 171 cycles of a quarter; issue slots are
+// 60% busy, the exponentials' unit 46%, shared memory 50%. At 32 x 512 positions of 8192 channels:
 //   two channels x eight states a thread 582 us; four x eight 710 (registers leave 12 warps an SM);
 //   steps held twice each, as pairs, instead of splat in registers 626; products in single
-//   instructions instead of pairs 598 to 650; loads through registers instead of asynchronous copies 737.
+//   instructions instead of pairs 598 to 650; three CTAs an SM instead of four 740 (695 with four then).
 // Whole calls: 16384 x 8192 channels 943 us (582 of it the scan, the rest the parts' ends, below);
-// 8 ragged prompts of up to 2045 positions x 4096 channels 292 us; one of 1021 x 2048 channels 35 us;
-// 3 x 509 of 64 states in fp32 104 us.
+// 8 ragged prompts of up to 2045 positions x 4096 channels 291 us; one of 1021 x 2048 channels 35 us;
+// 3 x 509 of 64 states in fp32 103 us.
 #include "gdn_ssm.h"
 #include "gdn_vec.cuh"
 
@@ -34,6 +34,7 @@ namespace {
 
 constexpr int kWarps = 4;  // of a CTA; they have nothing in common
 constexpr int kCtas = 4;   // of an SM
+
 // Two elements as they lie in memory.
 template <bool BF16>
 using Raw2 = typename std::conditional<BF16, uint32_t, float2>::type;
