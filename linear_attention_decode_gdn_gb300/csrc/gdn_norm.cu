@@ -16,10 +16,13 @@ namespace gdn {
 namespace {
 
 constexpr int kMaxThreads = 1024;
-constexpr int kRowWarps = 4;   // rows of a CTA where a warp takes one
-// Up to here a thread takes one vector, so that a row's loads are spread over as many threads as there are;
-// beyond, four, of which more rows fit an SM.
-constexpr int kFewRows = 608;
+constexpr int kRowWarps = 4;  // rows of a CTA where a warp takes one: up to 256 channels (16384 x 256: 7.0 us, 18.0 a CTA each)
+// Vectors of a thread, by the time at 64 / 256 / 1024 / 4096 / 16384 rows (bf16 into e4m3, a scale for 128):
+//   4096 channels: one 2.9 3.9 7.7 26.7 92 us, two 3.5 3.9 7.0 24.6 82, four 4.2 4.9 8.2 24.4 77;
+//   1024 channels: one 2.7 2.9 3.8 7.2 23.4, two 3.5 3.5 3.6 7.6 22.5, four in a warp 4.2 4.2 4.3 8.1 23.8.
+// So one where a row has an SM to itself, or where two would leave a warp or two; four from kManyVecs on
+// (2^24 elements), where they come from HBM and a thread should wait for much at once; else two.
+constexpr int64_t kManyVecs = 1 << 21;
 constexpr float kTop = 448.0f;    // the largest e4m3 value
 constexpr float kLeast = 1e-30f;  // scales are made as if the largest value were at least this
 
@@ -143,14 +146,15 @@ template <bool XB, bool RB, int OT>
 cudaError_t launch_row(const gdn_norm& p, cudaStream_t stream) {
   const int vecs = p.width / 8;
   auto threads = [&](int v) { return static_cast<unsigned>(((vecs + v - 1) / v + 31) / 32 * 32); };
-  if (p.rows > kFewRows) {
+  if (vecs <= 32) {
     const unsigned grid = static_cast<unsigned>((p.rows + kRowWarps - 1) / kRowWarps);
-    if (vecs <= 32) return launch_overlapped(gdn_norm_kernel<XB, RB, OT, 1, true>, p, dim3(grid), kRowWarps * 32, 0, 1u, stream);
-    if (vecs <= 128) return launch_overlapped(gdn_norm_kernel<XB, RB, OT, 4, true>, p, dim3(grid), kRowWarps * 32, 0, 1u, stream);
-    return launch_overlapped(gdn_norm_kernel<XB, RB, OT, 4, false>, p, dim3(p.rows), threads(4), 0, 1u, stream);
+    return launch_overlapped(gdn_norm_kernel<XB, RB, OT, 1, true>, p, dim3(grid), kRowWarps * 32, 0, 1u, stream);
   }
-  if (vecs <= kMaxThreads) return launch_overlapped(gdn_norm_kernel<XB, RB, OT, 1, false>, p, dim3(p.rows), threads(1), 0, 1u, stream);
-  return launch_overlapped(gdn_norm_kernel<XB, RB, OT, 4, false>, p, dim3(p.rows), threads(4), 0, 1u, stream);
+  if (vecs >= 512 && static_cast<int64_t>(p.rows) * vecs >= kManyVecs)
+    return launch_overlapped(gdn_norm_kernel<XB, RB, OT, 4, false>, p, dim3(p.rows), threads(4), 0, 1u, stream);
+  if (vecs <= 128 || (p.rows <= kSms && vecs <= kMaxThreads))
+    return launch_overlapped(gdn_norm_kernel<XB, RB, OT, 1, false>, p, dim3(p.rows), threads(1), 0, 1u, stream);
+  return launch_overlapped(gdn_norm_kernel<XB, RB, OT, 2, false>, p, dim3(p.rows), threads(2), 0, 1u, stream);
 }
 
 template <bool XB, bool RB>

@@ -73,7 +73,7 @@ def check_norm(gdn, x, residual, weight, out, group=0, eps=1e-6):
 
 
 @pytest.mark.parametrize("rows,width", [(1, 8), (3, 24), (5, 128), (2, 136), (257, 1024), (3, 2056), (66, 4096), (700, 4104), (9, 6144), (2, 8192), (3, 12008), (2, 16384),
-                                        (609, 8), (700, 256), (700, 264), (613, 1024), (610, 1032), (640, 16384)])
+                                        (609, 8), (700, 256), (700, 264), (613, 1024), (610, 1032), (640, 16384), (4100, 4096), (1025, 16384)])
 @pytest.mark.parametrize("kind,res", [(BF16, BF16), (BF16, FP32), (FP32, FP32), (FP32, BF16), (BF16, None), (FP32, None)])
 def test_norm(gdn, rows, width, kind, res):
     g = gen(rows * 31 + width)
