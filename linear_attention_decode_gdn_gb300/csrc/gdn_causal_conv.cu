@@ -10,7 +10,7 @@
 //     120 us with four positions in registers instead of sixteen in shared memory.
 //   8 ragged prompts of up to 4093 positions, 4096 channels: 57 us, 5.3 TB/s; issue slots 59% busy.
 //   one token of 64 requests x 6144 channels: 4.3 us, latency (5.6 with each thread loading its own
-//     taps); of 512 x 4096: 9.0 us, 3.7 TB/s (10.4 with one request a thread).
+//     taps); of 512 x 4096: 7.5 us, 4.5 TB/s (9.0 with one request's row on its way at a time).
 #include "gdn_ssm.h"
 #include "gdn_vec.cuh"
 
@@ -25,8 +25,10 @@ constexpr int kGroup = 4, kGroups = 4;  // positions that are loaded together, a
 // until the GPU is half empty.
 constexpr int kMinSteps = 8, kMaxSteps = 128;
 constexpr int64_t kEnough = 40000;
-// Requests that a thread takes one token of, where there are enough threads either way: 9.0 us at 4,
-// 10.5 at 1 and 2, 10.8 at 8 (512 x 4096 channels).
+// Requests that a thread takes one token of, from so many vectors in the batch on: of 512 x 4096 channels
+// 7.5 us at 4, 8.5 at 2, 9.3 at 8, 11.9 at 1; of 256 x 4096 6.2 at 4, 7.5 at 1; but of 64 x 6144 (49152
+// vectors) 4.3 at 1, 5.0 at 4.
+constexpr int64_t kManyItems = 100000;
 constexpr int kTokenRows = 4;
 
 struct ConvTask {
@@ -106,14 +108,17 @@ struct Weights {
 // would touch 32 lines each; the warp loads the 4 KB in order and hands them over in shared memory,
 // with places exchanged so that eight lanes meet all banks both ways.
 constexpr int kTapVecs = 256;
-__device__ __forceinline__ Weights load_weights(const gdn_conv& c, int d, float4* taps) {
+__device__ __forceinline__ void fetch_weights(const gdn_conv& c, int d, float4* taps) {
   const int lane = threadIdx.x & 31, first = __shfl_sync(0xffffffffu, d, 0);
 #pragma unroll
   for (int j = 0; j < kTapVecs / 32; ++j) {
     const int i = 32 * j + lane;
-    taps[i ^ (i >> 3 & 7)] = reinterpret_cast<const float4*>(c.w)[(first + i) % c.channels];
+    cp_async16(&taps[i ^ (i >> 3 & 7)], c.w + static_cast<int64_t>((first + i) % c.channels) * 4);
   }
-  __syncwarp();
+}
+// After what fetch_weights() asked for is there, for all lanes.
+__device__ __forceinline__ Weights take_weights(const gdn_conv& c, int d, const float4* taps) {
+  const int lane = threadIdx.x & 31;
   Weights r;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -122,6 +127,10 @@ __device__ __forceinline__ Weights load_weights(const gdn_conv& c, int d, float4
     r.bias[k] = c.bias != nullptr ? *reinterpret_cast<const f32x2*>(c.bias + d + 2 * k) : 0;
   }
   return r;
+}
+__device__ __forceinline__ void copies_arrived() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
 }
 template <bool BF16>
 __device__ __forceinline__ void pairs8(const Raw8<BF16>& r, f32x2 (&x)[4]) {
@@ -171,38 +180,74 @@ struct TokenTask {
 };
 template <bool BF16>
 __global__ void __launch_bounds__(kConvThreads) gdn_causal_conv_token_kernel(const TokenTask task) {
-  const gdn_conv& c = task.p.c;
+  // A lane's part of a slot's row is 48 (96) bytes, of which its own accesses would take 16 at a time, 48
+  // apart. Where a warp's lanes are all of one row (WHOLE) they take it in order, through shared
+  // memory, and kFlight requests' rows are on their way together.
+  constexpr int kFlight = BF16 ? 4 : 2, kPart = sizeof(Row<BF16>), kPartVecs = kPart / 16;
   __shared__ float4 taps[kConvThreads / 32][kTapVecs];
+  __shared__ uint4 parts[kConvThreads / 32][kFlight][32 * kPartVecs];
+  const gdn_conv& c = task.p.c;
   griddep_launch_dependents();
   griddep_wait();
-  const int vecs = c.channels / 8;
+  const int vecs = c.channels / 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kConvThreads + threadIdx.x;
   const int first = static_cast<int>(quotient(item, vecs)), d = static_cast<int>(item - static_cast<int64_t>(first) * vecs) * 8;
-  const Weights weights = load_weights(c, d, taps[threadIdx.x >> 5]);
-  const bool silu = (c.flags & GDN_CONV_SILU) != 0u;
-  for (int r = 0; r < task.rows; ++r) {
-    const int b = first * task.rows + r;
-    if (b >= c.batch) return;
-    const int slot = c.slot[b];
-    const Raw8<BF16> now = load8<BF16>(c.x, b * c.x_strides[0] + d);
-    const int len = c.seq_lens != nullptr ? c.seq_lens[b] : 1;
-    if (slot < 0) continue;
-    const bool bad_slot = slot >= c.num_slots, bad_len = len < 0 || len > 1;
-    if (bad_slot || bad_len) {
-      if (d == 0) atomic_status(task.p.status, bad_slot ? GDN_STATUS_BAD_SLOT : GDN_STATUS_BAD_LEN);
-      continue;
+  fetch_weights(c, d, taps[warp]);
+  Weights weights;
+  const bool silu = (c.flags & GDN_CONV_SILU) != 0u, whole = vecs % 32 == 0;
+  for (int r0 = 0; r0 < task.rows; r0 += kFlight) {
+    const int b0 = first * task.rows + r0;
+    int slot[kFlight];
+    Raw8<BF16> now[kFlight];
+#pragma unroll
+    for (int r = 0; r < kFlight; ++r) {
+      slot[r] = -1;
+      if (r0 + r >= task.rows || b0 + r >= c.batch) continue;
+      slot[r] = c.slot[b0 + r];
+      now[r] = load8<BF16>(c.x, (b0 + r) * c.x_strides[0] + d);
+      const int len = c.seq_lens != nullptr ? c.seq_lens[b0 + r] : 1;
+      if (slot[r] < 0 || (len == 1 && slot[r] < c.num_slots)) continue;
+      const bool bad_slot = slot[r] >= c.num_slots;
+      if (d == 0 && (bad_slot || len != 0)) atomic_status(task.p.status, bad_slot ? GDN_STATUS_BAD_SLOT : GDN_STATUS_BAD_LEN);
+      slot[r] = -1;
     }
-    if (len == 0) continue;
-    void* const row = row_at<BF16>(c, slot, d);
-    const Row<BF16> old = load_row<BF16>(row);
-    const Raw8<BF16> cols[3] = {column<BF16>(old, 1), column<BF16>(old, 2), now};
-    store_row<BF16>(row, cols);
-    f32x2 past[3][4], in[4];
-    pairs8<BF16>(column<BF16>(old, 0), past[0]);
-    pairs8<BF16>(cols[0], past[1]);
-    pairs8<BF16>(cols[1], past[2]);
-    pairs8<BF16>(now, in);
-    store8<BF16>(c.o, static_cast<int64_t>(b) * c.channels + d, output<BF16>(weights, past, in, silu));
+    if (whole) {
+#pragma unroll
+      for (int r = 0; r < kFlight; ++r) {
+        if (slot[r] < 0) continue;
+        const uint4* const from = static_cast<const uint4*>(row_at<BF16>(c, slot[r], d - 8 * lane));
+#pragma unroll
+        for (int i = 0; i < kPartVecs; ++i) cp_async16(&parts[warp][r][32 * i + lane], from + 32 * i + lane);
+      }
+    }
+    copies_arrived();
+    if (r0 == 0) weights = take_weights(c, d, taps[warp]);
+#pragma unroll
+    for (int r = 0; r < kFlight; ++r) {
+      if (slot[r] < 0) continue;
+      void* const row = row_at<BF16>(c, slot[r], d);
+      void* const at = whole ? static_cast<void*>(&parts[warp][r][lane * kPartVecs]) : row;
+      const Row<BF16> old = load_row<BF16>(at);
+      const Raw8<BF16> cols[3] = {column<BF16>(old, 1), column<BF16>(old, 2), now[r]};
+      store_row<BF16>(at, cols);
+      f32x2 past[3][4], in[4];
+      pairs8<BF16>(column<BF16>(old, 0), past[0]);
+      pairs8<BF16>(cols[0], past[1]);
+      pairs8<BF16>(cols[1], past[2]);
+      pairs8<BF16>(now[r], in);
+      store8<BF16>(c.o, static_cast<int64_t>(b0 + r) * c.channels + d, output<BF16>(weights, past, in, silu));
+    }
+    if (whole) {
+      __syncwarp();
+#pragma unroll
+      for (int r = 0; r < kFlight; ++r) {
+        if (slot[r] < 0) continue;
+        uint4* const to = static_cast<uint4*>(row_at<BF16>(c, slot[r], d - 8 * lane));
+#pragma unroll
+        for (int i = 0; i < kPartVecs; ++i) to[32 * i + lane] = parts[warp][r][32 * i + lane];
+      }
+      __syncwarp();
+    }
   }
 }
 
@@ -221,7 +266,9 @@ __global__ void __launch_bounds__(kConvThreads, 4) gdn_causal_conv_kernel(const 
   const int b = static_cast<int>(quotient(item, per)), in = static_cast<int>(item - b * per);
   const int chunk = in / vecs, vec = in - chunk * vecs, d = vec * 8;
   const int slot = b < c.batch ? c.slot[b] : -1;
-  const Weights weights = load_weights(c, d, taps[threadIdx.x >> 5]);  // while the slot is looked up
+  fetch_weights(c, d, taps[threadIdx.x >> 5]);  // while the slot is looked up
+  copies_arrived();
+  const Weights weights = take_weights(c, d, taps[threadIdx.x >> 5]);
   if (slot < 0) return;
   const int len = c.seq_lens != nullptr ? c.seq_lens[b] : c.num_tokens;
   const bool bad_slot = slot >= c.num_slots, bad_len = len < 0 || len > c.num_tokens;
@@ -295,7 +342,7 @@ cudaError_t launch_conv(const ConvTask& task, int64_t items, cudaStream_t stream
 template <bool BF16>
 cudaError_t launch_token(const ConvParams& p, cudaStream_t stream) {
   const int64_t vecs = p.c.channels / 8;
-  TokenTask task{p, vecs * p.c.batch >= 4 * kEnough ? kTokenRows : 1};
+  TokenTask task{p, vecs * p.c.batch >= kManyItems ? kTokenRows : 1};
   const int64_t items = vecs * ((p.c.batch + task.rows - 1) / task.rows);
   const unsigned grid = static_cast<unsigned>((items + kConvThreads - 1) / kConvThreads);
   return launch_overlapped(gdn_causal_conv_token_kernel<BF16>, task, dim3(grid), kConvThreads, 0, 1u, stream);
