@@ -67,22 +67,24 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 
-// A thread owns eight states of two channels, the states in pairs: LANES neighbouring lanes a pair of
-// channels, CH channels a warp, STEPS positions at a time in shared memory. Item i of a tile is the
-// pair of channels i % ROW of position i / ROW.
-template <int N_, bool BF16_>
+// A thread owns eight states of OWN channels (two, or one where prompts are few and short), the states
+// in pairs: LANES neighbouring lanes hold the same channels, a warp CH, STEPS positions at a time in
+// shared memory. Item i of a tile is the pair of channels i % ROW of position i / ROW.
+template <int N_, bool BF16_, int OWN_>
 struct Cfg {
+  static constexpr int OWN = OWN_;
   static constexpr int N = N_;
   static constexpr bool BF16 = BF16_;
-  static constexpr int LANES = N / 8, CH = 2 * (32 / LANES), ROW = CH / 2, STEPS = 8;
-  static constexpr int ITEMS = STEPS * ROW, U = ITEMS / 32;  // of u, dt, z, y; a lane's
+  static constexpr int LANES = N / 8, CH = OWN * (32 / LANES), ROW = CH / 2, STEPS = 8;
+  static constexpr int ITEMS = STEPS * ROW, U = (ITEMS + 31) / 32;  // of u, dt, z, y; a lane's
   static constexpr int ELEM = BF16 ? 2 : 4;
   // b and c in fp32 in shared memory; else every thread makes its own of bf16. A position's 2 N values
   // are converted by the warp for 512 / N channels: 582 against 612 us at N = 16 (scan of 32 x 512
   // positions, 8192 channels), but 740 against 670 at N = 32 and 461 against 346 at 64.
   static constexpr bool WIDEN = BF16 && N <= 16;
   static constexpr int COPY = STEPS * CH * ELEM / 16, NCOPY = STEPS * N * ELEM / 16;  // 16-byte copies of u, dt or z, and of b or c
-  static_assert(ITEMS % 32 == 0, "every lane has as many");
+  static_assert(CH % 8 == 0, "whole copies");
+  static_assert(ITEMS % 32 == 0 || ITEMS < 32, "every lane has as many");
 };
 
 // A warp's part of shared memory: two tiles as they lie in memory, one of which is being loaded,
@@ -145,12 +147,12 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) gdn_ssm_scan_kernel(const 
 
   // ---- this thread's states -----------------------------------------------------------------
   const int set = lane / C::LANES, part = lane % C::LANES;
-  const bool mine_live = set * 2 < count;
-  float* const state = s.state + (static_cast<int64_t>(slot) * s.channels + c0 + set * 2) * C::N + part * 8;
-  f32x2 h[2][4], a[2][4];  // [channel][pair of states]
-  auto load_states = [&](const float* from, f32x2 (&to)[2][4]) {
+  const bool mine_live = set * C::OWN < count;
+  float* const state = s.state + (static_cast<int64_t>(slot) * s.channels + c0 + set * C::OWN) * C::N + part * 8;
+  f32x2 h[C::OWN][4], a[C::OWN][4];  // [channel][pair of states]
+  auto load_states = [&](const float* from, f32x2 (&to)[C::OWN][4]) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::OWN; ++i) {
 #pragma unroll
       for (int j = 0; j < 4; j += 2) {
         ulonglong2 x = make_ulonglong2(0, 0);
@@ -159,30 +161,30 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) gdn_ssm_scan_kernel(const 
       }
     }
   };
-  auto store_states = [&](float* to, const f32x2 (&from)[2][4]) {
+  auto store_states = [&](float* to, const f32x2 (&from)[C::OWN][4]) {
     if (!mine_live) return;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < C::OWN; ++i)
 #pragma unroll
       for (int j = 0; j < 4; j += 2) *reinterpret_cast<ulonglong2*>(to + i * C::N + j * 2) = make_ulonglong2(from[i][j], from[i][j + 1]);
   };
-  load_states(s.a + static_cast<int64_t>(c0 + set * 2) * C::N + part * 8, a);
+  load_states(s.a + static_cast<int64_t>(c0 + set * C::OWN) * C::N + part * 8, a);
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < C::OWN; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) a[i][j] = mul2(a[i][j], both(kLog2e));
   // this thread's place in init, and in end and sum of part j
-  const int64_t mine = static_cast<int64_t>(c0 + set * 2) * C::N + part * 8, per_request = static_cast<int64_t>(s.channels) * C::N;
+  const int64_t mine = static_cast<int64_t>(c0 + set * C::OWN) * C::N + part * 8, per_request = static_cast<int64_t>(s.channels) * C::N;
   auto end_of = [&](int j) { return p.end + (static_cast<int64_t>(b) * (p.parts - 1) + j) * per_request + mine; };
-  auto sum_of = [&](int j) { return p.sum + (static_cast<int64_t>(b) * (p.parts - 1) + j) * s.channels + c0 + set * 2; };
+  auto sum_of = [&](int j) { return p.sum + (static_cast<int64_t>(b) * (p.parts - 1) + j) * s.channels + c0 + set * C::OWN; };
   load_states(p.parts == 1 || (SUMMARY && part_no == 0) ? state : part_no == 0 ? p.init + b * per_request + mine : end_of(part_no - 1), h);
-  f32x2 steps_sum[2] = {0, 0};  // both halves alike
+  f32x2 steps_sum[C::OWN] = {};  // both halves alike
   if (SUMMARY) {
     // the last part's scan overwrites the slot's state while others still begin
     if (part_no == 0) store_states(p.init + b * per_request + mine, h);
     if (last) return;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < C::OWN; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) h[i][j] = 0;
   }
@@ -243,6 +245,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) gdn_ssm_scan_kernel(const 
 #pragma unroll
     for (int k = 0; k < C::U; ++k) {
       const int i = lane + 32 * k;
+      if (C::ITEMS < 32 && i >= C::ITEMS) continue;
       f32x2 dt = pair_of<C::BF16>(reinterpret_cast<const Raw2<C::BF16>*>(raw.dt)[i]);
       if (softplus)
         dt = softplus_2(add2(fma2(dt, both(kLog2e), rest), bias));
@@ -265,9 +268,15 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) gdn_ssm_scan_kernel(const 
     // ---- the recurrence ----------------------------------------------------------------------------
 #pragma unroll
     for (int t = 0; t < C::STEPS; ++t) {
-      const ulonglong2 in = sm.in[t * C::ROW + set];
-      const float2 dt = unpack2(in.x), du = unpack2(in.y);
-      const f32x2 dts[2] = {both(dt.x), both(dt.y)}, dus[2] = {both(du.x), both(du.y)};
+      f32x2 dts[C::OWN], dus[C::OWN];
+      if constexpr (C::OWN == 2) {
+        const ulonglong2 in = sm.in[t * C::ROW + set];
+        const float2 dt = unpack2(in.x), du = unpack2(in.y);
+        dts[0] = both(dt.x), dts[1] = both(dt.y), dus[0] = both(du.x), dus[1] = both(du.y);
+      } else {
+        const float* const in = reinterpret_cast<const float*>(&sm.in[t * C::ROW + set / 2]) + set % 2;
+        dts[0] = both(in[0]), dus[0] = both(in[2]);
+      }
       f32x2 bb[4], cc[4] = {0, 0, 0, 0};
       if constexpr (C::WIDEN) {
         pairs8<false>(reinterpret_cast<const unsigned char*>(&sm.b[t][part * 8]), bb);
@@ -276,9 +285,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) gdn_ssm_scan_kernel(const 
         pairs8<C::BF16>(raw.b + (t * C::N + part * 8) * kE, bb);
         if (!SUMMARY) pairs8<C::BF16>(raw.c + (t * C::N + part * 8) * kE, cc);
       }
-      float sum[2];
+      float sum[C::OWN];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < C::OWN; ++i) {
         f32x2 acc = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -292,7 +301,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) gdn_ssm_scan_kernel(const 
       if constexpr (!SUMMARY) {
         // Sums over the lanes of a pair of channels: a lane keeps one channel and gives the other
         // away; further lanes add what is left.
-        if constexpr (C::LANES == 1) {
+        if constexpr (C::OWN == 1) {
+#pragma unroll
+          for (int off = C::LANES / 2; off > 0; off >>= 1) sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], off);
+          if (part == 0) sm.y[t][set] = sum[0];
+        } else if constexpr (C::LANES == 1) {
           *reinterpret_cast<float2*>(&sm.y[t][set * 2]) = make_float2(sum[0], sum[1]);
         } else {
           constexpr int kOwn = C::LANES / 2;
@@ -312,7 +325,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) gdn_ssm_scan_kernel(const 
 #pragma unroll
       for (int k = 0; k < C::U; ++k) {
         const int i = lane + 32 * k, t = i / C::ROW;
-        if (!pair_live || t0 + t >= end) continue;
+        if (!pair_live || t0 + t >= end || (C::ITEMS < 32 && i >= C::ITEMS)) continue;
         f32x2 y = fma2(skip, pair_of<C::BF16>(reinterpret_cast<const Raw2<C::BF16>*>(raw.u)[i]), reinterpret_cast<const f32x2*>(sm.y)[i]);
         if (gated) y = mul2(y, silu_2<!C::BF16>(pair_of<C::BF16>(reinterpret_cast<const Raw2<C::BF16>*>(raw.z)[i])));
         *reinterpret_cast<Raw2<C::BF16>*>(y_at + 32 / C::ROW * k * y_row) = raw_of<C::BF16>(y);
@@ -323,7 +336,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) gdn_ssm_scan_kernel(const 
 
   if (SUMMARY) {
     store_states(end_of(part_no), h);
-    if (mine_live && part == 0) *reinterpret_cast<float2*>(sum_of(part_no)) = make_float2(unpack2(steps_sum[0]).x, unpack2(steps_sum[1]).x);
+    if (mine_live && part == 0) {
+#pragma unroll
+      for (int i = 0; i < C::OWN; ++i) sum_of(part_no)[i] = unpack2(steps_sum[i]).x;
+    }
   } else if (last) {
     store_states(state, h);
   }
@@ -367,12 +383,14 @@ __global__ void __launch_bounds__(kJoinThreads) gdn_ssm_join_kernel(const ScanPa
 
 // How prompts are cut: as a rough model of the times says, whose constants are measured. A position
 // takes 0.18 us where a warp has its quarter of an SM to itself, 0.225 where two share one, and 0.09
-// for each of more, up to the four that fit and in rounds beyond. Parts take two thirds more of it
+// for each of more, up to the four that fit and in rounds beyond. With one channel a thread there are
+// twice the warps, which take 0.13, 0.15 and 0.058 each: sooner through a prompt where they have room
+// (64 positions of 2048 channels: 11.2 us, 14.5 with two), later where not (a full GPU: 656 and 584). Parts take two thirds more of it
 // for their ends, two launches, and 6 us a further round to begin (3 prompts of 509 positions of 64
 // states, 768 warps: 103 us in 3 parts, 113 in 11). Cuts that fill the GPU 1 to 4 times are compared with none:
 //   whole wins where there are enough warps (16 x 1024 positions of 4096 channels, 2048 warps: 342 us,
 //   417 in two parts) or few positions (2048 channels: 64 positions 14.5 us, 15.9 in two parts, but 96
-//   20.1 and 16.0; 768 warps: 200 positions 47.5 and 49.7);
+//   20.1 and 16.0, all with two channels a thread; 768 warps: 200 positions 47.5 and 49.7);
 //   parts elsewhere (16384 positions, 256 warps: 2906 us whole, 1009 in 9 parts, which fill 0.95 of the
 //   GPU, 943 in 19, which fill it twice, 1126 in 10, which leave half of the second round empty), and
 //   where prompts have lengths of their own, of which a whole one holds up the end (8 ragged prompts,
@@ -381,6 +399,7 @@ __global__ void __launch_bounds__(kJoinThreads) gdn_ssm_join_kernel(const ScanPa
 // A join goes through all parts in turn, so there are at most sqrt(T) of them, of 32 positions at least.
 struct Cut {
   int32_t parts, part;
+  int32_t own;  // channels of a thread
 };
 Cut cut_of(int32_t batch, int32_t tokens, int32_t channels, int32_t state_size, bool ragged) {
   constexpr int32_t kShortest = 32, kRound = 8, kQuarters = kSms * 4, kRounds = 4;
@@ -390,8 +409,14 @@ Cut cut_of(int32_t batch, int32_t tokens, int32_t channels, int32_t state_size, 
     const int64_t shared = (all_warps + kQuarters - 1) / kQuarters;
     return shared <= 1 ? 0.18 : shared <= 2 ? 0.225 : 0.09 * static_cast<double>(shared);
   };
-  Cut best{1, tokens};
+  auto position_of_one = [](int64_t all_warps) {  // with a channel a thread
+    const int64_t shared = (all_warps + kQuarters - 1) / kQuarters;
+    return shared <= 1 ? 0.13 : shared <= 2 ? 0.15 : 0.058 * static_cast<double>(shared);
+  };
+  Cut best{1, tokens, 2};
   double least = 2.5 + tokens * position(warps);
+  const double took_one = 2.5 + tokens * position_of_one(2 * warps);
+  if (state_size < 64 && took_one < least) least = took_one, best.own = 1;
   const int64_t most = static_cast<int64_t>(std::sqrt(static_cast<double>(tokens)));
   for (int rounds = 1; rounds <= kRounds; ++rounds) {
     int64_t parts = static_cast<int64_t>(kSms) * kCtas * kWarps * rounds / warps;
@@ -402,7 +427,7 @@ Cut cut_of(int32_t batch, int32_t tokens, int32_t channels, int32_t state_size, 
     parts = (tokens + part - 1) / part;
     const double all = static_cast<double>(part) * (5.0 / 3.0) * position(warps * parts);
     const double took = ragged ? 5.0 + 0.6 * all : 6.0 * rounds - 1.0 + all;
-    if (parts > 1 && took < least) least = took, best = {static_cast<int32_t>(parts), static_cast<int32_t>(part)};
+    if (parts > 1 && took < least) least = took, best = {static_cast<int32_t>(parts), static_cast<int32_t>(part), 2};
   }
   return best;
 }
@@ -418,11 +443,17 @@ cudaError_t launch_parts(ScanParams p, cudaStream_t stream) {
   return launch_overlapped(gdn_ssm_scan_kernel<C, SUMMARY>, p, dim3((p.tasks + kWarps - 1) / kWarps), kWarps * 32, kBytes, 1u, stream);
 }
 
-template <class C>
+template <int N, bool BF16>
 cudaError_t launch_scan(const SsmParams& given, void* workspace, cudaStream_t stream) {
+  using C = Cfg<N, BF16, 2>;
   const gdn_ssm& s = given.s;
   const Cut cut = cut_of(s.batch, s.num_tokens, s.channels, s.state_size, s.seq_lens != nullptr);
   ScanParams p{s, given.status, s.channels / s.num_groups, 0, cut.parts, cut.part, 0, nullptr, nullptr, nullptr};
+  if constexpr (N < 64) {  // a row of four channels would be no whole copy
+    using One = Cfg<N, BF16, 1>;
+    p.blocks = (p.per_group + One::CH - 1) / One::CH;
+    if (cut.own == 1) return launch_parts<One, false>(p, stream);
+  }
   p.blocks = (p.per_group + C::CH - 1) / C::CH;
   if (cut.parts > 1) {
     const int64_t states = static_cast<int64_t>(s.batch) * s.channels * s.state_size;
@@ -441,10 +472,10 @@ cudaError_t launch_scan(const SsmParams& given, void* workspace, cudaStream_t st
 template <bool BF16>
 cudaError_t launch_type(const SsmParams& p, void* workspace, cudaStream_t stream) {
   switch (p.s.state_size) {
-    case 8: return launch_scan<Cfg<8, BF16>>(p, workspace, stream);
-    case 16: return launch_scan<Cfg<16, BF16>>(p, workspace, stream);
-    case 32: return launch_scan<Cfg<32, BF16>>(p, workspace, stream);
-    default: return launch_scan<Cfg<64, BF16>>(p, workspace, stream);
+    case 8: return launch_scan<8, BF16>(p, workspace, stream);
+    case 16: return launch_scan<16, BF16>(p, workspace, stream);
+    case 32: return launch_scan<32, BF16>(p, workspace, stream);
+    default: return launch_scan<64, BF16>(p, workspace, stream);
   }
 }
 
