@@ -385,17 +385,18 @@ __global__ void __launch_bounds__(kJoinThreads) gdn_ssm_join_kernel(const ScanPa
 // takes 0.18 us where a warp has its quarter of an SM to itself, 0.225 where two share one, and 0.09
 // for each of more, up to the four that fit and in rounds beyond. With one channel a thread there are
 // twice the warps, which take 0.13, 0.15 and 0.058 each: sooner through a prompt where they have room
-// (64 positions of 2048 channels: 11.2 us, 14.5 with two), later where not (a full GPU: 656 and 584). Parts take two thirds more of it
-// for their ends, two launches, and 6 us a further round to begin (3 prompts of 509 positions of 64
-// states, 768 warps: 103 us in 3 parts, 113 in 11). Cuts that fill the GPU 1 to 4 times are compared with none:
+// (64 positions of 2048 channels: 11.2 us, 14.5 with two), later where not (a full GPU: 656 and 584).
+// Parts take two thirds more for their ends, two launches, and 6 us a further round to begin (3 prompts
+// of 509 positions of 64 states, 768 warps: 103 us in 3 parts, 113 in 11). Cuts that fill the GPU one
+// to four times are compared with none:
 //   whole wins where there are enough warps (16 x 1024 positions of 4096 channels, 2048 warps: 342 us,
-//   417 in two parts) or few positions (2048 channels: 64 positions 14.5 us, 15.9 in two parts, but 96
-//   20.1 and 16.0, all with two channels a thread; 768 warps: 200 positions 47.5 and 49.7);
+//   417 in two parts) or few positions (2048 channels, two a thread: 64 positions 14.5 us, 15.9 in two
+//   parts, but 96 20.1 and 16.0; 768 warps: 200 positions 47.5 and 49.7);
 //   parts elsewhere (16384 positions, 256 warps: 2906 us whole, 1009 in 9 parts, which fill 0.95 of the
 //   GPU, 943 in 19, which fill it twice, 1126 in 10, which leave half of the second round empty), and
 //   where prompts have lengths of their own, of which a whole one holds up the end (8 ragged prompts,
-//   1024 warps: 457 us whole, 292 in 7 parts; of equal length 477 and 471): parts without
-//   positions cost next to nothing, so 0.6 of the time is reckoned there.
+//   1024 warps: 457 us whole, 292 in 7 parts; of equal length 477 and 471): parts without positions
+//   cost next to nothing, so 0.6 of the time is reckoned there.
 // A join goes through all parts in turn, so there are at most sqrt(T) of them, of 32 positions at least.
 struct Cut {
   int32_t parts, part;
