@@ -524,7 +524,7 @@ typedef struct gdn_norm {
  * gdn_add_rms_norm -- r = x + residual (x alone without one), residual = r rounded to its type,
  *   o = r / sqrt(mean r^2 + eps) * weight, of the r that is not rounded yet.
  * In 8 bits each scale is s = max(m, 1e-30) / 448, m the largest |o| of its channels, and o holds
- * the e4m3 value next to o / s: o is about s times what is stored. A NaN makes its row NaN, an
+ * the e4m3 value next to the fp32 quotient o / s: o is about s times what is stored. A NaN makes its row NaN, an
  * infinity makes itself NaN and the rest of its row 0, as the formula says, and a scale whose
  * channels hold NaN is NaN. Squares are summed in fp32: a sum past its range (values above about
  * 1e19) counts as infinite.

@@ -1,0 +1,40 @@
+"""The calls of selective state space layers at edges that the other tests leave out: quantised values next
+to a border, states that grow."""
+import pytest
+import torch
+
+from test_gpu_selective import BF16, E4M3, FP32, gdn, gen, ints, randn  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- norm ---------------------------------------------------------------------------------------
+@pytest.mark.parametrize("rows,width,group", [(8191, 4096, 0), (8191, 4096, 128), (60000, 256, 128), (300, 4096, 0)])
+def test_norm_stores_the_quotients_nearest_value(gdn, rows, width, group):  # noqa: F811
+    """What is stored is e4m3(o / s), bit for bit, of the o and s that the call itself gives: a product with 1 / s is
+    up to one and a half roundings off, which puts quotients next to a border on its other side."""
+    g = gen(rows + group)
+    x, weight = randn(g, rows, width, dtype=BF16), 1 + 0.1 * randn(g, width)
+    o, q = torch.empty(rows, width, device="cuda"), torch.empty(rows, width, dtype=E4M3, device="cuda")
+    scales = torch.empty(rows, -(-width // (group or width)), device="cuda")
+    gdn.add_rms_norm(x, o, weight=weight)
+    gdn.add_rms_norm(x, q, weight=weight, scales=scales, group=group)
+    tops = o.abs().unflatten(1, (scales.shape[1], -1)).amax(-1)
+    assert torch.equal(scales, tops / torch.full_like(tops, 448))  # by a number torch multiplies with its inverse
+    want = (o.unflatten(1, (scales.shape[1], -1)) / scales[..., None]).flatten(1).to(E4M3)
+    wrong = q.view(torch.uint8) != want.view(torch.uint8)
+    assert not wrong.any(), (int(wrong.sum()), wrong.numel())
+
+
+@pytest.mark.parametrize("group", [0, 128])
+def test_norm_of_outputs_past_fp32(gdn, group):  # noqa: F811
+    """An output that weight makes infinite makes its scale infinite: itself NaN, the others of that scale 0."""
+    x, weight = torch.ones(2, 256, device="cuda"), torch.ones(256, device="cuda")
+    x[0, 3], weight[3] = 100.0, 3e38
+    x[1, 3] = 1e-30
+    q, scales = torch.empty(2, 256, dtype=E4M3, device="cuda"), torch.empty(2, 2 if group else 1, device="cuda")
+    gdn.add_rms_norm(x, q, weight=weight, scales=scales, group=group)
+    got, first = q.float(), group or 256
+    assert scales[0, 0] == float("inf") and torch.isfinite(scales[1]).all()
+    assert got[0, 3].isnan() and (got[0, :3] == 0).all() and (got[0, 4:first] == 0).all() and (got[0, first:] == 448).all()
+    assert torch.isfinite(got[1]).all() and (got[1, :3] == 448).all() and (got[1, 4:] == 448).all()
