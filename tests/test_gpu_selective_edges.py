@@ -37,4 +37,5 @@ def test_norm_of_outputs_past_fp32(gdn, group):  # noqa: F811
     got, first = q.float(), group or 256
     assert scales[0, 0] == float("inf") and torch.isfinite(scales[1]).all()
     assert got[0, 3].isnan() and (got[0, :3] == 0).all() and (got[0, 4:first] == 0).all() and (got[0, first:] == 448).all()
-    assert torch.isfinite(got[1]).all() and (got[1, :3] == 448).all() and (got[1, 4:] == 448).all()
+    # 1e-30 times 3e38 is 3e8, beside which 1 is below half of the least value, 2^-10
+    assert got[1, 3] == 448 and (got[1, :3] == 0).all() and (got[1, 4:first] == 0).all() and (got[1, first:] == 448).all()
