@@ -590,14 +590,16 @@ typedef struct gdn_ssm {
  * Positions past seq_lens are not read and their rows of y are left unchanged; a request of length
  * 0 changes nothing. A length outside [0, T] skips the request with GDN_STATUS_BAD_LEN.
  * workspace: gdn_ssm_workspace() bytes, 16-byte aligned (NULL where that is 0); its contents need
- * no care, but two calls that may run at the same time need one each.
+ * no care, but two calls that may run at the same time need one each. A call that scans its prompts
+ * whole, as it does where there are many or they are short, does not look at it.
  */
 int gdn_ssm_scan(const gdn_ssm *ssm, void *workspace, size_t workspace_bytes, int32_t *status, void *stream);
 
 /* gdn_ssm_step -- the same for one token of every request (num_tokens = 1, seq_lens NULL). */
 int gdn_ssm_step(const gdn_ssm *ssm, int32_t *status, void *stream);
 
-/* Bytes of workspace for a gdn_ssm_scan of these sizes (0 is an answer). Host only. */
+/* Bytes of workspace for every gdn_ssm_scan of these channels and states with no more requests and
+ * positions than these (0 is an answer): a program allocates once, for its largest. Host only. */
 int gdn_ssm_workspace(int32_t batch, int32_t num_tokens, int32_t channels, int32_t state_size, size_t *bytes);
 
 #ifdef __cplusplus

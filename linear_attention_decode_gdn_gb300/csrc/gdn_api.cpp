@@ -672,7 +672,7 @@ int gdn_causal_conv(const gdn_conv* conv, int32_t* status, void* stream) {
 int gdn_ssm_scan(const gdn_ssm* ssm, void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
   if (int rc = check_ssm(ssm)) return rc;
   if (ssm->batch == 0 || ssm->num_tokens == 0) return GDN_OK;
-  const size_t need = gdn::ssm_workspace_bytes(ssm->batch, ssm->num_tokens, ssm->channels, ssm->state_size);
+  const size_t need = gdn::ssm_scan_in_parts(*ssm) ? gdn::ssm_workspace_bytes(ssm->batch, ssm->num_tokens, ssm->channels, ssm->state_size) : 0;
   if (workspace_bytes < need || (need > 0 && workspace == nullptr))
     return fail(GDN_ERR_INVALID_ARG, "workspace of %zu bytes, %zu are needed (gdn_ssm_workspace)", workspace == nullptr ? 0 : workspace_bytes, need);
   if (need > 0 && !aligned16(workspace)) return fail(GDN_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");

@@ -28,6 +28,7 @@ struct ConvParams {
 cudaError_t launch_add_rms_norm(const gdn_norm& p, cudaStream_t stream);
 cudaError_t launch_causal_conv(const ConvParams& p, cudaStream_t stream);
 size_t ssm_workspace_bytes(int32_t batch, int32_t tokens, int32_t channels, int32_t state_size);
+bool ssm_scan_in_parts(const gdn_ssm& s);  // whether the call uses its workspace
 cudaError_t launch_ssm_scan(const SsmParams& p, void* workspace, cudaStream_t stream);
 cudaError_t launch_ssm_step(const SsmParams& p, cudaStream_t stream);
 

@@ -402,10 +402,20 @@ struct Cut {
   int32_t parts, part;
   int32_t own;  // channels of a thread
 };
-Cut cut_of(int32_t batch, int32_t tokens, int32_t channels, int32_t state_size, bool ragged) {
-  constexpr int32_t kShortest = 32, kRound = 8, kQuarters = kSms * 4, kRounds = 4;
+constexpr int32_t kShortest = 32, kRounds = 4;
+constexpr int64_t kResident = kSms * kCtas * kWarps;  // warps of a full GPU
+int64_t warps_of(int64_t batch, int32_t channels, int32_t state_size) {
   const int32_t of_warp = 512 / state_size;  // channels
-  const int64_t warps = static_cast<int64_t>(batch) * ((channels + of_warp - 1) / of_warp);
+  return batch * ((channels + of_warp - 1) / of_warp);
+}
+// of one prompt
+int64_t most_parts(int32_t tokens) {
+  const int64_t root = static_cast<int64_t>(std::sqrt(static_cast<double>(tokens))), whole = (tokens + kShortest - 1) / kShortest;
+  return root < whole ? root : whole;
+}
+Cut cut_of(int32_t batch, int32_t tokens, int32_t channels, int32_t state_size, bool ragged) {
+  constexpr int32_t kRound = 8, kQuarters = kSms * 4;
+  const int64_t warps = warps_of(batch, channels, state_size);
   auto position = [](int64_t all_warps) {  // us
     const int64_t shared = (all_warps + kQuarters - 1) / kQuarters;
     return shared <= 1 ? 0.18 : shared <= 2 ? 0.225 : 0.09 * static_cast<double>(shared);
@@ -418,9 +428,9 @@ Cut cut_of(int32_t batch, int32_t tokens, int32_t channels, int32_t state_size, 
   double least = 2.5 + tokens * position(warps);
   const double took_one = 2.5 + tokens * position_of_one(2 * warps);
   if (state_size < 64 && took_one < least) least = took_one, best.own = 1;
-  const int64_t most = static_cast<int64_t>(std::sqrt(static_cast<double>(tokens)));
+  const int64_t most = most_parts(tokens);
   for (int rounds = 1; rounds <= kRounds; ++rounds) {
-    int64_t parts = static_cast<int64_t>(kSms) * kCtas * kWarps * rounds / warps;
+    int64_t parts = kResident * rounds / warps;
     if (parts > most) parts = most;
     if (parts < 2) continue;
     int64_t part = (tokens + parts - 1) / parts;
@@ -482,15 +492,19 @@ cudaError_t launch_type(const SsmParams& p, void* workspace, cudaStream_t stream
 
 }  // namespace
 
+// What every call of these channels and states needs that has no more requests and positions, so that a
+// buffer of the largest serves all: prompts have at most most_parts() parts each and, as cuts fill the
+// GPU at most kRounds times, all of them together at most so many as there is room for. Of n parts there
+// are the states before them and after all but the last, and as many sums of steps.
 size_t ssm_workspace_bytes(int32_t batch, int32_t tokens, int32_t channels, int32_t state_size) {
-  if (batch == 0 || tokens == 0) return 0;
-  size_t most = 0;
-  for (bool ragged : {false, true}) {
-    const size_t parts = static_cast<size_t>(cut_of(batch, tokens, channels, state_size, ragged).parts);
-    const size_t bytes = parts > 1 ? static_cast<size_t>(batch) * channels * (parts * state_size + parts - 1) * sizeof(float) : 0;
-    if (bytes > most) most = bytes;
-  }
-  return most;
+  const int64_t each = most_parts(tokens), all = kResident * kRounds / warps_of(1, channels, state_size);
+  if (each < 2 || all < 2) return 0;
+  const int64_t parts = batch * each < all ? batch * each : all;
+  return static_cast<size_t>(parts) * channels * (state_size + 1) * sizeof(float);
+}
+
+bool ssm_scan_in_parts(const gdn_ssm& s) {
+  return cut_of(s.batch, s.num_tokens, s.channels, s.state_size, s.seq_lens != nullptr).parts > 1;
 }
 
 cudaError_t launch_ssm_scan(const SsmParams& given, void* workspace, cudaStream_t stream) {

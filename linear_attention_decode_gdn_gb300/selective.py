@@ -133,7 +133,7 @@ def causal_conv(x, weight, pool, slot, o, *, bias=None, silu=True, seq_lens=None
 
 
 def ssm_workspace_bytes(batch: int, num_tokens: int, channels: int, state_size: int) -> int:
-    """Bytes of workspace that ssm_scan needs."""
+    """Bytes of workspace for every ssm_scan of these channels and states with no more requests and positions."""
     out = ctypes.c_size_t()
     check(_abi.load().gdn_ssm_workspace(batch, num_tokens, channels, state_size, ctypes.byref(out)), "gdn_ssm_workspace")
     return out.value

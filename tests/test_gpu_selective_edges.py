@@ -3,7 +3,7 @@ to a border, states that grow."""
 import pytest
 import torch
 
-from test_gpu_selective import BF16, E4M3, FP32, gdn, gen, ints, randn  # noqa: F401
+from test_gpu_selective import BF16, E4M3, FP32, Layer, gdn, gen, randn  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +39,30 @@ def test_norm_of_outputs_past_fp32(gdn, group):  # noqa: F811
     assert got[0, 3].isnan() and (got[0, :3] == 0).all() and (got[0, 4:first] == 0).all() and (got[0, first:] == 448).all()
     # 1e-30 times 3e38 is 3e8, beside which 1 is below half of the least value, 2^-10
     assert got[1, 3] == 448 and (got[1, :3] == 0).all() and (got[1, 4:first] == 0).all() and (got[1, first:] == 448).all()
+
+
+# ---- recurrence -------------------------------------------------------------------------------------
+def test_one_workspace_for_all_admissions(gdn):  # noqa: F811
+    """A buffer of the largest batch serves smaller ones, which are cut into more parts, and none writes past it."""
+    D, N, most = 512, 16, (48, 700)
+    size = gdn.ssm_workspace_bytes(*most, D, N)
+    room = torch.full((size + 4096,), 77, dtype=torch.uint8, device="cuda")
+    for i, (B, T, lens) in enumerate([(48, 700, None), (4, 700, None), (1, 700, None), (16, 512, [512, 3] * 8), (3, 100, None), (1, 64, [64]), (2, 20, None),
+                                      (48, 700, [700 - 14 * j for j in range(48)])]):
+        layer, alone = (Layer(gdn, B, T, D, N, kind=(BF16, FP32)[i % 2], lens=lens, seed=i) for _ in range(2))
+        assert alone.workspace.numel() <= max(size, 16)
+        alone.call()
+        layer.workspace = room[:size]
+        layer.call()
+        torch.cuda.synchronize()
+        assert torch.equal(layer.y, alone.y) and torch.equal(layer.state, alone.state) and (room[size:] == 77).all()
+
+
+def test_scans_of_whole_prompts_need_no_workspace(gdn):  # noqa: F811
+    for B, T, D in ((2, 20, 64), (64, 300, 4096)):
+        layer, alone = (Layer(gdn, B, T, D, 16, seed=4) for _ in range(2))
+        alone.call()
+        layer.workspace = None
+        layer.call()
+        torch.cuda.synchronize()
+        assert torch.equal(layer.y, alone.y) and torch.equal(layer.state, alone.state)
