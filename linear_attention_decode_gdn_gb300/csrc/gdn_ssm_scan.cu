@@ -345,6 +345,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) gdn_ssm_scan_kernel(const 
   }
 }
 
+// A state after a part. The decays of a part may pass fp32 together (a > 0) where none does by itself:
+// a state of zero stays zero under them.
+__device__ __forceinline__ float joined(float x, float h, float end) { return h == 0.0f ? end : fmaf(ex2(x), h, end); }
+
 // Four states a thread, several parts' loads in flight.
 constexpr int kJoinThreads = 128, kJoinAhead = 8;
 __global__ void __launch_bounds__(kJoinThreads) gdn_ssm_join_kernel(const ScanParams p) {
@@ -374,8 +378,8 @@ __global__ void __launch_bounds__(kJoinThreads) gdn_ssm_join_kernel(const ScanPa
 #pragma unroll
     for (int j = 0; j < kJoinAhead; ++j) {
       if (j0 + j >= parts) break;
-      h = make_float4(fmaf(ex2(t[j] * a.x), h.x, e[j].x), fmaf(ex2(t[j] * a.y), h.y, e[j].y), fmaf(ex2(t[j] * a.z), h.z, e[j].z),
-                      fmaf(ex2(t[j] * a.w), h.w, e[j].w));
+      h = make_float4(joined(t[j] * a.x, h.x, e[j].x), joined(t[j] * a.y, h.y, e[j].y), joined(t[j] * a.z, h.z, e[j].z),
+                      joined(t[j] * a.w, h.w, e[j].w));
       *reinterpret_cast<float4*>(end + (j0 + j) * states) = h;
     }
   }

@@ -3,7 +3,7 @@ to a border, states that grow."""
 import pytest
 import torch
 
-from test_gpu_selective import BF16, E4M3, FP32, Layer, gdn, gen, randn  # noqa: F401
+from test_gpu_selective import BF16, E4M3, FP32, Layer, gdn, gen, ints, randn  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +66,24 @@ def test_scans_of_whole_prompts_need_no_workspace(gdn):  # noqa: F811
         layer.call()
         torch.cuda.synchronize()
         assert torch.equal(layer.y, alone.y) and torch.equal(layer.state, alone.state)
+
+
+@pytest.mark.parametrize("N", [8, 16, 32, 64])
+def test_scan_of_states_that_grow_keeps_zeros(gdn, N):  # noqa: F811
+    """With a > 0 the product of a part's decays passes fp32 (e^4 a position), and a state of zero stays zero."""
+    B, T, D = 1, 600, 64
+    u = torch.zeros(B, T, D, device="cuda")
+    u[:, T - 3:] = randn(gen(N), B, 3, D)
+    dt, a = torch.full_like(u, 2.0), torch.full((D, N), 2.0, device="cuda")
+    b, c = randn(gen(N + 1), B, T, 1, N), randn(gen(N + 2), B, T, 1, N)
+    state, y = torch.zeros(2, D, N, device="cuda"), torch.full_like(u, 7.0)
+    workspace = torch.empty(max(16, gdn.ssm_workspace_bytes(B, T, D, N)), dtype=torch.uint8, device="cuda")
+    gdn.ssm_scan(u, dt, a, b, c, state, ints([1]), y, workspace, softplus=False)
+    h = torch.zeros(D, N, dtype=torch.float64, device="cuda")
+    assert (y[:, :T - 3] == 0).all()
+    for t in range(T - 3, T):
+        h = h * torch.exp(torch.tensor(4.0, dtype=torch.float64)) + 2 * u[0, t].double()[:, None] * b[0, t].double()
+        want = (h * c[0, t].double()).sum(-1)
+        size = (h.abs() * c[0, t].double().abs()).sum(-1)  # every factor and sum is off by some roundings of what it adds to
+        assert ((y[0, t].double() - want).abs() <= size * 2.0 ** -18).all()
+    assert ((state[1].double() - h).abs() <= 2.0 ** -18 * h.abs().max()).all()
