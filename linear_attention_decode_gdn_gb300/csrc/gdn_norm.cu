@@ -160,7 +160,7 @@ cudaError_t launch_row(const gdn_norm& p, cudaStream_t stream) {
   const int vecs = p.width / 8;
   auto threads = [&](int v) { return static_cast<unsigned>(((vecs + v - 1) / v + 31) / 32 * 32); };
   if (vecs <= 32) {
-    const unsigned grid = static_cast<unsigned>((p.rows + kRowWarps - 1) / kRowWarps);
+    const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(p.rows) + kRowWarps - 1) / kRowWarps);
     return launch_overlapped(gdn_norm_kernel<XB, RB, OT, 1, true>, p, dim3(grid), kRowWarps * 32, 0, 1u, stream);
   }
   if (vecs >= 512 && static_cast<int64_t>(p.rows) * vecs >= kManyVecs)

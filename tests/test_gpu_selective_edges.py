@@ -41,6 +41,18 @@ def test_norm_of_outputs_past_fp32(gdn, group):  # noqa: F811
     assert got[1, 3] == 448 and (got[1, :3] == 0).all() and (got[1, 4:first] == 0).all() and (got[1, first:] == 448).all()
 
 
+def test_norm_of_the_most_rows(gdn):  # noqa: F811
+    """2^31 - 1 rows, the most that a call can name: four of them a CTA, counted past 32 bits."""
+    rows = 2 ** 31 - 1
+    x = randn(gen(9), 1, 8, dtype=BF16)
+    q, scales = torch.zeros(rows, 8, dtype=E4M3, device="cuda"), torch.zeros(rows, dtype=FP32, device="cuda")
+    gdn.add_rms_norm(x.expand(rows, 8), q, scales=scales)
+    one, scale = torch.empty(1, 8, dtype=E4M3, device="cuda"), torch.empty(1, device="cuda")
+    gdn.add_rms_norm(x, one, scales=scale)
+    whole, want = q.view(torch.int64).flatten(), one.view(torch.int64).flatten()
+    assert all((part == want).all() for part in whole.split(2 ** 28)) and all((part == scale).all() for part in scales.split(2 ** 28))
+
+
 # ---- recurrence -------------------------------------------------------------------------------------
 def test_one_workspace_for_all_admissions(gdn):  # noqa: F811
     """A buffer of the largest batch serves smaller ones, which are cut into more parts, and none writes past it."""
