@@ -497,8 +497,9 @@ int gdn_attn_workspace(const gdn_paged_kv *kv, int32_t batch, int32_t num_tokens
  *   gdn_ssm_step       one new token of every request.
  *
  * The conventions at the top of this file hold: slot-indexed pools, padding, status bits, streams,
- * no allocation. Outputs overlap no input of their call, but for the pools and the residual, which
- * are updated in place. A new request begins with zeros in its rows of the pools. All sums, states,
+ * no allocation. What a call writes may be an input of the same type and shape, row after row: the
+ * norm's o its x, the recurrence's y its u, dt or z; x may be the residual. Any other memory that a call
+ * both writes and reads, but for the pools and the residual, is refused (GDN_ERR_INVALID_ARG). A new request begins with zeros in its rows of the pools. All sums, states,
  * steps and norms are fp32. A call has at most 2^24 channels and 2^30 positions (batch * num_tokens).
  */
 #define GDN_TYPE_BF16 0

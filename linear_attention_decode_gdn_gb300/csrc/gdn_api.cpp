@@ -3,6 +3,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 
 #include <cuda_runtime_api.h>
 
@@ -309,6 +310,70 @@ bool rows_ok(const void* p, const int64_t* strides, const int32_t (&extents)[N],
   return aligned16(p) && strides_ok(strides, extents, bf16 ? 8 : 4);
 }
 
+// Memory of one tensor of a call: rows of `row` bytes, `extents` of them at `strides` bytes, the widest first.
+struct Memory {
+  const char* name;
+  uintptr_t at, end;
+  size_t row;
+  bool dense = true;  // row after row
+  int dims = 0;
+  size_t strides[3], extents[3];
+};
+Memory whole(const char* name, const void* p, size_t bytes) {
+  Memory m;
+  m.name = name, m.row = bytes;
+  m.at = reinterpret_cast<uintptr_t>(p), m.end = p == nullptr ? m.at : m.at + bytes;
+  return m;
+}
+// Rows of `width` elements of `size` bytes, extents and strides as the call gives them.
+template <int N>
+Memory rows_of(const char* name, const void* p, size_t size, size_t width, const int64_t* strides, const int32_t (&extents)[N]) {
+  Memory m = whole(name, p, size * width);
+  if (p == nullptr) return m;
+  size_t dense = width;
+  for (int i = N - 1; i >= 0; --i) {
+    const size_t stride = strides[i] * size, extent = extents[i];
+    if (extent == 1) continue;
+    m.dense = m.dense && static_cast<size_t>(strides[i]) == dense;
+    dense *= extent;
+    m.end += (extent - 1) * stride;
+    int k = m.dims++;
+    for (; k > 0 && m.strides[k - 1] < stride; --k) m.strides[k] = m.strides[k - 1], m.extents[k] = m.extents[k - 1];
+    m.strides[k] = stride, m.extents[k] = extent;
+  }
+  return m;
+}
+// Whether a row of m meets [lo, hi), of the part of m that begins at `at` and has the dimensions from `dim` on.
+// Of a dimension's parts those that reach into [lo, hi) are gone into. The first that lies in it whole
+// ends the search, so that two at most, at its ends, are gone into for nothing.
+bool meets(const Memory& m, uintptr_t lo, uintptr_t hi, int dim, uintptr_t at) {
+  if (dim == m.dims) return at < hi && at + m.row > lo;
+  size_t inner = m.row;  // bytes that one of the dimension's parts spans
+  for (int i = dim + 1; i < m.dims; ++i) inner += (m.extents[i] - 1) * m.strides[i];
+  const size_t step = m.strides[dim], last = step == 0 ? 0 : m.extents[dim] - 1;
+  for (size_t i = step > 0 && lo >= at + inner ? (lo - at - inner) / step + 1 : 0; i <= last && at + i * step < hi; ++i)
+    if (meets(m, lo, hi, dim + 1, at + i * step)) return true;
+  return false;
+}
+bool meets(const Memory& m, uintptr_t lo, uintptr_t hi) {
+  return m.at < hi && m.end > lo && m.at < m.end && lo < hi && meets(m, lo, hi, 0, m.at);
+}
+
+// A tensor that lies in one piece, against others of its call. Of those with `in_place` it may be the very
+// same: the kernel reads an element only where, and before, it writes there.
+struct Other {
+  const Memory& m;
+  bool in_place = false;
+};
+int check_apart(const Memory& out, std::initializer_list<Other> others) {
+  for (const Other& x : others) {
+    if (!meets(x.m, out.at, out.end)) continue;
+    if (x.in_place && x.m.dense && x.m.at == out.at && x.m.end == out.end) continue;
+    return fail(GDN_ERR_INVALID_ARG, "%s overlaps %s", out.name, x.m.name);
+  }
+  return GDN_OK;
+}
+
 int check_ssm_sizes(int32_t batch, int32_t num_tokens, int32_t channels, int32_t state_size) {
   if (batch < 0 || num_tokens < 0 || channels <= 0)
     return fail(GDN_ERR_INVALID_ARG, "batch and num_tokens must be >= 0, channels > 0");
@@ -342,6 +407,53 @@ int check_ssm(const gdn_ssm* s) {
   if (!aligned16(s->a) || !aligned16(s->skip) || !aligned16(s->dt_bias) || !aligned16(s->state) || !aligned16(s->y))
     return fail(GDN_ERR_UNSUPPORTED, "a, skip, dt_bias, state and y must be 16-byte aligned");
   return GDN_OK;
+}
+
+// Last of all: what a call writes shares no memory with what it reads.
+int check_norm_apart(const gdn_norm& n) {
+  const int32_t extents[1] = {n.rows};
+  const size_t rows = n.rows, width = n.width, wide = n.group != 0 ? n.group : width;
+  auto size = [](int type) -> size_t { return type == GDN_TYPE_FP32 ? 4 : type == GDN_TYPE_BF16 ? 2 : 1; };
+  const Memory o = whole("o", n.o, rows * width * size(n.o_type)), weight = whole("weight", n.weight, width * 4);
+  const Memory scales = whole("scales", n.o_type == GDN_TYPE_E4M3 ? n.scales : nullptr, rows * ((width + wide - 1) / wide) * 4);
+  const Memory x = rows_of("x", n.x, size(n.x_type), width, &n.x_stride, extents);
+  const Memory residual = rows_of("residual", n.residual, size(n.residual_type), width, &n.residual_stride, extents);
+  if (int rc = check_apart(o, {{x, n.x_type == n.o_type}, {residual}, {weight}, {scales}})) return rc;
+  if (int rc = check_apart(scales, {{x}, {residual}, {weight}})) return rc;
+  if (int rc = check_apart(weight, {{residual}})) return rc;
+  // x may be the residual itself. Rows of both at one distance meet in the first of either or nowhere; at
+  // two distances each of x is looked at, which ends soon, as such rows meet soon.
+  if (n.residual == nullptr || (x.at == residual.at && x.row == residual.row && (n.rows == 1 || n.x_stride == n.residual_stride)))
+    return GDN_OK;
+  bool met = meets(residual, x.at, x.at + x.row) || meets(x, residual.at, residual.at + residual.row);
+  if (!met && x.dims > 0 && x.strides[0] != residual.strides[0] && meets(x, residual.at, residual.end))
+    for (size_t i = 1; i < rows && !met; ++i) met = meets(residual, x.at + i * x.strides[0], x.at + i * x.strides[0] + x.row);
+  return met ? fail(GDN_ERR_INVALID_ARG, "residual overlaps x") : GDN_OK;
+}
+
+int check_conv_apart(const gdn_conv& c) {
+  const int32_t extents[2] = {c.batch, c.num_tokens};
+  const size_t size = (c.flags & GDN_QKV_BF16) != 0u ? 2 : 4, D = c.channels, B = c.batch;
+  const Memory x = rows_of("x", c.x, size, D, c.x_strides, extents), w = whole("w", c.w, D * 16);
+  const Memory bias = whole("bias", c.bias, D * 4);
+  const Memory slot = whole("slot", c.slot, B * 4), lens = whole("seq_lens", c.seq_lens, B * 4);
+  const Memory pool = whole("pool", c.pool, c.num_slots * D * 3 * size), o = whole("o", c.o, B * c.num_tokens * D * size);
+  if (int rc = check_apart(o, {{x}, {w}, {bias}, {pool}, {slot}, {lens}})) return rc;
+  return check_apart(pool, {{x}, {w}, {bias}, {slot}, {lens}});
+}
+
+int check_ssm_apart(const gdn_ssm& s, const void* workspace, size_t workspace_bytes) {
+  const int32_t two[2] = {s.batch, s.num_tokens}, three[3] = {s.batch, s.num_tokens, s.num_groups};
+  const size_t size = (s.flags & GDN_QKV_BF16) != 0u ? 2 : 4, D = s.channels, N = s.state_size, B = s.batch;
+  const Memory u = rows_of("u", s.u, size, D, s.u_strides, two), dt = rows_of("dt", s.dt, size, D, s.dt_strides, two);
+  const Memory z = rows_of("z", s.z, size, D, s.z_strides, two), b = rows_of("b", s.b, size, N, s.b_strides, three);
+  const Memory c = rows_of("c", s.c, size, N, s.c_strides, three), a = whole("a", s.a, D * N * 4), skip = whole("skip", s.skip, D * 4);
+  const Memory bias = whole("dt_bias", s.dt_bias, D * 4), slot = whole("slot", s.slot, B * 4), lens = whole("seq_lens", s.seq_lens, B * 4);
+  const Memory state = whole("state", s.state, s.num_slots * D * N * 4), y = whole("y", s.y, B * s.num_tokens * D * size);
+  const Memory scratch = whole("workspace", workspace, workspace_bytes);
+  if (int rc = check_apart(y, {{u, true}, {dt, true}, {z, true}, {b}, {c}, {a}, {skip}, {bias}, {slot}, {lens}, {state}})) return rc;
+  if (int rc = check_apart(state, {{u}, {dt}, {z}, {b}, {c}, {a}, {skip}, {bias}, {slot}, {lens}})) return rc;
+  return check_apart(scratch, {{u}, {dt}, {z}, {b}, {c}, {a}, {skip}, {bias}, {slot}, {lens}, {state}, {y}});
 }
 
 }  // namespace
@@ -643,6 +755,7 @@ int gdn_add_rms_norm(const gdn_norm* norm, void* stream) {
     return fail(GDN_ERR_UNSUPPORTED, "x, residual, weight and o must be 16-byte aligned, with row strides >= 0 that are multiples of 16 bytes");
   if (n.residual != nullptr && n.rows > 1 && n.residual_stride < n.width)
     return fail(GDN_ERR_INVALID_ARG, "rows of residual overlap");
+  if (int rc = check_norm_apart(n)) return rc;
   return launched(gdn::launch_add_rms_norm(n, static_cast<cudaStream_t>(stream)), "gdn_add_rms_norm");
 }
 
@@ -665,7 +778,7 @@ int gdn_causal_conv(const gdn_conv* conv, int32_t* status, void* stream) {
     return fail(GDN_ERR_UNSUPPORTED, "x must be 16-byte aligned, with strides >= 0 that are multiples of 16 bytes");
   if (!aligned16(c.w) || !aligned16(c.bias) || !aligned16(c.pool) || !aligned16(c.o))
     return fail(GDN_ERR_UNSUPPORTED, "w, bias, pool and o must be 16-byte aligned");
-  if (c.o == c.x) return fail(GDN_ERR_INVALID_ARG, "o overlaps x");
+  if (int rc = check_conv_apart(c)) return rc;
   return launched(gdn::launch_causal_conv({c, status}, static_cast<cudaStream_t>(stream)), "gdn_causal_conv");
 }
 
@@ -676,6 +789,7 @@ int gdn_ssm_scan(const gdn_ssm* ssm, void* workspace, size_t workspace_bytes, in
   if (workspace_bytes < need || (need > 0 && workspace == nullptr))
     return fail(GDN_ERR_INVALID_ARG, "workspace of %zu bytes, %zu are needed (gdn_ssm_workspace)", workspace == nullptr ? 0 : workspace_bytes, need);
   if (need > 0 && !aligned16(workspace)) return fail(GDN_ERR_UNSUPPORTED, "workspace must be 16-byte aligned");
+  if (int rc = check_ssm_apart(*ssm, workspace, need)) return rc;
   return launched(gdn::launch_ssm_scan({*ssm, status}, workspace, static_cast<cudaStream_t>(stream)), "gdn_ssm_scan");
 }
 
@@ -684,6 +798,7 @@ int gdn_ssm_step(const gdn_ssm* ssm, int32_t* status, void* stream) {
   if (ssm->num_tokens != 1 || ssm->seq_lens != nullptr)
     return fail(GDN_ERR_INVALID_ARG, "gdn_ssm_step takes one token of every request: num_tokens 1, seq_lens NULL");
   if (ssm->batch == 0) return GDN_OK;
+  if (int rc = check_ssm_apart(*ssm, nullptr, 0)) return rc;
   return launched(gdn::launch_ssm_step({*ssm, status}, static_cast<cudaStream_t>(stream)), "gdn_ssm_step");
 }
 

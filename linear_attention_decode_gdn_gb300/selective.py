@@ -3,7 +3,8 @@
 As in ``paged``: each function checks what the pointers cannot show (types, shapes, strides,
 devices), packs them into the C struct and calls the matching ``gdn_*`` function of libgdn on the
 current stream. All tensors of a call live on the current device. Where a tensor is wrong the call
-raises ``ValueError`` before anything is launched; what libgdn refuses raises ``GDNError``.
+raises ``ValueError`` before anything is launched; what libgdn refuses raises ``GDNError``: outputs
+that overlap inputs among it, but for o in place of x (norm) and y in place of u, dt or z (scan, step).
 """
 from __future__ import annotations
 

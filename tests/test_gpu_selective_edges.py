@@ -99,3 +99,66 @@ def test_scan_of_states_that_grow_keeps_zeros(gdn, N):  # noqa: F811
         size = (h.abs() * c[0, t].double().abs()).sum(-1)  # every factor and sum is off by some roundings of what it adds to
         assert ((y[0, t].double() - want).abs() <= size * 2.0 ** -18).all()
     assert ((state[1].double() - h).abs() <= 2.0 ** -18 * h.abs().max()).all()
+
+
+# ---- outputs in place of inputs -------------------------------------------------------------------------
+@pytest.mark.parametrize("rows,width", [(1, 2048), (5, 256), (300, 4096), (4200, 4104)])
+@pytest.mark.parametrize("kind", [BF16, FP32])
+def test_norm_in_place(gdn, rows, width, kind):  # noqa: F811
+    """The bits of separate tensors: o in x, x the residual itself, x and residual side by side in rows of both."""
+    g = gen(rows)
+    x, old, weight = randn(g, rows, width, dtype=kind), randn(g, rows, width, dtype=kind), randn(g, width)
+    want, sums = torch.empty_like(x), old.clone()
+    gdn.add_rms_norm(x, want, residual=sums, weight=weight)
+    o, residual = x.clone(), old.clone()
+    gdn.add_rms_norm(o, o, residual=residual, weight=weight)
+    assert torch.equal(o, want) and torch.equal(residual, sums)
+    both = torch.cat([x, old], 1)
+    o = torch.empty_like(x)
+    gdn.add_rms_norm(both[:, :width], o, residual=both[:, width:], weight=weight)
+    assert torch.equal(o, want) and torch.equal(both[:, :width], x) and torch.equal(both[:, width:], sums)
+    sums = x.clone()
+    gdn.add_rms_norm(x, want, residual=sums, weight=weight)
+    gdn.add_rms_norm(x, o, residual=x, weight=weight)
+    assert torch.equal(o, want) and torch.equal(x, sums)
+
+
+@pytest.mark.parametrize("B,T,D,lens", [(3, 1, 264, None), (2, 21, 64, None), (2, 900, 264, None), (3, 700, 64, [700, 0, 333])])
+def test_recurrence_in_place(gdn, B, T, D, lens):  # noqa: F811
+    for name in ("u", "dt", "z"):
+        first, second = (Layer(gdn, B, T, D, 16, kind=BF16, lens=lens, seed=T) for _ in range(2))
+        for layer in (first, second):
+            layer.z = layer.z.contiguous()
+        first.y = getattr(first, name).clone()
+        second.y = getattr(second, name)
+        first.call(), second.call()
+        torch.cuda.synchronize()
+        assert torch.equal(first.y.view(torch.int16), second.y.view(torch.int16)) and torch.equal(first.state, second.state)  # NaN past a prompt's end
+
+
+def test_step_in_place(gdn):  # noqa: F811
+    B, D, N = 300, 264, 16
+    for name in ("u", "dt", "z"):
+        g = gen(5)
+        x = {k: randn(g, B, D, dtype=BF16) for k in ("u", "dt", "z")}
+        a, b, c, state = -torch.rand(D, N, generator=g, device="cuda"), randn(g, B, 1, N, dtype=BF16), randn(g, B, 1, N, dtype=BF16), randn(g, B, D, N)
+        slot = torch.arange(B, dtype=torch.int32, device="cuda")
+        y, again = torch.empty_like(x["u"]), state.clone()
+        gdn.ssm_step(x["u"], x["dt"], a, b, c, state, slot, y, z=x["z"])
+        gdn.ssm_step(x["u"], x["dt"], a, b, c, again, slot, x[name], z=x["z"])
+        assert torch.equal(x[name], y) and torch.equal(again, state)
+
+
+def test_outputs_between_the_rows_of_inputs(gdn):  # noqa: F811
+    """Memory that rows of an input leave between them is no part of it."""
+    g = gen(6)
+    T, D = 40, 64
+    room = randn(g, 2, 3 * T * D, dtype=BF16)
+    x, o = room[:, :T * D].unflatten(1, (T, D)), room[0, T * D:].view(2, T, D)
+    w, pool = randn(g, D, 4), randn(g, 2, D, 3, dtype=BF16)
+    want, rows = torch.empty(2, T, D, dtype=BF16, device="cuda"), pool.clone()
+    gdn.causal_conv(x.contiguous(), w, rows, ints([1, 0]), want)
+    gdn.causal_conv(x, w, pool, ints([1, 0]), o)
+    assert torch.equal(o, want) and torch.equal(pool, rows)
+    with pytest.raises(gdn.GDNError, match="overlaps"):
+        gdn.causal_conv(x, w, pool, ints([1, 0]), room.view(-1)[T * D + 8:3 * T * D + 8].view(2, T, D))  # its last row meets the second request's first
