@@ -121,9 +121,9 @@ def causal_conv(x, weight, pool, slot, o, *, bias=None, silu=True, seq_lens=None
         ok = bias.dtype is _FP32 and bias.dim() == 1 and bias.numel() == channels and bias.is_contiguous() and bias.get_device() == at
         bias_ptr = bias.data_ptr()
     if not ok:
-        channels = shape[-1]
-        _refuse(at, x, "x", (2, 3), (), ((weight, (channels, 4), _FP32, "weight"), (bias, (channels,), _FP32, "bias"),
-                                         (pool, (*rows[:1], channels, 3), dtype, "pool"), (o, shape, dtype, "o")))
+        last = shape[-1:]
+        _refuse(at, x, "x", (2, 3), (), ((weight, (*last, 4), _FP32, "weight"), (bias, last, _FP32, "bias"),
+                                         (pool, (*rows[:1], *last, 3), dtype, "pool"), (o, shape, dtype, "o")))
     rc = _abi.load().gdn_causal_conv(
         _pack_conv(batch, tokens, channels, rows[0], (_abi.QKV_BF16 if dtype is _BF16 else 0) | (_abi.CONV_SILU if silu else 0), x.data_ptr(),
                    x0, x1, weight.data_ptr(), bias_ptr, pool.data_ptr(), _ints(slot, batch, "slot", at),
@@ -142,8 +142,12 @@ def ssm_workspace_bytes(batch: int, num_tokens: int, channels: int, state_size: 
 
 def _refuse_ssm(dims, at, u, dt, a, b, c, state, y, z, skip, dt_bias):
     dtype, shape, narrow, pool = u.dtype, u.shape, b.shape, state.shape
-    if len(narrow) != len(shape) + 1 or len(pool) != 3:
-        raise ValueError(f"b: {len(shape) + 1} dimensions [.., groups, state size]; state: [slots, channels, state size]")
+    if len(shape) != dims:
+        _refuse(at, u, "u", (dims,), (), ())
+    if len(narrow) != dims + 1:
+        raise ValueError(f"b: {dims + 1} dimensions [.., groups, state size], got {tuple(narrow)}")
+    if len(pool) != 3:
+        raise ValueError(f"state: [slots, channels, state size], got {tuple(pool)}")
     few, channels, n = (*shape[:-1], *narrow[-2:]), shape[-1], narrow[-1]
     _refuse(at, u, "u", (dims,), ((dt, shape, dtype, "dt"), (z, shape, dtype, "z"), (b, few, dtype, "b"), (c, few, dtype, "c")),
             ((a, (channels, n), _FP32, "a"), (skip, (channels,), _FP32, "skip"), (dt_bias, (channels,), _FP32, "dt_bias"),
@@ -158,19 +162,22 @@ def _pack(dims, u, dt, a, b, c, state, slot, y, z, skip, dt_bias, softplus, seq_
         _refuse_ssm(dims, at, u, dt, a, b, c, state, y, z, skip, dt_bias)
     batch, channels, groups, n = shape[0], shape[-1], narrow[-2], narrow[-1]
     z_ptr = z0 = z1 = 0
-    if dims == 2:  # no stride between the tokens of one
-        tokens = 1
-        (u0, ul), (t0, tl), (b0, b2, bl), (c0, c2, cl) = u.stride(), dt.stride(), b.stride(), c.stride()
-        u1 = t1 = b1 = c1 = 0
-        ok = narrow[0] == batch
-        if z is not None:
-            z0, zl = z.stride()
-    else:
-        tokens = shape[1]
-        (u0, u1, ul), (t0, t1, tl), (b0, b1, b2, bl), (c0, c1, c2, cl) = u.stride(), dt.stride(), b.stride(), c.stride()
-        ok = narrow[0] == batch and narrow[1] == tokens
-        if z is not None:
-            z0, z1, zl = z.stride()
+    try:
+        if dims == 2:  # no stride between the tokens of one
+            tokens = 1
+            (u0, ul), (t0, tl), (b0, b2, bl), (c0, c2, cl) = u.stride(), dt.stride(), b.stride(), c.stride()
+            u1 = t1 = b1 = c1 = 0
+            ok = narrow[0] == batch
+            if z is not None:
+                z0, zl = z.stride()
+        else:
+            tokens = shape[1]
+            (u0, u1, ul), (t0, t1, tl), (b0, b1, b2, bl), (c0, c1, c2, cl) = u.stride(), dt.stride(), b.stride(), c.stride()
+            ok = narrow[0] == batch and narrow[1] == tokens
+            if z is not None:
+                z0, z1, zl = z.stride()
+    except ValueError:  # another number of dimensions
+        ok = False
     ok = (ok and ul == tl == bl == cl == 1 and dt.dtype is dtype and b.dtype is dtype and c.dtype is dtype and y.dtype is dtype
           and dt.shape == shape and c.shape == narrow and y.shape == shape and a.shape == (channels, n) and pool[1] == channels and pool[2] == n
           and a.dtype is _FP32 and state.dtype is _FP32 and y.is_contiguous() and a.is_contiguous() and state.is_contiguous()

@@ -5,7 +5,8 @@ import random
 
 import pytest
 
-from test_selective_host import BAD, FAKE, NO, conv, gdn, norm, ssm  # noqa: F401
+from test_paged_tensors import On
+from test_selective_host import BAD, FAKE, NO, calls, conv, gdn, norm, selective, ssm  # noqa: F401
 
 
 def test_a_workspace_of_the_largest_call_serves_all(gdn):  # noqa: F811
@@ -92,3 +93,17 @@ def test_recurrence_refuses_shared_memory(gdn):  # noqa: F811
     for name in names:
         assert lib.gdn_ssm_scan(ctypes.byref(ssm(gdn, **{**at, **far, **long})), at[name] - size + 16, size, None, None) == BAD, name
         assert b"workspace overlaps" in lib.gdn_last_error()
+
+
+# ---- the binding's errors ----------------------------------------------------------------------------------
+def test_operands_of_any_number_of_dimensions_are_refused_by_name(selective):  # noqa: F811
+    for call, tensors in calls(selective):
+        for name, t in tensors.items():
+            if name in ("slot", "seq_lens", "status", "workspace"):  # lists, of any dimensions
+                continue
+            for shape in ((), (8,), (2, 8), (2, 4, 8), (2, 4, 2, 8), (1, 2, 4, 2, 8)):
+                if shape == tuple(t.shape):
+                    continue
+                with pytest.raises(ValueError, match=r"^\w+: .*\[|^\w+: .*\("):  # the operand, and what it should be
+                    call({**tensors, name: On(shape, t.dtype)})
+    assert selective.lib.calls == 0
