@@ -141,12 +141,14 @@ class HybridDecoder:
         run = {"gdn": self._recurrent, "ssm": self._selective, "attn": self._attention, "latent": self._latent}
         self._plan(None, self.slots)
         self.residual.copy_(self.x)
-        gdn.add_rms_norm(self.x, self.normed)
-        for i, layer in enumerate(self.layers):
+        added = None  # what the layer before gives, not yet in the residual
+        for layer in self.layers:
+            gdn.add_rms_norm(self.x if added is None else added, self.normed, residual=None if added is None else self.residual)
             added = run[layer["kind"]](layer, self.normed) @ layer["out"]
-            if i + 1 < len(self.layers):
-                gdn.add_rms_norm(added, self.normed, residual=self.residual)
-        torch.add(self.residual, added, out=self.y)
+        if added is None:
+            self.y.copy_(self.residual)
+        else:
+            torch.add(self.residual, added, out=self.y)
 
     def capture(self):
         """Captures eager() (which has to have run once) for step()."""

@@ -1,5 +1,8 @@
 """The calls of selective state space layers at edges that the other tests leave out: quantised values next
 to a border, states that grow."""
+import importlib.util
+import os
+
 import pytest
 import torch
 
@@ -162,3 +165,20 @@ def test_outputs_between_the_rows_of_inputs(gdn):  # noqa: F811
     assert torch.equal(o, want) and torch.equal(pool, rows)
     with pytest.raises(gdn.GDNError, match="overlaps"):
         gdn.causal_conv(x, w, pool, ints([1, 0]), room.view(-1)[T * D + 8:3 * T * D + 8].view(2, T, D))  # its last row meets the second request's first
+
+
+# ---- the example's stack -----------------------------------------------------------------------------------
+@pytest.mark.parametrize("layers", [0, 1, 2, 5])
+def test_hybrid_stacks_of_any_depth(gdn, layers):  # noqa: F811
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "hybrid_decode.py")
+    spec = importlib.util.spec_from_file_location("hybrid_decode", path)
+    hybrid = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(hybrid)
+    model = hybrid.HybridDecoder(3, heads=2, heads_kv=1, layers=layers, max_len=128)
+    model.admit([5, 1, 64])
+    model.step()
+    model.capture()
+    model.step()
+    torch.cuda.synchronize()
+    assert model.status.item() == 0 and model.length.tolist() == [7, 3, 66] and torch.isfinite(model.y).all()
+    assert torch.equal(model.y, model.x) == (layers == 0)
