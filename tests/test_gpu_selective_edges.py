@@ -1,12 +1,12 @@
-"""The calls of selective state space layers at edges that the other tests leave out: quantised values next
-to a border, states that grow."""
+"""The calls of selective state space layers at edges that the other tests leave out: quantised values next to a
+border, single tokens that are not what they should be, states that grow, outputs in place of inputs."""
 import importlib.util
 import os
 
 import pytest
 import torch
 
-from test_gpu_selective import BF16, E4M3, FP32, Layer, gdn, gen, ints, randn  # noqa: F401
+from test_gpu_selective import BF16, E, E4M3, FP32, HALF, Layer, check_conv, gdn, gen, ints, randn  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -56,6 +56,28 @@ def test_norm_of_the_most_rows(gdn):  # noqa: F811
     assert all((part == want).all() for part in whole.split(2 ** 28)) and all((part == scale).all() for part in scales.split(2 ** 28))
 
 
+# ---- convolution of single tokens ---------------------------------------------------------------------
+# From 100000 vectors of eight channels on a thread takes four requests (323 x 2568 are 103683 vectors): the last
+# group of a batch may be shorter, and where rows are no multiple of 256 channels a warp's lanes are of several groups.
+@pytest.mark.parametrize("B,D", [(321, 4096), (322, 2568), (323, 4104), (513, 1560), (323, 2568), (3, 64), (5, 264)])
+@pytest.mark.parametrize("kind", [BF16, FP32])
+def test_conv_of_single_tokens(gdn, kind, B, D):  # noqa: F811
+    rows = list(range(B + 2))[::-1]
+    assert check_conv(gdn, B, 1, D, kind, seed=B) == 0
+    assert check_conv(gdn, B, 1, D, kind, slot=[-1 - i if i % 3 == 1 else rows[i] for i in range(B)], silu=False, wide=2) == 0
+    assert check_conv(gdn, B, 1, D, kind, lens=[i % 5 != 2 for i in range(B)], slot=rows[:B], bias=False) == 0
+    # what is wrong leaves its request alone and none of its group: the last request, the first, one in the middle
+    bad = [rows[i] for i in range(B)]
+    bad[-1], bad[0] = B + 2, 2 ** 31 - 1
+    assert check_conv(gdn, B, 1, D, kind, slot=bad) == gdn.STATUS_BAD_SLOT
+    lens = [1] * B
+    lens[-1], lens[B // 2] = 2, -1
+    assert check_conv(gdn, B, 1, D, kind, lens=lens, slot=rows[:B]) == gdn.STATUS_BAD_LEN
+    lens[0], bad[-1] = 0, -7
+    assert check_conv(gdn, B, 1, D, kind, lens=lens, slot=bad) == gdn.STATUS_BAD_SLOT | (gdn.STATUS_BAD_LEN if bad[B // 2] >= 0 else 0)
+    assert check_conv(gdn, B, 1, D, kind, lens=[2] * B, slot=[-1] * B) == 0
+
+
 # ---- recurrence -------------------------------------------------------------------------------------
 def test_one_workspace_for_all_admissions(gdn):  # noqa: F811
     """A buffer of the largest batch serves smaller ones, which are cut into more parts, and none writes past it."""
@@ -81,6 +103,72 @@ def test_scans_of_whole_prompts_need_no_workspace(gdn):  # noqa: F811
         layer.call()
         torch.cuda.synchronize()
         assert torch.equal(layer.y, alone.y) and torch.equal(layer.state, alone.state)
+
+
+class Exact(Layer):
+    """A Layer whose tolerances count what the kernels round, and nothing for joining parts where there are none."""
+
+    def want(self):
+        D, N, T = self.D, self.N, self.T
+        # A prompt of at most 32 positions is never cut. Of others the steps of a part are summed, each sum rounded.
+        joined = T * E if T > 32 else 0.0
+        live = [b for b in range(self.B) if 0 <= self.slot[b] < self.num_slots and 0 <= self.lens[b] <= T]
+        rows, lens = torch.tensor([self.slot[b] for b in live], device="cuda"), ints([self.lens[b] for b in live])
+        u, dt, b, c = (torch.nan_to_num(x[live].double()) for x in (self.u, self.dt, self.b, self.c))
+        x = dt + (0 if self.bias is None else self.bias.double())
+        # Its argument is off by a rounding of dt and one of the sum, over which softplus has a relative slope of at
+        # most 1 + |x|; its exponential, series or logarithm and their sum are off by 8 roundings.
+        s = torch.nn.functional.softplus(x, threshold=1e3) if self.softplus else x
+        ds = (9 + x.abs() + dt.abs()) * E if self.softplus else torch.full_like(x, E)
+        a, state, off = self.a.double(), self.state.double(), torch.zeros(self.state.shape, dtype=torch.float64, device="cuda")
+        h, err = state[rows].clone(), off[rows].clone()
+        y, off_y = torch.full((self.B, T, D), float("nan"), dtype=torch.float64, device="cuda"), torch.zeros(self.B, T, D, dtype=torch.float64, device="cuda")
+        for t in range(T):
+            on = (t < lens)[:, None]
+            st, dst, ut = s[:, t, :, None], ds[:, t, :, None], u[:, t, :, None]
+            bt, ct = (v[:, t].repeat_interleave(D // self.G, 1) for v in (b, c))
+            decay, put = torch.exp(st * a), st * ut * bt
+            # two products and log2(e) make the exponent; 2^-22.5 of the result is the exponential's own
+            wrong = (st * a).abs() * (2.25 * E + dst + joined) + 3 * E
+            new = decay * h + put
+            err_new = decay * (err + h.abs() * wrong) + put.abs() * (dst + 2 * E) + new.abs() * E
+            h, err = torch.where(on[..., None], new, h), torch.where(on[..., None], err_new, err)
+            row, far = (h * ct).sum(-1), (err * ct.abs()).sum(-1) + (h * ct).abs().sum(-1) * (N // 4 + 4) * E
+            if self.skip is not None:
+                own = self.skip.double() * u[:, t]
+                row, far = row + own, far + E * (row + own).abs()
+            if self.z is not None:
+                z = torch.nan_to_num(self.z[live][:, t].double())
+                gate = z * torch.sigmoid(z)
+                row, far = row * gate, far * gate.abs() + 8 * E * (row * gate).abs()
+            y[live, t] = torch.where(on, row, torch.nan)
+            off_y[live, t] = (far + row.abs() * HALF[self.kind]) * 1.01 + 1e-35
+        state[rows], off[rows] = h, err * 1.01 + 1e-35
+        return y, off_y, state, off
+
+    def step(self):
+        one = lambda x: None if x is None else x[:, 0]  # noqa: E731
+        y = self.y[:, 0].contiguous()
+        self.gdn.ssm_step(one(self.u), one(self.dt), self.a, one(self.b), one(self.c), self.state, ints(self.slot), y, z=one(self.z), skip=self.skip,
+                          dt_bias=self.bias, softplus=self.softplus, status=self.status)
+        self.y = y[:, None]
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(z=False), dict(skip=False), dict(bias=False), dict(softplus=False), dict(softplus=False, bias=False, z=False, skip=False)])
+@pytest.mark.parametrize("N", [8, 16, 32, 64])
+@pytest.mark.parametrize("kind", [BF16, FP32])
+def test_step_and_short_scans_to_their_roundings(gdn, kind, N, kw):  # noqa: F811
+    for B, T, D, G in ((1, 1, 2048, 1), (37, 1, 264, 3), (2, 1, 72, 9)):
+        layer = Exact(gdn, B, T, D, N, G, kind, seed=N + B, **kw)
+        assert layer.check(layer.step) == 0
+    for B, T, D, G, lens in ((3, 1, 72, 1, None), (2, 17, 264, 1, None), (5, 32, 64, 4, [32, 8, 7, 1, 0]), (25, 21, 2048, 1, None)):
+        assert Exact(gdn, B, T, D, N, G, kind, lens, seed=N + T, **kw).check() == 0
+
+
+@pytest.mark.parametrize("B,T,D,N,lens", [(1, 64, 2048, 16, [64]), (1, 300, 264, 32, [300]), (16, 260, 1024, 16, [260] * 16), (40, 96, 2048, 8, [96] * 39 + [5]), (3, 500, 64, 64, None)])
+@pytest.mark.parametrize("kind", [BF16, FP32])
+def test_scans_to_their_roundings(gdn, kind, B, T, D, N, lens):  # noqa: F811
+    assert Exact(gdn, B, T, D, N, 1, kind, lens, seed=T).check() == 0
 
 
 @pytest.mark.parametrize("N", [8, 16, 32, 64])
