@@ -76,7 +76,7 @@ struct Cfg {
   static constexpr int N = N_;
   static constexpr bool BF16 = BF16_;
   static constexpr int LANES = N / 8, CH = OWN * (32 / LANES), ROW = CH / 2, STEPS = 8;
-  static constexpr int ITEMS = STEPS * ROW, U = (ITEMS + 31) / 32;  // of u, dt, z, y; a lane's
+  static constexpr int ITEMS = STEPS * ROW, U = ITEMS / 32;  // of u, dt, z, y; a lane's
   static constexpr int ELEM = BF16 ? 2 : 4;
   // b and c in fp32 in shared memory; else every thread makes its own of bf16. A position's 2 N values
   // are converted by the warp for 512 / N channels: 582 against 612 us at N = 16 (scan of 32 x 512
@@ -84,7 +84,7 @@ struct Cfg {
   static constexpr bool WIDEN = BF16 && N <= 16;
   static constexpr int COPY = STEPS * CH * ELEM / 16, NCOPY = STEPS * N * ELEM / 16;  // 16-byte copies of u, dt or z, and of b or c
   static_assert(CH % 8 == 0, "whole copies");
-  static_assert(ITEMS % 32 == 0 || ITEMS < 32, "every lane has as many");
+  static_assert(ITEMS % 32 == 0, "every lane has as many");
 };
 
 // A warp's part of shared memory: two tiles as they lie in memory, one of which is being loaded,
@@ -245,7 +245,6 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) gdn_ssm_scan_kernel(const 
 #pragma unroll
     for (int k = 0; k < C::U; ++k) {
       const int i = lane + 32 * k;
-      if (C::ITEMS < 32 && i >= C::ITEMS) continue;
       f32x2 dt = pair_of<C::BF16>(reinterpret_cast<const Raw2<C::BF16>*>(raw.dt)[i]);
       if (softplus)
         dt = softplus_2(add2(fma2(dt, both(kLog2e), rest), bias));
@@ -325,7 +324,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) gdn_ssm_scan_kernel(const 
 #pragma unroll
       for (int k = 0; k < C::U; ++k) {
         const int i = lane + 32 * k, t = i / C::ROW;
-        if (!pair_live || t0 + t >= end || (C::ITEMS < 32 && i >= C::ITEMS)) continue;
+        if (!pair_live || t0 + t >= end) continue;
         f32x2 y = fma2(skip, pair_of<C::BF16>(reinterpret_cast<const Raw2<C::BF16>*>(raw.u)[i]), reinterpret_cast<const f32x2*>(sm.y)[i]);
         if (gated) y = mul2(y, silu_2<!C::BF16>(pair_of<C::BF16>(reinterpret_cast<const Raw2<C::BF16>*>(raw.z)[i])));
         *reinterpret_cast<Raw2<C::BF16>*>(y_at + 32 / C::ROW * k * y_row) = raw_of<C::BF16>(y);
