@@ -528,7 +528,7 @@ typedef struct gdn_norm {
  * the e4m3 value next to the fp32 quotient o / s: o is about s times what is stored. A NaN makes its row NaN, an
  * infinity makes itself NaN and the rest of its row 0, as the formula says, and a scale whose
  * channels hold NaN is NaN. Squares are summed in fp32: a sum past its range (values above about
- * 1e19) counts as infinite.
+ * 1e19) counts as infinite, squares below it (values under about 1e-23) as nothing.
  */
 int gdn_add_rms_norm(const gdn_norm *norm, void *stream);
 

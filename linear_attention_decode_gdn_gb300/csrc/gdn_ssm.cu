@@ -127,7 +127,7 @@ cudaError_t launch_step(const SsmParams& given, cudaStream_t stream) {
   p.blocks = (p.per_group + CH - 1) / CH;
   p.columns = p.blocks * p.s.num_groups;
   const int64_t all = static_cast<int64_t>(p.columns) * p.s.batch;
-    p.rows = all >= 32768 ? 2 : 1;  // a is loaded once for both: 47.7 us at 2, 48.3 at 4, 50.3 at 1 (512 x 4096 channels)
+  p.rows = all >= 32768 ? 2 : 1;  // a is loaded once for both: 47.7 us at 2, 48.3 at 4, 50.3 at 1 (512 x 4096 channels)
   const int64_t warps = static_cast<int64_t>(p.columns) * ((p.s.batch + p.rows - 1) / p.rows);
   return launch_overlapped(gdn_ssm_step_kernel<N, BF16>, p, dim3(static_cast<unsigned>((warps + kStepWarps - 1) / kStepWarps)),
                            kStepWarps * 32, 0, 1u, stream);

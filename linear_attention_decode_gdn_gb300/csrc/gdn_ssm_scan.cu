@@ -33,7 +33,7 @@ namespace gdn {
 namespace {
 
 constexpr int kWarps = 4;  // of a CTA; they have nothing in common
-constexpr int kCtas = 4;   // of an SM
+constexpr int kCtas = 4;   // of an SM (two of fp32 with 8 states and two channels a thread, whose shared memory is 81 KB)
 
 // Two elements as they lie in memory.
 template <bool BF16>
@@ -97,7 +97,9 @@ struct WarpSmem {
   ulonglong2 in[C::ITEMS];
   float y[C::STEPS][C::CH];
   float b[C::WIDEN ? C::STEPS : 1][C::N], c[C::WIDEN ? C::STEPS : 1][C::N];
-  float bias[2][C::CH], skip[C::CH];  // bias: with softplus its product with log2(e), as the sum of two
+  // bias: with softplus its product with log2(e) and what its rounding lost. The step's argument is off
+  // by one rounding of dt and one of the sum, and by none of bias.
+  float bias[2][C::CH], skip[C::CH];
 };
 
 // Where the prompts' channels are too few for the GPU, prompts are cut into parts of `part` positions
@@ -400,6 +402,8 @@ __global__ void __launch_bounds__(kJoinThreads) gdn_ssm_join_kernel(const ScanPa
 //   where prompts have lengths of their own, of which a whole one holds up the end (8 ragged prompts,
 //   1024 warps: 457 us whole, 292 in 7 parts; of equal length 477 and 471): parts without positions
 //   cost next to nothing, so 0.6 of the time is reckoned there.
+// The model knows neither types nor groups: it takes four CTAs an SM also where two fit (kCtas), blocks
+// of 512 / N channels also where groups end inside them, and prompts with seq_lens for ragged ones.
 // A join goes through all parts in turn, so there are at most sqrt(T) of them, of 32 positions at least.
 struct Cut {
   int32_t parts, part;
